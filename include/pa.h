@@ -1,17 +1,22 @@
 /*
  * pa.h — C ABI of libpa, the GB300 (sm_103a) paged KV-cache decode path.
  *
- * Three device operations, each asynchronous on the caller's stream:
+ * Device operations, each asynchronous on the caller's stream:
  *
  *   pa_reshape_and_cache  write new tokens' K and V into fixed-size physical
- *                         blocks through a slot mapping (optionally as FP8
- *                         or INT8 with a scale per tensor or per KV head);
+ *                         blocks through a slot mapping (optionally as FP8,
+ *                         INT8 or four-bit codes with a scale per tensor or
+ *                         per KV head);
+ *   pa_gather_cache       read tokens' K and V back through a slot mapping,
+ *                         as the 16-bit values they stand for;
  *   pa_decode             single-query decode attention over the paged cache,
  *                         reached through per-sequence block tables;
  *   pa_prefill            causal attention of several new tokens per sequence
  *                         over the paged cache (the part of a prompt a
  *                         prefix-cache hit did not cover);
  *   pa_copy_blocks        whole-block copies, the copy step of copy-on-write;
+ *   pa_compact_blocks     whole-block moves that draw a pool's live blocks
+ *                         together, with the block tables renamed to match;
  *   pa_swap_blocks        whole-block moves between the device caches and a
  *                         pool in host memory (swap-out / swap-in).
  *
@@ -96,7 +101,9 @@ typedef enum {
   PA_BF16 = 1,      /* bfloat16 */
   PA_FP8_E4M3 = 2,  /* OCP E4M3 (max 448, no inf), one byte */
   PA_FP8_E5M2 = 3,  /* OCP E5M2 (max 57344), one byte */
-  PA_INT8 = 4       /* two's-complement int8 code, one byte */
+  PA_INT8 = 4,      /* two's-complement int8 code, one byte */
+  /* four-bit formats start at 16 */
+  PA_FP4 = 16       /* e2m1 codes, an e4m3 scale for every 16 (see below) */
 } pa_dtype;
 
 /*
@@ -109,6 +116,14 @@ typedef enum {
  * ([P3] §6.1; default 1.0 per tensor, one per head optionally, §6.3).
  * sk(h) is k_head_scales[h] when that pointer is not NULL, else k_scale
  * (likewise for V).
+ * PA_FP4 stores a token's row of one head as head_dim / 2 bytes of e2m1
+ * codes (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit; dimension 2j
+ * in the low half of byte j, 2j + 1 in the high half) and one e4m3 scale for
+ * every 16 consecutive dimensions.  A (block, head) tile is block_size rows
+ * of codes followed by its scales as [head_dim / 16, block_size] bytes, so a
+ * cache holds num_blocks * kv_heads tiles of block_size * head_dim * 9 / 16
+ * bytes.  Code c of a group with scale g means c * g * sk(h) in K and
+ * c * g * sv(h) in V.
  * Supported set: block_size in {8, 16, 32}; head_dim in {64, 128}.
  */
 typedef struct {
@@ -117,9 +132,9 @@ typedef struct {
   int32_t block_size;
   int32_t head_dim;
   int32_t dtype;     /* pa_dtype */
-  float k_scale;     /* one-byte caches only; must be > 0 and finite */
+  float k_scale;     /* coded (FP8, INT8, FP4) caches only; must be > 0 and finite */
   float v_scale;
-  /* One-byte caches only, else must be NULL: DEVICE float32 [kv_heads],
+  /* Coded caches only, else must be NULL: DEVICE float32 [kv_heads],
    * one scale per KV head (each > 0 and finite; not checked), or NULL for
    * the per-tensor scales above.  Read by the kernels, so they must stay
    * valid until the calls that use them have run. */
@@ -144,6 +159,11 @@ typedef struct {
  * for INT8 caches, the same quotient rounded to the nearest integer (ties
  * to even) and saturated to [-128, 127], with NaN stored as 0.  The scale
  * is head h's (see pa_cache_desc).
+ * For PA_FP4 caches the same quotients y are taken 16 dimensions at a time:
+ * the group's scale g is the largest |y| that is not NaN, divided by 6 and
+ * rounded to the nearest e4m3 value (ties to even, at most 448); a code is
+ * the e2m1 value nearest to y / g (ties to even, saturated to +-6), 0 for
+ * NaN, and 0 throughout when g is 0.
  * Slots must be distinct among the call's tokens.  A slot >= num_blocks *
  * block_size is skipped and reported as device error 2.
  */
@@ -152,6 +172,32 @@ PA_API pa_status pa_reshape_and_cache(const void *key, const void *value,
                                int32_t num_tokens, void *k_cache, void *v_cache,
                                const pa_cache_desc *cache, int *device_error,
                                pa_stream_t stream);
+
+/*
+ * pa_gather_cache — read T tokens' K and V back from the paged caches: the
+ * inverse of pa_reshape_and_cache.  For a caller that attends to, checks or
+ * re-encodes what the cache holds (a prompt's own attention over its stored
+ * values, a move to a cache of another type).
+ *
+ *   key, value     device, [num_tokens, kv_heads, head_dim] of dst_dtype,
+ *                  written: PA_F16 or PA_BF16; the cache's own type for
+ *                  16-bit caches.
+ *   slot_mapping   device int64 [num_tokens]: flat slot of token t; -1 marks
+ *                  a padding row, which is set to zero.  Slots may repeat.
+ *   k_cache/v_cache  device caches described by *cache, only read.
+ * For every token t with slot >= 0 and every head h:
+ *   row[t, h, :] = dec(cache[slot / block_size, h, slot % block_size, :])
+ * where dec is a bit copy for 16-bit caches and otherwise the value the codes
+ * stand for (code * scale in IEEE float32; for PA_FP4 the exact product of
+ * code and group scale, times the head's), rounded to nearest even.  A slot
+ * outside the cache leaves its row as it was and is reported as device
+ * error 2.
+ */
+PA_API pa_status pa_gather_cache(void *key, void *value, int32_t dst_dtype,
+                                 const int64_t *slot_mapping, int32_t num_tokens,
+                                 const void *k_cache, const void *v_cache,
+                                 const pa_cache_desc *cache, int *device_error,
+                                 pa_stream_t stream);
 
 /*
  * pa_decode_workspace_size — bytes of device workspace pa_decode needs for
@@ -193,7 +239,7 @@ PA_API size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads,
  *                  bytes, 256-byte aligned; contents need no initialisation.
  *                  Calls sharing one workspace must be stream-ordered.
  * Supported set: num_q_heads / kv_heads in {1, 2, 4, 8}; cache dtypes of
- * pa_cache_desc; one-byte caches accept q in PA_F16 or PA_BF16.
+ * pa_cache_desc; coded caches accept q in PA_F16 or PA_BF16.
  * Stream order: the call's first kernel may begin reading block_tables and
  * seq_lens while the kernel before it on the stream is still running, if
  * that kernel has signalled programmatic completion early
@@ -230,7 +276,7 @@ PA_API pa_status pa_decode(void *out, const void *q, int32_t q_dtype,
  *
  *   out, q         device [num_q_tokens, num_q_heads, head_dim] of q_dtype:
  *                  the cache dtype for 16-bit caches, PA_F16 or PA_BF16 for
- *                  one-byte ones; num_q_tokens = cu_q_lens[num_seqs].
+ *                  coded ones; num_q_tokens = cu_q_lens[num_seqs].
  *   cu_q_lens      device int32 [num_seqs + 1], non-decreasing, from 0;
  *                  every sequence's rows must lie in [0, num_q_tokens).
  *   max_q_len      host upper bound of n_s, used to size the grid.
@@ -242,7 +288,7 @@ PA_API pa_status pa_decode(void *out, const void *q, int32_t q_dtype,
  * block 0 instead and reports error 1; a stalled pipeline reports error 4.
  * Supported set: num_q_heads / kv_heads in {1, 2, 4, 8}; block_size and
  * head_dim as in pa_cache_desc; num_seqs and kv_heads <= 65535.  Needs no
- * workspace and allocates nothing.  With a one-byte cache the products run
+ * workspace and allocates nothing.  With a coded cache the products run
  * on fp16 operands: a bf16 q is rounded to fp16 after scaling each 128-row
  * query tile by a power of two that brings its largest |q| within 2^15.
  */
@@ -303,6 +349,34 @@ PA_API pa_status pa_decode_static_scratch(
 PA_API pa_status pa_copy_blocks(void *k_cache, void *v_cache, const pa_cache_desc *cache,
                          const int64_t *block_mapping, int32_t num_pairs,
                          int *device_error, pa_stream_t stream);
+
+/*
+ * pa_compact_blocks — move live blocks to other places of the same pool and
+ * rename them in the block tables, in one launch.  The pages have no
+ * counterpart: they hand blocks out from a free pool, so live blocks end up
+ * anywhere in it, and giving memory back ([P1] §2.1's pool sized to the
+ * device) needs them together.  pa_prefix_cache_compact plans the moves.
+ *
+ *   block_mapping  device int64 [num_pairs, 2]: (src, dst) physical blocks,
+ *                  strictly ascending by src.  Destinations must be distinct
+ *                  and never also a source.
+ *   block_tables   device int32 [num_seqs, max_blocks_per_seq], renamed in
+ *                  place: an entry among the first ceil(L_s / block_size) of
+ *                  row s that equals some src becomes its dst; entries behind
+ *                  them are left as they were.
+ *   seq_lens       device int32 [num_seqs], as in pa_decode.
+ * For each pair, block dst of k_cache and of v_cache becomes a bit-exact
+ * copy of block src.  A pair with an id outside the pool is skipped (its
+ * block is not renamed either); it and a src not above the one before it are
+ * reported as device error 5.  A length outside [0, max_blocks_per_seq *
+ * block_size] leaves its row as it was and is reported as device error 3.
+ * Calls that share block_tables must be stream-ordered, like every call that
+ * reads them.
+ */
+PA_API pa_status pa_compact_blocks(void *k_cache, void *v_cache, const pa_cache_desc *cache,
+                                   const int64_t *block_mapping, int32_t num_pairs,
+                                   int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                   const int32_t *seq_lens, int *device_error, pa_stream_t stream);
 
 typedef enum {
   PA_SWAP_OUT = 0, /* device cache block src -> second-pool block dst */
@@ -405,6 +479,24 @@ PA_API pa_status pa_prefix_cache_append_token(pa_prefix_cache *cache, int64_t se
                                               int32_t token, int64_t *slot);
 
 PA_API pa_status pa_prefix_cache_free_sequence(pa_prefix_cache *cache, int64_t seq_id);
+
+/* New sequence child (must not exist) with parent's tokens ([P1] §6.1: the
+ * beams of one prompt).  Full blocks are shared (reference count + 1); a
+ * partial last block is replaced by a fresh private one, and
+ * copy_pair[0..1] = (parent's block, child's block) to pass to
+ * pa_copy_blocks, or (-1, -1) when nothing has to be copied. */
+PA_API pa_status pa_prefix_cache_fork_sequence(pa_prefix_cache *cache, int64_t parent, int64_t child,
+                                               int64_t copy_pair[2]);
+
+/* Draws the kept blocks together: every block with a nonzero reference count
+ * or a key moves below the number of such blocks; sequences' tables, keys,
+ * reference counts and the free list's order of keyed blocks follow.
+ * Unkeyed free blocks keep no content and join the free list's front in
+ * ascending order.  Returns the number of moves; writes them to `pairs`
+ * (host int64 [capacity, 2]: (src, dst), ascending by src, as
+ * pa_compact_blocks takes them).  With fewer than that many rows of capacity
+ * (or pairs NULL) nothing is changed; -1 for a NULL handle. */
+PA_API int32_t pa_prefix_cache_compact(pa_prefix_cache *cache, int64_t *pairs, int32_t capacity);
 
 /* Block table of one sequence: returns its length (or -1 for an unknown
  * sequence) and copies up to `capacity` entries to `table` (nullable);

@@ -150,6 +150,48 @@ class PrefixCache:
                 self.free[b] = None          # most recently freed at the back
         del self.tokens[seq]
 
+    def fork_sequence(self, parent: int, child: int) -> Optional[Tuple[int, int]]:
+        """``child`` gets ``parent``'s tokens and shares its full blocks; a
+        partial last block is replaced by a fresh one.  Returns the (src,
+        dst) copy that needs, or None."""
+        if child in self.tables:
+            raise ValueError("sequence exists")
+        table, pair = list(self.tables[parent]), None
+        if len(self.tokens[parent]) % self.block_size:
+            if not self.free:
+                raise OutOfBlocks("no free block")
+            pair = (table[-1], self._take_fresh())
+            table[-1] = pair[1]
+        for b in table[:-1] if pair else table:
+            self.ref[b] += 1
+        self.tables[child] = table
+        self.tokens[child] = list(self.tokens[parent])
+        return pair
+
+    def compact(self) -> List[Tuple[int, int]]:
+        """Moves (src, dst) that bring every kept block (in use, or keyed)
+        below the number of kept blocks: those already there stay, the others
+        fill the unkept places in ascending order."""
+        kept = [b for b in range(self.num_blocks) if self.ref[b] or self.key_of[b] is not None]
+        n = len(kept)
+        holes = [b for b in range(n) if b not in set(kept)]
+        moves = list(zip([b for b in kept if b >= n], holes))
+        name = dict(moves)
+        keyed_free = [b for b in self.free if self.key_of[b] is not None]
+        ref, keys = list(self.ref), list(self.key_of)
+        for src, dst in moves:
+            ref[dst], keys[dst] = self.ref[src], self.key_of[src]
+            ref[src], keys[src] = 0, None
+        self.ref[:], self.key_of[:] = ref, keys
+        self.block_of = {k: name.get(b, b) for k, b in self.block_of.items()}
+        self.tables = {s: [name.get(b, b) for b in t] for s, t in self.tables.items()}
+        self.free.clear()
+        for b in range(n, self.num_blocks):
+            self.free[b] = None
+        for b in keyed_free:
+            self.free[name.get(b, b)] = None
+        return moves
+
     # -- views ----------------------------------------------------------
     def table(self, seq: int) -> List[int]:
         return list(self.tables[seq])

@@ -5,15 +5,24 @@ Argument marshalling only: every step runs in the CUDA kernels of
 functions carry the C ABI's names:
 
     pa_reshape_and_cache   write new tokens' K/V into the paged caches
+    pa_gather_cache        read tokens' K/V back from the paged caches
     pa_decode              paged single-query decode attention
     pa_prefill             paged causal attention of several new tokens per
                            sequence (the part a prefix hit did not cover)
     pa_copy_blocks         whole-block copies (copy-on-write)
+    pa_compact_blocks      whole-block moves that draw a pool's live blocks
+                           together, with the block tables renamed
     pa_swap_blocks         whole-block moves between the device caches and
                            a pool in page-locked host memory
     pa_decode_workspace_size
     PrefixCache            the host block pool with prefix caching
                            (pa_prefix_cache_*)
+
+Caches are ``[num_blocks, kv_heads, block_size, head_dim]`` tensors of the
+stored type (FP8 and INT8 also as uint8).  A four-bit cache
+(``cache_dtype="fp4"``) is a uint8 tensor ``[num_blocks, kv_heads, block_size,
+head_dim * 9 / 16]``: ``fp4_cache_shape`` gives it; the last two dimensions
+together are one tile of codes and scales (laid out in ``include/pa.h``).
 
 PyTorch supplies the device memory and the stream; there is no CPU or
 PyTorch fallback: if ``libpa.so`` is missing, every call raises.
@@ -29,17 +38,18 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpa.so")
 
-PA_F16, PA_BF16, PA_FP8_E4M3, PA_FP8_E5M2, PA_INT8 = 0, 1, 2, 3, 4
+PA_F16, PA_BF16, PA_FP8_E4M3, PA_FP8_E5M2, PA_INT8, PA_FP4 = 0, 1, 2, 3, 4, 16
 DTYPE_CODES = {"f16": PA_F16, "bf16": PA_BF16, "e4m3": PA_FP8_E4M3, "e5m2": PA_FP8_E5M2,
-               "int8": PA_INT8}
+               "int8": PA_INT8, "fp4": PA_FP4}
 _TORCH_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.int8: PA_INT8}
 if hasattr(torch, "float8_e4m3fn"):
     _TORCH_CODES[torch.float8_e4m3fn] = PA_FP8_E4M3
 if hasattr(torch, "float8_e5m2"):
     _TORCH_CODES[torch.float8_e5m2] = PA_FP8_E5M2
 
-EXPORTED = ("pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode", "pa_prefill",
-            "pa_decode_static_scratch", "pa_copy_blocks", "pa_swap_blocks",
+EXPORTED = ("pa_reshape_and_cache", "pa_gather_cache", "pa_decode_workspace_size", "pa_decode",
+            "pa_prefill", "pa_decode_static_scratch", "pa_copy_blocks", "pa_compact_blocks",
+            "pa_swap_blocks", "pa_prefix_cache_fork_sequence", "pa_prefix_cache_compact",
             "pa_status_string", "pa_last_cuda_error", "pa_selftest_wait_timeout",
             "pa_prefix_cache_create", "pa_prefix_cache_destroy", "pa_prefix_cache_add_sequence",
             "pa_prefix_cache_append_token", "pa_prefix_cache_free_sequence",
@@ -87,6 +97,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_reshape_and_cache.argtypes = [vp, vp, i32, i64p, i32, vp, vp,
                                          ctypes.POINTER(PaCacheDesc), vp, vp]
     lib.pa_reshape_and_cache.restype = ctypes.c_int
+    lib.pa_gather_cache.argtypes = lib.pa_reshape_and_cache.argtypes
+    lib.pa_gather_cache.restype = ctypes.c_int
     lib.pa_decode_workspace_size.argtypes = [i32] * 6
     lib.pa_decode_workspace_size.restype = ctypes.c_size_t
     lib.pa_decode.argtypes = [vp, vp, i32, i32, i32, vp, vp, ctypes.POINTER(PaCacheDesc),
@@ -99,6 +111,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_decode_static_scratch.restype = ctypes.c_int
     lib.pa_copy_blocks.argtypes = [vp, vp, ctypes.POINTER(PaCacheDesc), vp, i32, vp, vp]
     lib.pa_copy_blocks.restype = ctypes.c_int
+    lib.pa_compact_blocks.argtypes = [vp, vp, ctypes.POINTER(PaCacheDesc), vp, i32, vp, i32, i32, vp, vp, vp]
+    lib.pa_compact_blocks.restype = ctypes.c_int
     lib.pa_prefill.argtypes = [vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, ctypes.POINTER(PaCacheDesc),
                                vp, i32, vp, ctypes.c_float, vp, vp]
     lib.pa_prefill.restype = ctypes.c_int
@@ -113,6 +127,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_prefix_cache_add_sequence.argtypes = [vp, i64, vp, i32, i32p]
     lib.pa_prefix_cache_append_token.argtypes = [vp, i64, i32, ctypes.POINTER(ctypes.c_int64)]
     lib.pa_prefix_cache_free_sequence.argtypes = [vp, i64]
+    lib.pa_prefix_cache_fork_sequence.argtypes = [vp, i64, i64, ctypes.POINTER(ctypes.c_int64)]
+    lib.pa_prefix_cache_compact.argtypes = [vp, vp, i32]
+    lib.pa_prefix_cache_compact.restype = i32
     lib.pa_prefix_cache_block_table.argtypes = [vp, i64, vp, i32, i32p]
     lib.pa_prefix_cache_block_table.restype = i32
     lib.pa_prefix_cache_block_tables.argtypes = [vp, vp, i32, vp, i32, vp]
@@ -122,7 +139,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_prefix_cache_ref_count.argtypes = [vp, i32]
     lib.pa_prefix_cache_ref_count.restype = i32
     for name in ("pa_prefix_cache_add_sequence", "pa_prefix_cache_append_token",
-                 "pa_prefix_cache_free_sequence", "pa_prefix_cache_block_tables",
+                 "pa_prefix_cache_free_sequence", "pa_prefix_cache_fork_sequence",
+                 "pa_prefix_cache_block_tables",
                  "pa_prefix_cache_get_stats"):
         getattr(lib, name).restype = ctypes.c_int
     lib.pa_selftest_wait_timeout.argtypes = [vp, vp]
@@ -165,7 +183,7 @@ def _cache_code(k_cache: torch.Tensor, cache_dtype) -> int:
         return DTYPE_CODES[cache_dtype] if isinstance(cache_dtype, str) else int(cache_dtype)
     if k_cache.dtype in _TORCH_CODES:
         return _TORCH_CODES[k_cache.dtype]
-    raise ValueError("cache_dtype is required for a byte-typed FP8 cache")
+    raise ValueError("cache_dtype is required for a byte-typed cache")
 
 
 def _scale_arg(scale, kv_heads: int, name: str):
@@ -180,6 +198,11 @@ def _scale_arg(scale, kv_heads: int, name: str):
     return float(scale), None
 
 
+def fp4_cache_shape(num_blocks: int, kv_heads: int, block_size: int, head_dim: int):
+    """Shape of the uint8 tensor that holds a four-bit K (or V) cache."""
+    return num_blocks, kv_heads, block_size, head_dim * 9 // 16
+
+
 def cache_desc(k_cache: torch.Tensor, cache_dtype=None, k_scale=1.0,
                v_scale=1.0) -> PaCacheDesc:
     """Descriptor of a cache pair; k_scale / v_scale are numbers (per tensor)
@@ -188,14 +211,33 @@ def cache_desc(k_cache: torch.Tensor, cache_dtype=None, k_scale=1.0,
     if k_cache.dim() != 4:
         raise ValueError("cache must be [num_blocks, kv_heads, block_size, head_dim]")
     nb, h, bs, d = k_cache.shape
+    code = _cache_code(k_cache, cache_dtype)
+    if code == PA_FP4:
+        if k_cache.element_size() != 1 or d % 9:
+            raise ValueError("a four-bit cache is a one-byte tensor [num_blocks, kv_heads, block_size, "
+                             "head_dim * 9 / 16]")
+        d = d // 9 * 16
     ks, kp = _scale_arg(k_scale, h, "k_scale")
     vs, vp = _scale_arg(v_scale, h, "v_scale")
-    return PaCacheDesc(nb, h, bs, d, _cache_code(k_cache, cache_dtype), ks, vs, kp, vp)
+    return PaCacheDesc(nb, h, bs, d, code, ks, vs, kp, vp)
 
 
 def _require(t: torch.Tensor, name: str) -> None:
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
+
+
+def _check_fp4(desc, k_cache, v_cache, q=None, seqs=None, block_tables=None, seq_lens=None) -> None:
+    """Shapes that the C ABI of a four-bit cache takes on trust."""
+    if desc.dtype != PA_FP4:
+        return
+    if v_cache.shape != k_cache.shape or v_cache.element_size() != 1:
+        raise ValueError("k_cache and v_cache must have one shape and be one-byte tensors")
+    if q is not None and (q.dim() != 3 or q.shape[2] != desc.head_dim):
+        raise ValueError(f"q/out must be [rows, Hq, {desc.head_dim}]")
+    if block_tables is not None and (block_tables.dim() != 2 or block_tables.shape[0] < seqs
+                                     or seq_lens.numel() < seqs):
+        raise ValueError("block_tables must be [S, width] and seq_lens [S]")
 
 
 def pa_reshape_and_cache(key, value, slot_mapping, k_cache, v_cache, cache_dtype=None,
@@ -211,12 +253,42 @@ def pa_reshape_and_cache(key, value, slot_mapping, k_cache, v_cache, cache_dtype
     src = _TORCH_CODES.get(key.dtype)
     if src is None or key.dtype != value.dtype:
         raise ValueError("key/value must be float16 or bfloat16 of one dtype")
+    _check_fp4(desc, k_cache, v_cache)
+    if desc.dtype == PA_FP4 and (key.shape != value.shape or
+                                 key.numel() != slot_mapping.numel() * desc.kv_heads * desc.head_dim):
+        raise ValueError(f"key/value must be [T, {desc.kv_heads}, {desc.head_dim}] with one slot a row")
     lib = load_library()
     _check(lib.pa_reshape_and_cache(key.data_ptr(), value.data_ptr(), src,
                                     slot_mapping.data_ptr(), slot_mapping.numel(),
                                     k_cache.data_ptr(), v_cache.data_ptr(),
                                     ctypes.byref(desc), _ptr(device_error), _stream(stream)),
            "pa_reshape_and_cache")
+
+
+def pa_gather_cache(key, value, slot_mapping, k_cache, v_cache, cache_dtype=None,
+                    k_scale=1.0, v_scale=1.0, device_error=None, stream=None) -> None:
+    """Read rows ``key/value [T, kv_heads, head_dim]`` (float16 or bfloat16,
+    written) back from the caches: the values that the stored rows of
+    ``slot_mapping`` stand for, zero where it is -1."""
+    for t, n in ((key, "key"), (value, "value"), (slot_mapping, "slot_mapping"),
+                 (k_cache, "k_cache"), (v_cache, "v_cache")):
+        _require(t, n)
+    if slot_mapping.dtype != torch.int64:
+        raise ValueError("slot_mapping must be int64")
+    desc = cache_desc(k_cache, cache_dtype, k_scale, v_scale)
+    dst = _TORCH_CODES.get(key.dtype)
+    if dst is None or key.dtype != value.dtype:
+        raise ValueError("key/value must be float16 or bfloat16 of one dtype")
+    rows = (slot_mapping.numel(), desc.kv_heads, desc.head_dim)
+    if tuple(key.shape) != rows or tuple(value.shape) != rows:
+        raise ValueError(f"key/value must be [{', '.join(map(str, rows))}]")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and dtype")
+    lib = load_library()
+    _check(lib.pa_gather_cache(key.data_ptr(), value.data_ptr(), dst, slot_mapping.data_ptr(),
+                               slot_mapping.numel(), k_cache.data_ptr(), v_cache.data_ptr(),
+                               ctypes.byref(desc), _ptr(device_error), _stream(stream)),
+           "pa_gather_cache")
 
 
 def pa_decode_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
@@ -240,6 +312,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len: int
     qcode = _TORCH_CODES.get(q.dtype)
     if qcode not in (PA_F16, PA_BF16) or out.dtype != q.dtype or tuple(out.shape) != (S, Hq, D):
         raise ValueError("q/out must be float16 or bfloat16 [S, Hq, head_dim] of one dtype")
+    _check_fp4(desc, k_cache, v_cache, q, S, block_tables, seq_lens)
     need = pa_decode_workspace_size(S, Hq, desc.kv_heads, D, max_seq_len, partition_size)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
@@ -270,6 +343,7 @@ def pa_prefill(out, q, cu_q_lens, k_cache, v_cache, block_tables, seq_lens, max_
     qcode = _TORCH_CODES.get(q.dtype)
     if out.dtype != q.dtype or out.shape != q.shape or q.dim() != 3:
         raise ValueError("q/out must be [T, Hq, head_dim] of one dtype")
+    _check_fp4(desc, k_cache, v_cache, q, cu_q_lens.numel() - 1, block_tables, seq_lens)
     lib = load_library()
     _check(lib.pa_prefill(out.data_ptr(), q.data_ptr(), -1 if qcode is None else qcode, q.shape[0],
                           cu_q_lens.data_ptr(), cu_q_lens.numel() - 1, q.shape[1], int(max_q_len),
@@ -297,6 +371,7 @@ def pa_decode_static_scratch(out, q, k_cache, v_cache, block_tables, seq_lens,
         _require(t, n)
     desc = cache_desc(k_cache, cache_dtype, k_scale, v_scale)
     S, Hq, D = q.shape
+    _check_fp4(desc, k_cache, v_cache, q, S, block_tables, seq_lens)
     need = pa_decode_workspace_size(S, Hq, desc.kv_heads, D, max_seq_len, partition_size)
     if need > STATIC_SCRATCH_BYTES:
         raise PaError(f"pa_decode_static_scratch: these sizes need {need} bytes of scratch, "
@@ -331,6 +406,31 @@ def pa_copy_blocks(k_cache, v_cache, block_mapping, cache_dtype=None, device_err
                               block_mapping.data_ptr(), block_mapping.shape[0],
                               _ptr(device_error), _stream(stream)),
            "pa_copy_blocks")
+
+
+def pa_compact_blocks(k_cache, v_cache, block_mapping, block_tables, seq_lens, cache_dtype=None,
+                      device_error=None, stream=None) -> None:
+    """Move block src to dst for each row of ``block_mapping [n, 2]`` (int64,
+    ascending by src, as ``PrefixCache.compact`` gives them) and rename the
+    blocks in ``block_tables`` (int32 ``[S, width]``, in place)."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (block_mapping, "block_mapping"),
+                 (block_tables, "block_tables"), (seq_lens, "seq_lens")):
+        _require(t, n)
+    if block_mapping.dtype != torch.int64 or block_mapping.dim() != 2 or block_mapping.shape[1] != 2:
+        raise ValueError("block_mapping must be int64 [n, 2]")
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise ValueError("block_tables and seq_lens must be int32")
+    if block_tables.dim() != 2 or seq_lens.numel() != block_tables.shape[0]:
+        raise ValueError("block_tables must be [S, width] and seq_lens [S]")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and dtype")
+    desc = cache_desc(k_cache, cache_dtype)
+    lib = load_library()
+    _check(lib.pa_compact_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc),
+                                 block_mapping.data_ptr(), block_mapping.shape[0], block_tables.data_ptr(),
+                                 block_tables.shape[0], max(1, block_tables.shape[1]), seq_lens.data_ptr(),
+                                 _ptr(device_error), _stream(stream)),
+           "pa_compact_blocks")
 
 
 def pa_swap_blocks(k_cache, v_cache, host_k, host_v, block_mapping, direction: str,
@@ -409,6 +509,25 @@ class PrefixCache:
 
     def free_sequence(self, seq: int) -> None:
         _check(self._lib.pa_prefix_cache_free_sequence(self._h, int(seq)), "free_sequence")
+
+    def fork_sequence(self, parent: int, child: int):
+        """New sequence ``child`` with ``parent``'s tokens, its full blocks
+        shared.  Returns the (src, dst) block pair to pass to
+        ``pa_copy_blocks``, or None when nothing has to be copied."""
+        pair = (ctypes.c_int64 * 2)()
+        _check(self._lib.pa_prefix_cache_fork_sequence(self._h, int(parent), int(child), pair), "fork_sequence")
+        return None if pair[0] < 0 else (pair[0], pair[1])
+
+    def compact(self):
+        """Draw the kept blocks (in use or keyed) together at the front of
+        the pool.  Returns the moves as int64 ``[n, 2]`` (src, dst), for
+        ``pa_compact_blocks``; tables read after this name the new blocks."""
+        import numpy as np
+        n = self._lib.pa_prefix_cache_compact(self._h, None, 0)
+        pairs = np.zeros((max(n, 1), 2), dtype=np.int64)
+        if self._lib.pa_prefix_cache_compact(self._h, pairs.ctypes.data, n) != n:
+            raise PaError("compact failed")
+        return pairs[:n]
 
     def table(self, seq: int):
         import numpy as np

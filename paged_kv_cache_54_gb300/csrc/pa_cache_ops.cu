@@ -3,6 +3,7 @@
 // one 16-byte vector of the destination per iteration of a grid-stride loop,
 // so reads and writes of a warp are contiguous 512-byte runs.
 #include "pa_common.cuh"
+#include "pa_fp4.h"
 #include "pa_host.h"
 
 namespace pa {
@@ -188,16 +189,6 @@ __global__ void selftest_wait_kernel(int *err) {
   if (threadIdx.x == 0 && !mbar_wait(&bar, 0, nullptr)) record_error(err, kErrTimeout);
 }
 
-int grid_for(long long work_items, int threads) {
-  DeviceInfo info;
-  int sms = current_device_info(&info) ? info.sm_count : 148;
-  long long blocks = (work_items + threads - 1) / threads;
-  long long cap = static_cast<long long>(sms) * 8;
-  if (blocks > cap) blocks = cap;
-  if (blocks < 1) blocks = 1;
-  return static_cast<int>(blocks);
-}
-
 }  // namespace
 }  // namespace pa
 
@@ -217,6 +208,10 @@ extern "C" pa_status pa_reshape_and_cache(const void *key, const void *value, in
   if (!supported_cache_shape(cache)) return PA_ERR_UNSUPPORTED;
   const int dst = cache->dtype;
   if ((dst == PA_F16 || dst == PA_BF16) && dst != src_dtype) return PA_ERR_UNSUPPORTED;
+
+  if (dst == PA_FP4)
+    return write_fp4(key, value, src_dtype, slot_mapping, num_tokens, k_cache, v_cache, cache, device_error,
+                     reinterpret_cast<cudaStream_t>(stream));
 
   const int H = cache->kv_heads, D = cache->head_dim, bs = cache->block_size;
   const long long nslots = static_cast<long long>(cache->num_blocks) * bs;
@@ -260,8 +255,7 @@ extern "C" pa_status pa_copy_blocks(void *k_cache, void *v_cache, const pa_cache
   if (!aligned16(k_cache) || !aligned16(v_cache) || (reinterpret_cast<uintptr_t>(block_mapping) & 7u))
     return PA_ERR_INVALID;
   if (!supported_cache_shape(cache)) return PA_ERR_UNSUPPORTED;
-  const long long block_bytes = static_cast<long long>(cache->kv_heads) * cache->block_size *
-                                cache->head_dim * elt_bytes(cache->dtype);
+  const long long block_bytes = cache_block_bytes(cache);
   const long long work = static_cast<long long>(num_pairs) * 2 * (block_bytes / 16);
   const int threads = 256;
   const int blocks = grid_for(work, threads);
@@ -289,8 +283,7 @@ extern "C" pa_status pa_swap_blocks(void *k_cache, void *v_cache, const pa_cache
   if (e != cudaSuccess) return cuda_fail(e);
   uint8_t *hk = nullptr, *hv = nullptr;
   if (!device_view(host_k, device, &hk) || !device_view(host_v, device, &hv)) return PA_ERR_UNSUPPORTED;
-  const long long block_bytes = static_cast<long long>(cache->kv_heads) * cache->block_size *
-                                cache->head_dim * elt_bytes(cache->dtype);
+  const long long block_bytes = cache_block_bytes(cache);
   const long long work = static_cast<long long>(num_pairs) * 2 * (block_bytes / 16);
   const int threads = 256;
   const int blocks = grid_for((work + kSwapUnroll - 1) / kSwapUnroll, threads);

@@ -11,7 +11,7 @@
 
 namespace pa {
 
-enum DType : int { kF16 = 0, kBF16 = 1, kE4M3 = 2, kE5M2 = 3, kI8 = 4 };
+enum DType : int { kF16 = 0, kBF16 = 1, kE4M3 = 2, kE5M2 = 3, kI8 = 4, kFP4 = 16 };
 
 enum DevErr : int {
   kErrNone = 0,

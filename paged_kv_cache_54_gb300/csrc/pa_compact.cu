@@ -1,0 +1,87 @@
+// pa_compact_blocks: whole-block moves inside one pool, and the block tables
+// renamed to match, in one launch.  The moves and the renaming touch
+// different memory, so nothing orders them.
+#include <limits.h>
+
+#include "pa_common.cuh"
+#include "pa_host.h"
+
+namespace pa {
+namespace {
+
+constexpr int kCompactThreads = 256;
+
+__global__ void __launch_bounds__(kCompactThreads) compact_kernel(
+    uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache, const int64_t *__restrict__ mapping, int num_pairs,
+    long long block_bytes, long long num_blocks, int32_t *__restrict__ tables, int num_seqs, int max_blocks,
+    int block_size, const int32_t *__restrict__ seq_lens, int *err) {
+  const long long thread = blockIdx.x * static_cast<long long>(kCompactThreads) + threadIdx.x;
+  const long long threads = static_cast<long long>(gridDim.x) * kCompactThreads;
+  // the table entries in use, each looked up among the sources
+  const long long entries = static_cast<long long>(num_seqs) * max_blocks;
+  for (long long i = thread; i < entries; i += threads) {
+    const int s = static_cast<int>(i / max_blocks);
+    const int j = static_cast<int>(i - static_cast<long long>(s) * max_blocks);
+    const int L = __ldg(seq_lens + s);
+    if (L < 0 || L > static_cast<long long>(max_blocks) * block_size) {
+      if (j == 0) record_error(err, kErrSeqLen);
+      continue;
+    }
+    if (static_cast<long long>(j) * block_size >= L) continue;  // behind the last block
+    const int32_t b = tables[i];
+    int lo = 0, hi = num_pairs;  // the first pair whose source is b or above
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(mapping + 2 * mid) < b) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo == num_pairs || __ldg(mapping + 2 * lo) != b || b < 0 || b >= num_blocks) continue;
+    const long long dst = __ldg(mapping + 2 * lo + 1);
+    if (dst >= 0 && dst < num_blocks) tables[i] = static_cast<int32_t>(dst);
+  }
+  // the moves
+  const long long vecs = block_bytes / 16;
+  const long long total = static_cast<long long>(num_pairs) * 2 * vecs;
+  for (long long i = thread; i < total; i += threads) {
+    const long long pair = i / (2 * vecs);
+    const long long r = i - pair * 2 * vecs;
+    const int which = r >= vecs;
+    const long long v = r - which * vecs;
+    const long long src = __ldg(mapping + 2 * pair);
+    const long long dst = __ldg(mapping + 2 * pair + 1);
+    if (v == 0 && which == 0 && pair > 0 && __ldg(mapping + 2 * pair - 2) >= src) record_error(err, kErrCopyIndex);
+    if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
+      if (v == 0 && which == 0) record_error(err, kErrCopyIndex);
+      continue;
+    }
+    uint8_t *base = which ? v_cache : k_cache;
+    const uint4 x = *reinterpret_cast<const uint4 *>(base + src * block_bytes + v * 16);
+    *reinterpret_cast<uint4 *>(base + dst * block_bytes + v * 16) = x;
+  }
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_compact_blocks(void *k_cache, void *v_cache, const pa_cache_desc *cache,
+                                       const int64_t *block_mapping, int32_t num_pairs, int32_t *block_tables,
+                                       int32_t num_seqs, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                       int *device_error, pa_stream_t stream) {
+  if (!valid_cache_desc(cache) || num_pairs < 0 || num_seqs < 0 || max_blocks_per_seq <= 0) return PA_ERR_INVALID;
+  if (num_pairs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_mapping || (num_seqs > 0 && (!block_tables || !seq_lens))) return PA_ERR_INVALID;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || (reinterpret_cast<uintptr_t>(block_mapping) & 7u) ||
+      (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
+    return PA_ERR_INVALID;
+  if (!supported_cache_shape(cache)) return PA_ERR_UNSUPPORTED;
+  const long long block_bytes = cache_block_bytes(cache);
+  const long long work = static_cast<long long>(num_pairs) * 2 * (block_bytes / 16) +
+                         static_cast<long long>(num_seqs) * max_blocks_per_seq;
+  compact_kernel<<<grid_for(work, kCompactThreads), kCompactThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), block_mapping, num_pairs, block_bytes,
+      cache->num_blocks, block_tables, num_seqs, max_blocks_per_seq, cache->block_size, seq_lens, device_error);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "pa_decode_params.h"
+#include "pa_fp4.h"
 
 namespace pa {
 namespace {
@@ -116,7 +117,7 @@ extern "C" pa_status pa_decode(void *out, const void *q, int32_t q_dtype, int32_
   if (G != 1 && G != 2 && G != 4 && G != 8) return PA_ERR_UNSUPPORTED;
   if (!supported_cache_shape(cache)) return PA_ERR_UNSUPPORTED;
   if (q_dtype != PA_F16 && q_dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
-  const bool byte_codes = cache->dtype >= PA_FP8_E4M3;  // FP8 or INT8, with scales
+  const bool byte_codes = cache->dtype >= PA_FP8_E4M3;  // FP8, INT8 or FP4, with scales
   if (!byte_codes && q_dtype != cache->dtype) return PA_ERR_UNSUPPORTED;
   if (partition_size != 0 &&
       (partition_size < kStageTok || partition_size > kMaxPartition ||
@@ -163,6 +164,9 @@ extern "C" pa_status pa_decode(void *out, const void *q, int32_t q_dtype, int32_
   p.part_ml = reinterpret_cast<float2 *>(ws + w.ml_off);
   p.part_o = reinterpret_cast<float *>(ws + w.o_off);
   p.err = device_error;
+
+  if (cache->dtype == PA_FP4)
+    return dispatch_decode_fp4(q_dtype, cache->head_dim, G, p, dev, reinterpret_cast<cudaStream_t>(stream));
 
   if (!encode_cache_map(&p.tmap_k, k_cache, cache) ||
       !encode_cache_map(&p.tmap_v, v_cache, cache))  // tiled views for the swizzled (tensor-path) stages

@@ -1,0 +1,43 @@
+// Device helpers of the four-bit cache format: e2m1 codes, two to a byte,
+// with one e4m3 scale for every 16.
+#pragma once
+
+#include "pa_common.cuh"
+
+namespace pa {
+
+constexpr int kFp4Group = 16;
+
+// bytes of one token's row of one head: its codes, its scales, both
+__host__ __device__ constexpr int fp4_code_bytes(int head_dim) { return head_dim / 2; }
+__host__ __device__ constexpr int fp4_scale_bytes(int head_dim) { return head_dim / kFp4Group; }
+__host__ __device__ constexpr int fp4_row_bytes(int head_dim) { return head_dim / 16 * 9; }
+
+// Eight codes in one word -> four half2 (code 2i in the low half of o[i]).
+// Every e2m1 value is an fp16 value, so this is exact.
+__device__ __forceinline__ void e2m1x8_to_half2x4(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+
+// Two e4m3 scales (low byte first) -> half2, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(d) : "r"(two));
+  return d;
+}
+
+// The product of a code (at most two significant bits, at most 6) and a
+// group scale (four bits, at most 448) has at most six significant bits, is
+// at most 2688 and a multiple of 2^-10: every one is an fp16 value, so this
+// multiplication is exact.
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+}  // namespace pa

@@ -36,6 +36,16 @@ bool current_device_info(DeviceInfo *out) {
   return true;
 }
 
+int grid_for(long long work_items, int threads) {
+  DeviceInfo info;
+  int sms = current_device_info(&info) ? info.sm_count : 148;
+  long long blocks = (work_items + threads - 1) / threads;
+  long long cap = static_cast<long long>(sms) * 8;
+  if (blocks > cap) blocks = cap;
+  if (blocks < 1) blocks = 1;
+  return static_cast<int>(blocks);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;

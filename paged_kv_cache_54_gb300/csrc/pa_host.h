@@ -20,6 +20,10 @@ struct DeviceInfo {
 // Properties of the current device, queried once per device.
 bool current_device_info(DeviceInfo *out);
 
+// CTAs of a grid-stride kernel over work_items: one thread an item, at most
+// eight CTAs an SM.
+int grid_for(long long work_items, int threads);
+
 // Record the text of a failed CUDA call for pa_last_cuda_error() and return
 // PA_ERR_CUDA.
 pa_status cuda_fail(cudaError_t err);
@@ -33,7 +37,7 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool valid_cache_desc(const pa_cache_desc *c) {
   if (c == nullptr) return false;
   if (c->num_blocks <= 0 || c->kv_heads <= 0 || c->block_size <= 0 || c->head_dim <= 0) return false;
-  if (c->dtype < PA_F16 || c->dtype > PA_INT8) return false;
+  if ((c->dtype < PA_F16 || c->dtype > PA_INT8) && c->dtype != PA_FP4) return false;
   if (c->dtype >= PA_FP8_E4M3) {
     if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f)) return false;
     if (c->k_scale > 3.0e38f || c->v_scale > 3.0e38f) return false;
@@ -51,6 +55,13 @@ inline bool valid_cache_desc(const pa_cache_desc *c) {
 inline bool supported_cache_shape(const pa_cache_desc *c) {
   return (c->block_size == 8 || c->block_size == 16 || c->block_size == 32) &&
          (c->head_dim == 64 || c->head_dim == 128);
+}
+
+// Bytes of one block of all KV heads, of K or of V.
+inline long long cache_block_bytes(const pa_cache_desc *c) {
+  const long long elems = static_cast<long long>(c->kv_heads) * c->block_size * c->head_dim;
+  if (c->dtype == PA_FP4) return elems / 16 * 9;  // 8 bytes of codes and a scale byte for every 16
+  return c->dtype >= PA_FP8_E4M3 ? elems : 2 * elems;
 }
 
 }  // namespace pa

@@ -119,7 +119,7 @@ extern "C" pa_status pa_prefill(void *out, const void *q, int32_t q_dtype, int32
   const int G = num_q_heads / cache->kv_heads;
   if (G != 1 && G != 2 && G != 4 && G != 8) return PA_ERR_UNSUPPORTED;
   if (!supported_cache_shape(cache)) return PA_ERR_UNSUPPORTED;
-  const bool byte_codes = cache->dtype >= PA_FP8_E4M3;  // FP8 or INT8, with scales
+  const bool byte_codes = cache->dtype >= PA_FP8_E4M3;  // FP8, INT8 or FP4, with scales
   if (byte_codes ? (q_dtype != PA_F16 && q_dtype != PA_BF16) : q_dtype != cache->dtype)
     return PA_ERR_UNSUPPORTED;
   if (num_seqs > 65535 || cache->kv_heads > 65535) return PA_ERR_UNSUPPORTED;      // grid limits
@@ -158,6 +158,7 @@ extern "C" pa_status pa_prefill(void *out, const void *q, int32_t q_dtype, int32
     case PA_FP8_E4M3: return dispatch_prefill_e4m3(q_dtype, D, G, p, num_seqs, max_q_len, s);
     case PA_FP8_E5M2: return dispatch_prefill_e5m2(q_dtype, D, G, p, num_seqs, max_q_len, s);
     case PA_INT8: return dispatch_prefill_i8(q_dtype, D, G, p, num_seqs, max_q_len, s);
+    case PA_FP4: return dispatch_prefill_fp4(q_dtype, D, G, p, num_seqs, max_q_len, s);
   }
   return PA_ERR_UNSUPPORTED;
 }

@@ -48,7 +48,7 @@
 // TMEM: all 512 columns (per tile S / P: 2 x 64, O: head_dim); one CTA per
 // SM, five K/V stages in flight.
 //
-// One-byte caches (FP8 e4m3 / e5m2, INT8): the products take fp16 operands.
+// Coded caches (FP8 e4m3 / e5m2, INT8, FP4): the products take fp16 operands.
 // The TMA warp copies each (block, head) tile of codes whole (one bulk copy
 // per block for K and for V) into a ring of four code slots; warps 12..15,
 // one on each SM sub-partition, widen the codes exactly to fp16 into three
@@ -58,11 +58,14 @@
 // the block is launched with.  A bf16 query tile is rewritten in place as
 // fp16 by its softmax warps, times a power of two that brings its largest
 // entry within fp16's range; the factor, and the K scale, go into the score
-// scale, the V scale into the output.
+// scale, the V scale into the output.  Four-bit caches have three code slots
+// and four 16-bit stages; their group scales are applied while widening (a
+// code times its group's scale is an fp16 value, so that stays exact).
 #include <limits.h>
 #include <math.h>
 
 #include "pa_common.cuh"
+#include "pa_fp4.cuh"
 #include "pa_host.h"
 
 namespace pa {
@@ -128,18 +131,29 @@ constexpr float kPfLazy = 8.f;  // rescale O only when the row maximum grows by 
 
 
 
-template <int D, bool KV8>
+// caches whose codes are widened to 16-bit stages
+__host__ __device__ constexpr bool is_coded(int kv) { return is_byte(kv) || kv == kFP4; }
+// bytes of a token's row of one head as stored: codes (and their scales)
+__host__ __device__ constexpr int stored_row_bytes(int kv, int head_dim) {
+  return kv == kFP4 ? fp4_row_bytes(head_dim) : head_dim;
+}
+
+template <int D, int KVT>
 struct PfLayout {
+  static constexpr bool KV8 = is_coded(KVT);
   static constexpr int NH = D / 64;  // 128-byte halves of a 16-bit row
-  static constexpr int NS = KV8 ? 3 : kPfStages;  // 16-bit K/V stages
-  static constexpr int NC = KV8 ? kPfCodeSlots : 0;  // code slots
+  // 16-bit K/V stages, and code slots.  Four-bit slots are small enough to
+  // leave room for a fourth stage.
+  static constexpr int NS = KVT == kFP4 ? 4 : KV8 ? 3 : kPfStages;
+  static constexpr int NC = KVT == kFP4 ? 3 : KV8 ? kPfCodeSlots : 0;
   static constexpr int Q_OFF = 1024;
   static constexpr int Q_HALF = kPfTileRows * 128;
   static constexpr int Q_TILE = NH * Q_HALF;
   static constexpr int STAGE_OFF = Q_OFF + kPfTiles * Q_TILE;
   static constexpr int STAGE_BYTES = 2 * NH * kPfHalf;  // K halves, then V halves
   static constexpr int CODE_OFF = STAGE_OFF + NS * STAGE_BYTES;
-  static constexpr int CODE_BYTES = 2 * kPfKeys * D;    // K codes [key][d], then V codes
+  static constexpr int CODE_V = kPfKeys * stored_row_bytes(KVT, D);  // K tiles as stored, then V tiles
+  static constexpr int CODE_BYTES = 2 * CODE_V;
   static constexpr int SMEM = CODE_OFF + NC * CODE_BYTES;
 };
 
@@ -204,6 +218,61 @@ __device__ __forceinline__ void widen_codes(const uint8_t *slot, uint8_t *stage,
   }
 }
 
+// The same for four-bit codes: 8 bytes of codes and their scale make two
+// 16-byte chunks.  A warp iteration takes 32 groups, lane = (key, half, group
+// of 16 in the half); a slot holds whole (block, head) tiles, each its codes
+// and then its scales [group][token].  The lanes of the upper half write
+// their two chunks in the other order, so that the eight lanes of a store
+// phase (one key's groups, both halves) hit eight different chunks.
+template <int D, int PARTS>
+__device__ __forceinline__ void widen_fp4(const uint8_t *slot, uint8_t *stage, int keys, int bs, int lane, int part) {
+  constexpr int NH = D / 64;
+  constexpr int GPR = D / kFp4Group;     // groups of a row
+  constexpr int KPI = 32 / GPR;          // keys per warp iteration
+  constexpr int ITERS = kPfKeys / KPI / PARTS;
+  const int kr = lane / GPR, g = lane % GPR, hf = g >> 2, gh = g & 3;
+  const int bs_sh = 31 - __clz(bs), tile = bs * fp4_row_bytes(D);
+  const int swap = NH == 2 ? hf : 0;
+#pragma unroll
+  for (int tv = 0; tv < 2; ++tv) {
+    const uint8_t *src = slot + tv * kPfKeys * fp4_row_bytes(D);
+    uint8_t *dst = stage + tv * NH * kPfHalf;
+    uint2 w[ITERS];
+    uint32_t s[ITERS];
+#pragma unroll
+    for (int m = 0; m < ITERS; ++m) {  // the loads before the stores, which may alias them for all the compiler knows
+      const int key = (m * PARTS + part) * KPI + kr;
+      const uint8_t *t = src + (key >> bs_sh) * tile;
+      const int off = key & (bs - 1);
+      w[m] = make_uint2(0u, 0u);
+      s[m] = 0u;
+      if (key < keys) {
+        w[m] = *reinterpret_cast<const uint2 *>(t + off * fp4_code_bytes(D) + g * 8);
+        s[m] = t[bs * fp4_code_bytes(D) + g * bs + off];
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < ITERS; ++m) {
+      const int key = (m * PARTS + part) * KPI + kr;
+      if (key >= keys) continue;
+      const uint32_t s2 = e4m3x2_to_half2(s[m] * 0x0101u);
+      uint32_t a[4], b[4];
+      e2m1x8_to_half2x4(w[m].x, a);
+      e2m1x8_to_half2x4(w[m].y, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = hmul2_bits(a[i], s2);
+        b[i] = hmul2_bits(b[i], s2);
+      }
+      const uint4 lo = make_uint4(a[0], a[1], a[2], a[3]), hi = make_uint4(b[0], b[1], b[2], b[3]);
+      uint8_t *row = dst + kv_row_off<NH>(key, hf);
+      const int c = 2 * gh, k7 = key & 7;
+      *reinterpret_cast<uint4 *>(row + (((c + swap) ^ k7) << 4)) = swap ? hi : lo;
+      *reinterpret_cast<uint4 *>(row + (((c + 1 - swap) ^ k7) << 4)) = swap ? lo : hi;
+    }
+  }
+}
+
 __device__ __forceinline__ void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -252,10 +321,10 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
 // decode's merge combines with the other partitions.
 template <int DT, int KVT, int D, int G, bool SD>
 __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
-  constexpr bool KV8 = is_byte(KVT);
+  constexpr bool KV8 = is_coded(KVT);
   constexpr int MT = KV8 ? kF16 : DT;          // the products' operand type
   constexpr bool QCONV = KV8 && DT == kBF16;   // q is rewritten as fp16 first
-  using Lay = PfLayout<D, KV8>;
+  using Lay = PfLayout<D, KVT>;
   constexpr int NH = Lay::NH;
   constexpr int NS = Lay::NS;
   constexpr int NC = Lay::NC;
@@ -363,13 +432,13 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
     }
     if constexpr (KV8) {
       uint8_t *cb = codes + (i % NC) * Lay::CODE_BYTES;
-      const uint32_t tile = static_cast<uint32_t>(bs) * D;
+      const uint32_t tile = static_cast<uint32_t>(bs) * stored_row_bytes(KVT, D);
       if (lane == 0) mbar_arrive_expect_tx(&hdr.code_full[i % NC], 2u * nblk * tile);
       __syncwarp();
       if (lane < nblk) {
         const size_t off = (static_cast<size_t>(phys) * p.num_kv_heads + h) * tile;
         bulk_g2s(cb + lane * tile, p.k_cache + off, tile, &hdr.code_full[i % NC]);
-        bulk_g2s(cb + kPfKeys * D + lane * tile, p.v_cache + off, tile, &hdr.code_full[i % NC]);
+        bulk_g2s(cb + Lay::CODE_V + lane * tile, p.v_cache + off, tile, &hdr.code_full[i % NC]);
       }
     } else {
       const int st = i % NS;
@@ -478,10 +547,12 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
         named_bar_sync(1 + t, kPfTileRows);
         amax = fmaxf(fmaxf(hdr.qmax[t][0], hdr.qmax[t][1]), fmaxf(hdr.qmax[t][2], hdr.qmax[t][3]));
         float f = 1.f;
-        if (amax > 16384.f && amax <= 3.0e38f) {
+        // (four-bit caches scale small tiles up as well, so that their
+        // entries keep their eight bits in fp16)
+        if (amax > (KVT == kFP4 ? 0.f : 16384.f) && amax <= 3.0e38f) {
           int ex;
           frexpf(amax, &ex);
-          f = ldexpf(1.f, 14 - ex);
+          f = ldexpf(1.f, min(14 - ex, 100));
         }
         if (ok) {
   #pragma unroll
@@ -803,8 +874,12 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
           break;
         }
         const int keys = min(bpt, (kv_end - i * kPfKeys + bs - 1) / bs) * bs;
-        widen_codes<KVT, D, kPfConvWarps>(codes + (i % NC) * Lay::CODE_BYTES, stages + st * Lay::STAGE_BYTES, keys,
-                                          lane, q);
+        if constexpr (KVT == kFP4)
+          widen_fp4<D, kPfConvWarps>(codes + (i % NC) * Lay::CODE_BYTES, stages + st * Lay::STAGE_BYTES, keys, bs, lane,
+                                     q);
+        else
+          widen_codes<KVT, D, kPfConvWarps>(codes + (i % NC) * Lay::CODE_BYTES, stages + st * Lay::STAGE_BYTES, keys,
+                                            lane, q);
         // the 16-bit stage visible to the tensor cores, and the code slot's
         // reads ordered before the bulk copy that refills it
         fence_proxy_async_smem();
@@ -830,7 +905,7 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
 }
 
 template <int DT, int KVT, int D, int G>
-__global__ void __launch_bounds__(pf_threads(is_byte(KVT)), 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(pf_threads(is_coded(KVT)), 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
   prefill_body<DT, KVT, D, G, false>(p);
 }
 
@@ -847,7 +922,7 @@ __global__ void __launch_bounds__(pf_threads(false), 1) wide_decode_kernel(const
 
 template <int DT, int KVT, int D, int G>
 pa_status launch_prefill(const PrefillParams &p, int num_seqs, int max_q_len, cudaStream_t stream) {
-  using Lay = PfLayout<D, is_byte(KVT)>;
+  using Lay = PfLayout<D, KVT>;
   constexpr int QC = kPfRows / G;
   static bool configured[64];  // per device: dynamic shared memory already allowed
   int dev = 0;
@@ -860,7 +935,7 @@ pa_status launch_prefill(const PrefillParams &p, int num_seqs, int max_q_len, cu
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
   const dim3 grid((max_q_len + QC - 1) / QC, num_seqs, p.num_kv_heads);
-  prefill_kernel<DT, KVT, D, G><<<grid, pf_threads(is_byte(KVT)), Lay::SMEM, stream>>>(p);
+  prefill_kernel<DT, KVT, D, G><<<grid, pf_threads(is_coded(KVT)), Lay::SMEM, stream>>>(p);
   e = cudaGetLastError();
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
@@ -869,7 +944,7 @@ pa_status launch_prefill(const PrefillParams &p, int num_seqs, int max_q_len, cu
 // kernel before it (the plan).
 template <int DT, int D, int G>
 pa_status launch_wide(const PrefillParams &p, int grid_x, cudaStream_t stream) {
-  using Lay = PfLayout<D, false>;
+  using Lay = PfLayout<D, DT>;
   static bool configured[64];  // per device: dynamic shared memory already allowed
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -919,7 +994,7 @@ pa_status by_group(int G, const PrefillParams &p, int num_seqs, int max_q_len, c
 template <int KVT>
 pa_status dispatch_prefill(int q_dtype, int head_dim, int G, const PrefillParams &p, int num_seqs,
                            int max_q_len, cudaStream_t s) {
-  if constexpr (is_byte(KVT)) {
+  if constexpr (is_coded(KVT)) {
     if (q_dtype == kF16)
       return head_dim == 64 ? by_group<kF16, KVT, 64>(G, p, num_seqs, max_q_len, s)
                             : by_group<kF16, KVT, 128>(G, p, num_seqs, max_q_len, s);
@@ -942,5 +1017,7 @@ pa_status dispatch_prefill_e5m2(int q_dtype, int head_dim, int G, const PrefillP
                                 int max_q_len, cudaStream_t s);
 pa_status dispatch_prefill_i8(int q_dtype, int head_dim, int G, const PrefillParams &p, int num_seqs,
                               int max_q_len, cudaStream_t s);
+pa_status dispatch_prefill_fp4(int q_dtype, int head_dim, int G, const PrefillParams &p, int num_seqs,
+                               int max_q_len, cudaStream_t s);
 
 }  // namespace pa

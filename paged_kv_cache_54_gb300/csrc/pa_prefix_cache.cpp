@@ -246,6 +246,80 @@ PA_API pa_status pa_prefix_cache_free_sequence(pa_prefix_cache *c, int64_t seq_i
   return PA_OK;
 }
 
+PA_API pa_status pa_prefix_cache_fork_sequence(pa_prefix_cache *c, int64_t parent, int64_t child,
+                                               int64_t copy_pair[2]) {
+  if (c == nullptr || copy_pair == nullptr) return PA_ERR_INVALID;
+  auto it = c->seqs.find(parent);
+  if (it == c->seqs.end() || c->seqs.count(child)) return PA_ERR_INVALID;
+  const bool partial = it->second.tokens.size() % c->block_size != 0;
+  if (partial && c->free_count == 0) return PA_ERR_OUT_OF_BLOCKS;
+  Sequence *s;
+  try {
+    Sequence copy = it->second;
+    s = &c->seqs.emplace(child, std::move(copy)).first->second;
+  } catch (...) {
+    return PA_ERR_INVALID;  // out of host memory
+  }
+  copy_pair[0] = copy_pair[1] = -1;
+  if (partial) {  // the one block either sequence may still write
+    copy_pair[0] = s->table.back();
+    copy_pair[1] = s->table.back() = c->take_fresh();
+  }
+  for (size_t j = 0; j + (partial ? 1 : 0) < s->table.size(); ++j) ++c->ref[s->table[j]];
+  return PA_OK;
+}
+
+// Kept blocks (in use, or free with a key) below their count n stay; the k-th
+// one at or above n moves to the k-th unkept block below it.
+PA_API int32_t pa_prefix_cache_compact(pa_prefix_cache *c, int64_t *pairs, int32_t capacity) {
+  if (c == nullptr) return -1;
+  const int32_t nb = c->num_blocks;
+  auto kept = [c](int32_t b) { return c->ref[b] > 0 || c->has_key[b]; };
+  int32_t n = 0, moves = 0;
+  for (int32_t b = 0; b < nb; ++b) n += kept(b);
+  for (int32_t b = n; b < nb; ++b) moves += kept(b);
+  if (pairs == nullptr || capacity < moves) return moves;
+  std::vector<int32_t> name, keyed_free;
+  try {
+    name.resize(nb);
+    keyed_free.reserve(nb);
+  } catch (...) {
+    return -1;  // out of host memory: nothing has changed
+  }
+  for (int32_t b = c->head; b >= 0; b = c->next[b])
+    if (c->has_key[b]) keyed_free.push_back(b);
+  int32_t hole = 0, m = 0;
+  for (int32_t b = 0; b < nb; ++b) name[b] = b;
+  const size_t bs = static_cast<size_t>(c->block_size);
+  for (int32_t b = n; b < nb; ++b) {
+    if (!kept(b)) continue;
+    while (kept(hole)) ++hole;  // (filled holes are kept by then; there are as many as moves)
+    name[b] = hole;
+    pairs[2 * m] = b;
+    pairs[2 * m + 1] = hole;
+    ++m;
+    c->ref[hole] = c->ref[b];
+    c->ref[b] = 0;
+    c->has_key[hole] = c->has_key[b];
+    if (c->has_key[b]) {
+      c->key[hole] = c->key[b];
+      c->parent_key[hole] = c->parent_key[b];
+      std::memcpy(&c->key_tokens[hole * bs], &c->key_tokens[b * bs], sizeof(int32_t) * bs);
+      c->has_key[b] = 0;
+    }
+  }
+  for (auto &kv : c->block_of) kv.second = name[kv.second];
+  for (auto &kv : c->seqs)
+    for (int32_t &b : kv.second.table) b = name[b];
+  c->head = c->tail = -1;
+  c->free_count = 0;
+  std::memset(c->in_free.data(), 0, c->in_free.size());
+  for (int32_t b = 0; b < nb; ++b)
+    if (!kept(b)) c->push_back(b);
+  for (int32_t b : keyed_free) c->push_back(name[b]);
+  return moves;
+}
+
 PA_API int32_t pa_prefix_cache_block_table(const pa_prefix_cache *c, int64_t seq_id, int32_t *table,
                                            int32_t capacity, int32_t *num_tokens) {
   if (c == nullptr) return -1;
