@@ -165,8 +165,12 @@ extern "C" pa_status pa_decode(void *out, const void *q, int32_t q_dtype, int32_
   p.part_o = reinterpret_cast<float *>(ws + w.o_off);
   p.err = device_error;
 
-  if (cache->dtype == PA_FP4)
-    return dispatch_decode_fp4(q_dtype, cache->head_dim, G, p, dev, reinterpret_cast<cudaStream_t>(stream));
+  if (cache->dtype == PA_FP4) {
+    auto *go = cache->block_size == 8    ? dispatch_decode_fp4_b8
+               : cache->block_size == 16 ? dispatch_decode_fp4_b16
+                                         : dispatch_decode_fp4_b32;
+    return go(q_dtype, cache->head_dim, G, p, dev, reinterpret_cast<cudaStream_t>(stream));
+  }
 
   if (!encode_cache_map(&p.tmap_k, k_cache, cache) ||
       !encode_cache_map(&p.tmap_v, v_cache, cache))  // tiled views for the swizzled (tensor-path) stages

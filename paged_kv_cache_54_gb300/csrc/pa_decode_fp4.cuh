@@ -1,0 +1,880 @@
+// Paged decode attention over a four-bit cache (PA_FP4) for sm_103a.
+//
+// Work decomposition.  The (sequence, KV head) pairs, in sequence order, are
+// laid end to end in units of 64 tokens (a pair's tokens, and one unit for
+// what a piece costs beside them), and CTA b of n takes the units
+// [b U / n, (b + 1) U / n) of the U in all: equal shares whatever the
+// lengths, found by each CTA from a scan of the lengths (no plan launch, no
+// claims).  A CTA's share is a run of pieces, one per pair it touches.  A
+// pair that falls to one CTA whole is written out by it; the pieces of a cut
+// pair leave (m, l, O / l) partials, joined by a merge kernel (the
+// flash-decoding reduction).  Partials live in the layout every cache type's
+// workspace has, [sequence, partition, query head]: piece j of a pair uses
+// the place of partition j.  A share is at least two partitions long, so a
+// pair of L tokens has at most ceil(L / 2P) + 1 pieces, which is at most the
+// workspace's max_parts when that is two or more; when it is one, pairs are
+// dealt out whole.
+//
+// A CTA is four warps, four CTAs to an SM.  Within a piece warp w takes the 32-token steps w,
+// w + 4, ..., each warp with its own online softmax; the four states meet
+// in shared memory at the piece's end.  A warp's steps stream through a ring
+// of its own in shared memory, filled by 16-byte asynchronous copies three
+// steps ahead, so no warp waits for another within a piece.  (Tensor copies
+// of whole tiles would be fewer instructions, but an SM starts about one per
+// 100 clocks, and a tile of 16 tokens is 1152 bytes: half the HBM rate.)
+//
+// A step is two slices of 16 tokens; a slice is two small products on mma.sync m16n8k16 with fp16 operands
+// and fp32 accumulation, S^T = K Q^T and O^T = V^T P^T: tokens, then head
+// dimensions, as M, and the query group padded to 8 as N.  Codes widen to
+// fp16 exactly (a code times its group's scale is an fp16 value), so the only
+// roundings are those of P to fp16 and of the output.
+//
+// Fragment orders (lane = 4 gq + tq), chosen so that every lane reads runs of
+// its own:
+//   S^T: row gq is token 2 gq, row gq + 8 token 2 gq + 1.  Lane tq's columns
+//     are the dimensions [tq D/4, (tq + 1) D/4): k-step kk uses its local
+//     dimensions 4kk .. 4kk + 3.
+//   O^T: column k = 2tq, 2tq + 1, 2tq + 8, 2tq + 9 is token 4 tq + 0, 1, 2, 3.
+//     Lane gq's rows are the dimensions [gq D/8, (gq + 1) D/8): m-tile mi has
+//     local dimension mi in row gq and D/16 + mi in row gq + 8.
+// The two codes of one A register of V^T come from two tokens: the code words
+// of a token pair are interleaved (even dimensions, odd dimensions) so that
+// one conversion of a byte gives the pair.
+#pragma once
+
+#include "pa_fp4.cuh"
+#include "pa_fp4.h"
+
+namespace pa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kFpThreads = 32 * kWarps;
+constexpr int kCtas = 4;        // CTAs an SM
+constexpr int kSlice = 16;      // tokens of the products
+constexpr int kStep = 32;       // tokens of a warp's step
+constexpr int kUnit = 64;       // tokens of a unit of work
+constexpr int kPairCost = 5;    // units that a pair costs beside its tokens'
+constexpr float kLazy = 8.f;    // rescale when the maximum grows by more (base 2)
+constexpr float kWritten = -1.f;  // l of a partial that marks the end of a pair's pieces
+
+struct Fp4Params {
+  void *out;
+  const uint8_t *q;
+  const uint8_t *k_cache;
+  const uint8_t *v_cache;
+  const int32_t *block_tables;
+  const int32_t *seq_lens;
+  int num_seqs, num_q_heads, num_kv_heads, num_blocks, max_blocks;
+  int len_cap, max_parts, partition_size;
+  float qk_scale_log2, v_scale;
+  const float *k_head_scale, *v_head_scale;
+  float2 *part_ml;
+  float *part_o;
+  int *err;
+};
+
+// Codes and scales of one slice as a lane reads them.
+template <int D>
+struct KSlice {
+  static constexpr int W = D / 32;  // words of a row a lane reads (8 codes each)
+  uint32_t c[2][W];   // tokens 2gq, 2gq + 1
+  uint32_t s[W / 2];  // their scales (two bytes), one for each 16 local dimensions
+};
+template <int D>
+struct VSlice {
+  static constexpr int W = D / 64;
+  uint32_t c[4][W];  // tokens 4tq .. 4tq + 3
+  uint32_t s;        // their scales in the lane's group
+};
+
+template <int D>
+struct State {
+  static constexpr int KSTEPS = D / 16;
+  static constexpr int MT = D / 16;
+  uint32_t qb[KSTEPS][2];
+  float o[MT][4];
+  float m[2], l[2];
+  float mult;
+};
+
+// q rows of the group (G x D at `q`) as B fragments: column gq is query gq,
+// lane tq's local dimensions.  bf16 queries are rounded to fp16 after a
+// multiplication by the power of two that brings the group's largest entry
+// into [2^13, 2^14), undone on the scores, so that nothing overflows and what
+// underflows is 2^-38 of the largest.
+template <int QT, int D, int G>
+__device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float scale) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  constexpr int QW = D / 8;  // words of the lane
+  uint32_t w[QW];
+  const uint4 *row = reinterpret_cast<const uint4 *>(q + (static_cast<size_t>(gq < G ? gq : 0) * D + tq * (D / 4)) * 2);
+#pragma unroll
+  for (int i = 0; i < QW / 4; ++i) {
+    const uint4 x = gq < G ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u);
+    w[4 * i] = x.x;
+    w[4 * i + 1] = x.y;
+    w[4 * i + 2] = x.z;
+    w[4 * i + 3] = x.w;
+  }
+  float f = 1.f;
+  if constexpr (QT == kBF16) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < QW; ++i) {
+      const float2 x = half2_bits_to_float2<kBF16>(w[i]);
+      top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top > 0.f && top <= 3.4e38f) {
+      int e;
+      frexpf(top, &e);
+      f = ldexpf(1.f, min(14 - e, 100));
+    }
+#pragma unroll
+    for (int i = 0; i < QW; ++i) {
+      const float2 x = half2_bits_to_float2<kBF16>(w[i]);
+      w[i] = pack2_rn<kF16>(x.x * f, x.y * f);
+    }
+  }
+  // the scores' multiplier is positive: its sign goes to q, and a zero one
+  // becomes zero queries
+#pragma unroll
+  for (int i = 0; i < QW; ++i) w[i] = scale > 0.f ? w[i] : scale < 0.f ? w[i] ^ 0x80008000u : 0u;
+  st.mult = scale == 0.f ? 1.f : fabsf(scale) / f;
+#pragma unroll
+  for (int kk = 0; kk < State<D>::KSTEPS; ++kk) {
+    st.qb[kk][0] = w[2 * kk];
+    st.qb[kk][1] = w[2 * kk + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < State<D>::MT; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
+  st.m[0] = st.m[1] = -INFINITY;
+  st.l[0] = st.l[1] = 0.f;
+}
+
+__device__ __forceinline__ uint32_t lo2(uint32_t h) { return __byte_perm(h, h, 0x1010); }
+__device__ __forceinline__ uint32_t hi2(uint32_t h) { return __byte_perm(h, h, 0x3232); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// c = A * B with a zero addend (no registers to clear first)
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// S^T of a slice, unscaled: s[0], s[1] are token 2gq against queries 2tq and
+// 2tq + 1, s[2], s[3] token 2gq + 1.
+template <int D>
+__device__ __forceinline__ void scores(const State<D> &st, const KSlice<D> &c, float (&s)[4]) {
+  float acc[2][4];
+#pragma unroll
+  for (int w = 0; w < KSlice<D>::W; ++w) {
+    const uint32_t s2 = e4m3x2_to_half2(c.s[w / 2]);
+    const uint32_t s0 = lo2(s2), s1 = hi2(s2);
+    uint32_t a[4], b[4];
+    e2m1x8_to_half2x4(c.c[0][w], a);
+    e2m1x8_to_half2x4(c.c[1][w], b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = hmul2_bits(a[i], s0);
+      b[i] = hmul2_bits(b[i], s1);
+    }
+    if (w == 0) {
+      mma_first(acc[0], a[0], b[0], a[1], b[1], st.qb[0][0], st.qb[0][1]);
+      mma_first(acc[1], a[2], b[2], a[3], b[3], st.qb[1][0], st.qb[1][1]);
+    } else {
+      mma16816<kF16>(acc[0], a[0], b[0], a[1], b[1], st.qb[2 * w][0], st.qb[2 * w][1]);
+      mma16816<kF16>(acc[1], a[2], b[2], a[3], b[3], st.qb[2 * w + 1][0], st.qb[2 * w + 1][1]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = acc[0][i] + acc[1][i];
+}
+
+// the low nibbles of a's bytes and the high nibbles of b's
+__device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(d) : "r"(a), "r"(b), "n"(0x0f0f0f0f));
+  return d;
+}
+
+// O^T += V^T P^T of a slice; p: its weights, laid out as its scores.
+template <int D>
+__device__ __forceinline__ void accumulate(State<D> &st, const VSlice<D> &c, const float (&p)[4]) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const uint32_t pa = pack2_rn<kF16>(p[0], p[2]), pb = pack2_rn<kF16>(p[1], p[3]);  // tokens 2gq, 2gq + 1
+  const int from0 = (2 * tq) * 4 + (gq >> 1), from1 = from0 + 4;
+  const uint32_t a0 = __shfl_sync(0xffffffffu, pa, from0), b0 = __shfl_sync(0xffffffffu, pb, from0);
+  const uint32_t a1 = __shfl_sync(0xffffffffu, pa, from1), b1 = __shfl_sync(0xffffffffu, pb, from1);
+  const uint32_t w0 = (gq & 1) ? b0 : a0, w1 = (gq & 1) ? b1 : a1;
+  const uint32_t sA = e4m3x2_to_half2(c.s), sB = e4m3x2_to_half2(c.s >> 16);  // tokens (4tq, +1), (+2, +3)
+  uint32_t eA[VSlice<D>::W][4], oA[VSlice<D>::W][4], eB[VSlice<D>::W][4], oB[VSlice<D>::W][4];
+#pragma unroll
+  for (int w = 0; w < VSlice<D>::W; ++w) {
+    const uint32_t v0 = c.c[0][w], v1 = c.c[1][w], v2 = c.c[2][w], v3 = c.c[3][w];
+    e2m1x8_to_half2x4(low_nibbles(v0, v1 << 4), eA[w]);
+    e2m1x8_to_half2x4(low_nibbles(v0 >> 4, v1), oA[w]);
+    e2m1x8_to_half2x4(low_nibbles(v2, v3 << 4), eB[w]);
+    e2m1x8_to_half2x4(low_nibbles(v2 >> 4, v3), oB[w]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      eA[w][i] = hmul2_bits(eA[w][i], sA);
+      oA[w][i] = hmul2_bits(oA[w][i], sA);
+      eB[w][i] = hmul2_bits(eB[w][i], sB);
+      oB[w][i] = hmul2_bits(oB[w][i], sB);
+    }
+  }
+#pragma unroll
+  for (int mi = 0; mi < State<D>::MT; ++mi) {
+    // local dimensions mi (row gq) and MT + mi (row gq + 8)
+    const int lo = mi, hi = State<D>::MT + mi;
+    const uint32_t r0 = (lo & 1) ? oA[lo / 8][lo % 8 / 2] : eA[lo / 8][lo % 8 / 2];
+    const uint32_t r1 = (hi & 1) ? oA[hi / 8][hi % 8 / 2] : eA[hi / 8][hi % 8 / 2];
+    const uint32_t r2 = (lo & 1) ? oB[lo / 8][lo % 8 / 2] : eB[lo / 8][lo % 8 / 2];
+    const uint32_t r3 = (hi & 1) ? oB[hi / 8][hi % 8 / 2] : eB[hi / 8][hi % 8 / 2];
+    mma16816<kF16>(st.o[mi], r0, r1, r2, r3, w0, w1);
+  }
+}
+
+// ---- a warp's ring of steps in shared memory
+//
+// A slot holds two slices, each K's 16 rows of codes, V's, and each one's
+// scales as [group][token].  The 16-byte chunks of a 128-byte line of code
+// rows are exchanged within the line (slot ^ swizzle(line)) so that the eight
+// lanes (K) or sixteen (V) of a shared-memory phase read different banks.
+constexpr int kRing = 2;  // slots a warp
+
+template <int D>
+struct Ring {
+  static constexpr int CODES = kSlice * D / 2;
+  static constexpr int SCALES = kSlice * D / kFp4Group;
+  static constexpr int V = CODES, KS = 2 * CODES, VS = KS + SCALES, SLICE = VS + SCALES, SLOT = 2 * SLICE;
+  static constexpr int CHUNKS = CODES / 16;  // 16-byte chunks of a slice's codes: 64 or 32
+  __device__ __forceinline__ static int swizzle(int line) {
+    return D == 128 ? (2 * ((line >> 1) & 3)) ^ (4 * (line & 1)) : 2 * (line & 3);
+  }
+  // place of the 16-byte chunk c of a slice's rows (row-major)
+  __device__ __forceinline__ static int place(int c) { return (c >> 3) * 128 + (((c & 7) ^ swizzle(c >> 3)) << 4); }
+};
+
+// The lane's codes and scales of a slice.
+template <int D>
+__device__ __forceinline__ KSlice<D> read_k(const uint8_t *slice) {
+  using R = Ring<D>;
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  KSlice<D> k;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {  // rows 2gq, 2gq + 1
+    if constexpr (D == 128) {
+      const uint4 x = lds128(slice + R::place((2 * gq + r) * 4 + tq));
+      k.c[r][0] = x.x;
+      k.c[r][1] = x.y;
+      k.c[r][2] = x.z;
+      k.c[r][3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2 *>(slice + R::place((2 * gq + r) * 2 + (tq >> 1)) + (tq & 1) * 8);
+      k.c[r][0] = x.x;
+      k.c[r][1] = x.y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < KSlice<D>::W / 2; ++i)
+    k.s[i] = *reinterpret_cast<const uint16_t *>(slice + R::KS + (tq * (D / 64) + i) * 16 + 2 * gq);
+  return k;
+}
+template <int D>
+__device__ __forceinline__ VSlice<D> read_v(const uint8_t *slice) {
+  using R = Ring<D>;
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  VSlice<D> v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {  // rows 4tq .. 4tq + 3
+    if constexpr (D == 128) {
+      const uint2 x =
+          *reinterpret_cast<const uint2 *>(slice + R::V + R::place((4 * tq + r) * 4 + (gq >> 1)) + (gq & 1) * 8);
+      v.c[r][0] = x.x;
+      v.c[r][1] = x.y;
+    } else {
+      v.c[r][0] =
+          *reinterpret_cast<const uint32_t *>(slice + R::V + R::place((4 * tq + r) * 2 + (gq >> 2)) + (gq & 3) * 4);
+    }
+  }
+  v.s = *reinterpret_cast<const uint32_t *>(slice + R::VS + (gq * (D / 8) / kFp4Group) * 16 + 4 * tq);
+  return v;
+}
+
+// The step in a slot, n of its 32 tokens valid (1..32).  Places behind them
+// may hold any bits, NaN scales among them: their scores become -inf and
+// their V scales 0.
+template <int D>
+__device__ __forceinline__ void attend(State<D> &st, const uint8_t *slot, int n) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  float a[4], b[4];
+  scores<D>(st, read_k<D>(slot), a);
+  scores<D>(st, read_k<D>(slot + Ring<D>::SLICE), b);
+  if (n < kStep) {  // warp-uniform
+    if (2 * gq >= n) a[0] = a[1] = -INFINITY;
+    if (2 * gq + 1 >= n) a[2] = a[3] = -INFINITY;
+    if (kSlice + 2 * gq >= n) b[0] = b[1] = -INFINITY;
+    if (kSlice + 2 * gq + 1 >= n) b[2] = b[3] = -INFINITY;
+  }
+  // ---- online softmax of query columns 2tq, 2tq + 1
+  float x0 = fmaxf(fmaxf(a[0], a[2]), fmaxf(b[0], b[2])), x1 = fmaxf(fmaxf(a[1], a[3]), fmaxf(b[1], b[3]));
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+  }
+  x0 *= st.mult;
+  x1 *= st.mult;
+  const bool up0 = x0 > st.m[0] + kLazy, up1 = x1 > st.m[1] + kLazy;
+  if (__any_sync(0xffffffffu, up0 || up1)) {
+    const float f0 = up0 ? ex2(st.m[0] - x0) : 1.f, f1 = up1 ? ex2(st.m[1] - x1) : 1.f;
+    if (up0) st.m[0] = x0;
+    if (up1) st.m[1] = x1;
+#pragma unroll
+    for (int i = 0; i < State<D>::MT; ++i) {
+      st.o[i][0] *= f0;
+      st.o[i][2] *= f0;
+      st.o[i][1] *= f1;
+      st.o[i][3] *= f1;
+    }
+    st.l[0] *= f0;
+    st.l[1] *= f1;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = ex2(fmaf(a[i], st.mult, -st.m[i & 1]));
+    b[i] = ex2(fmaf(b[i], st.mult, -st.m[i & 1]));
+  }
+  st.l[0] += (a[0] + a[2]) + (b[0] + b[2]);
+  st.l[1] += (a[1] + a[3]) + (b[1] + b[3]);
+  VSlice<D> va = read_v<D>(slot), vb = read_v<D>(slot + Ring<D>::SLICE);
+  if (n < kStep) {
+    const int la = n - 4 * tq, lb = la - kSlice;  // valid ones of the lane's four tokens of a slice
+    va.s &= la >= 4 ? 0xffffffffu : la <= 0 ? 0u : (1u << (8 * la)) - 1u;
+    vb.s &= lb >= 4 ? 0xffffffffu : lb <= 0 ? 0u : (1u << (8 * lb)) - 1u;
+  }
+  accumulate<D>(st, va, a);
+  accumulate<D>(st, vb, b);
+}
+
+// 16 or 8 bytes from global to shared memory (address in the shared window).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t *src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// What a lane needs to start the copies of a step into a slot: its own places
+// in the first tile and in the slot, so that a copy costs one multiply-add
+// for its source.
+template <int D, int BS>
+struct Copier {
+  using R = Ring<D>;
+  static constexpr uint32_t TILE = BS * fp4_row_bytes(D), CODES = BS * fp4_code_bytes(D);
+  static constexpr int GROUPS = D / kFp4Group;
+  static constexpr int BLOCKS = kStep / BS;  // of a step: 1, 2 or 4
+  // Chunks lane and lane + 32 of a slice go to place(lane) and, two pairs of
+  // lines on, to place(lane) ^ 64 past 512 bytes.
+  static constexpr int ROUNDS = R::CHUNKS / 32;
+  const uint8_t *k, *v;  // the lane's chunk of a slice in the first tile
+  const uint8_t *scale;  // the lane's scale row there, of K or of V
+  uint32_t chunk, row;   // places in a slot of the chunk and of the scale row
+
+  __device__ __forceinline__ explicit Copier(const Fp4Params &p) {
+    const int lane = threadIdx.x & 31;
+    // (blocks of 8 at D 64: the upper half of the lanes copies a slice's second block)
+    const int c = BLOCKS == 4 && ROUNDS == 1 ? lane & 15 : lane;
+    k = p.k_cache + c * 16;
+    v = p.v_cache + c * 16;
+    chunk = R::place(lane);
+    scale = (lane / GROUPS & 1 ? p.v_cache : p.k_cache) + CODES + lane % GROUPS * BS;
+    row = R::KS + lane % (2 * GROUPS) * 16;
+    // the upper lanes' scale rows: the second slice's, or (blocks of 8) a
+    // slice's second block's 8 bytes
+    if (lane >= 2 * GROUPS) {
+      row += BLOCKS == 4 ? 8 : R::SLICE;
+      if (BLOCKS == 1) scale += 16;
+    }
+  }
+  __device__ __forceinline__ static const uint8_t *at(const uint8_t *base, uint32_t tile) {
+    return base + static_cast<uint64_t>(tile) * TILE;
+  }
+  // t[i]: the tiles (block * KV heads + head) of the step's blocks
+  __device__ __forceinline__ void operator()(uint32_t slot, const uint32_t (&t)[BLOCKS]) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t to0 = slot + chunk, to1 = slot + (chunk ^ 64u) + 512;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // the slices
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const uint32_t tile = BLOCKS == 4 ? (ROUNDS == 2 ? t[(2 * half + i) % BLOCKS] : lane < 16 ? t[2 * half % BLOCKS] : t[(2 * half + 1) % BLOCKS])
+                                          : t[half * (BLOCKS - 1)];
+        // bytes past the lane's chunk of the tile: the first slice, the first 32 chunks
+        const int off = (BLOCKS == 1 ? half * R::CODES : 0) + (BLOCKS == 4 ? 0 : i * 512);
+        const uint32_t dst = (i == 0 ? to0 : to1) + half * R::SLICE;
+        copy_async<16>(dst, at(k, tile) + off);
+        copy_async<16>(dst + R::V, at(v, tile) + off);
+      }
+    }
+    const bool upper = lane >= 2 * GROUPS;
+    if constexpr (BLOCKS < 4) {  // rows of 16: (slice, K | V, group)
+      if (4 * GROUPS == 32 || lane < 4 * GROUPS)
+        copy_async<16>(slot + row, at(scale, upper ? t[BLOCKS - 1] : t[0]));
+    } else {  // of 8: (block of the slice, K | V, group)
+      if (4 * GROUPS == 32 || lane < 4 * GROUPS) {
+        copy_async<8>(slot + row, at(scale, upper ? t[1] : t[0]));
+        copy_async<8>(slot + row + R::SLICE, at(scale, upper ? t[BLOCKS - 1] : t[BLOCKS - 2]));
+      }
+    }
+  }
+};
+
+// Rows of the warps' states in shared memory, padded so that the rows
+// of neighbouring queries start 4 banks apart.
+template <int D>
+constexpr int kRow = D + 4;
+
+__device__ __forceinline__ int clamp_length(int L, int cap) { return min(max(L, 0), cap); }
+
+// A piece of a pair: tokens [t0, t1) of sequence s for KV head h.
+struct Piece {
+  int s, h, L, t0, t1;
+  bool first, last;  // whether it holds the pair's first, last token
+};
+
+template <int QT, int D, int G, int BS>
+__global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __grid_constant__ Fp4Params p) {
+  // the warps' rings, then their states at a piece's end, [warp][query][kRow<D>]
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int RING = kRing * Ring<D>::SLOT;
+  float *s_o = reinterpret_cast<float *>(smem + kWarps * RING);
+  __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+  __shared__ long long s_wsum[kWarps];
+  __shared__ long long s_base;
+  __shared__ int s_first;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
+  const int S = p.num_seqs, H = p.num_kv_heads;
+
+  // ---- the share: units of all pairs before each thread's run of sequences
+  // (lengths only: this kernel may start before the one ahead of it ends)
+  auto length = [&](int s) { return clamp_length(__ldg(p.seq_lens + s), p.len_cap); };
+  auto units = [&](int L) { return kPairCost + max(1, (L + kUnit - 1) / kUnit); };  // of a pair
+  const int per = (S + kFpThreads - 1) / kFpThreads;
+  const int a0 = min(S, tid * per), a1 = min(S, a0 + per);
+  long long mine = 0;
+  for (int s = a0; s < a1; ++s) {
+    const int L = __ldg(p.seq_lens + s);
+    if (blockIdx.x == 0 && (L < 0 || L > p.len_cap)) record_error(p.err, kErrSeqLen);
+    mine += static_cast<long long>(units(clamp_length(L, p.len_cap))) * H;
+  }
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) s_wsum[warp] = upto;
+  __syncthreads();
+  long long U = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_wsum[w];
+    U += s_wsum[w];
+  }
+  before += upto - mine;  // units before this thread's run
+  const bool cut = p.max_parts > 1;
+  long long n = gridDim.x;
+  if (cut) n = min(n, max(1ll, U * kUnit / (2ll * p.partition_size)));
+  const long long b = blockIdx.x;
+  const long long u0 = b * U / n;
+  long long left = b < n ? (b + 1) * U / n - u0 : 0;  // units of the share not yet taken
+  // the sequence that holds unit u0, and the units before it
+  if (left > 0 && before <= u0 && u0 < before + mine) {
+    long long base = before;
+    int s = a0;
+    for (; s < a1 - 1; ++s) {
+      const long long x = static_cast<long long>(units(length(s))) * H;
+      if (u0 < base + x) break;
+      base += x;
+    }
+    s_first = s;
+    s_base = base;
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  launch_dependents();  // the merge (or the next call, which waits for this grid)
+  if (left <= 0) return;
+  // the next piece: KV head h of sequence s from unit off of the pair
+  int s = s_first, h, off, number = 0;  // number: the first piece's among its pair's
+  {
+    const int nu = units(length(s));
+    const long long rel = u0 - s_base;
+    h = static_cast<int>(rel / nu);
+    off = static_cast<int>(rel - static_cast<long long>(h) * nu);
+    // (counted from the holder of the pair's first token)
+    if (off > kPairCost) number = static_cast<int>(b - ((u0 - off + kPairCost + 1) * n - 1) / U);
+    if (!cut && off > 0) {  // whole pairs go to the CTA that holds their first unit
+      left -= nu - off;
+      off = 0;
+      ++h;
+    }
+  }
+  auto advance = [&](Piece &x) {
+    if (left <= 0) return false;
+    if (h == H) {
+      h = off = 0;
+      ++s;
+    }
+    x.s = s;
+    x.h = h;
+    x.L = length(s);
+    const int nu = units(x.L);
+    const int end = cut && left < nu - off ? off + static_cast<int>(left) : nu;
+    left -= end - off;
+    x.first = off <= kPairCost;
+    x.last = end == nu;
+    x.t0 = max(0, off - kPairCost) * kUnit;
+    x.t1 = min(x.L, (end - kPairCost) * kUnit);
+    off = end;
+    if (x.last) {
+      off = 0;
+      ++h;
+    }
+    return end > kPairCost;  // (else the share ends before the pair's first token)
+  };
+
+  uint8_t *ring = smem + warp * RING;
+  const uint32_t ring_addr = smem_addr(ring);
+  const Copier<D, BS> copy(p);
+  constexpr int BLOCKS = Copier<D, BS>::BLOCKS, WIN = 32 / BLOCKS;  // steps of a window of blocks
+  // The warp's steps i = 0, 1, ... of a piece: from token t0 + 32 (warp + 4 i).
+  auto steps_of = [&](const Piece &x) {
+    const int t = x.t0 + kStep * warp;
+    return t < x.t1 ? (x.t1 - t + kStep * kWarps - 1) / (kStep * kWarps) : 0;
+  };
+  // The tiles of steps i0 .. i0 + WIN - 1: lane i has that of block i % BLOCKS
+  // of step i0 + i / BLOCKS (past the last block, the last one's).
+  auto window = [&](const Piece &x, int i0, int steps) {
+    uint32_t tile = 0;
+    const int i = i0 + lane / BLOCKS;
+    if (i < steps) {
+      const int t = x.t0 + kStep * (warp + kWarps * i);
+      int blk = __ldg(p.block_tables + static_cast<size_t>(x.s) * p.max_blocks +
+                      min(t / BS + lane % BLOCKS, (x.L - 1) / BS));
+      if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
+        record_error(p.err, kErrBlockIndex);
+        blk = 0;
+      }
+      tile = static_cast<uint32_t>(blk) * H + x.h;
+    }
+    return tile;
+  };
+  uint32_t slot = 0;  // the ring slot in use; the next step goes to the other
+  auto issue = [&](uint32_t win, int i, uint32_t to) {  // step i of its window
+    uint32_t t[BLOCKS];
+#pragma unroll
+    for (int j = 0; j < BLOCKS; ++j) t[j] = __shfl_sync(0xffffffffu, win, i * BLOCKS + j);
+    copy(ring_addr + to, t);
+  };
+
+  Piece cur, nxt;
+  if (!advance(cur)) return;
+  int steps = steps_of(cur);
+  uint32_t win = window(cur, 0, steps);
+  if (steps > 0) issue(win, 0, slot);
+  while (true) {  // the pieces of the share
+    // ahead of this piece's loop: its next window, the next piece and its first window
+    uint32_t win2 = window(cur, WIN, steps);
+    const bool more = advance(nxt);
+    const int nsteps = more ? steps_of(nxt) : 0;
+    const uint32_t nwin = more ? window(nxt, 0, nsteps) : 0;
+    State<D> st;
+    float qk = p.qk_scale_log2, vsc = p.v_scale;
+    if (p.k_head_scale != nullptr) {
+      qk *= __ldg(p.k_head_scale + cur.h);
+      vsc = __ldg(p.v_head_scale + cur.h);
+    }
+    load_q<QT, D, G>(st, p.q + (static_cast<size_t>(cur.s) * p.num_q_heads + cur.h * G) * D * 2, qk);
+    if (steps == 0 && nsteps > 0) issue(nwin, 0, slot);
+    int valid = cur.t1 - cur.t0 - kStep * warp;  // tokens from the step's first to the piece's end
+    for (int i = 0, w = 1; i < steps; ++i, ++w, valid -= kStep * kWarps) {  // w: the next step's place in its window
+      cp_async_commit();
+      cp_async_wait<0>();  // the step has landed for this lane
+      __syncwarp();        // and for the others; the one before has been read by all
+      const uint32_t other = slot ^ Ring<D>::SLOT;
+      if (i + 1 < steps) {
+        if (w == WIN) {
+          win = win2;
+          win2 = window(cur, i + 1 + WIN, steps);
+          w = 0;
+        }
+        issue(win, w, other);
+      } else if (nsteps > 0) {
+        issue(nwin, 0, other);
+      }
+      attend<D>(st, ring + slot, min(kStep, valid));
+      slot = other;
+    }
+
+    // ---- the warps' states meet (the last piece's have been read by then)
+    __syncthreads();
+    float l0 = st.l[0], l1 = st.l[1];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int j = 2 * tq + r;
+      if (j < G) {
+        float *dst = s_o + (warp * G + j) * kRow<D> + gq * (D / 8);
+        if (gq == 0) {
+          s_m[warp][j] = st.m[r];
+          s_l[warp][j] = r ? l1 : l0;
+        }
+#pragma unroll
+        for (int i = 0; i < State<D>::MT; i += 4) {
+          *reinterpret_cast<float4 *>(dst + i) = make_float4(st.o[i][r], st.o[i + 1][r], st.o[i + 2][r], st.o[i + 3][r]);
+          *reinterpret_cast<float4 *>(dst + D / 16 + i) =
+              make_float4(st.o[i][2 + r], st.o[i + 1][2 + r], st.o[i + 2][2 + r], st.o[i + 3][2 + r]);
+        }
+      }
+    }
+    __syncthreads();
+    {
+      constexpr int E = D / 32;  // columns a lane
+      const int piece = cur.first ? 0 : number;
+      for (int j = warp; j < G; j += kWarps) {  // a warp joins queries warp, warp + 4
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][j]);
+        float den = 0.f, x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = s_m[w][j] == -INFINITY ? 0.f : ex2(s_m[w][j] - M);
+          den = fmaf(f, s_l[w][j], den);
+          const float *src = s_o + (w * G + j) * kRow<D> + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = fmaf(f, src[e], x[e]);
+        }
+        const float inv = den == 0.f ? 0.f : vsc / den;
+        const int hq = cur.h * G + j;
+        if (cur.first && cur.last) {
+          uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) +
+                                                       (static_cast<size_t>(cur.s) * p.num_q_heads + hq) * D + lane * E);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) out[e / 2] = pack2_rn<QT>(x[e] * inv, x[e + 1] * inv);
+        } else {
+          const size_t at = (static_cast<size_t>(cur.s) * p.max_parts + piece) * p.num_q_heads + hq;
+#pragma unroll
+          for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<float2 *>(p.part_o + at * D + lane * E + e) = make_float2(x[e] * inv, x[e + 1] * inv);
+          if (lane == 0) p.part_ml[at] = make_float2(M, den);
+        }
+        // the end of the pair's pieces (none at all when the output is written)
+        if (lane == 0 && cur.last && cut) {
+          const int e = cur.first ? 0 : piece + 1;
+          if (e < p.max_parts)
+            p.part_ml[(static_cast<size_t>(cur.s) * p.max_parts + e) * p.num_q_heads + hq] = make_float2(0.f, kWritten);
+        }
+      }
+    }
+    if (!more) break;
+    cur = nxt;
+    steps = nsteps;
+    win = nwin;
+  }
+}
+
+// One CTA per (sequence, query head): joins its pieces' partials,
+// out = sum_j w_j o_j / sum_j w_j with w_j = exp2(m_j - M) l_j, up to the mark
+// that ends them.  Warp w takes the pieces w, w + 4, ..., eight of them in
+// flight; lane l owns D / 32 columns.
+constexpr int kMergeWarps = 4;
+
+template <int QT, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const __grid_constant__ Fp4Params p) {
+  constexpr int E = D / 32;
+  __shared__ float s_o[kMergeWarps][D];
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int s = blockIdx.x / p.num_q_heads, hq = blockIdx.x % p.num_q_heads;
+  grid_dependency_wait();
+  const size_t at = static_cast<size_t>(s) * p.max_parts * p.num_q_heads + hq;
+  const float2 *ml = p.part_ml + at;
+  const float *po = p.part_o + at * D + lane * E;
+  const size_t stride = p.num_q_heads;
+  float M = -INFINITY, den = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int j0 = 0; j0 < p.max_parts; j0 += 32 * kMergeWarps) {
+    // this round's places: lane l of every warp looks at all of the round's
+    // marks, and keeps the piece j0 + warp + 4 l
+    int cnt = 0;  // pieces of the round
+    bool open = true;
+#pragma unroll
+    for (int r = 0; r < kMergeWarps; ++r) {
+      const int j = j0 + 32 * r + lane;
+      const float l = j < p.max_parts ? ml[j * stride].y : kWritten;
+      const unsigned ended = __ballot_sync(0xffffffffu, l == kWritten);
+      if (open) cnt += ended ? __ffs(ended) - 1 : 32;
+      open = open && !ended;
+    }
+    if (j0 == 0 && cnt == 0) return;  // written by the CTA that held the whole pair
+    const int mine = cnt > warp ? (cnt - warp + kMergeWarps - 1) / kMergeWarps : 0;
+    float2 x = make_float2(-INFINITY, 0.f);
+    if (lane < mine) x = ml[(j0 + warp + kMergeWarps * lane) * stride];
+    float top = x.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float N = fmaxf(M, top);
+    const float old = M == -INFINITY ? 0.f : ex2(M - N);
+    M = N;
+    const float w = x.x == -INFINITY ? 0.f : ex2(x.x - N) * x.y;
+    float ws = w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+    den = den * old + ws;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= old;
+#pragma unroll 8
+    for (int k = 0; k < mine; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float *src = po + (j0 + warp + kMergeWarps * k) * stride * D;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(src + e);
+        acc[e] = fmaf(wk, v.x, acc[e]);
+        acc[e + 1] = fmaf(wk, v.y, acc[e + 1]);
+      }
+    }
+    if (!open) break;
+  }
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = den;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+  __syncthreads();
+  const int d = threadIdx.x * 2;
+  if (d >= D) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_m[w]);
+  float l = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - top);
+    l = fmaf(f, s_l[w], l);
+    a = fmaf(f, s_o[w][d], a);
+    b = fmaf(f, s_o[w][d + 1], b);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + (static_cast<size_t>(s) * p.num_q_heads + hq) * D + d) =
+      pack2_rn<QT>(a * inv, b * inv);
+}
+
+template <int QT, int D, int G, int BS>
+pa_status launch(const Fp4Params &p, const DeviceInfo &dev, cudaStream_t stream) {
+  constexpr int smem = kWarps * (kRing * Ring<D>::SLOT + G * kRow<D> * 4);
+  static_assert(kCtas * (smem + 2048) <= kSmemPerSm, "the CTAs of an SM fit its shared memory");
+  static bool configured[64];  // per device: dynamic shared memory already allowed
+  int id = 0;
+  cudaError_t e = cudaGetDevice(&id);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (id < 0 || id >= 64 || !configured[id]) {
+    e = cudaFuncSetAttribute(decode_fp4_kernel<QT, D, G, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (id >= 0 && id < 64) configured[id] = true;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  // no more CTAs than pairs (when they are dealt out whole) or than the
+  // longest lengths give units
+  const long long pairs = static_cast<long long>(p.num_seqs) * p.num_kv_heads;
+  const long long most = p.max_parts > 1 ? pairs * p.max_parts : pairs;
+  const long long slots = static_cast<long long>(dev.sm_count) * kCtas;
+  cfg.gridDim = dim3(static_cast<unsigned>(most < slots ? most : slots));
+  cfg.blockDim = dim3(kFpThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, decode_fp4_kernel<QT, D, G, BS>, p);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (p.max_parts > 1) {
+    cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.num_q_heads);
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, D>, p);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return PA_OK;
+}
+
+template <int BS, int QT, int D>
+pa_status by_group(int group, const Fp4Params &p, const DeviceInfo &dev, cudaStream_t s) {
+  switch (group) {
+    case 1: return launch<QT, D, 1, BS>(p, dev, s);
+    case 2: return launch<QT, D, 2, BS>(p, dev, s);
+    case 4: return launch<QT, D, 4, BS>(p, dev, s);
+    case 8: return launch<QT, D, 8, BS>(p, dev, s);
+  }
+  return PA_ERR_UNSUPPORTED;
+}
+
+// The instantiations of one block size.
+template <int BS>
+pa_status dispatch(int q_dtype, int head_dim, int group, const DecodeParams &d, const DeviceInfo &dev,
+                   cudaStream_t stream) {
+  Fp4Params p{};
+  p.out = d.out;
+  p.q = d.q;
+  p.k_cache = d.k_cache;
+  p.v_cache = d.v_cache;
+  p.block_tables = d.block_tables;
+  p.seq_lens = d.seq_lens;
+  p.num_seqs = d.num_seqs;
+  p.num_q_heads = d.num_q_heads;
+  p.num_kv_heads = d.num_kv_heads;
+  p.num_blocks = d.num_blocks;
+  p.max_blocks = d.max_blocks;
+  p.len_cap = d.len_cap;
+  p.max_parts = d.max_parts;
+  p.partition_size = d.partition_size;
+  p.qk_scale_log2 = d.qk_scale_log2;
+  p.v_scale = d.v_scale;
+  p.k_head_scale = d.k_head_scale;
+  p.v_head_scale = d.v_head_scale;
+  p.part_ml = d.part_ml;
+  p.part_o = d.part_o;
+  p.err = d.err;
+  if (q_dtype == kF16)
+    return head_dim == 64 ? by_group<BS, kF16, 64>(group, p, dev, stream)
+                          : by_group<BS, kF16, 128>(group, p, dev, stream);
+  return head_dim == 64 ? by_group<BS, kBF16, 64>(group, p, dev, stream)
+                        : by_group<BS, kBF16, 128>(group, p, dev, stream);
+}
+
+}  // namespace
+}  // namespace pa

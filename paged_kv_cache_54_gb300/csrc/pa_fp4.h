@@ -10,8 +10,13 @@ namespace pa {
 pa_status write_fp4(const void *key, const void *value, int src_dtype, const int64_t *slots, int num_tokens,
                     void *k_cache, void *v_cache, const pa_cache_desc *cache, int *err, cudaStream_t stream);
 
-// pa_decode over a PA_FP4 cache (pa_decode_fp4.cu)
-pa_status dispatch_decode_fp4(int q_dtype, int head_dim, int group, const DecodeParams &p, const DeviceInfo &dev,
-                              cudaStream_t stream);
+// pa_decode over a PA_FP4 cache (pa_decode_fp4.cuh), a translation unit for
+// each block size
+pa_status dispatch_decode_fp4_b8(int q_dtype, int head_dim, int group, const DecodeParams &p, const DeviceInfo &dev,
+                                 cudaStream_t stream);
+pa_status dispatch_decode_fp4_b16(int q_dtype, int head_dim, int group, const DecodeParams &p, const DeviceInfo &dev,
+                                  cudaStream_t stream);
+pa_status dispatch_decode_fp4_b32(int q_dtype, int head_dim, int group, const DecodeParams &p, const DeviceInfo &dev,
+                                  cudaStream_t stream);
 
 }  // namespace pa
