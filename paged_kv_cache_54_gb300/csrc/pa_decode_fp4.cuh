@@ -95,7 +95,8 @@ struct State {
   uint32_t qb[KSTEPS][2];
   float o[MT][4];
   float m[2], l[2];
-  float mult;
+  float top[2];      // unscaled scores above these bring the maximum up
+  float mult, lift;  // of the scores, and its reciprocal
 };
 
 // q rows of the group (G x D at `q`) as B fragments: column gq is query gq,
@@ -143,6 +144,8 @@ __device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float sca
 #pragma unroll
   for (int i = 0; i < QW; ++i) w[i] = scale > 0.f ? w[i] : scale < 0.f ? w[i] ^ 0x80008000u : 0u;
   st.mult = scale == 0.f ? 1.f : fabsf(scale) / f;
+  st.lift = 1.f / st.mult;
+  st.top[0] = st.top[1] = -INFINITY;
 #pragma unroll
   for (int kk = 0; kk < State<D>::KSTEPS; ++kk) {
     st.qb[kk][0] = w[2 * kk];
@@ -163,10 +166,24 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// c += A * B, fp16 operands
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // c = A * B with a zero addend (no registers to clear first)
 __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -193,8 +210,8 @@ __device__ __forceinline__ void scores(const State<D> &st, const KSlice<D> &c, f
       mma_first(acc[0], a[0], b[0], a[1], b[1], st.qb[0][0], st.qb[0][1]);
       mma_first(acc[1], a[2], b[2], a[3], b[3], st.qb[1][0], st.qb[1][1]);
     } else {
-      mma16816<kF16>(acc[0], a[0], b[0], a[1], b[1], st.qb[2 * w][0], st.qb[2 * w][1]);
-      mma16816<kF16>(acc[1], a[2], b[2], a[3], b[3], st.qb[2 * w + 1][0], st.qb[2 * w + 1][1]);
+      mma(acc[0], a[0], b[0], a[1], b[1], st.qb[2 * w][0], st.qb[2 * w][1]);
+      mma(acc[1], a[2], b[2], a[3], b[3], st.qb[2 * w + 1][0], st.qb[2 * w + 1][1]);
     }
   }
 #pragma unroll
@@ -242,7 +259,7 @@ __device__ __forceinline__ void accumulate(State<D> &st, const VSlice<D> &c, con
     const uint32_t r1 = (hi & 1) ? oA[hi / 8][hi % 8 / 2] : eA[hi / 8][hi % 8 / 2];
     const uint32_t r2 = (lo & 1) ? oB[lo / 8][lo % 8 / 2] : eB[lo / 8][lo % 8 / 2];
     const uint32_t r3 = (hi & 1) ? oB[hi / 8][hi % 8 / 2] : eB[hi / 8][hi % 8 / 2];
-    mma16816<kF16>(st.o[mi], r0, r1, r2, r3, w0, w1);
+    mma(st.o[mi], r0, r1, r2, r3, w0, w1);
   }
 }
 
@@ -328,20 +345,28 @@ __device__ __forceinline__ void attend(State<D> &st, const uint8_t *slot, int n)
     if (kSlice + 2 * gq >= n) b[0] = b[1] = -INFINITY;
     if (kSlice + 2 * gq + 1 >= n) b[2] = b[3] = -INFINITY;
   }
-  // ---- online softmax of query columns 2tq, 2tq + 1
-  float x0 = fmaxf(fmaxf(a[0], a[2]), fmaxf(b[0], b[2])), x1 = fmaxf(fmaxf(a[1], a[3]), fmaxf(b[1], b[3]));
+  // ---- online softmax of query columns 2tq, 2tq + 1.  The maximum is brought
+  // up, and the state rescaled, only when some score passes it by 2^8; each
+  // lane compares its own scores, so a step that does not need it shuffles
+  // nothing.
+  float x0 = fmaxf(max3(a[0], a[2], b[0]), b[2]), x1 = fmaxf(max3(a[1], a[3], b[1]), b[3]);
+  if (__any_sync(0xffffffffu, x0 > st.top[0] || x1 > st.top[1])) {
 #pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
-    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
-  }
-  x0 *= st.mult;
-  x1 *= st.mult;
-  const bool up0 = x0 > st.m[0] + kLazy, up1 = x1 > st.m[1] + kLazy;
-  if (__any_sync(0xffffffffu, up0 || up1)) {
-    const float f0 = up0 ? ex2(st.m[0] - x0) : 1.f, f1 = up1 ? ex2(st.m[1] - x1) : 1.f;
-    if (up0) st.m[0] = x0;
-    if (up1) st.m[1] = x1;
+    for (int o = 4; o < 32; o <<= 1) {
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+    }
+    const bool up0 = x0 > st.top[0], up1 = x1 > st.top[1];
+    const float n0 = x0 * st.mult, n1 = x1 * st.mult;
+    const float f0 = up0 ? ex2(st.m[0] - n0) : 1.f, f1 = up1 ? ex2(st.m[1] - n1) : 1.f;
+    if (up0) {
+      st.m[0] = n0;
+      st.top[0] = fmaf(kLazy, st.lift, x0);
+    }
+    if (up1) {
+      st.m[1] = n1;
+      st.top[1] = fmaf(kLazy, st.lift, x1);
+    }
 #pragma unroll
     for (int i = 0; i < State<D>::MT; ++i) {
       st.o[i][0] *= f0;
