@@ -42,6 +42,8 @@
 // one conversion of a byte gives the pair.
 #pragma once
 
+#include <limits.h>
+
 #include "pa_fp4.cuh"
 #include "pa_fp4.h"
 
@@ -522,6 +524,7 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
   }
   before += upto - mine;  // units before this thread's run
   const bool cut = p.max_parts > 1;
+  // (cut pairs' pieces have their places when a share is two partitions long)
   long long n = gridDim.x;
   if (cut) n = min(n, max(1ll, U * kUnit / (2ll * p.partition_size)));
   const long long b = blockIdx.x;
@@ -728,20 +731,24 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
   }
 }
 
-// One CTA per (sequence, query head): joins its pieces' partials,
+// W warps per (sequence, query head) join its pieces' partials,
 // out = sum_j w_j o_j / sum_j w_j with w_j = exp2(m_j - M) l_j, up to the mark
-// that ends them.  Warp w takes the pieces w, w + 4, ..., eight of them in
-// flight; lane l owns D / 32 columns.
+// that ends them.  Warp w takes the pieces w, w + W, ..., eight of them in
+// flight; lane l owns D / 32 columns.  One warp is enough when there are many
+// heads to fill the SMs; few heads have many pieces each.
 constexpr int kMergeWarps = 4;
 
-template <int QT, int D>
+template <int QT, int D, int W>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const __grid_constant__ Fp4Params p) {
   constexpr int E = D / 32;
   __shared__ float s_o[kMergeWarps][D];
   __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int s = blockIdx.x / p.num_q_heads, hq = blockIdx.x % p.num_q_heads;
+  __shared__ int s_end[kMergeWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
+  const long long head = W == kMergeWarps ? blockIdx.x : blockIdx.x * static_cast<long long>(kMergeWarps / W) + warp / W;
   grid_dependency_wait();
+  if (W == 1 && head >= static_cast<long long>(p.num_seqs) * p.num_q_heads) return;
+  const int s = static_cast<int>(head / p.num_q_heads), hq = static_cast<int>(head % p.num_q_heads);
   const size_t at = static_cast<size_t>(s) * p.max_parts * p.num_q_heads + hq;
   const float2 *ml = p.part_ml + at;
   const float *po = p.part_o + at * D + lane * E;
@@ -749,23 +756,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const __gri
   float M = -INFINITY, den = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int j0 = 0; j0 < p.max_parts; j0 += 32 * kMergeWarps) {
-    // this round's places: lane l of every warp looks at all of the round's
-    // marks, and keeps the piece j0 + warp + 4 l
-    int cnt = 0;  // pieces of the round
-    bool open = true;
+  for (int j0 = 0; j0 < p.max_parts; j0 += 32 * W) {
+    // this round: lane l has piece j0 + w0 + W l, and the first mark is the end
+    const int j = j0 + w0 + W * lane;
+    float2 x = make_float2(-INFINITY, kWritten);
+    if (j < p.max_parts) x = ml[j * stride];
+    const unsigned marks = __ballot_sync(0xffffffffu, x.y == kWritten);
+    int end = marks ? j0 + w0 + W * (__ffs(marks) - 1) : INT_MAX;
+    if constexpr (W > 1) {
+      if (j0 > 0) __syncthreads();  // (the round before has been read)
+      if (lane == 0) s_end[warp] = end;
+      __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kMergeWarps; ++r) {
-      const int j = j0 + 32 * r + lane;
-      const float l = j < p.max_parts ? ml[j * stride].y : kWritten;
-      const unsigned ended = __ballot_sync(0xffffffffu, l == kWritten);
-      if (open) cnt += ended ? __ffs(ended) - 1 : 32;
-      open = open && !ended;
+      for (int w = 0; w < W; ++w) end = min(end, s_end[w]);
     }
-    if (j0 == 0 && cnt == 0) return;  // written by the CTA that held the whole pair
-    const int mine = cnt > warp ? (cnt - warp + kMergeWarps - 1) / kMergeWarps : 0;
-    float2 x = make_float2(-INFINITY, 0.f);
-    if (lane < mine) x = ml[(j0 + warp + kMergeWarps * lane) * stride];
+    if (end == 0) return;  // written by the CTA that held the whole pair
+    const int mine = min(32, (min(end, j0 + 32 * W) - j0 - w0 + W - 1) / W);  // (negative: none)
+    if (lane >= mine) x = make_float2(-INFINITY, 0.f);
     float top = x.x;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -779,42 +786,57 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const __gri
     den = den * old + ws;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= old;
-#pragma unroll 8
-    for (int k = 0; k < mine; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float *src = po + (j0 + warp + kMergeWarps * k) * stride * D;
+    const float *src = po + (j0 + w0) * stride * D;
+    for (int k0 = 0; k0 < mine; k0 += 8) {
+      float2 v[8][E / 2];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(src + e);
-        acc[e] = fmaf(wk, v.x, acc[e]);
-        acc[e + 1] = fmaf(wk, v.y, acc[e + 1]);
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e)
+          v[k][e] = k0 + k < mine ? reinterpret_cast<const float2 *>(src + (k0 + k) * W * stride * D)[e]
+                                  : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          acc[2 * e] = fmaf(wk, v[k][e].x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(wk, v[k][e].y, acc[2 * e + 1]);
+        }
       }
     }
-    if (!open) break;
+    if (end <= j0 + 32 * W) break;
   }
-  if (lane == 0) {
-    s_m[warp] = M;
-    s_l[warp] = den;
+  uint16_t *out = static_cast<uint16_t *>(p.out) + (static_cast<size_t>(s) * p.num_q_heads + hq) * D;
+  if constexpr (W == 1) {
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      reinterpret_cast<uint32_t *>(out + lane * E)[e / 2] = pack2_rn<QT>(acc[e] * inv, acc[e + 1] * inv);
+  } else {
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = den;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    const int d = threadIdx.x * 2;
+    if (d >= D) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w]);
+    float l = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - top);
+      l = fmaf(f, s_l[w], l);
+      a = fmaf(f, s_o[w][d], a);
+      b = fmaf(f, s_o[w][d + 1], b);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint32_t *>(out + d) = pack2_rn<QT>(a * inv, b * inv);
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
-  __syncthreads();
-  const int d = threadIdx.x * 2;
-  if (d >= D) return;
-  float top = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_m[w]);
-  float l = 0.f, a = 0.f, b = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - top);
-    l = fmaf(f, s_l[w], l);
-    a = fmaf(f, s_o[w][d], a);
-    b = fmaf(f, s_o[w][d + 1], b);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + (static_cast<size_t>(s) * p.num_q_heads + hq) * D + d) =
-      pack2_rn<QT>(a * inv, b * inv);
 }
 
 template <int QT, int D, int G, int BS>
@@ -848,10 +870,12 @@ pa_status launch(const Fp4Params &p, const DeviceInfo &dev, cudaStream_t stream)
   e = cudaLaunchKernelEx(&cfg, decode_fp4_kernel<QT, D, G, BS>, p);
   if (e != cudaSuccess) return cuda_fail(e);
   if (p.max_parts > 1) {
-    cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.num_q_heads);
+    const long long heads = static_cast<long long>(p.num_seqs) * p.num_q_heads;
+    const bool many = heads >= dev.sm_count * 8;
+    cfg.gridDim = dim3(static_cast<unsigned>(many ? (heads + kMergeWarps - 1) / kMergeWarps : heads));
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, merge_fp4_kernel<QT, D>, p);
+    e = cudaLaunchKernelEx(&cfg, many ? merge_fp4_kernel<QT, D, 1> : merge_fp4_kernel<QT, D, kMergeWarps>, p);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   return PA_OK;
