@@ -1,10 +1,33 @@
-// Cache write in four bits: each thread takes one group of 16 dimensions of
-// one row of K and of V, so that the group's scale needs no other thread.
+// Cache write in four bits.
+//
+// A thread takes one group of 16 dimensions of one row, of K and of V: the
+// group's scale needs no other thread, 32 bytes of each are in flight, and the
+// stores of a row's groups are consecutive 8-byte runs of codes.  Moving the
+// rows bounds it (2 bytes in and 9/16 out an element) as long as an element
+// costs few instructions: at the HBM rate an SM has about 14 of them for
+// each (128 lanes x 1.9 GHz over 9 elements a clock).  Two divisions an
+// element would be more than that, so:
+//   - the quotient by a group's scale g uses one reciprocal a group.  With
+//     r the correctly rounded 1 / g, q0 = y r and the exact remainder
+//     e = y - q0 g (an fma), q0 + e r is the correctly rounded y / g
+//     (Markstein, IBM J. Res. Dev. 34, 1990), so ties stay ties and the
+//     conversion to e2m1 rounds them to even;
+//   - the quotient by the head's scale the same way, and not at all when that
+//     is 1;
+//   - groups that those steps do not hold for (NaN, infinities, quotients out
+//     of range) are found on the packed 16-bit values and go the long way.
 #include "pa_fp4.cuh"
 #include "pa_fp4.h"
 
 namespace pa {
 namespace {
+
+// a / b in the binary32 arithmetic above: r is 1 / b correctly rounded, and
+// neither quotient nor remainder overflows or matters when it underflows.
+__device__ __forceinline__ float divide(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
 
 // e2m1 code of y / g in the low four bits: nearest, ties to even, +-6 beyond;
 // 0 for NaN.  g > 0.
@@ -15,85 +38,142 @@ __device__ __forceinline__ uint32_t e2m1_code(float y, float g) {
   return m | (signbit(y) ? 8u : 0u);
 }
 
-// One group: 16 values at `in` -> 8 bytes of codes and the e4m3 scale byte.
+// A group by divisions, NaN left out: any input.  Codes and scale byte.
 template <int SRC>
-__device__ __forceinline__ uint32_t quantise_group(const uint8_t *in, float scale, uint2 &codes) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4 *>(in));
-  const uint4 b = __ldg(reinterpret_cast<const uint4 *>(in) + 1);
+__device__ __noinline__ uint3 quantise_any(uint4 a, uint4 b, float scale) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float y[16], top = 0.f;
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 f = half2_bits_to_float2<SRC>(w[i]);
-    y[2 * i] = __fdiv_rn(f.x, scale);
-    y[2 * i + 1] = __fdiv_rn(f.y, scale);
-    top = fmaxf(top, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));  // fmaxf leaves NaN out
+    top = fmaxf(top, fmaxf(fabsf(__fdiv_rn(f.x, scale)), fabsf(__fdiv_rn(f.y, scale))));  // (fmaxf leaves NaN out)
   }
   const uint32_t g8 = __nv_cvt_float_to_fp8(__fdiv_rn(top, 6.f), __NV_SATFINITE, __NV_E4M3);
   const float g = byte2_to_float2<kE4M3>(g8).x;
-  codes = make_uint2(0u, 0u);
+  uint32_t c[2] = {0u, 0u};
   if (g8 != 0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      codes.x |= e2m1_code(y[i], g) << (4 * i);
-      codes.y |= e2m1_code(y[8 + i], g) << (4 * i);
+      const float2 f = half2_bits_to_float2<SRC>(w[i]);
+      c[i >> 2] |= (e2m1_code(__fdiv_rn(f.x, scale), g) | e2m1_code(__fdiv_rn(f.y, scale), g) << 4) << (8 * (i & 3));
     }
   }
-  return g8;
+  return make_uint3(c[0], c[1], g8);
 }
 
+// largest magnitude of the 16 values, NaN if there is one
 template <int SRC>
+__device__ __forceinline__ float largest(const uint32_t (&w)[8]) {
+  uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const uint32_t a = w[i] & 0x7fff7fffu;
+    if constexpr (SRC == kF16)
+      asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(a));
+    else
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(a));
+  }
+  const float2 f = half2_bits_to_float2<SRC>(m);
+  return f.x != f.x ? f.x : f.y != f.y ? f.y : fmaxf(f.x, f.y);
+}
+
+// One group: 16 values (32 bytes) -> 8 bytes of codes and the e4m3 scale
+// byte.  r is 1 / scale correctly rounded, `plain` whether scale lies
+// within 2^-60 .. 2^60.
+template <int SRC>
+__device__ __forceinline__ uint3 quantise_group(uint4 a, uint4 b, float scale, float r, bool plain) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const float top = largest<SRC>(w);
+  if (!(plain && top <= 0x1p60f)) return quantise_any<SRC>(a, b, scale);  // (NaN too)
+  // (the quotient of the largest is the largest quotient: rounding keeps order)
+  const float ytop = scale == 1.f ? top : divide(top, scale, r);
+  const uint32_t g8 = __nv_cvt_float_to_fp8(__fdiv_rn(ytop, 6.f), __NV_SATFINITE, __NV_E4M3);
+  if (g8 == 0) return make_uint3(0u, 0u, 0u);
+  const float g = byte2_to_float2<kE4M3>(g8).x, rg = __frcp_rn(g);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float2 f = half2_bits_to_float2<SRC>(w[i]);
+    if (scale != 1.f) {
+      f.x = divide(f.x, scale, r);
+      f.y = divide(f.y, scale, r);
+    }
+    f.x = divide(f.x, g, rg);
+    f.y = divide(f.y, g, rg);
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
+        : "=r"(c[i])
+        : "f"(f.x), "f"(f.y));
+  }
+  return make_uint3(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410), g8);
+}
+
+// IDX: the type that counts the groups.  GPR: groups of a row.
+template <int SRC, int GPR, class IDX>
 __global__ void __launch_bounds__(256) write_fp4_kernel(
-    const uint8_t *__restrict__ key, const uint8_t *__restrict__ value, const int64_t *__restrict__ slots,
-    int num_tokens, int kv_heads, int head_dim, int block_size, long long num_slots, uint8_t *__restrict__ k_cache,
+    const uint8_t *__restrict__ key, const uint8_t *__restrict__ value, const int64_t *__restrict__ slots, IDX total,
+    uint32_t kv_heads, int bs_shift, long long num_slots, uint8_t *__restrict__ k_cache,
     uint8_t *__restrict__ v_cache, float k_scale, float v_scale, const float *__restrict__ k_head_scales,
     const float *__restrict__ v_head_scales, int *err) {
   launch_dependents();  // no block table or length is written here
-  const int gpr = head_dim / kFp4Group;  // groups of a row
-  const int code_bytes = block_size * fp4_code_bytes(head_dim);
-  const long long tile = code_bytes + block_size * gpr;
-  const long long total = static_cast<long long>(num_tokens) * kv_heads * gpr;
-  for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int g = static_cast<int>(i % gpr);
-    const long long th = i / gpr;
-    const int h = static_cast<int>(th % kv_heads);
-    const long long t = th / kv_heads;
+  const uint32_t code_bytes = 8u * GPR << bs_shift, tile = 9u * GPR << bs_shift;
+  for (IDX i = blockIdx.x * static_cast<IDX>(256) + threadIdx.x; i < total; i += static_cast<IDX>(gridDim.x) * 256) {
+    const uint32_t g = static_cast<uint32_t>(i) % GPR;
+    const IDX th = i / GPR, t = th / kv_heads;
+    const uint32_t h = static_cast<uint32_t>(th - t * kv_heads);
     const long long slot = __ldg(slots + t);
+    const uint4 *ks = reinterpret_cast<const uint4 *>(key) + static_cast<size_t>(i) * 2;
+    const uint4 *vs = reinterpret_cast<const uint4 *>(value) + static_cast<size_t>(i) * 2;
+    const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
     if (slot < 0) continue;  // padding row
     if (slot >= num_slots) {
       if (h == 0 && g == 0) record_error(err, kErrSlot);
       continue;
     }
-    const long long blk = slot / block_size;
-    const int off = static_cast<int>(slot - blk * block_size);
-    const size_t base = (static_cast<size_t>(blk) * kv_heads + h) * tile;
-    const size_t src = (static_cast<size_t>(th) * head_dim + g * kFp4Group) * 2;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const float *head_scales = which == 0 ? k_head_scales : v_head_scales;
-      const float scale = head_scales != nullptr ? __ldg(head_scales + h) : (which == 0 ? k_scale : v_scale);
-      uint8_t *out = (which == 0 ? k_cache : v_cache) + base;
-      uint2 codes;
-      const uint32_t g8 = quantise_group<SRC>((which == 0 ? key : value) + src, scale, codes);
-      *reinterpret_cast<uint2 *>(out + off * (head_dim / 2) + g * 8) = codes;
-      out[code_bytes + g * block_size + off] = static_cast<uint8_t>(g8);
+    float sk = k_scale, sv = v_scale;
+    if (k_head_scales != nullptr) {
+      sk = __ldg(k_head_scales + h);
+      sv = __ldg(v_head_scales + h);
     }
+    const uint32_t off = static_cast<uint32_t>(slot) & ((1u << bs_shift) - 1);
+    const size_t base = (static_cast<size_t>(slot >> bs_shift) * kv_heads + h) * tile;
+    const size_t at = base + off * (8 * GPR) + g * 8, sat = base + code_bytes + (g << bs_shift) + off;
+    const uint3 ck = quantise_group<SRC>(k0, k1, sk, __frcp_rn(sk), sk >= 0x1p-60f && sk <= 0x1p60f);
+    *reinterpret_cast<uint2 *>(k_cache + at) = make_uint2(ck.x, ck.y);
+    k_cache[sat] = static_cast<uint8_t>(ck.z);
+    const uint3 cv = quantise_group<SRC>(v0, v1, sv, __frcp_rn(sv), sv >= 0x1p-60f && sv <= 0x1p60f);
+    *reinterpret_cast<uint2 *>(v_cache + at) = make_uint2(cv.x, cv.y);
+    v_cache[sat] = static_cast<uint8_t>(cv.z);
   }
+}
+
+template <int SRC, int GPR>
+void launch_write(const void *key, const void *value, const int64_t *slots, long long groups, void *k_cache,
+                  void *v_cache, const pa_cache_desc *c, int *err, cudaStream_t stream) {
+  const int shift = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
+  const long long num_slots = static_cast<long long>(c->num_blocks) * c->block_size;
+  const int blocks = grid_for(groups, 256);
+  auto go = [&](auto kern, auto total) {
+    kern<<<blocks, 256, 0, stream>>>(static_cast<const uint8_t *>(key), static_cast<const uint8_t *>(value), slots,
+                                     total, c->kv_heads, shift, num_slots, static_cast<uint8_t *>(k_cache),
+                                     static_cast<uint8_t *>(v_cache), c->k_scale, c->v_scale, c->k_head_scales,
+                                     c->v_head_scales, err);
+  };
+  // (32-bit indexes divide in a quarter of the instructions; the last step past the end must not wrap)
+  if (groups < 0xf0000000ll)
+    go(write_fp4_kernel<SRC, GPR, uint32_t>, static_cast<uint32_t>(groups));
+  else
+    go(write_fp4_kernel<SRC, GPR, uint64_t>, static_cast<uint64_t>(groups));
 }
 
 }  // namespace
 
 pa_status write_fp4(const void *key, const void *value, int src_dtype, const int64_t *slots, int num_tokens,
                     void *k_cache, void *v_cache, const pa_cache_desc *cache, int *err, cudaStream_t stream) {
-  const long long work = static_cast<long long>(num_tokens) * cache->kv_heads * (cache->head_dim / kFp4Group);
-  const int threads = 256;
-  auto *kern = src_dtype == PA_F16 ? write_fp4_kernel<kF16> : write_fp4_kernel<kBF16>;
-  kern<<<grid_for(work, threads), threads, 0, stream>>>(
-      static_cast<const uint8_t *>(key), static_cast<const uint8_t *>(value), slots, num_tokens, cache->kv_heads,
-      cache->head_dim, cache->block_size, static_cast<long long>(cache->num_blocks) * cache->block_size,
-      static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), cache->k_scale, cache->v_scale,
-      cache->k_head_scales, cache->v_head_scales, err);
+  const long long groups = static_cast<long long>(num_tokens) * cache->kv_heads * (cache->head_dim / kFp4Group);
+  auto *go = src_dtype == PA_F16 ? (cache->head_dim == 64 ? launch_write<kF16, 4> : launch_write<kF16, 8>)
+                                 : (cache->head_dim == 64 ? launch_write<kBF16, 4> : launch_write<kBF16, 8>);
+  go(key, value, slots, groups, k_cache, v_cache, cache, err, stream);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }

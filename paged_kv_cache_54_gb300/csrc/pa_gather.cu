@@ -1,85 +1,119 @@
 // pa_gather_cache: rows of K and V read back from the paged caches as 16-bit
-// values, the inverse of the cache write.  A thread moves eight values (16
-// bytes of output) of K and of V.
+// values, the inverse of the cache write.  A thread moves 16 values (one
+// group of a four-bit cache, 32 bytes of output) of K and of V; memory bounds
+// it.
 #include "pa_fp4.cuh"
 #include "pa_host.h"
 
 namespace pa {
 namespace {
 
-// eight values from `in` (their group's scale byte at `g8` for kFP4) -> 16-bit words
+struct Words {  // 16 values of 16 bits
+  uint4 a, b;
+};
+
+// 16 values from `in` (for kFP4 with their scale byte at `g8`)
 template <int KV, int DST>
-__device__ __forceinline__ uint4 read8(const uint8_t *in, const uint8_t *g8, float scale) {
+__device__ __forceinline__ Words read16(const uint8_t *in, const uint8_t *g8, float scale) {
   if constexpr (KV == kF16 || KV == kBF16) {
-    return __ldg(reinterpret_cast<const uint4 *>(in));
+    return {__ldg(reinterpret_cast<const uint4 *>(in)), __ldg(reinterpret_cast<const uint4 *>(in) + 1)};
   } else {
-    uint32_t o[4];
+    uint32_t h[8], o[8];  // fp16 pairs, results
     if constexpr (KV == kFP4) {
-      uint32_t h[4];
-      e2m1x8_to_half2x4(__ldg(reinterpret_cast<const uint32_t *>(in)), h);
+      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(in));
       const uint32_t g = __ldg(g8);
-      const uint32_t g2 = e4m3x2_to_half2(g | (g << 8));
+      const uint32_t g2 = e4m3x2_to_half2(g * 0x0101u);
+      uint32_t x[4], y[4];
+      e2m1x8_to_half2x4(w.x, x);
+      e2m1x8_to_half2x4(w.y, y);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = half2_bits_to_float2<kF16>(hmul2_bits(h[i], g2));
-        o[i] = pack2_rn<DST>(f.x * scale, f.y * scale);
+        h[i] = hmul2_bits(x[i], g2);
+        h[4 + i] = hmul2_bits(y[i], g2);
       }
     } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(in));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = byte2_to_float2<KV>((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
-        o[i] = pack2_rn<DST>(f.x * scale, f.y * scale);
-      }
+      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(in));
+      byte4_to_half2x2<KV>(w.x, h[0], h[1]);
+      byte4_to_half2x2<KV>(w.y, h[2], h[3]);
+      byte4_to_half2x2<KV>(w.z, h[4], h[5]);
+      byte4_to_half2x2<KV>(w.w, h[6], h[7]);
     }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = half2_bits_to_float2<kF16>(h[i]);
+      o[i] = pack2_rn<DST>(f.x * scale, f.y * scale);
+    }
+    return {make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7])};
   }
 }
 
-template <int KV, int DST>
+// IDX: the type that counts the groups of 16.
+template <int KV, int DST, class IDX>
 __global__ void __launch_bounds__(256) gather_kernel(uint8_t *__restrict__ key, uint8_t *__restrict__ value,
-                                                     const int64_t *__restrict__ slots, int num_tokens, int kv_heads,
-                                                     int head_dim, int block_size, long long num_slots,
+                                                     const int64_t *__restrict__ slots, IDX total, uint32_t kv_heads,
+                                                     int gpr_shift, int bs_shift, long long num_slots,
                                                      const uint8_t *__restrict__ k_cache,
                                                      const uint8_t *__restrict__ v_cache, float k_scale, float v_scale,
                                                      const float *__restrict__ k_head_scales,
                                                      const float *__restrict__ v_head_scales, int *err) {
   launch_dependents();  // no block table or length is written here
-  const int cpr = head_dim / 8;  // 16-byte chunks of an output row
-  const long long total = static_cast<long long>(num_tokens) * kv_heads * cpr;
-  for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int c = static_cast<int>(i % cpr);
-    const long long th = i / cpr;
-    const int h = static_cast<int>(th % kv_heads);
-    const long long t = th / kv_heads;
+  for (IDX i = blockIdx.x * static_cast<IDX>(256) + threadIdx.x; i < total; i += static_cast<IDX>(gridDim.x) * 256) {
+    const uint32_t g = static_cast<uint32_t>(i) & ((1u << gpr_shift) - 1);
+    const IDX th = i >> gpr_shift, t = th / kv_heads;
+    const uint32_t h = static_cast<uint32_t>(th - t * kv_heads);
     const long long slot = __ldg(slots + t);
-    uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
     if (slot >= num_slots) {
-      if (h == 0 && c == 0) record_error(err, kErrSlot);
+      if (h == 0 && g == 0) record_error(err, kErrSlot);
       continue;
     }
+    Words k = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, v = k;
     if (slot >= 0) {
-      const long long blk = slot / block_size;
-      const int off = static_cast<int>(slot - blk * block_size);
-      const size_t tile = static_cast<size_t>(blk) * kv_heads + h;
-      const float sk = k_head_scales != nullptr ? __ldg(k_head_scales + h) : k_scale;
-      const float sv = v_head_scales != nullptr ? __ldg(v_head_scales + h) : v_scale;
-      if constexpr (KV == kFP4) {
-        const size_t at = tile * (block_size * fp4_row_bytes(head_dim));
-        const size_t g8 = at + block_size * fp4_code_bytes(head_dim) + (c / 2) * block_size + off;
-        const size_t in = at + off * fp4_code_bytes(head_dim) + c * 4;
-        k = read8<KV, DST>(k_cache + in, k_cache + g8, sk);
-        v = read8<KV, DST>(v_cache + in, v_cache + g8, sv);
+      const uint32_t off = static_cast<uint32_t>(slot) & ((1u << bs_shift) - 1);
+      const size_t tile = static_cast<size_t>(slot >> bs_shift) * kv_heads + h;
+      float sk = k_scale, sv = v_scale;
+      if (k_head_scales != nullptr) {
+        sk = __ldg(k_head_scales + h);
+        sv = __ldg(v_head_scales + h);
+      }
+      if constexpr (KV == kFP4) {  // 8 bytes of codes a group, then the scales [group][token]
+        const size_t at = tile * (9u << (gpr_shift + bs_shift));
+        const size_t g8 = at + (8u << (gpr_shift + bs_shift)) + (g << bs_shift) + off;
+        const size_t in = at + (off << (gpr_shift + 3)) + g * 8;
+        k = read16<KV, DST>(k_cache + in, k_cache + g8, sk);
+        v = read16<KV, DST>(v_cache + in, v_cache + g8, sv);
       } else {
-        const size_t in = ((tile * block_size + off) * head_dim + c * 8) * elt_bytes(KV);
-        k = read8<KV, DST>(k_cache + in, nullptr, sk);
-        v = read8<KV, DST>(v_cache + in, nullptr, sv);
+        const size_t in = (((tile << bs_shift) + off) << gpr_shift | g) * (kFp4Group * elt_bytes(KV));
+        k = read16<KV, DST>(k_cache + in, nullptr, sk);
+        v = read16<KV, DST>(v_cache + in, nullptr, sv);
       }
     }
-    reinterpret_cast<uint4 *>(key)[i] = k;
-    reinterpret_cast<uint4 *>(value)[i] = v;
+    uint4 *ko = reinterpret_cast<uint4 *>(key) + static_cast<size_t>(i) * 2;
+    uint4 *vo = reinterpret_cast<uint4 *>(value) + static_cast<size_t>(i) * 2;
+    ko[0] = k.a;
+    ko[1] = k.b;
+    vo[0] = v.a;
+    vo[1] = v.b;
   }
+}
+
+template <int KV, int DST>
+void launch_gather(void *key, void *value, const int64_t *slots, int num_tokens, const void *k_cache,
+                   const void *v_cache, const pa_cache_desc *c, int *err, cudaStream_t stream) {
+  const int gpr_shift = c->head_dim == 64 ? 2 : 3, bs_shift = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
+  const long long groups = static_cast<long long>(num_tokens) * c->kv_heads << gpr_shift;
+  const long long num_slots = static_cast<long long>(c->num_blocks) * c->block_size;
+  const int blocks = grid_for(groups, 256);
+  auto go = [&](auto kern, auto total) {
+    kern<<<blocks, 256, 0, stream>>>(static_cast<uint8_t *>(key), static_cast<uint8_t *>(value), slots, total,
+                                     c->kv_heads, gpr_shift, bs_shift, num_slots, static_cast<const uint8_t *>(k_cache),
+                                     static_cast<const uint8_t *>(v_cache), c->k_scale, c->v_scale, c->k_head_scales,
+                                     c->v_head_scales, err);
+  };
+  // (32-bit indexes divide in a quarter of the instructions; the last step past the end must not wrap)
+  if (groups < 0xf0000000ll)
+    go(gather_kernel<KV, DST, uint32_t>, static_cast<uint32_t>(groups));
+  else
+    go(gather_kernel<KV, DST, uint64_t>, static_cast<uint64_t>(groups));
 }
 
 }  // namespace
@@ -100,25 +134,18 @@ extern "C" pa_status pa_gather_cache(void *key, void *value, int32_t dst_dtype, 
   if (!supported_cache_shape(cache)) return PA_ERR_UNSUPPORTED;
   const int kv = cache->dtype;
   if ((kv == PA_F16 || kv == PA_BF16) && kv != dst_dtype) return PA_ERR_UNSUPPORTED;
-  const int threads = 256;
-  const int blocks =
-      grid_for(static_cast<long long>(num_tokens) * cache->kv_heads * (cache->head_dim / 8), threads);
-  auto launch = [&](auto kern) {
-    kern<<<blocks, threads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        static_cast<uint8_t *>(key), static_cast<uint8_t *>(value), slot_mapping, num_tokens, cache->kv_heads,
-        cache->head_dim, cache->block_size, static_cast<long long>(cache->num_blocks) * cache->block_size,
-        static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), cache->k_scale, cache->v_scale,
-        cache->k_head_scales, cache->v_head_scales, device_error);
-  };
   const bool f16 = dst_dtype == PA_F16;
+  decltype(&launch_gather<kF16, kF16>) go = nullptr;
   switch (kv) {
-    case PA_F16: launch(gather_kernel<kF16, kF16>); break;
-    case PA_BF16: launch(gather_kernel<kBF16, kBF16>); break;
-    case PA_FP8_E4M3: launch(f16 ? gather_kernel<kE4M3, kF16> : gather_kernel<kE4M3, kBF16>); break;
-    case PA_FP8_E5M2: launch(f16 ? gather_kernel<kE5M2, kF16> : gather_kernel<kE5M2, kBF16>); break;
-    case PA_INT8: launch(f16 ? gather_kernel<kI8, kF16> : gather_kernel<kI8, kBF16>); break;
-    case PA_FP4: launch(f16 ? gather_kernel<kFP4, kF16> : gather_kernel<kFP4, kBF16>); break;
+    case PA_F16: go = launch_gather<kF16, kF16>; break;
+    case PA_BF16: go = launch_gather<kBF16, kBF16>; break;
+    case PA_FP8_E4M3: go = f16 ? launch_gather<kE4M3, kF16> : launch_gather<kE4M3, kBF16>; break;
+    case PA_FP8_E5M2: go = f16 ? launch_gather<kE5M2, kF16> : launch_gather<kE5M2, kBF16>; break;
+    case PA_INT8: go = f16 ? launch_gather<kI8, kF16> : launch_gather<kI8, kBF16>; break;
+    default: go = f16 ? launch_gather<kFP4, kF16> : launch_gather<kFP4, kBF16>; break;
   }
+  go(key, value, slot_mapping, num_tokens, k_cache, v_cache, cache, device_error,
+     reinterpret_cast<cudaStream_t>(stream));
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
