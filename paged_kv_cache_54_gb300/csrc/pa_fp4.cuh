@@ -40,4 +40,32 @@ __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
   return d;
 }
 
+// 32 bytes as one access where the address allows it (two of 16 otherwise):
+// lanes then touch whole sectors of consecutive addresses.
+struct Words32 {
+  uint4 a, b;
+};
+__device__ __forceinline__ Words32 load32(const uint8_t *p, bool wide) {
+  Words32 w;
+  if (wide) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w.a.x), "=r"(w.a.y), "=r"(w.a.z), "=r"(w.a.w), "=r"(w.b.x), "=r"(w.b.y), "=r"(w.b.z), "=r"(w.b.w)
+        : "l"(p));
+  } else {
+    w.a = __ldg(reinterpret_cast<const uint4 *>(p));
+    w.b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+  }
+  return w;
+}
+__device__ __forceinline__ void store32(uint8_t *p, const Words32 &w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w.a.x), "r"(w.a.y),
+                 "r"(w.a.z), "r"(w.a.w), "r"(w.b.x), "r"(w.b.y), "r"(w.b.z), "r"(w.b.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = w.a;
+    reinterpret_cast<uint4 *>(p)[1] = w.b;
+  }
+}
+
 }  // namespace pa

@@ -26,7 +26,21 @@ namespace {
 // neither quotient nor remainder overflows or matters when it underflows.
 __device__ __forceinline__ float divide(float a, float b, float r) {
   const float q = a * r;
-  return fmaf(fmaf(-q, b, a), r, q);
+  return fmaf(fmaf(q, -b, a), r, q);
+}
+// The same for two values at once (packed arithmetic, each lane rounded as
+// the scalar): nb is -b twice, r2 is r twice.
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ uint64_t divide2(uint64_t a, uint64_t nb, uint64_t r2) {
+  uint64_t q, e, d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(a), "l"(r2));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(nb), "l"(a));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(e), "l"(r2), "l"(q));
+  return d;
 }
 
 // e2m1 code of y / g in the low four bits: nearest, ties to even, +-6 beyond;
@@ -79,101 +93,116 @@ __device__ __forceinline__ float largest(const uint32_t (&w)[8]) {
 
 // One group: 16 values (32 bytes) -> 8 bytes of codes and the e4m3 scale
 // byte.  r is 1 / scale correctly rounded, `plain` whether scale lies
-// within 2^-60 .. 2^60.
+// within 2^-60 .. 2^60; table[c] is the value of scale code c and its
+// reciprocal.
 template <int SRC>
-__device__ __forceinline__ uint3 quantise_group(uint4 a, uint4 b, float scale, float r, bool plain) {
+__device__ __forceinline__ uint3 quantise_group(uint4 a, uint4 b, float scale, float r, bool plain,
+                                                const float2 *table) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   const float top = largest<SRC>(w);
   if (!(plain && top <= 0x1p60f)) return quantise_any<SRC>(a, b, scale);  // (NaN too)
   // (the quotient of the largest is the largest quotient: rounding keeps order)
   const float ytop = scale == 1.f ? top : divide(top, scale, r);
-  const uint32_t g8 = __nv_cvt_float_to_fp8(__fdiv_rn(ytop, 6.f), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t g8 = __nv_cvt_float_to_fp8(divide(ytop, 6.f, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
   if (g8 == 0) return make_uint3(0u, 0u, 0u);
-  const float g = byte2_to_float2<kE4M3>(g8).x, rg = __frcp_rn(g);
-  uint32_t c[8];
+  const float2 g = table[g8];
+  const uint64_t ng = twice(-g.x), rg = twice(g.y), ns = twice(-scale), rs = twice(r);
+  uint64_t y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float2 f = half2_bits_to_float2<SRC>(w[i]);
-    if (scale != 1.f) {
-      f.x = divide(f.x, scale, r);
-      f.y = divide(f.y, scale, r);
-    }
-    f.x = divide(f.x, g, rg);
-    f.y = divide(f.y, g, rg);
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
-        : "=r"(c[i])
-        : "f"(f.x), "f"(f.y));
+    const float2 f = half2_bits_to_float2<SRC>(w[i]);
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y[i]) : "f"(f.x), "f"(f.y));
   }
+  if (scale != 1.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = divide2(y[i], ns, rs);
+  }
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm("{\n\t.reg .b8 b;\n\t.reg .f32 x, y;\n\tmov.b64 {x, y}, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, y, x;\n\tcvt.u32.u8 %0, b;\n\t}"
+        : "=r"(c[i])
+        : "l"(divide2(y[i], ng, rg)));
   return make_uint3(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
                     __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410), g8);
 }
 
-// IDX: the type that counts the groups.  GPR: groups of a row.
-template <int SRC, int GPR, class IDX>
+// GPR: groups of a row.  A thread keeps one head and group (idx of the
+// kv_heads * GPR of a token) and walks the tokens t, t + step, ...: its scales
+// and places are set up once, and no index is divided on the way.
+template <int SRC, int GPR>
 __global__ void __launch_bounds__(256) write_fp4_kernel(
-    const uint8_t *__restrict__ key, const uint8_t *__restrict__ value, const int64_t *__restrict__ slots, IDX total,
-    uint32_t kv_heads, int bs_shift, long long num_slots, uint8_t *__restrict__ k_cache,
-    uint8_t *__restrict__ v_cache, float k_scale, float v_scale, const float *__restrict__ k_head_scales,
-    const float *__restrict__ v_head_scales, int *err) {
+    const uint8_t *__restrict__ key, const uint8_t *__restrict__ value, const int64_t *__restrict__ slots,
+    int num_tokens, int step, bool wide, uint32_t kv_heads, int bs_shift, long long num_slots,
+    uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache, float k_scale, float v_scale,
+    const float *__restrict__ k_head_scales, const float *__restrict__ v_head_scales, int *err) {
+  __shared__ float2 table[128];
   launch_dependents();  // no block table or length is written here
-  const uint32_t code_bytes = 8u * GPR << bs_shift, tile = 9u * GPR << bs_shift;
-  for (IDX i = blockIdx.x * static_cast<IDX>(256) + threadIdx.x; i < total; i += static_cast<IDX>(gridDim.x) * 256) {
-    const uint32_t g = static_cast<uint32_t>(i) % GPR;
-    const IDX th = i / GPR, t = th / kv_heads;
-    const uint32_t h = static_cast<uint32_t>(th - t * kv_heads);
-    const long long slot = __ldg(slots + t);
-    const uint4 *ks = reinterpret_cast<const uint4 *>(key) + static_cast<size_t>(i) * 2;
-    const uint4 *vs = reinterpret_cast<const uint4 *>(value) + static_cast<size_t>(i) * 2;
-    const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
-    if (slot < 0) continue;  // padding row
-    if (slot >= num_slots) {
-      if (h == 0 && g == 0) record_error(err, kErrSlot);
-      continue;
-    }
+  if (threadIdx.x < 128) {
+    const float g = byte2_to_float2<kE4M3>(threadIdx.x).x;
+    table[threadIdx.x] = make_float2(g, __frcp_rn(g));
+  }
+  __syncthreads();
+  const uint32_t code_bytes = 8u * GPR << bs_shift, tile = 9u * GPR << bs_shift, bs_mask = (1u << bs_shift) - 1;
+  const long long per_token = static_cast<long long>(kv_heads) * GPR, places = per_token * step;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < places; i += gridDim.x * 256ll) {
+    const int t0 = static_cast<int>(i / per_token);
+    const uint32_t idx = static_cast<uint32_t>(i - t0 * per_token), h = idx / GPR, g = idx % GPR;
     float sk = k_scale, sv = v_scale;
     if (k_head_scales != nullptr) {
       sk = __ldg(k_head_scales + h);
       sv = __ldg(v_head_scales + h);
     }
-    const uint32_t off = static_cast<uint32_t>(slot) & ((1u << bs_shift) - 1);
-    const size_t base = (static_cast<size_t>(slot >> bs_shift) * kv_heads + h) * tile;
-    const size_t at = base + off * (8 * GPR) + g * 8, sat = base + code_bytes + (g << bs_shift) + off;
-    const uint3 ck = quantise_group<SRC>(k0, k1, sk, __frcp_rn(sk), sk >= 0x1p-60f && sk <= 0x1p60f);
-    *reinterpret_cast<uint2 *>(k_cache + at) = make_uint2(ck.x, ck.y);
-    k_cache[sat] = static_cast<uint8_t>(ck.z);
-    const uint3 cv = quantise_group<SRC>(v0, v1, sv, __frcp_rn(sv), sv >= 0x1p-60f && sv <= 0x1p60f);
-    *reinterpret_cast<uint2 *>(v_cache + at) = make_uint2(cv.x, cv.y);
-    v_cache[sat] = static_cast<uint8_t>(cv.z);
+    const float rk = __frcp_rn(sk), rv = __frcp_rn(sv);
+    const bool pk = sk >= 0x1p-60f && sk <= 0x1p60f, pv = sv >= 0x1p-60f && sv <= 0x1p60f;
+    const size_t head = static_cast<size_t>(h) * tile;
+    for (long long t = t0; t < num_tokens; t += step) {
+      const long long slot = __ldg(slots + t);
+      const size_t src = (static_cast<size_t>(t) * per_token + idx) * 32;
+      const Words32 k = load32(key + src, wide), v = load32(value + src, wide);
+      if (slot < 0) continue;  // padding row
+      if (slot >= num_slots) {
+        if (idx == 0) record_error(err, kErrSlot);
+        continue;
+      }
+      const uint32_t off = static_cast<uint32_t>(slot) & bs_mask;
+      const size_t base = static_cast<size_t>(slot >> bs_shift) * kv_heads * tile + head;
+      const size_t at = base + off * (8 * GPR) + g * 8, sat = base + code_bytes + (g << bs_shift) + off;
+      const uint3 ck = quantise_group<SRC>(k.a, k.b, sk, rk, pk, table);
+      *reinterpret_cast<uint2 *>(k_cache + at) = make_uint2(ck.x, ck.y);
+      k_cache[sat] = static_cast<uint8_t>(ck.z);
+      const uint3 cv = quantise_group<SRC>(v.a, v.b, sv, rv, pv, table);
+      *reinterpret_cast<uint2 *>(v_cache + at) = make_uint2(cv.x, cv.y);
+      v_cache[sat] = static_cast<uint8_t>(cv.z);
+    }
   }
 }
 
 template <int SRC, int GPR>
-void launch_write(const void *key, const void *value, const int64_t *slots, long long groups, void *k_cache,
+void launch_write(const void *key, const void *value, const int64_t *slots, int num_tokens, void *k_cache,
                   void *v_cache, const pa_cache_desc *c, int *err, cudaStream_t stream) {
   const int shift = c->block_size == 8 ? 3 : c->block_size == 16 ? 4 : 5;
   const long long num_slots = static_cast<long long>(c->num_blocks) * c->block_size;
-  const int blocks = grid_for(groups, 256);
-  auto go = [&](auto kern, auto total) {
-    kern<<<blocks, 256, 0, stream>>>(static_cast<const uint8_t *>(key), static_cast<const uint8_t *>(value), slots,
-                                     total, c->kv_heads, shift, num_slots, static_cast<uint8_t *>(k_cache),
-                                     static_cast<uint8_t *>(v_cache), c->k_scale, c->v_scale, c->k_head_scales,
-                                     c->v_head_scales, err);
-  };
-  // (32-bit indexes divide in a quarter of the instructions; the last step past the end must not wrap)
-  if (groups < 0xf0000000ll)
-    go(write_fp4_kernel<SRC, GPR, uint32_t>, static_cast<uint32_t>(groups));
-  else
-    go(write_fp4_kernel<SRC, GPR, uint64_t>, static_cast<uint64_t>(groups));
+  const long long per_token = static_cast<long long>(c->kv_heads) * GPR;
+  const int blocks = grid_for(num_tokens * per_token, 256);
+  const bool wide = ((reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value)) & 31u) == 0;
+  long long step = blocks * 256ll / per_token;  // tokens that the grid holds at a time
+  if (step < 1) step = 1;
+  if (step > num_tokens) step = num_tokens;
+  write_fp4_kernel<SRC, GPR><<<blocks, 256, 0, stream>>>(
+      static_cast<const uint8_t *>(key), static_cast<const uint8_t *>(value), slots, num_tokens,
+      static_cast<int>(step), wide, c->kv_heads, shift, num_slots, static_cast<uint8_t *>(k_cache),
+      static_cast<uint8_t *>(v_cache), c->k_scale, c->v_scale, c->k_head_scales, c->v_head_scales, err);
 }
 
 }  // namespace
 
 pa_status write_fp4(const void *key, const void *value, int src_dtype, const int64_t *slots, int num_tokens,
                     void *k_cache, void *v_cache, const pa_cache_desc *cache, int *err, cudaStream_t stream) {
-  const long long groups = static_cast<long long>(num_tokens) * cache->kv_heads * (cache->head_dim / kFp4Group);
   auto *go = src_dtype == PA_F16 ? (cache->head_dim == 64 ? launch_write<kF16, 4> : launch_write<kF16, 8>)
                                  : (cache->head_dim == 64 ? launch_write<kBF16, 4> : launch_write<kBF16, 8>);
-  go(key, value, slots, groups, k_cache, v_cache, cache, err, stream);
+  go(key, value, slots, num_tokens, k_cache, v_cache, cache, err, stream);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }

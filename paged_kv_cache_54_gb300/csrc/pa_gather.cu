@@ -8,13 +8,9 @@
 namespace pa {
 namespace {
 
-struct Words {  // 16 values of 16 bits
-  uint4 a, b;
-};
-
 // 16 values from `in` (for kFP4 with their scale byte at `g8`)
 template <int KV, int DST>
-__device__ __forceinline__ Words read16(const uint8_t *in, const uint8_t *g8, float scale) {
+__device__ __forceinline__ Words32 read16(const uint8_t *in, const uint8_t *g8, float scale) {
   if constexpr (KV == kF16 || KV == kBF16) {
     return {__ldg(reinterpret_cast<const uint4 *>(in)), __ldg(reinterpret_cast<const uint4 *>(in) + 1)};
   } else {
@@ -50,7 +46,7 @@ __device__ __forceinline__ Words read16(const uint8_t *in, const uint8_t *g8, fl
 // IDX: the type that counts the groups of 16.
 template <int KV, int DST, class IDX>
 __global__ void __launch_bounds__(256) gather_kernel(uint8_t *__restrict__ key, uint8_t *__restrict__ value,
-                                                     const int64_t *__restrict__ slots, IDX total, uint32_t kv_heads,
+                                                     const int64_t *__restrict__ slots, IDX total, bool wide, uint32_t kv_heads,
                                                      int gpr_shift, int bs_shift, long long num_slots,
                                                      const uint8_t *__restrict__ k_cache,
                                                      const uint8_t *__restrict__ v_cache, float k_scale, float v_scale,
@@ -66,7 +62,7 @@ __global__ void __launch_bounds__(256) gather_kernel(uint8_t *__restrict__ key, 
       if (h == 0 && g == 0) record_error(err, kErrSlot);
       continue;
     }
-    Words k = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, v = k;
+    Words32 k = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, v = k;
     if (slot >= 0) {
       const uint32_t off = static_cast<uint32_t>(slot) & ((1u << bs_shift) - 1);
       const size_t tile = static_cast<size_t>(slot >> bs_shift) * kv_heads + h;
@@ -87,12 +83,8 @@ __global__ void __launch_bounds__(256) gather_kernel(uint8_t *__restrict__ key, 
         v = read16<KV, DST>(v_cache + in, nullptr, sv);
       }
     }
-    uint4 *ko = reinterpret_cast<uint4 *>(key) + static_cast<size_t>(i) * 2;
-    uint4 *vo = reinterpret_cast<uint4 *>(value) + static_cast<size_t>(i) * 2;
-    ko[0] = k.a;
-    ko[1] = k.b;
-    vo[0] = v.a;
-    vo[1] = v.b;
+    store32(key + static_cast<size_t>(i) * 32, k, wide);
+    store32(value + static_cast<size_t>(i) * 32, v, wide);
   }
 }
 
@@ -103,8 +95,9 @@ void launch_gather(void *key, void *value, const int64_t *slots, int num_tokens,
   const long long groups = static_cast<long long>(num_tokens) * c->kv_heads << gpr_shift;
   const long long num_slots = static_cast<long long>(c->num_blocks) * c->block_size;
   const int blocks = grid_for(groups, 256);
+  const bool wide = ((reinterpret_cast<uintptr_t>(key) | reinterpret_cast<uintptr_t>(value)) & 31u) == 0;
   auto go = [&](auto kern, auto total) {
-    kern<<<blocks, 256, 0, stream>>>(static_cast<uint8_t *>(key), static_cast<uint8_t *>(value), slots, total,
+    kern<<<blocks, 256, 0, stream>>>(static_cast<uint8_t *>(key), static_cast<uint8_t *>(value), slots, total, wide,
                                      c->kv_heads, gpr_shift, bs_shift, num_slots, static_cast<const uint8_t *>(k_cache),
                                      static_cast<const uint8_t *>(v_cache), c->k_scale, c->v_scale, c->k_head_scales,
                                      c->v_head_scales, err);
