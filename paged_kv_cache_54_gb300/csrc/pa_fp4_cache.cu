@@ -157,10 +157,22 @@ __global__ void __launch_bounds__(256) write_fp4_kernel(
     const float rk = __frcp_rn(sk), rv = __frcp_rn(sv);
     const bool pk = sk >= 0x1p-60f && sk <= 0x1p60f, pv = sv >= 0x1p-60f && sv <= 0x1p60f;
     const size_t head = static_cast<size_t>(h) * tile;
+    // the next token's rows are loaded while this one's are quantised
+    long long slot_n = __ldg(slots + t0);
+    const size_t src0 = (static_cast<size_t>(t0) * per_token + idx) * 32;
+    const size_t stride = static_cast<size_t>(step) * per_token * 32;
+    const uint8_t *ks = key + src0, *vs = value + src0;
+    Words32 k_n = load32(ks, wide), v_n = load32(vs, wide);
     for (long long t = t0; t < num_tokens; t += step) {
-      const long long slot = __ldg(slots + t);
-      const size_t src = (static_cast<size_t>(t) * per_token + idx) * 32;
-      const Words32 k = load32(key + src, wide), v = load32(value + src, wide);
+      const long long slot = slot_n;
+      const Words32 k = k_n, v = v_n;
+      if (t + step < num_tokens) {
+        slot_n = __ldg(slots + t + step);
+        ks += stride;
+        vs += stride;
+        k_n = load32(ks, wide);
+        v_n = load32(vs, wide);
+      }
       if (slot < 0) continue;  // padding row
       if (slot >= num_slots) {
         if (idx == 0) record_error(err, kErrSlot);
