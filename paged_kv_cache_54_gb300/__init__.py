@@ -31,6 +31,7 @@ PyTorch fallback: if ``libpa.so`` is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -168,13 +169,23 @@ def _check(status: int, what: str) -> None:
         raise cls(f"{what} failed: {msg} (status {status})")
 
 
+# The current device and its current stream as a number.  (The stream object
+# that torch.cuda.current_stream() builds costs 3 us, a third of a small call.)
+_current_device = torch.cuda.current_device
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _current_stream = torch._C._cuda_getCurrentRawStream
+else:  # pragma: no cover
+    def _current_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -189,6 +200,8 @@ def _cache_code(k_cache: torch.Tensor, cache_dtype) -> int:
 def _scale_arg(scale, kv_heads: int, name: str):
     """(per-tensor value, per-head device pointer) of a scale argument: a
     number, or a contiguous float32 CUDA tensor of one scale per KV head."""
+    if type(scale) is float:
+        return scale, None
     if isinstance(scale, torch.Tensor):
         if (not scale.is_cuda or scale.dtype != torch.float32 or not scale.is_contiguous()
                 or scale.numel() != kv_heads):
@@ -203,11 +216,8 @@ def fp4_cache_shape(num_blocks: int, kv_heads: int, block_size: int, head_dim: i
     return num_blocks, kv_heads, block_size, head_dim * 9 // 16
 
 
-def cache_desc(k_cache: torch.Tensor, cache_dtype=None, k_scale=1.0,
-               v_scale=1.0) -> PaCacheDesc:
-    """Descriptor of a cache pair; k_scale / v_scale are numbers (per tensor)
-    or float32 CUDA tensors [kv_heads] (per head; the tensors must outlive
-    the calls that use the descriptor)."""
+def _cache_fields(k_cache, cache_dtype, k_scale, v_scale):
+    """The fields of a cache pair's descriptor."""
     if k_cache.dim() != 4:
         raise ValueError("cache must be [num_blocks, kv_heads, block_size, head_dim]")
     nb, h, bs, d = k_cache.shape
@@ -219,7 +229,28 @@ def cache_desc(k_cache: torch.Tensor, cache_dtype=None, k_scale=1.0,
         d = d // 9 * 16
     ks, kp = _scale_arg(k_scale, h, "k_scale")
     vs, vp = _scale_arg(v_scale, h, "v_scale")
-    return PaCacheDesc(nb, h, bs, d, code, ks, vs, kp, vp)
+    return nb, h, bs, d, code, ks, vs, kp, vp
+
+
+def cache_desc(k_cache: torch.Tensor, cache_dtype=None, k_scale=1.0,
+               v_scale=1.0) -> PaCacheDesc:
+    """Descriptor of a cache pair; k_scale / v_scale are numbers (per tensor)
+    or float32 CUDA tensors [kv_heads] (per head; the tensors must outlive
+    the calls that use the descriptor)."""
+    return PaCacheDesc(*_cache_fields(k_cache, cache_dtype, k_scale, v_scale))
+
+
+@functools.lru_cache(maxsize=256)
+def _desc_of(*fields):
+    """A descriptor that nobody changes, made once for its fields."""
+    desc = PaCacheDesc(*fields)
+    return desc, ctypes.byref(desc)
+
+
+def _describe(k_cache, cache_dtype, k_scale, v_scale):
+    """(KV heads, head dim, type code, reference to the descriptor)."""
+    fields = _cache_fields(k_cache, cache_dtype, k_scale, v_scale)
+    return fields[1], fields[3], fields[4], _desc_of(*fields)[1]
 
 
 def _require(t: torch.Tensor, name: str) -> None:
@@ -227,14 +258,24 @@ def _require(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
-def _check_fp4(desc, k_cache, v_cache, q=None, seqs=None, block_tables=None, seq_lens=None) -> None:
+def _require_all(names: str, *tensors) -> None:
+    """Contiguous tensors of one device, the current one (the device a call
+    launches on); names: theirs, separated by spaces."""
+    for i, t in enumerate(tensors):
+        if not t.is_cuda or not t.is_contiguous():
+            _require(t, names.split()[i])
+    device = _current_device()
+    for i, t in enumerate(tensors):
+        if t.get_device() != device:
+            raise ValueError(f"{names.split()[i]} must be on the current device, cuda:{device}")
+
+
+def _check_fp4(head_dim, k_cache, v_cache, q=None, seqs=None, block_tables=None, seq_lens=None) -> None:
     """Shapes that the C ABI of a four-bit cache takes on trust."""
-    if desc.dtype != PA_FP4:
-        return
     if v_cache.shape != k_cache.shape or v_cache.element_size() != 1:
         raise ValueError("k_cache and v_cache must have one shape and be one-byte tensors")
-    if q is not None and (q.dim() != 3 or q.shape[2] != desc.head_dim):
-        raise ValueError(f"q/out must be [rows, Hq, {desc.head_dim}]")
+    if q is not None and (q.dim() != 3 or q.shape[2] != head_dim):
+        raise ValueError(f"q/out must be [rows, Hq, {head_dim}]")
     if block_tables is not None and (block_tables.dim() != 2 or block_tables.shape[0] < seqs
                                      or seq_lens.numel() < seqs):
         raise ValueError("block_tables must be [S, width] and seq_lens [S]")
@@ -244,24 +285,22 @@ def pa_reshape_and_cache(key, value, slot_mapping, k_cache, v_cache, cache_dtype
                          k_scale=1.0, v_scale=1.0, device_error=None,
                          stream=None) -> None:
     """Write rows ``key/value [T, kv_heads, head_dim]`` into the caches."""
-    for t, n in ((key, "key"), (value, "value"), (slot_mapping, "slot_mapping"),
-                 (k_cache, "k_cache"), (v_cache, "v_cache")):
-        _require(t, n)
+    _require_all("key value slot_mapping k_cache v_cache", key, value, slot_mapping, k_cache, v_cache)
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
-    desc = cache_desc(k_cache, cache_dtype, k_scale, v_scale)
+    H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
     src = _TORCH_CODES.get(key.dtype)
     if src is None or key.dtype != value.dtype:
         raise ValueError("key/value must be float16 or bfloat16 of one dtype")
-    _check_fp4(desc, k_cache, v_cache)
-    if desc.dtype == PA_FP4 and (key.shape != value.shape or
-                                 key.numel() != slot_mapping.numel() * desc.kv_heads * desc.head_dim):
-        raise ValueError(f"key/value must be [T, {desc.kv_heads}, {desc.head_dim}] with one slot a row")
+    if code == PA_FP4:
+        _check_fp4(d, k_cache, v_cache)
+        if key.shape != value.shape or key.numel() != slot_mapping.numel() * H * d:
+            raise ValueError(f"key/value must be [T, {H}, {d}] with one slot a row")
     lib = load_library()
     _check(lib.pa_reshape_and_cache(key.data_ptr(), value.data_ptr(), src,
                                     slot_mapping.data_ptr(), slot_mapping.numel(),
                                     k_cache.data_ptr(), v_cache.data_ptr(),
-                                    ctypes.byref(desc), _ptr(device_error), _stream(stream)),
+                                    ref, _ptr(device_error), _stream(stream)),
            "pa_reshape_and_cache")
 
 
@@ -270,24 +309,22 @@ def pa_gather_cache(key, value, slot_mapping, k_cache, v_cache, cache_dtype=None
     """Read rows ``key/value [T, kv_heads, head_dim]`` (float16 or bfloat16,
     written) back from the caches: the values that the stored rows of
     ``slot_mapping`` stand for, zero where it is -1."""
-    for t, n in ((key, "key"), (value, "value"), (slot_mapping, "slot_mapping"),
-                 (k_cache, "k_cache"), (v_cache, "v_cache")):
-        _require(t, n)
+    _require_all("key value slot_mapping k_cache v_cache", key, value, slot_mapping, k_cache, v_cache)
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
-    desc = cache_desc(k_cache, cache_dtype, k_scale, v_scale)
+    H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
     dst = _TORCH_CODES.get(key.dtype)
     if dst is None or key.dtype != value.dtype:
         raise ValueError("key/value must be float16 or bfloat16 of one dtype")
-    rows = (slot_mapping.numel(), desc.kv_heads, desc.head_dim)
-    if tuple(key.shape) != rows or tuple(value.shape) != rows:
+    rows = (slot_mapping.numel(), H, d)
+    if key.shape != rows or value.shape != rows:
         raise ValueError(f"key/value must be [{', '.join(map(str, rows))}]")
     if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must have one shape and dtype")
     lib = load_library()
     _check(lib.pa_gather_cache(key.data_ptr(), value.data_ptr(), dst, slot_mapping.data_ptr(),
                                slot_mapping.numel(), k_cache.data_ptr(), v_cache.data_ptr(),
-                               ctypes.byref(desc), _ptr(device_error), _stream(stream)),
+                               ref, _ptr(device_error), _stream(stream)),
            "pa_gather_cache")
 
 
@@ -302,23 +339,22 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len: int
               partition_size: int = 0, workspace=None, device_error=None,
               stream=None) -> torch.Tensor:
     """Paged decode attention; writes ``out [S, Hq, head_dim]`` (q's dtype)."""
-    for t, n in ((out, "out"), (q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-                 (block_tables, "block_tables"), (seq_lens, "seq_lens")):
-        _require(t, n)
+    _require_all("out q k_cache v_cache block_tables seq_lens", out, q, k_cache, v_cache, block_tables, seq_lens)
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("block_tables and seq_lens must be int32")
-    desc = cache_desc(k_cache, cache_dtype, k_scale, v_scale)
+    H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
     S, Hq, D = q.shape
     qcode = _TORCH_CODES.get(q.dtype)
-    if qcode not in (PA_F16, PA_BF16) or out.dtype != q.dtype or tuple(out.shape) != (S, Hq, D):
+    if qcode not in (PA_F16, PA_BF16) or out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("q/out must be float16 or bfloat16 [S, Hq, head_dim] of one dtype")
-    _check_fp4(desc, k_cache, v_cache, q, S, block_tables, seq_lens)
-    need = pa_decode_workspace_size(S, Hq, desc.kv_heads, D, max_seq_len, partition_size)
+    if code == PA_FP4:
+        _check_fp4(d, k_cache, v_cache, q, S, block_tables, seq_lens)
     if workspace is None:
+        need = pa_decode_workspace_size(S, Hq, H, D, max_seq_len, partition_size)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     lib = load_library()
     _check(lib.pa_decode(out.data_ptr(), q.data_ptr(), qcode, S, Hq, k_cache.data_ptr(),
-                         v_cache.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(),
+                         v_cache.data_ptr(), ref, block_tables.data_ptr(),
                          block_tables.shape[1], seq_lens.data_ptr(), max_seq_len, scale,
                          partition_size, workspace.data_ptr(), workspace.numel(),
                          _ptr(device_error), _stream(stream)),
@@ -333,21 +369,20 @@ def pa_prefill(out, q, cu_q_lens, k_cache, v_cache, block_tables, seq_lens, max_
     s's are rows cu_q_lens[s]..cu_q_lens[s+1]-1, its last tokens) over the
     paged cache; writes ``out`` like ``q``.  One-byte caches take their
     ``cache_dtype`` and scales as in ``pa_decode``."""
-    for t, n in ((out, "out"), (q, "q"), (cu_q_lens, "cu_q_lens"), (k_cache, "k_cache"),
-                 (v_cache, "v_cache"), (block_tables, "block_tables"), (seq_lens, "seq_lens")):
-        _require(t, n)
+    _require_all("out q cu_q_lens k_cache v_cache block_tables seq_lens", out, q, cu_q_lens, k_cache, v_cache, block_tables, seq_lens)
     if cu_q_lens.dtype != torch.int32 or block_tables.dtype != torch.int32 or \
             seq_lens.dtype != torch.int32:
         raise ValueError("cu_q_lens, block_tables and seq_lens must be int32")
-    desc = cache_desc(k_cache, cache_dtype, k_scale, v_scale)
+    H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
     qcode = _TORCH_CODES.get(q.dtype)
     if out.dtype != q.dtype or out.shape != q.shape or q.dim() != 3:
         raise ValueError("q/out must be [T, Hq, head_dim] of one dtype")
-    _check_fp4(desc, k_cache, v_cache, q, cu_q_lens.numel() - 1, block_tables, seq_lens)
+    if code == PA_FP4:
+        _check_fp4(d, k_cache, v_cache, q, cu_q_lens.numel() - 1, block_tables, seq_lens)
     lib = load_library()
     _check(lib.pa_prefill(out.data_ptr(), q.data_ptr(), -1 if qcode is None else qcode, q.shape[0],
                           cu_q_lens.data_ptr(), cu_q_lens.numel() - 1, q.shape[1], int(max_q_len),
-                          k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc),
+                          k_cache.data_ptr(), v_cache.data_ptr(), ref,
                           block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
                           scale, _ptr(device_error), _stream(stream)),
            "pa_prefill")
@@ -366,20 +401,19 @@ def pa_decode_static_scratch(out, q, k_cache, v_cache, block_tables, seq_lens,
     scratch than that are rejected (use ``pa_decode`` with a workspace).
     Calls that overlap on the GPU race on the shared scratch.
     """
-    for t, n in ((out, "out"), (q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-                 (block_tables, "block_tables"), (seq_lens, "seq_lens")):
-        _require(t, n)
-    desc = cache_desc(k_cache, cache_dtype, k_scale, v_scale)
+    _require_all("out q k_cache v_cache block_tables seq_lens", out, q, k_cache, v_cache, block_tables, seq_lens)
+    H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
     S, Hq, D = q.shape
-    _check_fp4(desc, k_cache, v_cache, q, S, block_tables, seq_lens)
-    need = pa_decode_workspace_size(S, Hq, desc.kv_heads, D, max_seq_len, partition_size)
+    if code == PA_FP4:
+        _check_fp4(d, k_cache, v_cache, q, S, block_tables, seq_lens)
+    need = pa_decode_workspace_size(S, Hq, H, D, max_seq_len, partition_size)
     if need > STATIC_SCRATCH_BYTES:
         raise PaError(f"pa_decode_static_scratch: these sizes need {need} bytes of scratch, "
                       f"more than its fixed {STATIC_SCRATCH_BYTES}; use pa_decode")
     lib = load_library()
     _check(lib.pa_decode_static_scratch(
         out.data_ptr(), q.data_ptr(), _TORCH_CODES.get(q.dtype, -1), S, Hq,
-        k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), ref, block_tables.data_ptr(),
         block_tables.shape[1], seq_lens.data_ptr(), max_seq_len, scale, partition_size,
         _ptr(device_error), _stream(stream)), "pa_decode_static_scratch")
     return out
@@ -396,13 +430,12 @@ def pa_selftest_wait_timeout(device_error, stream=None) -> None:
 def pa_copy_blocks(k_cache, v_cache, block_mapping, cache_dtype=None, device_error=None,
                    stream=None) -> None:
     """For each (src, dst) row of ``block_mapping [n, 2]`` copy block src to dst."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (block_mapping, "block_mapping")):
-        _require(t, n)
+    _require_all("k_cache v_cache block_mapping", k_cache, v_cache, block_mapping)
     if block_mapping.dtype != torch.int64:
         raise ValueError("block_mapping must be int64")
-    desc = cache_desc(k_cache, cache_dtype)
+    ref = _describe(k_cache, cache_dtype, 1.0, 1.0)[3]
     lib = load_library()
-    _check(lib.pa_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc),
+    _check(lib.pa_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ref,
                               block_mapping.data_ptr(), block_mapping.shape[0],
                               _ptr(device_error), _stream(stream)),
            "pa_copy_blocks")
@@ -413,9 +446,7 @@ def pa_compact_blocks(k_cache, v_cache, block_mapping, block_tables, seq_lens, c
     """Move block src to dst for each row of ``block_mapping [n, 2]`` (int64,
     ascending by src, as ``PrefixCache.compact`` gives them) and rename the
     blocks in ``block_tables`` (int32 ``[S, width]``, in place)."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (block_mapping, "block_mapping"),
-                 (block_tables, "block_tables"), (seq_lens, "seq_lens")):
-        _require(t, n)
+    _require_all("k_cache v_cache block_mapping block_tables seq_lens", k_cache, v_cache, block_mapping, block_tables, seq_lens)
     if block_mapping.dtype != torch.int64 or block_mapping.dim() != 2 or block_mapping.shape[1] != 2:
         raise ValueError("block_mapping must be int64 [n, 2]")
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
@@ -424,9 +455,9 @@ def pa_compact_blocks(k_cache, v_cache, block_mapping, block_tables, seq_lens, c
         raise ValueError("block_tables must be [S, width] and seq_lens [S]")
     if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must have one shape and dtype")
-    desc = cache_desc(k_cache, cache_dtype)
+    ref = _describe(k_cache, cache_dtype, 1.0, 1.0)[3]
     lib = load_library()
-    _check(lib.pa_compact_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc),
+    _check(lib.pa_compact_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ref,
                                  block_mapping.data_ptr(), block_mapping.shape[0], block_tables.data_ptr(),
                                  block_tables.shape[0], max(1, block_tables.shape[1]), seq_lens.data_ptr(),
                                  _ptr(device_error), _stream(stream)),
@@ -443,8 +474,7 @@ def pa_swap_blocks(k_cache, v_cache, host_k, host_v, block_mapping, direction: s
     device block src -> host block dst; "in": host block src -> device
     block dst.
     """
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache"), (block_mapping, "block_mapping")):
-        _require(t, n)
+    _require_all("k_cache v_cache block_mapping", k_cache, v_cache, block_mapping)
     for t, n in ((host_k, "host_k"), (host_v, "host_v")):
         if not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
             raise ValueError(f"{n} must be contiguous, in page-locked host memory or on the device")
@@ -457,9 +487,9 @@ def pa_swap_blocks(k_cache, v_cache, host_k, host_v, block_mapping, direction: s
     codes = {"out": PA_SWAP_OUT, "in": PA_SWAP_IN}
     if direction not in codes:
         raise ValueError('direction must be "out" or "in"')
-    desc = cache_desc(k_cache, cache_dtype)
+    ref = _describe(k_cache, cache_dtype, 1.0, 1.0)[3]
     lib = load_library()
-    _check(lib.pa_swap_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc),
+    _check(lib.pa_swap_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ref,
                               host_k.data_ptr(), host_v.data_ptr(), host_k.shape[0],
                               block_mapping.data_ptr(), block_mapping.shape[0], codes[direction],
                               _ptr(device_error), _stream(stream)),
