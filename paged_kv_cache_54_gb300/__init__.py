@@ -189,19 +189,17 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _cache_code(k_cache: torch.Tensor, cache_dtype) -> int:
+def _cache_code(dtype: torch.dtype, cache_dtype) -> int:
     if cache_dtype is not None:
         return DTYPE_CODES[cache_dtype] if isinstance(cache_dtype, str) else int(cache_dtype)
-    if k_cache.dtype in _TORCH_CODES:
-        return _TORCH_CODES[k_cache.dtype]
+    if dtype in _TORCH_CODES:
+        return _TORCH_CODES[dtype]
     raise ValueError("cache_dtype is required for a byte-typed cache")
 
 
 def _scale_arg(scale, kv_heads: int, name: str):
     """(per-tensor value, per-head device pointer) of a scale argument: a
     number, or a contiguous float32 CUDA tensor of one scale per KV head."""
-    if type(scale) is float:
-        return scale, None
     if isinstance(scale, torch.Tensor):
         if (not scale.is_cuda or scale.dtype != torch.float32 or not scale.is_contiguous()
                 or scale.numel() != kv_heads):
@@ -216,20 +214,18 @@ def fp4_cache_shape(num_blocks: int, kv_heads: int, block_size: int, head_dim: i
     return num_blocks, kv_heads, block_size, head_dim * 9 // 16
 
 
-def _cache_fields(k_cache, cache_dtype, k_scale, v_scale):
-    """The fields of a cache pair's descriptor."""
-    if k_cache.dim() != 4:
+def _cache_shape(shape, dtype, cache_dtype):
+    """(num_blocks, kv_heads, block_size, head_dim, type code) of a cache tensor."""
+    if len(shape) != 4:
         raise ValueError("cache must be [num_blocks, kv_heads, block_size, head_dim]")
-    nb, h, bs, d = k_cache.shape
-    code = _cache_code(k_cache, cache_dtype)
+    nb, h, bs, d = shape
+    code = _cache_code(dtype, cache_dtype)
     if code == PA_FP4:
-        if k_cache.element_size() != 1 or d % 9:
+        if dtype.itemsize != 1 or d % 9:
             raise ValueError("a four-bit cache is a one-byte tensor [num_blocks, kv_heads, block_size, "
                              "head_dim * 9 / 16]")
         d = d // 9 * 16
-    ks, kp = _scale_arg(k_scale, h, "k_scale")
-    vs, vp = _scale_arg(v_scale, h, "v_scale")
-    return nb, h, bs, d, code, ks, vs, kp, vp
+    return nb, h, bs, d, code
 
 
 def cache_desc(k_cache: torch.Tensor, cache_dtype=None, k_scale=1.0,
@@ -237,20 +233,28 @@ def cache_desc(k_cache: torch.Tensor, cache_dtype=None, k_scale=1.0,
     """Descriptor of a cache pair; k_scale / v_scale are numbers (per tensor)
     or float32 CUDA tensors [kv_heads] (per head; the tensors must outlive
     the calls that use the descriptor)."""
-    return PaCacheDesc(*_cache_fields(k_cache, cache_dtype, k_scale, v_scale))
+    shape = _cache_shape(k_cache.shape, k_cache.dtype, cache_dtype)
+    ks, kp = _scale_arg(k_scale, shape[1], "k_scale")
+    vs, vp = _scale_arg(v_scale, shape[1], "v_scale")
+    return PaCacheDesc(*shape, ks, vs, kp, vp)
 
 
 @functools.lru_cache(maxsize=256)
-def _desc_of(*fields):
-    """A descriptor that nobody changes, made once for its fields."""
-    desc = PaCacheDesc(*fields)
-    return desc, ctypes.byref(desc)
+def _described(shape, dtype, cache_dtype, ks, vs, kp, vp):
+    """(KV heads, head dim, type code, reference to the descriptor) of a cache
+    tensor of this shape and type: a function of its arguments' values, made
+    once for each."""
+    fields = _cache_shape(shape, dtype, cache_dtype)
+    return fields[1], fields[3], fields[4], ctypes.byref(PaCacheDesc(*fields, ks, vs, kp, vp))
 
 
 def _describe(k_cache, cache_dtype, k_scale, v_scale):
-    """(KV heads, head dim, type code, reference to the descriptor)."""
-    fields = _cache_fields(k_cache, cache_dtype, k_scale, v_scale)
-    return fields[1], fields[3], fields[4], _desc_of(*fields)[1]
+    kp = vp = None
+    if type(k_scale) is not float or type(v_scale) is not float:
+        heads = k_cache.shape[1] if k_cache.dim() == 4 else -1
+        k_scale, kp = _scale_arg(k_scale, heads, "k_scale")
+        v_scale, vp = _scale_arg(v_scale, heads, "v_scale")
+    return _described(k_cache.shape, k_cache.dtype, cache_dtype, k_scale, v_scale, kp, vp)
 
 
 def _require(t: torch.Tensor, name: str) -> None:
@@ -261,12 +265,12 @@ def _require(t: torch.Tensor, name: str) -> None:
 def _require_all(names: str, *tensors) -> None:
     """Contiguous tensors of one device, the current one (the device a call
     launches on); names: theirs, separated by spaces."""
-    for i, t in enumerate(tensors):
-        if not t.is_cuda or not t.is_contiguous():
-            _require(t, names.split()[i])
+    if not tensors[0].is_cuda:  # (no question to a driver that may not be there)
+        _require(tensors[0], names.split()[0])
     device = _current_device()
     for i, t in enumerate(tensors):
-        if t.get_device() != device:
+        if t.get_device() != device or not t.is_contiguous():
+            _require(t, names.split()[i])
             raise ValueError(f"{names.split()[i]} must be on the current device, cuda:{device}")
 
 
