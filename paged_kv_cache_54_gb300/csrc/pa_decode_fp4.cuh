@@ -57,6 +57,12 @@ constexpr int kSlice = 16;      // tokens of the products
 constexpr int kStep = 32;       // tokens of a warp's step
 constexpr int kUnit = 64;       // tokens of a unit of work
 constexpr int kPairCost = 5;    // units that a pair costs beside its tokens'
+// Pairs of up to 512 tokens are dealt out whole, and there is no merge.  Whole
+// against cut, us of one call in a graph: 1 x 8 pairs of up to 256 tokens
+// 4.8 / 7.6, of 512 6.2 / 6.8, of 1024 9.3 / 7.0; 4 x 4 of 512 8.2 / 6.8;
+// 16 x 8 of 512 9.7 / 10.7; 64 x 8 of 512 14.0 / 14.9; 128 x 8 of 2048
+// 59.0 / 54.9.
+constexpr int kWholeTokens = 512;
 constexpr float kLazy = 8.f;    // rescale when the maximum grows by more (base 2)
 constexpr float kWritten = -1.f;  // l of a partial that marks the end of a pair's pieces
 
@@ -69,6 +75,7 @@ struct Fp4Params {
   const int32_t *seq_lens;
   int num_seqs, num_q_heads, num_kv_heads, num_blocks, max_blocks;
   int len_cap, max_parts, partition_size;
+  int cut;  // whether a pair may be cut among CTAs (and the merge follows)
   float qk_scale_log2, v_scale;
   const float *k_head_scale, *v_head_scale;
   float2 *part_ml;
@@ -523,7 +530,7 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
     U += s_wsum[w];
   }
   before += upto - mine;  // units before this thread's run
-  const bool cut = p.max_parts > 1;
+  const bool cut = p.cut != 0;
   // (cut pairs' pieces have their places when a share is two partitions long)
   long long n = gridDim.x;
   if (cut) n = min(n, max(1ll, U * kUnit / (2ll * p.partition_size)));
@@ -859,7 +866,7 @@ pa_status launch(const Fp4Params &p, const DeviceInfo &dev, cudaStream_t stream)
   // no more CTAs than pairs (when they are dealt out whole) or than the
   // longest lengths give units
   const long long pairs = static_cast<long long>(p.num_seqs) * p.num_kv_heads;
-  const long long most = p.max_parts > 1 ? pairs * p.max_parts : pairs;
+  const long long most = p.cut ? pairs * p.max_parts : pairs;
   const long long slots = static_cast<long long>(dev.sm_count) * kCtas;
   cfg.gridDim = dim3(static_cast<unsigned>(most < slots ? most : slots));
   cfg.blockDim = dim3(kFpThreads);
@@ -869,7 +876,7 @@ pa_status launch(const Fp4Params &p, const DeviceInfo &dev, cudaStream_t stream)
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, decode_fp4_kernel<QT, D, G, BS>, p);
   if (e != cudaSuccess) return cuda_fail(e);
-  if (p.max_parts > 1) {
+  if (p.cut) {
     const long long heads = static_cast<long long>(p.num_seqs) * p.num_q_heads;
     const bool many = heads >= dev.sm_count * 8;
     cfg.gridDim = dim3(static_cast<unsigned>(many ? (heads + kMergeWarps - 1) / kMergeWarps : heads));
@@ -911,6 +918,7 @@ pa_status dispatch(int q_dtype, int head_dim, int group, const DecodeParams &d, 
   p.len_cap = d.len_cap;
   p.max_parts = d.max_parts;
   p.partition_size = d.partition_size;
+  p.cut = d.max_parts > 1 && d.len_cap > kWholeTokens;
   p.qk_scale_log2 = d.qk_scale_log2;
   p.v_scale = d.v_scale;
   p.k_head_scale = d.k_head_scale;

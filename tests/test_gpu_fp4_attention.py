@@ -263,3 +263,12 @@ def test_a_serving_run(tmp_path):
             assert torch.equal(before, after)                  # nothing but places has changed
     a, qa, _, _ = outputs([0, 1, 3])
     check([0, 1, 3], a, qa)
+
+
+@pytest.mark.parametrize("lens", [[512], [512, 1, 0, 500] * 12, [65] * 700, [511, 64, 65, 300, 2] * 150])
+def test_decode_deals_short_sequences_out_whole(lens):
+    for pad in (0, 40):                                        # a looser bound on the lengths lets them be cut
+        c = Case(60, lens, 2, 2, 64, 16, "bf16", per_head=True, width_pad=pad)
+        g = c.device()
+        c.decode(g, max_len=max(lens) + 16 * pad)
+        c.check(g, f"pad {pad}")
