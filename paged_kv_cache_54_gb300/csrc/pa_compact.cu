@@ -1,6 +1,12 @@
 // pa_compact_blocks: whole-block moves inside one pool, and the block tables
 // renamed to match, in one launch.  The moves and the renaming touch
 // different memory, so nothing orders them.
+//
+// The moves are bound by memory: a warp takes 4 KB of a block of K or V at a
+// time, each lane eight 16-byte loads before its stores, so that nothing but
+// the pair's two ids is looked up on the way.  A table entry in use is looked
+// up among the sources, which ascend; a compaction's sources all lie at the
+// pool's end, so most entries are below the first one and end there.
 #include <limits.h>
 
 #include "pa_common.cuh"
@@ -29,6 +35,7 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(
     }
     if (static_cast<long long>(j) * block_size >= L) continue;  // behind the last block
     const int32_t b = tables[i];
+    if (b < __ldg(mapping)) continue;  // below every source
     int lo = 0, hi = num_pairs;  // the first pair whose source is b or above
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -40,23 +47,34 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(
     if (dst >= 0 && dst < num_blocks) tables[i] = static_cast<int32_t>(dst);
   }
   // the moves
+  constexpr int kVecs = 8;  // of a lane's step
   const long long vecs = block_bytes / 16;
-  const long long total = static_cast<long long>(num_pairs) * 2 * vecs;
-  for (long long i = thread; i < total; i += threads) {
-    const long long pair = i / (2 * vecs);
-    const long long r = i - pair * 2 * vecs;
-    const int which = r >= vecs;
-    const long long v = r - which * vecs;
+  const uint32_t parts = static_cast<uint32_t>((vecs + 32 * kVecs - 1) / (32 * kVecs));  // steps of a block
+  const long long total = static_cast<long long>(num_pairs) * 2 * parts;
+  const int lane = threadIdx.x & 31;
+  for (long long i = thread >> 5; i < total; i += threads >> 5) {
+    const long long half = i / parts;  // (pair, K | V)
+    const uint32_t part = static_cast<uint32_t>(i - half * parts);
+    const long long pair = half >> 1;
     const long long src = __ldg(mapping + 2 * pair);
     const long long dst = __ldg(mapping + 2 * pair + 1);
-    if (v == 0 && which == 0 && pair > 0 && __ldg(mapping + 2 * pair - 2) >= src) record_error(err, kErrCopyIndex);
+    const bool reports = lane == 0 && part == 0 && (half & 1) == 0;
+    if (reports && pair > 0 && __ldg(mapping + 2 * pair - 2) >= src) record_error(err, kErrCopyIndex);
     if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
-      if (v == 0 && which == 0) record_error(err, kErrCopyIndex);
+      if (reports) record_error(err, kErrCopyIndex);
       continue;
     }
-    uint8_t *base = which ? v_cache : k_cache;
-    const uint4 x = *reinterpret_cast<const uint4 *>(base + src * block_bytes + v * 16);
-    *reinterpret_cast<uint4 *>(base + dst * block_bytes + v * 16) = x;
+    uint8_t *base = (half & 1) ? v_cache : k_cache;
+    const uint4 *from = reinterpret_cast<const uint4 *>(base + src * block_bytes);
+    uint4 *to = reinterpret_cast<uint4 *>(base + dst * block_bytes);
+    const long long v0 = static_cast<long long>(part) * (32 * kVecs) + lane;
+    uint4 x[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if (v0 + 32 * u < vecs) x[u] = from[v0 + 32 * u];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      if (v0 + 32 * u < vecs) to[v0 + 32 * u] = x[u];
   }
 }
 
@@ -77,8 +95,9 @@ extern "C" pa_status pa_compact_blocks(void *k_cache, void *v_cache, const pa_ca
     return PA_ERR_INVALID;
   if (!supported_cache_shape(cache)) return PA_ERR_UNSUPPORTED;
   const long long block_bytes = cache_block_bytes(cache);
-  const long long work = static_cast<long long>(num_pairs) * 2 * (block_bytes / 16) +
-                         static_cast<long long>(num_seqs) * max_blocks_per_seq;
+  const long long moves = static_cast<long long>(num_pairs) * 2 * ((block_bytes / 16 + 255) / 256) * 32;  // threads
+  const long long entries = static_cast<long long>(num_seqs) * max_blocks_per_seq;
+  const long long work = moves > entries ? moves : entries;
   compact_kernel<<<grid_for(work, kCompactThreads), kCompactThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), block_mapping, num_pairs, block_bytes,
       cache->num_blocks, block_tables, num_seqs, max_blocks_per_seq, cache->block_size, seq_lens, device_error);
