@@ -60,7 +60,8 @@
 // entry within fp16's range; the factor, and the K scale, go into the score
 // scale, the V scale into the output.  Four-bit caches have three code slots
 // and four 16-bit stages; their group scales are applied while widening (a
-// code times its group's scale is an fp16 value, so that stays exact).
+// code times its group's scale is an fp16 value, so that stays exact), and a
+// bf16 query row has a power of two of its own.
 #include <limits.h>
 #include <math.h>
 
@@ -223,55 +224,73 @@ __device__ __forceinline__ void widen_codes(const uint8_t *slot, uint8_t *stage,
 // of 16 in the half); a slot holds whole (block, head) tiles, each its codes
 // and then its scales [group][token].  The lanes of the upper half write
 // their two chunks in the other order, so that the eight lanes of a store
-// phase (one key's groups, both halves) hit eight different chunks.
+// phase (one key's groups, both halves) hit eight different chunks.  A
+// lane's keys are a multiple of 8 apart, so its places in a stage step by
+// constants; its places in a slot depend on the block size and are kept.
 template <int D, int PARTS>
-__device__ __forceinline__ void widen_fp4(const uint8_t *slot, uint8_t *stage, int keys, int bs, int lane, int part) {
-  constexpr int NH = D / 64;
-  constexpr int GPR = D / kFp4Group;     // groups of a row
-  constexpr int KPI = 32 / GPR;          // keys per warp iteration
-  constexpr int ITERS = kPfKeys / KPI / PARTS;
-  const int kr = lane / GPR, g = lane % GPR, hf = g >> 2, gh = g & 3;
-  const int bs_sh = 31 - __clz(bs), tile = bs * fp4_row_bytes(D);
-  const int swap = NH == 2 ? hf : 0;
-#pragma unroll
-  for (int tv = 0; tv < 2; ++tv) {
-    const uint8_t *src = slot + tv * kPfKeys * fp4_row_bytes(D);
-    uint8_t *dst = stage + tv * NH * kPfHalf;
-    uint2 w[ITERS];
-    uint32_t s[ITERS];
-#pragma unroll
-    for (int m = 0; m < ITERS; ++m) {  // the loads before the stores, which may alias them for all the compiler knows
-      const int key = (m * PARTS + part) * KPI + kr;
-      const uint8_t *t = src + (key >> bs_sh) * tile;
-      const int off = key & (bs - 1);
-      w[m] = make_uint2(0u, 0u);
-      s[m] = 0u;
-      if (key < keys) {
-        w[m] = *reinterpret_cast<const uint2 *>(t + off * fp4_code_bytes(D) + g * 8);
-        s[m] = t[bs * fp4_code_bytes(D) + g * bs + off];
-      }
-    }
+struct Fp4Widener {
+  static constexpr int NH = D / 64;
+  static constexpr int GPR = D / kFp4Group;  // groups of a row
+  static constexpr int KPI = 32 / GPR;       // keys per warp iteration
+  static constexpr int STEP = PARTS * KPI;   // keys between a lane's iterations
+  static constexpr int ITERS = kPfKeys / STEP;
+  static_assert(STEP % 8 == 0, "a lane's keys must keep their row in the atom");
+  int key0;
+  uint32_t code[ITERS], scale[ITERS];  // places in a slot
+  uint32_t first, second;              // places in a stage of the two chunks (of key0)
+  bool swap;
+
+  __device__ __forceinline__ Fp4Widener(int bs, int lane, int part) {
+    const int kr = lane / GPR, g = lane % GPR, hf = g >> 2, gh = g & 3;
+    const int bs_sh = 31 - __clz(bs), tile = bs * fp4_row_bytes(D);
+    key0 = part * KPI + kr;
 #pragma unroll
     for (int m = 0; m < ITERS; ++m) {
-      const int key = (m * PARTS + part) * KPI + kr;
-      if (key >= keys) continue;
-      const uint32_t s2 = e4m3x2_to_half2(s[m] * 0x0101u);
-      uint32_t a[4], b[4];
-      e2m1x8_to_half2x4(w[m].x, a);
-      e2m1x8_to_half2x4(w[m].y, b);
+      const int key = key0 + m * STEP, off = key & (bs - 1), at = (key >> bs_sh) * tile;
+      code[m] = at + off * fp4_code_bytes(D) + g * 8;
+      scale[m] = at + bs * fp4_code_bytes(D) + g * bs + off;
+    }
+    swap = NH == 2 && hf;
+    const uint32_t row = kv_row_off<NH>(key0, hf);
+    const int c = 2 * gh, k7 = key0 & 7;
+    first = row + (((c + swap) ^ k7) << 4);
+    second = row + (((c + 1 - swap) ^ k7) << 4);
+  }
+  // keys: those of the slot (a multiple of 8)
+  __device__ __forceinline__ void operator()(const uint8_t *slot, uint8_t *stage, int keys) const {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = hmul2_bits(a[i], s2);
-        b[i] = hmul2_bits(b[i], s2);
+    for (int tv = 0; tv < 2; ++tv) {
+      const uint8_t *src = slot + tv * kPfKeys * fp4_row_bytes(D);
+      uint8_t *dst = stage + tv * NH * kPfHalf;
+      uint2 w[ITERS];
+      uint32_t s[ITERS];
+#pragma unroll
+      for (int m = 0; m < ITERS; ++m) {  // the loads before the stores, which may alias them for all the compiler knows
+        if (key0 + m * STEP < keys) {
+          w[m] = *reinterpret_cast<const uint2 *>(src + code[m]);
+          s[m] = src[scale[m]];
+        }
       }
-      const uint4 lo = make_uint4(a[0], a[1], a[2], a[3]), hi = make_uint4(b[0], b[1], b[2], b[3]);
-      uint8_t *row = dst + kv_row_off<NH>(key, hf);
-      const int c = 2 * gh, k7 = key & 7;
-      *reinterpret_cast<uint4 *>(row + (((c + swap) ^ k7) << 4)) = swap ? hi : lo;
-      *reinterpret_cast<uint4 *>(row + (((c + 1 - swap) ^ k7) << 4)) = swap ? lo : hi;
+#pragma unroll
+      for (int m = 0; m < ITERS; ++m) {
+        if (key0 + m * STEP < keys) {
+          const uint32_t s2 = e4m3x2_to_half2(s[m] * 0x0101u);
+          uint32_t a[4], b[4];
+          e2m1x8_to_half2x4(swap ? w[m].y : w[m].x, a);
+          e2m1x8_to_half2x4(swap ? w[m].x : w[m].y, b);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = hmul2_bits(a[i], s2);
+            b[i] = hmul2_bits(b[i], s2);
+          }
+          uint8_t *at = dst + m * (STEP / 8 * NH * kPfAtom);
+          *reinterpret_cast<uint4 *>(at + first) = make_uint4(a[0], a[1], a[2], a[3]);
+          *reinterpret_cast<uint4 *>(at + second) = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+      }
     }
   }
-}
+};
 
 __device__ __forceinline__ void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -469,7 +488,7 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
         mbar_init(&hdr.code_empty[c], kPfConvWarps);
       }
       for (int t = 0; t < kPfTiles; ++t) {
-        mbar_init(&hdr.q_ready[t], 1);
+        mbar_init(&hdr.q_ready[t], KVT == kFP4 ? kPfTileRows : 1);  // each row's thread, or one for all
         mbar_init(&hdr.s_full[t][0], 1);
         mbar_init(&hdr.s_full[t][1], 1);
         mbar_init(&hdr.p_full[t][0], kPfTileRows);
@@ -522,7 +541,51 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
           vsc = __ldg(p.v_head_scale + h);
         }
       }
-      if constexpr (QCONV) {
+      if constexpr (QCONV && KVT == kFP4) {
+        // the row's q, rewritten in place as fp16 by its own thread, times the
+        // power of two that brings its largest entry into [2^13, 2^14): small
+        // rows keep their eight bits, and no thread waits for another's.  Lane
+        // order within a row follows its swizzle, so no banks collide.
+        ok = __all_sync(0xffffffffu, mbar_wait(&hdr.q_full, 0, abort));
+        uint8_t *row = qs + t * Lay::Q_TILE + r * 128;
+        constexpr int CH = NH * 8;  // 16-byte chunks of a row
+        uint4 v[CH];
+        float amax = 0.f;
+        if (ok) {
+  #pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            v[j] = lds128(row + (j / 8) * Lay::Q_HALF + (((j & 7) ^ (r & 7)) << 4));
+            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+  #pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float2 x = half2_bits_to_float2<kBF16>(w[u]);
+              amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+          }
+        }
+        float f = 1.f;
+        if (amax > 0.f && amax <= 3.0e38f) {
+          int ex;
+          frexpf(amax, &ex);
+          f = ldexpf(1.f, min(14 - ex, 100));
+        }
+        if (ok) {
+  #pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+  #pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float2 x = half2_bits_to_float2<kBF16>(w[u]);
+              w[u] = pack2_rn<kF16>(x.x * f, x.y * f);
+            }
+            *reinterpret_cast<uint4 *>(row + (j / 8) * Lay::Q_HALF + (((j & 7) ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        fence_proxy_async_smem();  // the rewritten row visible to the tensor cores
+        mbar_arrive(&hdr.q_ready[t]);
+        c /= f;
+      } else if constexpr (QCONV) {
         // the tile's q (bf16, swizzled in place; a pure elementwise rewrite
         // keeps the layout): scale by 2^e so that max |q| <= 2^15, round to fp16
         ok = __all_sync(0xffffffffu, mbar_wait(&hdr.q_full, 0, abort));
@@ -547,12 +610,10 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
         named_bar_sync(1 + t, kPfTileRows);
         amax = fmaxf(fmaxf(hdr.qmax[t][0], hdr.qmax[t][1]), fmaxf(hdr.qmax[t][2], hdr.qmax[t][3]));
         float f = 1.f;
-        // (four-bit caches scale small tiles up as well, so that their
-        // entries keep their eight bits in fp16)
-        if (amax > (KVT == kFP4 ? 0.f : 16384.f) && amax <= 3.0e38f) {
+        if (amax > 16384.f && amax <= 3.0e38f) {
           int ex;
           frexpf(amax, &ex);
-          f = ldexpf(1.f, min(14 - ex, 100));
+          f = ldexpf(1.f, 14 - ex);
         }
         if (ok) {
   #pragma unroll
@@ -860,6 +921,7 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
       // ------------------------------------------------------------ widening
       // warp 12 + q widens warp-iterations q, q + 4, ... of every stage
       const int q = warp - kPfConvWarp0;
+      const Fp4Widener<D, kPfConvWarps> widen(bs, lane, q);  // (four-bit caches)
       bool ok = true;
       for (int i = 0; i < n_stages; ++i) {
         const int st = i % NS;
@@ -875,8 +937,7 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
         }
         const int keys = min(bpt, (kv_end - i * kPfKeys + bs - 1) / bs) * bs;
         if constexpr (KVT == kFP4)
-          widen_fp4<D, kPfConvWarps>(codes + (i % NC) * Lay::CODE_BYTES, stages + st * Lay::STAGE_BYTES, keys, bs, lane,
-                                     q);
+          widen(codes + (i % NC) * Lay::CODE_BYTES, stages + st * Lay::STAGE_BYTES, keys);
         else
           widen_codes<KVT, D, kPfConvWarps>(codes + (i % NC) * Lay::CODE_BYTES, stages + st * Lay::STAGE_BYTES, keys,
                                             lane, q);
