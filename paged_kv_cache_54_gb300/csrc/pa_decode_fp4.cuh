@@ -64,6 +64,7 @@ constexpr int kPairCost = 5;    // units that a pair costs beside its tokens'
 // 59.0 / 54.9.
 constexpr int kWholeTokens = 512;
 constexpr float kLazy = 8.f;    // rescale when the maximum grows by more (base 2)
+constexpr float kFar = 0x1p24f;
 constexpr float kWritten = -1.f;  // l of a partial that marks the end of a pair's pieces
 
 struct Fp4Params {
@@ -104,14 +105,15 @@ struct State {
   uint32_t qb[KSTEPS][2];
   float o[MT][4];
   float m[2], l[2];
-  float top[2];      // unscaled scores above these bring the maximum up
-  float mult, lift;  // of the scores, and its reciprocal
+  float top[2];            // unscaled scores above these bring the maximum up
+  float mult[2], lift[2];  // of the scores, and their reciprocals
+  bool far;                // some maximum is past 2^24 (warp-uniform)
 };
 
 // q rows of the group (G x D at `q`) as B fragments: column gq is query gq,
 // lane tq's local dimensions.  bf16 queries are rounded to fp16 after a
-// multiplication by the power of two that brings the group's largest entry
-// into [2^13, 2^14), undone on the scores, so that nothing overflows and what
+// multiplication by the power of two that brings the query's largest entry
+// into [2^13, 2^14), undone on its scores, so that nothing overflows and what
 // underflows is 2^-38 of the largest.
 template <int QT, int D, int G>
 __device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float scale) {
@@ -136,7 +138,7 @@ __device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float sca
       top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
     }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = 1; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (top > 0.f && top <= 3.4e38f) {
       int e;
       frexpf(top, &e);
@@ -152,9 +154,14 @@ __device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float sca
   // becomes zero queries
 #pragma unroll
   for (int i = 0; i < QW; ++i) w[i] = scale > 0.f ? w[i] : scale < 0.f ? w[i] ^ 0x80008000u : 0u;
-  st.mult = scale == 0.f ? 1.f : fabsf(scale) / f;
-  st.lift = 1.f / st.mult;
-  st.top[0] = st.top[1] = -INFINITY;
+  st.far = false;
+  const float mult = scale == 0.f ? 1.f : fabsf(scale) / f;  // of query gq
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    st.mult[r] = __shfl_sync(0xffffffffu, mult, (2 * tq + r) * 4);
+    st.lift[r] = 1.f / st.mult[r];
+    st.top[r] = -INFINITY;
+  }
 #pragma unroll
   for (int kk = 0; kk < State<D>::KSTEPS; ++kk) {
     st.qb[kk][0] = w[2 * kk];
@@ -366,15 +373,15 @@ __device__ __forceinline__ void attend(State<D> &st, const uint8_t *slot, int n)
       x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
     }
     const bool up0 = x0 > st.top[0], up1 = x1 > st.top[1];
-    const float n0 = x0 * st.mult, n1 = x1 * st.mult;
+    const float n0 = x0 * st.mult[0], n1 = x1 * st.mult[1];
     const float f0 = up0 ? ex2(st.m[0] - n0) : 1.f, f1 = up1 ? ex2(st.m[1] - n1) : 1.f;
     if (up0) {
       st.m[0] = n0;
-      st.top[0] = fmaf(kLazy, st.lift, x0);
+      st.top[0] = fmaf(kLazy, st.lift[0], x0);
     }
     if (up1) {
       st.m[1] = n1;
-      st.top[1] = fmaf(kLazy, st.lift, x1);
+      st.top[1] = fmaf(kLazy, st.lift[1], x1);
     }
 #pragma unroll
     for (int i = 0; i < State<D>::MT; ++i) {
@@ -385,11 +392,21 @@ __device__ __forceinline__ void attend(State<D> &st, const uint8_t *slot, int n)
     }
     st.l[0] *= f0;
     st.l[1] *= f1;
+    st.far = __any_sync(0xffffffffu, !(fmaxf(fabsf(st.m[0]), fabsf(st.m[1])) <= kFar));
   }
+  if (!st.far) {
+    // (the rounding of m is one factor of all of a query's weights: at most 2)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a[i] = ex2(fmaf(a[i], st.mult, -st.m[i & 1]));
-    b[i] = ex2(fmaf(b[i], st.mult, -st.m[i & 1]));
+    for (int i = 0; i < 4; ++i) {
+      a[i] = ex2(fmaf(a[i], st.mult[i & 1], -st.m[i & 1]));
+      b[i] = ex2(fmaf(b[i], st.mult[i & 1], -st.m[i & 1]));
+    }
+  } else {  // scores whose product has to be rounded as the maximum's was
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = ex2(__fsub_rn(__fmul_rn(a[i], st.mult[i & 1]), st.m[i & 1]));
+      b[i] = ex2(__fsub_rn(__fmul_rn(b[i], st.mult[i & 1]), st.m[i & 1]));
+    }
   }
   st.l[0] += (a[0] + a[2]) + (b[0] + b[2]);
   st.l[1] += (a[1] + a[3]) + (b[1] + b[3]);

@@ -666,6 +666,16 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
           }
           mx = fmax3(a, b, fmaxf(sv[31], sv[63])) * c;
           cm = c;
+          if constexpr (KVT == kFP4) {
+            // past 2^24 the products have to be rounded as the maximum's was
+            // (in the fma its rounding is a factor of the row's weights, up
+            // to 2 below that, past fp16 above)
+            if (__any_sync(0xffffffffu, !(fabsf(mx) <= 0x1p24f))) {
+  #pragma unroll
+              for (int j = 0; j < kPfKeys; ++j) sv[j] = __fmul_rn(sv[j], c);
+              cm = 1.f;
+            }
+          }
         } else {
           float mx0 = -INFINITY, mx1 = -INFINITY;
   #pragma unroll

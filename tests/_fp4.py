@@ -93,6 +93,10 @@ class Case:
         and sum).  A score is a sum of D exact products in fp32, scaled: D + 8
         roundings, taken at 2^-23 of sum |q k|, and the exponential's own 2^-20.
         """
+        with np.errstate(invalid="ignore", over="ignore"):
+            return self._plain()
+
+    def _plain(self):
         k = F4.cache_values(self.k, self.D, self.ks)
         v = F4.cache_values(self.v, self.D, self.vs)
         q = self.q.double().numpy()

@@ -272,3 +272,65 @@ def test_decode_deals_short_sequences_out_whole(lens):
         g = c.device()
         c.decode(g, max_len=max(lens) + 16 * pad)
         c.check(g, f"pad {pad}")
+
+
+@pytest.mark.parametrize("op", ["decode", "prefill"])
+def test_a_query_of_infinities_leaves_the_others_alone(op):
+    c = Case(61, [300, 70], 4, 2, 128, 16, "bf16", new=None if op == "decode" else [9, 70])
+    c.q[0, 1] = float("inf")
+    c.q[1, 6] = float("nan")
+    c.q[0, 5] *= 1e30
+    c.q[1, 2] *= 1e-30
+    g = c.device()
+    getattr(c, op)(g)
+    torch.cuda.synchronize()
+    want, bound = c.plain()
+    got = g.out.double().cpu().numpy()
+    rows = np.ones(got.shape[:2], bool)
+    rows[0, 1] = rows[1, 6] = rows[0, 5] = False               # (scores of 1e30 leave one weight: nothing to compare)
+    assert (np.abs(got - want) <= bound)[rows].all()
+    assert np.isfinite(got[0, 5]).all()
+
+
+def test_caches_past_four_gigabytes():
+    """Blocks whose bytes lie past 2^32: written, decoded, prefilled, moved."""
+    bs, H, D = 16, 8, 128
+    block = H * bs * D * 9 // 16
+    nb = (5 << 30) // block
+    rng = np.random.default_rng(62)
+    kc, vc = (torch.empty(pa.fp4_cache_shape(nb, H, bs, D), dtype=torch.uint8, device=DEV) for _ in range(2))
+    high = (nb - 1 - rng.permutation(1000)[:20]).astype(np.int32)
+    assert int(high.min()) * block > 1 << 32
+    c = Case(63, [300], 4, H, D, bs, "bf16", new=[37])
+    table = torch.from_numpy(high[None, :19].copy()).to(DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kw = dict(cache_dtype="fp4", k_scale=0.05, v_scale=0.05, device_error=err)
+    slots = torch.tensor([int(high[p // bs]) * bs + p % bs for p in range(300)], device=DEV)
+    rows = [torch.randn(300, H, D, generator=torch.Generator().manual_seed(i)).bfloat16().to(DEV) for i in range(2)]
+    pa.pa_reshape_and_cache(*rows, slots, kc, vc, **kw)
+    back = [torch.empty_like(r) for r in rows]
+    pa.pa_gather_cache(*back, slots, kc, vc, **kw)
+    # the same tokens in a small pool give the same codes, outputs and read-back
+    small = [torch.empty(pa.fp4_cache_shape(19, H, bs, D), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    order = torch.arange(19, dtype=torch.int32, device=DEV)[None].contiguous()
+    pa.pa_reshape_and_cache(*rows, torch.arange(300, device=DEV), *small, **kw)
+    lens = torch.tensor([300], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 37], dtype=torch.int32, device=DEV)
+    q = c.q.to(DEV)
+
+    def outs(k, v, t):
+        a, b = torch.empty_like(q[:1]), torch.empty_like(q)
+        pa.pa_decode(a, q[-1:].contiguous(), k, v, t, lens, 300, 0.05, **kw)
+        pa.pa_prefill(b, q, cu, k, v, t, lens, 37, 0.05, **kw)
+        return a, b
+
+    want = outs(*small, order)
+    for a, b in zip(outs(kc, vc, table), want):
+        assert torch.equal(a, b)
+    pairs = torch.tensor(sorted((int(b), 5 + i) for i, b in enumerate(high[:19])), dtype=torch.int64, device=DEV)
+    pa.pa_compact_blocks(kc, vc, pairs, table, lens, cache_dtype="fp4", device_error=err)
+    for a, b in zip(outs(kc, vc, table), want):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and int(table.max()) < 24
+    assert (back[0].float() - rows[0].float()).abs().max() < 1.0
