@@ -759,17 +759,20 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
 // out = sum_j w_j o_j / sum_j w_j with w_j = exp2(m_j - M) l_j, up to the mark
 // that ends them.  Warp w takes the pieces w, w + W, ..., eight of them in
 // flight; lane l owns D / 32 columns.  One warp is enough when there are many
-// heads to fill the SMs; few heads have many pieces each.
-constexpr int kMergeWarps = 4;
+// heads to fill the SMs (CTAs of four heads); few heads have many pieces
+// each, and get sixteen warps (one CTA): a sequence of 131071 tokens has 76
+// pieces a KV head.
+constexpr int kMergeFew = 16;
+__host__ __device__ constexpr int merge_warps(int W) { return W == 1 ? 4 : W; }  // of a CTA
 
 template <int QT, int D, int W>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_fp4_kernel(const __grid_constant__ Fp4Params p) {
-  constexpr int E = D / 32;
-  __shared__ float s_o[kMergeWarps][D];
-  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
-  __shared__ int s_end[kMergeWarps];
+__global__ void __launch_bounds__(32 * merge_warps(W)) merge_fp4_kernel(const __grid_constant__ Fp4Params p) {
+  constexpr int E = D / 32, CW = merge_warps(W);
+  __shared__ float s_o[W][D];
+  __shared__ float s_m[W], s_l[W];
+  __shared__ int s_end[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % W;
-  const long long head = W == kMergeWarps ? blockIdx.x : blockIdx.x * static_cast<long long>(kMergeWarps / W) + warp / W;
+  const long long head = W == 1 ? blockIdx.x * static_cast<long long>(CW) + warp : blockIdx.x;
   grid_dependency_wait();
   if (W == 1 && head >= static_cast<long long>(p.num_seqs) * p.num_q_heads) return;
   const int s = static_cast<int>(head / p.num_q_heads), hq = static_cast<int>(head % p.num_q_heads);
@@ -896,10 +899,11 @@ pa_status launch(const Fp4Params &p, const DeviceInfo &dev, cudaStream_t stream)
   if (p.cut) {
     const long long heads = static_cast<long long>(p.num_seqs) * p.num_q_heads;
     const bool many = heads >= dev.sm_count * 8;
-    cfg.gridDim = dim3(static_cast<unsigned>(many ? (heads + kMergeWarps - 1) / kMergeWarps : heads));
-    cfg.blockDim = dim3(32 * kMergeWarps);
+    const int warps = merge_warps(many ? 1 : kMergeFew);
+    cfg.gridDim = dim3(static_cast<unsigned>(many ? (heads + warps - 1) / warps : heads));
+    cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, many ? merge_fp4_kernel<QT, D, 1> : merge_fp4_kernel<QT, D, kMergeWarps>, p);
+    e = cudaLaunchKernelEx(&cfg, many ? merge_fp4_kernel<QT, D, 1> : merge_fp4_kernel<QT, D, kMergeFew>, p);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   return PA_OK;
