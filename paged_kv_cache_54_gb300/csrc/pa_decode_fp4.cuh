@@ -89,7 +89,9 @@ template <int D>
 struct KSlice {
   static constexpr int W = D / 32;  // words of a row a lane reads (8 codes each)
   uint32_t c[2][W];   // tokens 2gq, 2gq + 1
-  uint32_t s[W / 2];  // their scales (two bytes), one for each 16 local dimensions
+  // their scales (two bytes), one for each 16 local dimensions; spread: of the
+  // groups of columns 2tq and 2tq + 1
+  uint32_t s[2];
 };
 template <int D>
 struct VSlice {
@@ -110,8 +112,18 @@ struct State {
   bool far;                // some maximum is past 2^24 (warp-uniform)
 };
 
-// q rows of the group (G x D at `q`) as B fragments: column gq is query gq,
-// lane tq's local dimensions.  bf16 queries are rounded to fp16 after a
+// Few queries leave columns of the scores' product unused.  When a query's
+// groups of 16 dimensions fit them too (G D / 16 <= 8), each gets a column of
+// its own, Q laid out block-diagonally: a token's score is then the sum of
+// its groups' columns, each times the group's scale in fp32, and no code is
+// scaled before the product.  64 sequences of 512..4096 tokens, 32/32 heads:
+// 127 us with the codes scaled, 116 us so.
+template <int D, int G>
+constexpr bool kSpread = G * D / kFp4Group <= 8;
+
+// q rows of the group (G x D at `q`) as B fragments: column gq is query gq
+// (spread: group gq % (D / 16) of query gq / (D / 16)), lane tq's local
+// dimensions.  bf16 queries are rounded to fp16 after a
 // multiplication by the power of two that brings the query's largest entry
 // into [2^13, 2^14), undone on its scores, so that nothing overflows and what
 // underflows is 2^-38 of the largest.
@@ -120,10 +132,12 @@ __device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float sca
   const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
   constexpr int QW = D / 8;  // words of the lane
   uint32_t w[QW];
-  const uint4 *row = reinterpret_cast<const uint4 *>(q + (static_cast<size_t>(gq < G ? gq : 0) * D + tq * (D / 4)) * 2);
+  const int query = kSpread<D, G> ? gq / (D / kFp4Group) : gq;  // of column gq
+  const uint4 *row =
+      reinterpret_cast<const uint4 *>(q + (static_cast<size_t>(query < G ? query : 0) * D + tq * (D / 4)) * 2);
 #pragma unroll
   for (int i = 0; i < QW / 4; ++i) {
-    const uint4 x = gq < G ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 x = query < G ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u);
     w[4 * i] = x.x;
     w[4 * i + 1] = x.y;
     w[4 * i + 2] = x.z;
@@ -155,10 +169,17 @@ __device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float sca
 #pragma unroll
   for (int i = 0; i < QW; ++i) w[i] = scale > 0.f ? w[i] : scale < 0.f ? w[i] ^ 0x80008000u : 0u;
   st.far = false;
-  const float mult = scale == 0.f ? 1.f : fabsf(scale) / f;  // of query gq
+  const float mult = scale == 0.f ? 1.f : fabsf(scale) / f;  // of column gq
+  if constexpr (kSpread<D, G>) {  // a column keeps one group's dimensions
+    const int group = gq % (D / kFp4Group);
+#pragma unroll
+    for (int i = 0; i < QW; ++i)  // word i: local dimensions 2i, 2i + 1
+      if (tq * (D / 64) + i / 8 != group) w[i] = 0u;
+  }
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    st.mult[r] = __shfl_sync(0xffffffffu, mult, (2 * tq + r) * 4);
+    // (the lane's scores are of columns 2tq and 2tq + 1: one query's, when spread)
+    st.mult[r] = __shfl_sync(0xffffffffu, mult, (2 * tq + (kSpread<D, G> ? 0 : r)) * 4);
     st.lift[r] = 1.f / st.mult[r];
     st.top[r] = -INFINITY;
   }
@@ -234,6 +255,36 @@ __device__ __forceinline__ void scores(const State<D> &st, const KSlice<D> &c, f
   for (int i = 0; i < 4; ++i) s[i] = acc[0][i] + acc[1][i];
 }
 
+// The same when spread: s[0] is token 2gq, s[1] token 2gq + 1, against the
+// query of columns 2tq and 2tq + 1, in every lane that has the query.
+template <int D>
+__device__ __forceinline__ void scores_spread(const State<D> &st, const KSlice<D> &c, float (&s)[2]) {
+  float acc[2][4];
+#pragma unroll
+  for (int w = 0; w < KSlice<D>::W; ++w) {
+    uint32_t a[4], b[4];
+    e2m1x8_to_half2x4(c.c[0][w], a);
+    e2m1x8_to_half2x4(c.c[1][w], b);
+    if (w == 0) {
+      mma_first(acc[0], a[0], b[0], a[1], b[1], st.qb[0][0], st.qb[0][1]);
+      mma_first(acc[1], a[2], b[2], a[3], b[3], st.qb[1][0], st.qb[1][1]);
+    } else {
+      mma(acc[0], a[0], b[0], a[1], b[1], st.qb[2 * w][0], st.qb[2 * w][1]);
+      mma(acc[1], a[2], b[2], a[3], b[3], st.qb[2 * w + 1][0], st.qb[2 * w + 1][1]);
+    }
+  }
+  // scales of tokens 2gq, 2gq + 1 in the groups of columns 2tq and 2tq + 1
+  const float2 g0 = half2_bits_to_float2<kF16>(e4m3x2_to_half2(c.s[0]));
+  const float2 g1 = half2_bits_to_float2<kF16>(e4m3x2_to_half2(c.s[1]));
+  s[0] = fmaf(acc[0][1] + acc[1][1], g1.x, (acc[0][0] + acc[1][0]) * g0.x);
+  s[1] = fmaf(acc[0][3] + acc[1][3], g1.y, (acc[0][2] + acc[1][2]) * g0.y);
+#pragma unroll
+  for (int o = 1; o < D / 32; o <<= 1) {  // the lanes of one query
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+    s[1] += __shfl_xor_sync(0xffffffffu, s[1], o);
+  }
+}
+
 // the low nibbles of a's bytes and the high nibbles of b's
 __device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -241,15 +292,30 @@ __device__ __forceinline__ uint32_t low_nibbles(uint32_t a, uint32_t b) {
   return d;
 }
 
-// O^T += V^T P^T of a slice; p: its weights, laid out as its scores.
-template <int D>
-__device__ __forceinline__ void accumulate(State<D> &st, const VSlice<D> &c, const float (&p)[4]) {
+// P^T of a slice as B fragments (column gq: query gq; w0: tokens 4tq, 4tq + 1,
+// w1: 4tq + 2, 4tq + 3) from its weights, laid out as its scores.
+__device__ __forceinline__ void weights(const float (&p)[4], uint32_t &w0, uint32_t &w1) {
   const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
   const uint32_t pa = pack2_rn<kF16>(p[0], p[2]), pb = pack2_rn<kF16>(p[1], p[3]);  // tokens 2gq, 2gq + 1
   const int from0 = (2 * tq) * 4 + (gq >> 1), from1 = from0 + 4;
   const uint32_t a0 = __shfl_sync(0xffffffffu, pa, from0), b0 = __shfl_sync(0xffffffffu, pb, from0);
   const uint32_t a1 = __shfl_sync(0xffffffffu, pa, from1), b1 = __shfl_sync(0xffffffffu, pb, from1);
-  const uint32_t w0 = (gq & 1) ? b0 : a0, w1 = (gq & 1) ? b1 : a1;
+  w0 = (gq & 1) ? b0 : a0;
+  w1 = (gq & 1) ? b1 : a1;
+}
+// The same when spread (queries past the group's repeat one of them).
+template <int D, int G>
+__device__ __forceinline__ void weights_spread(const float (&p)[2], uint32_t &w0, uint32_t &w1) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  const uint32_t pk = pack2_rn<kF16>(p[0], p[1]);
+  const int from = (2 * tq) * 4 + (G == 2 ? 2 * (gq & 1) : 0);  // (query 1's scores are in lanes tq 2 and 3)
+  w0 = __shfl_sync(0xffffffffu, pk, from);
+  w1 = __shfl_sync(0xffffffffu, pk, from + 4);
+}
+
+// O^T += V^T P^T of a slice.
+template <int D>
+__device__ __forceinline__ void accumulate(State<D> &st, const VSlice<D> &c, uint32_t w0, uint32_t w1) {
   const uint32_t sA = e4m3x2_to_half2(c.s), sB = e4m3x2_to_half2(c.s >> 16);  // tokens (4tq, +1), (+2, +3)
   uint32_t eA[VSlice<D>::W][4], oA[VSlice<D>::W][4], eB[VSlice<D>::W][4], oB[VSlice<D>::W][4];
 #pragma unroll
@@ -301,7 +367,7 @@ struct Ring {
 };
 
 // The lane's codes and scales of a slice.
-template <int D>
+template <int D, bool SPREAD>
 __device__ __forceinline__ KSlice<D> read_k(const uint8_t *slice) {
   using R = Ring<D>;
   const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
@@ -320,9 +386,11 @@ __device__ __forceinline__ KSlice<D> read_k(const uint8_t *slice) {
       k.c[r][1] = x.y;
     }
   }
+  constexpr bool TWO = SPREAD || D == 128;
+  const int group = SPREAD ? 2 * tq % (D / kFp4Group) : tq * (D / 64);
 #pragma unroll
-  for (int i = 0; i < KSlice<D>::W / 2; ++i)
-    k.s[i] = *reinterpret_cast<const uint16_t *>(slice + R::KS + (tq * (D / 64) + i) * 16 + 2 * gq);
+  for (int i = 0; i < (TWO ? 2 : 1); ++i)
+    k.s[i] = *reinterpret_cast<const uint16_t *>(slice + R::KS + (group + i) * 16 + 2 * gq);
   return k;
 }
 template <int D>
@@ -353,8 +421,8 @@ template <int D>
 __device__ __forceinline__ void attend(State<D> &st, const uint8_t *slot, int n) {
   const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
   float a[4], b[4];
-  scores<D>(st, read_k<D>(slot), a);
-  scores<D>(st, read_k<D>(slot + Ring<D>::SLICE), b);
+  scores<D>(st, read_k<D, false>(slot), a);
+  scores<D>(st, read_k<D, false>(slot + Ring<D>::SLICE), b);
   if (n < kStep) {  // warp-uniform
     if (2 * gq >= n) a[0] = a[1] = -INFINITY;
     if (2 * gq + 1 >= n) a[2] = a[3] = -INFINITY;
@@ -416,8 +484,74 @@ __device__ __forceinline__ void attend(State<D> &st, const uint8_t *slot, int n)
     va.s &= la >= 4 ? 0xffffffffu : la <= 0 ? 0u : (1u << (8 * la)) - 1u;
     vb.s &= lb >= 4 ? 0xffffffffu : lb <= 0 ? 0u : (1u << (8 * lb)) - 1u;
   }
-  accumulate<D>(st, va, a);
-  accumulate<D>(st, vb, b);
+  uint32_t w0, w1;
+  weights(a, w0, w1);
+  accumulate<D>(st, va, w0, w1);
+  weights(b, w0, w1);
+  accumulate<D>(st, vb, w0, w1);
+}
+
+// The same when spread: a lane has two tokens' scores a slice, of one query,
+// and its state in m[0], l[0], top[0].
+template <int D, int G>
+__device__ __forceinline__ void attend_spread(State<D> &st, const uint8_t *slot, int n) {
+  const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
+  float a[2], b[2];
+  scores_spread<D>(st, read_k<D, true>(slot), a);
+  scores_spread<D>(st, read_k<D, true>(slot + Ring<D>::SLICE), b);
+  if (n < kStep) {
+    if (2 * gq >= n) a[0] = -INFINITY;
+    if (2 * gq + 1 >= n) a[1] = -INFINITY;
+    if (kSlice + 2 * gq >= n) b[0] = -INFINITY;
+    if (kSlice + 2 * gq + 1 >= n) b[1] = -INFINITY;
+  }
+  float x = fmaxf(max3(a[0], a[1], b[0]), b[1]);
+  if (__any_sync(0xffffffffu, x > st.top[0])) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    const bool up = x > st.top[0];
+    const float y = x * st.mult[0], f = up ? ex2(st.m[0] - y) : 1.f;
+    if (up) {
+      st.m[0] = y;
+      st.top[0] = fmaf(kLazy, st.lift[0], x);
+    }
+    st.l[0] *= f;
+    // columns 2tq and 2tq + 1 of O^T: queries 0 and 1 in lanes tq 0
+    const float f1 = G == 2 ? __shfl_sync(0xffffffffu, f, gq * 4 + 2) : f;
+#pragma unroll
+    for (int i = 0; i < State<D>::MT; ++i) {
+      st.o[i][0] *= f;
+      st.o[i][2] *= f;
+      st.o[i][1] *= f1;
+      st.o[i][3] *= f1;
+    }
+    st.far = __any_sync(0xffffffffu, !(fabsf(st.m[0]) <= kFar));
+  }
+  if (!st.far) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = ex2(fmaf(a[i], st.mult[0], -st.m[0]));
+      b[i] = ex2(fmaf(b[i], st.mult[0], -st.m[0]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = ex2(__fsub_rn(__fmul_rn(a[i], st.mult[0]), st.m[0]));
+      b[i] = ex2(__fsub_rn(__fmul_rn(b[i], st.mult[0]), st.m[0]));
+    }
+  }
+  st.l[0] += (a[0] + a[1]) + (b[0] + b[1]);
+  VSlice<D> va = read_v<D>(slot), vb = read_v<D>(slot + Ring<D>::SLICE);
+  if (n < kStep) {
+    const int la = n - 4 * tq, lb = la - kSlice;
+    va.s &= la >= 4 ? 0xffffffffu : la <= 0 ? 0u : (1u << (8 * la)) - 1u;
+    vb.s &= lb >= 4 ? 0xffffffffu : lb <= 0 ? 0u : (1u << (8 * lb)) - 1u;
+  }
+  uint32_t w0, w1;
+  weights_spread<D, G>(a, w0, w1);
+  accumulate<D>(st, va, w0, w1);
+  weights_spread<D, G>(b, w0, w1);
+  accumulate<D>(st, vb, w0, w1);
 }
 
 // 16 or 8 bytes from global to shared memory (address in the shared window).
@@ -678,10 +812,17 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
       } else if (nsteps > 0) {
         issue(nwin, 0, other);
       }
-      attend<D>(st, ring + slot, min(kStep, valid));
+      if constexpr (kSpread<D, G>)
+        attend_spread<D, G>(st, ring + slot, min(kStep, valid));
+      else
+        attend<D>(st, ring + slot, min(kStep, valid));
       slot = other;
     }
 
+    if constexpr (kSpread<D, G> && G == 2) {  // query 1's statistics to the lanes of its column of O^T
+      st.m[1] = __shfl_sync(0xffffffffu, st.m[0], gq * 4 + 2);
+      st.l[1] = __shfl_sync(0xffffffffu, st.l[0], gq * 4 + 2);
+    }
     // ---- the warps' states meet (the last piece's have been read by then)
     __syncthreads();
     float l0 = st.l[0], l1 = st.l[1];
