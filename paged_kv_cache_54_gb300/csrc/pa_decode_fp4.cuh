@@ -1,8 +1,8 @@
 // Paged decode attention over a four-bit cache (PA_FP4) for sm_103a.
 //
 // Work decomposition.  The (sequence, KV head) pairs, in sequence order, are
-// laid end to end in units of 64 tokens (a pair's tokens, and one unit for
-// what a piece costs beside them), and CTA b of n takes the units
+// laid end to end in units of 64 tokens (a pair's tokens, and kPairCost units
+// for what a piece costs beside them), and CTA b of n takes the units
 // [b U / n, (b + 1) U / n) of the U in all: equal shares whatever the
 // lengths, found by each CTA from a scan of the lengths (no plan launch, no
 // claims).  A CTA's share is a run of pieces, one per pair it touches.  A
@@ -10,24 +10,39 @@
 // pair leave (m, l, O / l) partials, joined by a merge kernel (the
 // flash-decoding reduction).  Partials live in the layout every cache type's
 // workspace has, [sequence, partition, query head]: piece j of a pair uses
-// the place of partition j.  A share is at least two partitions long, so a
-// pair of L tokens has at most ceil(L / 2P) + 1 pieces, which is at most the
-// workspace's max_parts when that is two or more; when it is one, pairs are
-// dealt out whole.
+// the place of partition j.  A share is at least two partitions (2P tokens)
+// long, so a pair of L tokens has at most L / 2P + 2 pieces, and that many
+// places whenever max_parts is two or more; calls of short sequences deal
+// pairs out whole.  Sequences that share blocks are each read on their own:
+// shared blocks come from L2, but are widened once for each.
 //
-// A CTA is four warps, four CTAs to an SM.  Within a piece warp w takes the 32-token steps w,
-// w + 4, ..., each warp with its own online softmax; the four states meet
-// in shared memory at the piece's end.  A warp's steps stream through a ring
-// of its own in shared memory, filled by 16-byte asynchronous copies three
-// steps ahead, so no warp waits for another within a piece.  (Tensor copies
-// of whole tiles would be fewer instructions, but an SM starts about one per
-// 100 clocks, and a tile of 16 tokens is 1152 bytes: half the HBM rate.)
+// A CTA is four warps, and an SM holds four CTAs.  Within a piece warp w takes
+// the 32-token steps w, w + 4, ..., each warp with its own online softmax; the
+// four states meet in shared memory at the piece's end.  A warp's steps
+// stream through a two-slot ring of its own in shared memory: 16-byte
+// asynchronous copies bring the next step, which may be the next piece's
+// first, while one is worked on, so warps wait for one another only where a
+// piece ends.  (Tensor copies of whole tiles would be fewer instructions, but
+// an SM starts about one per 100 clocks, and a tile of 16 tokens is 1152
+// bytes: half the HBM rate.)
 //
-// A step is two slices of 16 tokens; a slice is two small products on mma.sync m16n8k16 with fp16 operands
-// and fp32 accumulation, S^T = K Q^T and O^T = V^T P^T: tokens, then head
-// dimensions, as M, and the query group padded to 8 as N.  Codes widen to
-// fp16 exactly (a code times its group's scale is an fp16 value), so the only
-// roundings are those of P to fp16 and of the output.
+// A step is two slices of 16 tokens; a slice is two small products on
+// mma.sync m16n8k16 with fp16 operands and fp32 accumulation, S^T = K Q^T and
+// O^T = V^T P^T: tokens, then head dimensions, as M, and the query group
+// padded to 8 as N.  Codes widen to fp16 exactly (a code times its group's
+// scale is an fp16 value), so the only roundings are those of P to fp16 and
+// of the output.
+//
+// What bounds it: the bytes and the instructions, about equally.  One
+// sequence of 1048575 tokens, 64/8 heads (1.21 GB): 207 us, 5.8 TB/s; the
+// copies alone take 184 us, the products alone 188 us, at 285 warp
+// instructions a slice, 62% of the issue slots.  32/32 heads of 64 sequences
+// of 512..4096 tokens (681 MB): 116 us, 5.9 TB/s.  128 sequences of 256..32768
+// tokens, 64/8 heads (1.0 GB): 181 us, 5.5 TB/s.  The rest of a short call:
+// 1.2 us until the shares are known, 5 us until the first steps have landed,
+// 1 us a piece for its end, 4 us for the merge.  Five CTAs an SM (96
+// registers) took 3% longer than four, two CTAs of eight warps 8%, copies two
+// steps ahead the same.
 //
 // Fragment orders (lane = 4 gq + tq), chosen so that every lane reads runs of
 // its own:
@@ -56,7 +71,11 @@ constexpr int kCtas = 4;        // CTAs an SM
 constexpr int kSlice = 16;      // tokens of the products
 constexpr int kStep = 32;       // tokens of a warp's step
 constexpr int kUnit = 64;       // tokens of a unit of work
-constexpr int kPairCost = 5;    // units that a pair costs beside its tokens'
+// Units that a pair is charged beside its tokens': its q, its first step's
+// latency, the join.  128 sequences of 256..32768 tokens, 64/8 heads: 200 us
+// at 1, 189 at 3, 181 at 5, 183 at 8; 64 of 512..4096, 32/32 heads: 118, 116,
+// 116, 118.
+constexpr int kPairCost = 5;
 // Pairs of up to 512 tokens are dealt out whole, and there is no merge.  Whole
 // against cut, us of one call in a graph: 1 x 8 pairs of up to 256 tokens
 // 4.8 / 7.6, of 512 6.2 / 6.8, of 1024 9.3 / 7.0; 4 x 4 of 512 8.2 / 6.8;
@@ -606,8 +625,8 @@ struct Copier {
     for (int half = 0; half < 2; ++half) {  // the slices
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
-        const uint32_t tile = BLOCKS == 4 ? (ROUNDS == 2 ? t[(2 * half + i) % BLOCKS] : lane < 16 ? t[2 * half % BLOCKS] : t[(2 * half + 1) % BLOCKS])
-                                          : t[half * (BLOCKS - 1)];
+        const uint32_t even = t[2 * half % BLOCKS], odd = t[(2 * half + 1) % BLOCKS];  // (blocks of 8: the slice's two)
+        const uint32_t tile = BLOCKS < 4 ? t[half * (BLOCKS - 1)] : (ROUNDS == 2 ? i == 0 : lane < 16) ? even : odd;
         // bytes past the lane's chunk of the tile: the first slice, the first 32 chunks
         const int off = (BLOCKS == 1 ? half * R::CODES : 0) + (BLOCKS == 4 ? 0 : i * 512);
         const uint32_t dst = (i == 0 ? to0 : to1) + half * R::SLICE;
@@ -842,7 +861,8 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
         }
 #pragma unroll
         for (int i = 0; i < State<D>::MT; i += 4) {
-          *reinterpret_cast<float4 *>(dst + i) = make_float4(st.o[i][r], st.o[i + 1][r], st.o[i + 2][r], st.o[i + 3][r]);
+          *reinterpret_cast<float4 *>(dst + i) =
+              make_float4(st.o[i][r], st.o[i + 1][r], st.o[i + 2][r], st.o[i + 3][r]);
           *reinterpret_cast<float4 *>(dst + D / 16 + i) =
               make_float4(st.o[i][2 + r], st.o[i + 1][2 + r], st.o[i + 2][2 + r], st.o[i + 3][2 + r]);
         }
@@ -870,8 +890,8 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
         const float inv = den == 0.f ? 0.f : vsc / den;
         const int hq = cur.h * G + j;
         if (cur.first && cur.last) {
-          uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) +
-                                                       (static_cast<size_t>(cur.s) * p.num_q_heads + hq) * D + lane * E);
+          const size_t at = (static_cast<size_t>(cur.s) * p.num_q_heads + hq) * D + lane * E;
+          uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + at);
 #pragma unroll
           for (int e = 0; e < E; e += 2) out[e / 2] = pack2_rn<QT>(x[e] * inv, x[e + 1] * inv);
         } else {

