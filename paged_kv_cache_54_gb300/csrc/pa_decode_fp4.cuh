@@ -919,10 +919,12 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
 // W warps per (sequence, query head) join its pieces' partials,
 // out = sum_j w_j o_j / sum_j w_j with w_j = exp2(m_j - M) l_j, up to the mark
 // that ends them.  Warp w takes the pieces w, w + W, ..., eight of them in
-// flight; lane l owns D / 32 columns.  One warp is enough when there are many
-// heads to fill the SMs (CTAs of four heads); few heads have many pieces
-// each, and get sixteen warps (one CTA): a sequence of 131071 tokens has 76
-// pieces a KV head.
+// flight; lane l owns D / 32 columns.  One warp (CTAs of four heads) is enough
+// for pairs in one or a few pieces, as when there are as many pairs as SMs;
+// fewer pairs have more pieces each and get sixteen warps a head: one
+// sequence of 131071 tokens with 8 KV heads has 76, and its call took 38.2 us
+// with four warps a head, 36.4 with sixteen; 48 sequences of 1000..9000 with
+// 8 KV and 16 query heads 51.5 with sixteen, 47.1 with one.
 constexpr int kMergeFew = 16;
 __host__ __device__ constexpr int merge_warps(int W) { return W == 1 ? 4 : W; }  // of a CTA
 
@@ -1059,7 +1061,7 @@ pa_status launch(const Fp4Params &p, const DeviceInfo &dev, cudaStream_t stream)
   if (e != cudaSuccess) return cuda_fail(e);
   if (p.cut) {
     const long long heads = static_cast<long long>(p.num_seqs) * p.num_q_heads;
-    const bool many = heads >= dev.sm_count * 8;
+    const bool many = pairs >= dev.sm_count;
     const int warps = merge_warps(many ? 1 : kMergeFew);
     cfg.gridDim = dim3(static_cast<unsigned>(many ? (heads + warps - 1) / warps : heads));
     cfg.blockDim = dim3(32 * warps);
