@@ -25,7 +25,8 @@
  *   pa_prefix_cache_*     the block pool with prefix caching: full blocks
  *                         keyed by their content and everything before it,
  *                         shared through reference counts, kept after their
- *                         last user until needed again.
+ *                         last user until needed again; forking, and moves
+ *                         that draw the kept blocks together.
  *
  * Pages that state the problem (cited by title and section):
  *   [P1] "【性能飞跃】从 OOM 到丝滑推理:深度工程化 RAG 架构下的内存管理艺术"
@@ -239,7 +240,9 @@ PA_API size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads,
  *                  bytes, 256-byte aligned; contents need no initialisation.
  *                  Calls sharing one workspace must be stream-ordered.
  * Supported set: num_q_heads / kv_heads in {1, 2, 4, 8}; cache dtypes of
- * pa_cache_desc; coded caches accept q in PA_F16 or PA_BF16.
+ * pa_cache_desc; coded caches accept q in PA_F16 or PA_BF16.  Blocks that
+ * sequences share may be read once for several of them, except in a PA_FP4
+ * cache, which is read sequence by sequence.
  * Stream order: the call's first kernel may begin reading block_tables and
  * seq_lens while the kernel before it on the stream is still running, if
  * that kernel has signalled programmatic completion early
@@ -495,7 +498,8 @@ PA_API pa_status pa_prefix_cache_fork_sequence(pa_prefix_cache *cache, int64_t p
  * ascending order.  Returns the number of moves; writes them to `pairs`
  * (host int64 [capacity, 2]: (src, dst), ascending by src, as
  * pa_compact_blocks takes them).  With fewer than that many rows of capacity
- * (or pairs NULL) nothing is changed; -1 for a NULL handle. */
+ * (or pairs NULL) nothing is changed; -1 for a NULL handle or when host
+ * memory runs out (nothing is changed then either). */
 PA_API int32_t pa_prefix_cache_compact(pa_prefix_cache *cache, int64_t *pairs, int32_t capacity);
 
 /* Block table of one sequence: returns its length (or -1 for an unknown
