@@ -55,6 +55,16 @@ def test_decode_long_sequence_with_a_loose_length_bound():
     c.check(g)
 
 
+@pytest.mark.parametrize("P", [0, 64])
+@pytest.mark.parametrize("lens,G,H", [([1] * 19 + [20011], 1, 8), ([20011, 0, 5] + [600] * 17, 4, 8), ([80021], 2, 1)])
+def test_decode_joins_more_pieces_than_a_round_of_the_merge(lens, G, H, P):
+    # 160 pairs, the longest in over 32 pieces (one warp a head); one pair in over 512 (sixteen)
+    c = Case(13, lens, G, H, 64, 32, "bf16")
+    g = c.device()
+    c.decode(g, P)
+    c.check(g, f"P {P}")
+
+
 @pytest.mark.parametrize("scale,gain", [(-0.05, 1.0), (0.0, 1.0), (0.5, 1.0), (1e-6, 3e4), (1e3, 1e-5)])
 def test_decode_scales_and_query_ranges(scale, gain):
     c = Case(9, [300, 77], 8, 2, 128, 16, "bf16", scale=scale, q_gain=gain)
