@@ -246,11 +246,14 @@ PA_API size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads,
  * Stream order: the call's first kernel may begin reading block_tables and
  * seq_lens while the kernel before it on the stream is still running, if
  * that kernel has signalled programmatic completion early
- * (griddepcontrol.launch_dependents).  pa_reshape_and_cache and
- * pa_copy_blocks do so; they never write those arrays.  A caller's kernel
- * that writes block_tables or seq_lens must not signal before its writes.
- * Everything else the call reads (q, the caches) is read only after all
- * earlier work on the stream has completed.
+ * (griddepcontrol.launch_dependents).  pa_reshape_and_cache,
+ * pa_gather_cache, pa_copy_blocks and a pa_decode over a PA_FP4 cache do so;
+ * they never write those arrays.  A caller's kernel that writes block_tables
+ * or seq_lens must not signal before its writes.  Everything else the call
+ * reads (q, the caches) is read, and everything it writes (out, the
+ * workspace) written, only after all earlier work on the stream has
+ * completed, so memory that an earlier call on the stream still reads may be
+ * handed to this one.
  */
 PA_API pa_status pa_decode(void *out, const void *q, int32_t q_dtype,
                     int32_t num_seqs, int32_t num_q_heads,

@@ -217,10 +217,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   if (tid < kPlanBuckets) s_hist[tid] = 0;
   launch_dependents();  // the decode grid may become resident; it waits for us
   // This kernel is a programmatic dependent of whatever precedes it on the
-  // stream: it reads only the block tables and lengths (which the cache
-  // writes before it never touch) and writes only this call's workspace, and
-  // it waits for the preceding kernel before it ends, so the decode that
-  // waits for it also follows every kernel before the call.
+  // stream: until it has waited for that kernel it reads only the block
+  // tables and lengths (which the cache writes before it never touch) and
+  // writes nothing but shared memory.  The workspace is written after the
+  // wait: its memory may be what the kernel before it still reads (a freed
+  // row, slot or query tensor that an allocator handed out again).  The
+  // decode that waits for this kernel also follows every kernel before the
+  // call.
   //
   // Wide chunks: W = p.wide_seqs sequences from a multiple of W whose rows
   // all agree over a full partition become one wide item (decoded on the
@@ -272,8 +275,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int L = clamp_len(__ldg(p.seq_lens + s), p.len_cap, s >= s_lo ? p.err : nullptr);
     if (len_smem) s_len[s - r0] = L;
   }
-  if (compare)  // (the workspace region is 256-byte aligned and padded: whole words)
+  if (compare) {  // (the workspace region is 256-byte aligned and padded: whole words)
+    if (nslots > kPlanSmemSlots) grid_dependency_wait();  // the flags are in the workspace
     for (int i = tid * 4; i < nslots; i += 4 * kPlanThreads) *reinterpret_cast<uint32_t *>(mis + i) = 0u;
+  }
   if (use_wide) {  // every chunk's flags (a CTA's run may reach into a chunk another's starts)
     for (int i = tid; i < (nchunks << mp_sh); i += kPlanThreads) {
       const int c = i >> mp_sh, q = i & ((1 << mp_sh) - 1);
@@ -427,6 +432,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
         __syncthreads();
       }
+      grid_dependency_wait();  // the first writes to the workspace follow
     }
     int sl = i0 >> mp_sh, q = i0 & ((1 << mp_sh) - 1);
     for (int i = i0; i < i1; ++i) {
@@ -463,7 +469,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     p.work[2] = tot.y;
     p.work[0] = 0;
   }
-  grid_dependency_wait();
 }
 
 // ----------------------------------------------------------------------------

@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
   }
   __syncthreads();
   grid_dependency_wait();
-  launch_dependents();  // the merge (or the next call, which waits for this grid)
+  launch_dependents();  // the merge (or the next call, which waits for this grid before it writes)
   if (left <= 0) return;
   // the next piece: KV head h of sequence s from unit off of the pair
   int s = s_first, h, off, number = 0;  // number: the first piece's among its pair's
