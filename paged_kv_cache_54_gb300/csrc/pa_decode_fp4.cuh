@@ -142,10 +142,8 @@ constexpr bool kSpread = G * D / kFp4Group <= 8;
 
 // q rows of the group (G x D at `q`) as B fragments: column gq is query gq
 // (spread: group gq % (D / 16) of query gq / (D / 16)), lane tq's local
-// dimensions.  bf16 queries are rounded to fp16 after a
-// multiplication by the power of two that brings the query's largest entry
-// into [2^13, 2^14), undone on its scores, so that nothing overflows and what
-// underflows is 2^-38 of the largest.
+// dimensions.  bf16 queries are rounded to fp16 after a multiplication by the
+// query's own power of two, undone on its scores.
 template <int QT, int D, int G>
 __device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float scale) {
   const int lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
@@ -172,11 +170,7 @@ __device__ __forceinline__ void load_q(State<D> &st, const uint8_t *q, float sca
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (top > 0.f && top <= 3.4e38f) {
-      int e;
-      frexpf(top, &e);
-      f = ldexpf(1.f, min(14 - e, 100));
-    }
+    f = query_factor(top, scale);
 #pragma unroll
     for (int i = 0; i < QW; ++i) {
       const float2 x = half2_bits_to_float2<kBF16>(w[i]);

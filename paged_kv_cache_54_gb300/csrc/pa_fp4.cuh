@@ -40,6 +40,22 @@ __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
   return d;
 }
 
+// Power of two that a bf16 query row is multiplied by before it is rounded
+// to fp16 (its scores' multiplier becomes scale / it): its largest magnitude,
+// top, comes to lie in [2^13, 2^14), so that nothing overflows and what
+// underflows is 2^-38 of the largest.  It stays small enough for the
+// multiplier to be a normal number, at least 2^-101: a multiplier that
+// underflowed to zero would turn masked scores into NaN.  (Where that limit
+// holds, the scores are below 2^-50 whatever the keys are.)  1 for rows of
+// zeros and rows with an infinity.
+__device__ __forceinline__ float query_factor(float top, float scale) {
+  if (!(top > 0.f && top < INFINITY)) return 1.f;
+  int e, es = 0;
+  frexpf(top, &e);
+  if (fabsf(scale) < 1.f) frexpf(scale, &es);
+  return ldexpf(1.f, min(min(14 - e, 126), es + 100));
+}
+
 // 32 bytes as one access where the address allows it (two of 16 otherwise):
 // lanes then touch whole sectors of consecutive addresses.
 struct Words32 {

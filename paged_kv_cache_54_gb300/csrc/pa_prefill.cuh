@@ -545,9 +545,9 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
         }
       }
       if constexpr (QCONV && KVT == kFP4) {
-        // the row's q, rewritten in place as fp16 by its own thread, times the
-        // power of two that brings its largest entry into [2^13, 2^14): small
-        // rows keep their eight bits, and no thread waits for another's.  Lane
+        // the row's q, rewritten in place as fp16 by its own thread, times its
+        // own power of two: small rows keep their eight bits, and no thread
+        // waits for another's.  Lane
         // order within a row follows its swizzle, so no banks collide.
         ok = __all_sync(0xffffffffu, mbar_wait(&hdr.q_full, 0, abort));
         uint8_t *row = qs + t * Lay::Q_TILE + r * 128;
@@ -566,12 +566,7 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
             }
           }
         }
-        float f = 1.f;
-        if (amax > 0.f && amax <= 3.0e38f) {
-          int ex;
-          frexpf(amax, &ex);
-          f = ldexpf(1.f, min(14 - ex, 100));
-        }
+        const float f = query_factor(amax, c);
         if (ok) {
   #pragma unroll
           for (int j = 0; j < CH; ++j) {
@@ -658,7 +653,9 @@ __device__ __forceinline__ void prefill_body(const PrefillParams &p) {
         // and with a positive scale the maximum is taken on the raw scores and
         // the scale folded into the exponent's one fma.  Otherwise the scores
         // are scaled, then masked (key position > row position: -inf).
-        const bool plain = c > 0.f && __all_sync(0xffffffffu, k0 + kPfKeys - 1 <= pos);
+        // (One decision for the warp: it votes again below, and rows have
+        // multipliers of their own.)
+        const bool plain = __all_sync(0xffffffffu, c > 0.f && k0 + kPfKeys - 1 <= pos);
         float mx, cm;
         if (plain) {
           float a = sv[0], b = sv[32];  // two chains of 3-input maxima
