@@ -296,7 +296,11 @@ PA_API pa_status pa_decode(void *out, const void *q, int32_t q_dtype,
  * head_dim as in pa_cache_desc; num_seqs and kv_heads <= 65535.  Needs no
  * workspace and allocates nothing.  With a coded cache the products run
  * on fp16 operands: a bf16 q is rounded to fp16 after scaling each 128-row
- * query tile by a power of two that brings its largest |q| within 2^15.
+ * query tile by a power of two that brings its largest |q| within 2^15; with
+ * a PA_FP4 cache (in pa_decode too) after scaling each row of a query head
+ * on its own, up or down, by the power of two that brings its largest |q|
+ * into [2^13, 2^14) (less where scale is so small that |scale| over that
+ * power would be below 2^-100).
  */
 PA_API pa_status pa_prefill(void *out, const void *q, int32_t q_dtype, int32_t num_q_tokens,
                             const int32_t *cu_q_lens, int32_t num_seqs, int32_t num_q_heads,
