@@ -31,19 +31,35 @@ __device__ __forceinline__ float divide(float a, float b, float r) {
   const float q = a * r;
   return fmaf(fmaf(q, -b, a), r, q);
 }
-// The same for two values at once (packed arithmetic, each lane rounded as
-// the scalar): nb is -b twice, r2 is r twice.
+// The negated quotient of two values at once (packed arithmetic, each lane
+// rounded as the scalar): b is the divisor twice, nr is -r twice.  A zero
+// keeps its sign this way round: for a = -0 the steps are q = +0, e = +0 + -0
+// = +0, -0 + +0 = +0, and for a = +0 they end in -0 (with the positive
+// quotient the last sum would be +0 for both).
 __device__ __forceinline__ uint64_t twice(float x) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(x));
   return d;
 }
-__device__ __forceinline__ uint64_t divide2(uint64_t a, uint64_t nb, uint64_t r2) {
+__device__ __forceinline__ uint64_t negated_quotient(uint64_t a, uint64_t b, uint64_t nr) {
   uint64_t q, e, d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(a), "l"(r2));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(nb), "l"(a));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(e), "l"(r2), "l"(q));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(a), "l"(nr));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(b), "l"(a));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(e), "l"(nr), "l"(q));
   return d;
+}
+
+// e2m1 codes of -y / g of 16 values (g2 is g twice, nrg -1 / g twice)
+__device__ __forceinline__ uint2 e2m1_codes(const uint64_t (&y)[8], uint64_t g2, uint64_t nrg) {
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm("{\n\t.reg .b8 b;\n\t.reg .f32 x, y;\n\tmov.b64 {x, y}, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, y, x;\n\tcvt.u32.u8 %0, b;\n\t}"
+        : "=r"(c[i])
+        : "l"(negated_quotient(y[i], g2, nrg)));
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }
 
 // e2m1 code of y / g in the low four bits: nearest, ties to even, +-6 beyond;
@@ -109,26 +125,22 @@ __device__ __forceinline__ uint3 quantise_group(uint4 a, uint4 b, float scale, f
   const uint32_t g8 = __nv_cvt_float_to_fp8(divide(ytop, 6.f, 1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
   if (g8 == 0) return make_uint3(0u, 0u, 0u);
   const float2 g = table[g8];
-  const uint64_t ng = twice(-g.x), rg = twice(g.y), ns = twice(-scale), rs = twice(r);
+  const uint64_t g2 = twice(g.x), nrg = twice(-g.y), s2 = twice(scale), nrs = twice(-r);
   uint64_t y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 f = half2_bits_to_float2<SRC>(w[i]);
     asm("mov.b64 %0, {%1, %2};" : "=l"(y[i]) : "f"(f.x), "f"(f.y));
   }
-  if (scale != 1.f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = divide2(y[i], ns, rs);
+  // (both quotients, or one and the codes' signs turned round)
+  if (scale == 1.f) {
+    const uint2 c = e2m1_codes(y, g2, nrg);
+    return make_uint3(c.x ^ 0x88888888u, c.y ^ 0x88888888u, g8);
   }
-  uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    asm("{\n\t.reg .b8 b;\n\t.reg .f32 x, y;\n\tmov.b64 {x, y}, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, y, x;\n\tcvt.u32.u8 %0, b;\n\t}"
-        : "=r"(c[i])
-        : "l"(divide2(y[i], ng, rg)));
-  return make_uint3(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
-                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410), g8);
+  for (int i = 0; i < 8; ++i) y[i] = negated_quotient(y[i], s2, nrs);
+  const uint2 c = e2m1_codes(y, g2, nrg);
+  return make_uint3(c.x, c.y, g8);
 }
 
 // GPR: groups of a row.  A thread keeps one head and group (idx of the
