@@ -190,9 +190,9 @@ PA_API pa_status pa_reshape_and_cache(const void *key, const void *value,
  *   row[t, h, :] = dec(cache[slot / block_size, h, slot % block_size, :])
  * where dec is a bit copy for 16-bit caches and otherwise the value the codes
  * stand for (code * scale in IEEE float32; for PA_FP4 the exact product of
- * code and group scale, times the head's), rounded to nearest even.  A slot
- * outside the cache leaves its row as it was and is reported as device
- * error 2.
+ * code and group scale, times the head's), rounded to nearest even.  Any
+ * other slot outside the cache (below -1, or num_blocks * block_size and
+ * above) leaves its row as it was and is reported as device error 2.
  */
 PA_API pa_status pa_gather_cache(void *key, void *value, int32_t dst_dtype,
                                  const int64_t *slot_mapping, int32_t num_tokens,

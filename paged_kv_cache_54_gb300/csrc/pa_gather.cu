@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) gather_kernel(uint8_t *__restrict__ key, 
     const IDX th = i >> gpr_shift, t = th / kv_heads;
     const uint32_t h = static_cast<uint32_t>(th - t * kv_heads);
     const long long slot = __ldg(slots + t);
-    if (slot >= num_slots) {
+    if (slot < -1 || slot >= num_slots) {  // (-1: a padding row)
       if (h == 0 && g == 0) record_error(err, kErrSlot);
       continue;
     }

@@ -47,3 +47,22 @@ def test_codes_bit_for_bit(T, H, D, bs, src, scale):
             c, g = F4.unpack_tile(got[t // bs, h], bs, D)
             assert (g[t % bs] == groups[t, h]).all() and (c[t % bs] == codes[t, h]).all(), (t, h)
     assert zeros > 0
+
+
+@pytest.mark.parametrize("cache_dtype", ["bf16", "int8", "fp4"])
+@pytest.mark.parametrize("bad", [-2, -(1 << 40), -(1 << 63), 64, 1 << 40])
+def test_gather_leaves_rows_of_bad_slots_and_reports_them(cache_dtype, bad):
+    nb, H, bs, D = 4, 3, 16, 64
+    shape = pa.fp4_cache_shape(nb, H, bs, D) if cache_dtype == "fp4" else (nb, H, bs, D)
+    dtype = {"bf16": torch.bfloat16, "int8": torch.int8, "fp4": torch.uint8}[cache_dtype]
+    caches = [torch.full(shape, 0x22, dtype=torch.uint8, device=DEV).to(dtype) for _ in range(2)]
+    out = [torch.full((5, H, D), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    slots = torch.tensor([3, bad, -1, bad, 63], device=DEV)
+    pa.pa_gather_cache(*out, slots, *caches, cache_dtype=cache_dtype, device_error=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 2
+    for o in out:
+        assert (o[1] == 7).all() and (o[3] == 7).all()         # as they were
+        assert (o[2] == 0).all()                               # the padding row
+        assert (o[0] != 7).all() and (o[0] != 0).all() and torch.equal(o[0], o[4])
