@@ -262,20 +262,28 @@ def _require(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
-def _require_all(names: str, *tensors) -> None:
-    """Contiguous tensors of one device, the current one (the device a call
-    launches on); names: theirs, separated by spaces."""
+def _require_all(names: str, *tensors) -> str | None:
+    """Contiguous CUDA tensors; names: theirs, separated by spaces.  Returns
+    the name of one that is not on the current device (the device a call
+    launches on, which then has to have access to it), or None."""
     if not tensors[0].is_cuda:  # (no question to a driver that may not be there)
         _require(tensors[0], names.split()[0])
-    device = _current_device()
+    device, away = _current_device(), None
     for i, t in enumerate(tensors):
         if t.get_device() != device or not t.is_contiguous():
             _require(t, names.split()[i])
-            raise ValueError(f"{names.split()[i]} must be on the current device, cuda:{device}")
+            away = names.split()[i]
+    return away
 
 
-def _check_fp4(head_dim, k_cache, v_cache, q=None, seqs=None, block_tables=None, seq_lens=None) -> None:
-    """Shapes that the C ABI of a four-bit cache takes on trust."""
+def _require_here(away: str | None) -> None:
+    if away is not None:
+        raise ValueError(f"{away} must be on the current device, cuda:{_current_device()}")
+
+
+def _check_fp4(away, head_dim, k_cache, v_cache, q=None, seqs=None, block_tables=None, seq_lens=None) -> None:
+    """Places and shapes that the C ABI of a four-bit cache takes on trust."""
+    _require_here(away)
     if v_cache.shape != k_cache.shape or v_cache.element_size() != 1:
         raise ValueError("k_cache and v_cache must have one shape and be one-byte tensors")
     if q is not None and (q.dim() != 3 or q.shape[2] != head_dim):
@@ -289,7 +297,7 @@ def pa_reshape_and_cache(key, value, slot_mapping, k_cache, v_cache, cache_dtype
                          k_scale=1.0, v_scale=1.0, device_error=None,
                          stream=None) -> None:
     """Write rows ``key/value [T, kv_heads, head_dim]`` into the caches."""
-    _require_all("key value slot_mapping k_cache v_cache", key, value, slot_mapping, k_cache, v_cache)
+    away = _require_all("key value slot_mapping k_cache v_cache", key, value, slot_mapping, k_cache, v_cache)
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
     H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
@@ -297,7 +305,7 @@ def pa_reshape_and_cache(key, value, slot_mapping, k_cache, v_cache, cache_dtype
     if src is None or key.dtype != value.dtype:
         raise ValueError("key/value must be float16 or bfloat16 of one dtype")
     if code == PA_FP4:
-        _check_fp4(d, k_cache, v_cache)
+        _check_fp4(away, d, k_cache, v_cache)
         if key.shape != value.shape or key.numel() != slot_mapping.numel() * H * d:
             raise ValueError(f"key/value must be [T, {H}, {d}] with one slot a row")
     lib = load_library()
@@ -313,7 +321,7 @@ def pa_gather_cache(key, value, slot_mapping, k_cache, v_cache, cache_dtype=None
     """Read rows ``key/value [T, kv_heads, head_dim]`` (float16 or bfloat16,
     written) back from the caches: the values that the stored rows of
     ``slot_mapping`` stand for, zero where it is -1."""
-    _require_all("key value slot_mapping k_cache v_cache", key, value, slot_mapping, k_cache, v_cache)
+    _require_here(_require_all("key value slot_mapping k_cache v_cache", key, value, slot_mapping, k_cache, v_cache))
     if slot_mapping.dtype != torch.int64:
         raise ValueError("slot_mapping must be int64")
     H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
@@ -343,7 +351,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len: int
               partition_size: int = 0, workspace=None, device_error=None,
               stream=None) -> torch.Tensor:
     """Paged decode attention; writes ``out [S, Hq, head_dim]`` (q's dtype)."""
-    _require_all("out q k_cache v_cache block_tables seq_lens", out, q, k_cache, v_cache, block_tables, seq_lens)
+    away = _require_all("out q k_cache v_cache block_tables seq_lens", out, q, k_cache, v_cache, block_tables, seq_lens)
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("block_tables and seq_lens must be int32")
     H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
@@ -352,7 +360,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len: int
     if qcode not in (PA_F16, PA_BF16) or out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("q/out must be float16 or bfloat16 [S, Hq, head_dim] of one dtype")
     if code == PA_FP4:
-        _check_fp4(d, k_cache, v_cache, q, S, block_tables, seq_lens)
+        _check_fp4(away, d, k_cache, v_cache, q, S, block_tables, seq_lens)
     if workspace is None:
         need = pa_decode_workspace_size(S, Hq, H, D, max_seq_len, partition_size)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
@@ -373,7 +381,7 @@ def pa_prefill(out, q, cu_q_lens, k_cache, v_cache, block_tables, seq_lens, max_
     s's are rows cu_q_lens[s]..cu_q_lens[s+1]-1, its last tokens) over the
     paged cache; writes ``out`` like ``q``.  One-byte caches take their
     ``cache_dtype`` and scales as in ``pa_decode``."""
-    _require_all("out q cu_q_lens k_cache v_cache block_tables seq_lens", out, q, cu_q_lens, k_cache, v_cache, block_tables, seq_lens)
+    away = _require_all("out q cu_q_lens k_cache v_cache block_tables seq_lens", out, q, cu_q_lens, k_cache, v_cache, block_tables, seq_lens)
     if cu_q_lens.dtype != torch.int32 or block_tables.dtype != torch.int32 or \
             seq_lens.dtype != torch.int32:
         raise ValueError("cu_q_lens, block_tables and seq_lens must be int32")
@@ -382,7 +390,7 @@ def pa_prefill(out, q, cu_q_lens, k_cache, v_cache, block_tables, seq_lens, max_
     if out.dtype != q.dtype or out.shape != q.shape or q.dim() != 3:
         raise ValueError("q/out must be [T, Hq, head_dim] of one dtype")
     if code == PA_FP4:
-        _check_fp4(d, k_cache, v_cache, q, cu_q_lens.numel() - 1, block_tables, seq_lens)
+        _check_fp4(away, d, k_cache, v_cache, q, cu_q_lens.numel() - 1, block_tables, seq_lens)
     lib = load_library()
     _check(lib.pa_prefill(out.data_ptr(), q.data_ptr(), -1 if qcode is None else qcode, q.shape[0],
                           cu_q_lens.data_ptr(), cu_q_lens.numel() - 1, q.shape[1], int(max_q_len),
@@ -405,11 +413,11 @@ def pa_decode_static_scratch(out, q, k_cache, v_cache, block_tables, seq_lens,
     scratch than that are rejected (use ``pa_decode`` with a workspace).
     Calls that overlap on the GPU race on the shared scratch.
     """
-    _require_all("out q k_cache v_cache block_tables seq_lens", out, q, k_cache, v_cache, block_tables, seq_lens)
+    away = _require_all("out q k_cache v_cache block_tables seq_lens", out, q, k_cache, v_cache, block_tables, seq_lens)
     H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
     S, Hq, D = q.shape
     if code == PA_FP4:
-        _check_fp4(d, k_cache, v_cache, q, S, block_tables, seq_lens)
+        _check_fp4(away, d, k_cache, v_cache, q, S, block_tables, seq_lens)
     need = pa_decode_workspace_size(S, Hq, H, D, max_seq_len, partition_size)
     if need > STATIC_SCRATCH_BYTES:
         raise PaError(f"pa_decode_static_scratch: these sizes need {need} bytes of scratch, "
@@ -434,10 +442,12 @@ def pa_selftest_wait_timeout(device_error, stream=None) -> None:
 def pa_copy_blocks(k_cache, v_cache, block_mapping, cache_dtype=None, device_error=None,
                    stream=None) -> None:
     """For each (src, dst) row of ``block_mapping [n, 2]`` copy block src to dst."""
-    _require_all("k_cache v_cache block_mapping", k_cache, v_cache, block_mapping)
+    away = _require_all("k_cache v_cache block_mapping", k_cache, v_cache, block_mapping)
     if block_mapping.dtype != torch.int64:
         raise ValueError("block_mapping must be int64")
-    ref = _describe(k_cache, cache_dtype, 1.0, 1.0)[3]
+    _, _, code, ref = _describe(k_cache, cache_dtype, 1.0, 1.0)
+    if code == PA_FP4:
+        _require_here(away)
     lib = load_library()
     _check(lib.pa_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ref,
                               block_mapping.data_ptr(), block_mapping.shape[0],
@@ -450,7 +460,7 @@ def pa_compact_blocks(k_cache, v_cache, block_mapping, block_tables, seq_lens, c
     """Move block src to dst for each row of ``block_mapping [n, 2]`` (int64,
     ascending by src, as ``PrefixCache.compact`` gives them) and rename the
     blocks in ``block_tables`` (int32 ``[S, width]``, in place)."""
-    _require_all("k_cache v_cache block_mapping block_tables seq_lens", k_cache, v_cache, block_mapping, block_tables, seq_lens)
+    _require_here(_require_all("k_cache v_cache block_mapping block_tables seq_lens", k_cache, v_cache, block_mapping, block_tables, seq_lens))
     if block_mapping.dtype != torch.int64 or block_mapping.dim() != 2 or block_mapping.shape[1] != 2:
         raise ValueError("block_mapping must be int64 [n, 2]")
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
@@ -478,7 +488,7 @@ def pa_swap_blocks(k_cache, v_cache, host_k, host_v, block_mapping, direction: s
     device block src -> host block dst; "in": host block src -> device
     block dst.
     """
-    _require_all("k_cache v_cache block_mapping", k_cache, v_cache, block_mapping)
+    away = _require_all("k_cache v_cache block_mapping", k_cache, v_cache, block_mapping)
     for t, n in ((host_k, "host_k"), (host_v, "host_v")):
         if not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
             raise ValueError(f"{n} must be contiguous, in page-locked host memory or on the device")
@@ -491,7 +501,9 @@ def pa_swap_blocks(k_cache, v_cache, host_k, host_v, block_mapping, direction: s
     codes = {"out": PA_SWAP_OUT, "in": PA_SWAP_IN}
     if direction not in codes:
         raise ValueError('direction must be "out" or "in"')
-    ref = _describe(k_cache, cache_dtype, 1.0, 1.0)[3]
+    _, _, code, ref = _describe(k_cache, cache_dtype, 1.0, 1.0)
+    if code == PA_FP4:
+        _require_here(away)
     lib = load_library()
     _check(lib.pa_swap_blocks(k_cache.data_ptr(), v_cache.data_ptr(), ref,
                               host_k.data_ptr(), host_v.data_ptr(), host_k.shape[0],
