@@ -254,6 +254,8 @@ def _describe(k_cache, cache_dtype, k_scale, v_scale):
         heads = k_cache.shape[1] if k_cache.dim() == 4 else -1
         k_scale, kp = _scale_arg(k_scale, heads, "k_scale")
         v_scale, vp = _scale_arg(v_scale, heads, "v_scale")
+    if type(cache_dtype) is not str and cache_dtype is not None:
+        cache_dtype = _cache_code(k_cache.dtype, cache_dtype)  # (a key that cannot change its value)
     return _described(k_cache.shape, k_cache.dtype, cache_dtype, k_scale, v_scale, kp, vp)
 
 

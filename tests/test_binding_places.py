@@ -96,3 +96,15 @@ def test_four_bit_caches_and_newer_calls_stay_on_the_current_device(lib, call, c
         with pytest.raises(ValueError, match="must be on the current device"):
             _calls(cache_dtype, 1)[call]()
         assert lib.calls == [call]
+
+
+def test_a_type_given_as_a_number_object_is_read_at_every_call():
+    """Codes held in arrays: not hashable, or changed between two calls."""
+    import numpy as np
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.uint8)
+    code = lambda x: pa._describe(k, x, 1.0, 1.0)[2]           # noqa: E731
+    assert code("int8") == code(pa.PA_INT8) == code(np.int64(pa.PA_INT8)) == code(np.array(pa.PA_INT8)) == pa.PA_INT8
+    t = torch.tensor(pa.PA_INT8)
+    assert code(t) == pa.PA_INT8
+    t.fill_(pa.PA_FP8_E4M3)
+    assert code(t) == pa.PA_FP8_E4M3
