@@ -76,11 +76,18 @@ constexpr int kUnit = 64;       // tokens of a unit of work
 // at 1, 189 at 3, 181 at 5, 183 at 8; 64 of 512..4096, 32/32 heads: 118, 116,
 // 116, 118.
 constexpr int kPairCost = 5;
-// Pairs of up to 512 tokens are dealt out whole, and there is no merge.  Whole
-// against cut, us of one call in a graph: 1 x 8 pairs of up to 256 tokens
-// 4.8 / 7.6, of 512 6.2 / 6.8, of 1024 9.3 / 7.0; 4 x 4 of 512 8.2 / 6.8;
-// 16 x 8 of 512 9.7 / 10.7; 64 x 8 of 512 14.0 / 14.9; 128 x 8 of 2048
-// 59.0 / 54.9.
+// Pairs of up to 512 tokens are dealt out whole, and there is no merge; with
+// no more pairs than CTAs fit the GPU, each has a CTA of its own.  Whole
+// against cut, us of one call among others in a graph (64/8 heads; the
+// pairs' lengths from an eighth of the bound to the bound):
+//   pairs        8          64         256        608        768        2048
+//   of 256    4.5/8.0    4.7/10.0   5.9/10.9   8.5/14.1  13.0/16.1  24.8/24.7
+//   of 512    6.1/7.3    6.3/10.4   7.8/12.8  11.8/16.6  17.1/19.5  33.5/33.5
+//   of 1024   9.2/7.5    9.4/11.6  11.7/15.1  18.2/22.2  24.1/25.4  51.3/53.5
+// and with 1024 tokens each 9.2/7.6, 9.6/13.5, 12.3/17.9, 20.4/23.1,
+// 36.5/34.6, 72.7/73.1: a bound of 512 never loses, one of 1024 does with few
+// pairs and with a little more than a CTA's worth each.  16 pairs of 32/32
+// heads and up to 512 tokens: 5.4/6.9.
 constexpr int kWholeTokens = 512;
 constexpr float kLazy = 8.f;    // rescale when the maximum grows by more (base 2)
 constexpr float kFar = 0x1p24f;
@@ -667,59 +674,69 @@ __global__ void __launch_bounds__(kFpThreads, kCtas) decode_fp4_kernel(const __g
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int S = p.num_seqs, H = p.num_kv_heads;
 
-  // ---- the share: units of all pairs before each thread's run of sequences
+  // ---- the share: its first piece is KV head h of sequence s from unit off
+  // of the pair, the number-th of the pair's pieces; left: units not yet taken
   // (lengths only: this kernel may start before the one ahead of it ends)
   auto length = [&](int s) { return clamp_length(__ldg(p.seq_lens + s), p.len_cap); };
-  auto units = [&](int L) { return kPairCost + max(1, (L + kUnit - 1) / kUnit); };  // of a pair
-  const int per = (S + kFpThreads - 1) / kFpThreads;
-  const int a0 = min(S, tid * per), a1 = min(S, a0 + per);
-  long long mine = 0;
-  for (int s = a0; s < a1; ++s) {
+  auto checked_length = [&](int s, bool reports) {
     const int L = __ldg(p.seq_lens + s);
-    if (blockIdx.x == 0 && (L < 0 || L > p.len_cap)) record_error(p.err, kErrSeqLen);
-    mine += static_cast<long long>(units(clamp_length(L, p.len_cap))) * H;
-  }
-  long long upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  if (lane == 31) s_wsum[warp] = upto;
-  __syncthreads();
-  long long U = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_wsum[w];
-    U += s_wsum[w];
-  }
-  before += upto - mine;  // units before this thread's run
+    if (reports && (L < 0 || L > p.len_cap)) record_error(p.err, kErrSeqLen);
+    return clamp_length(L, p.len_cap);
+  };
+  auto units = [&](int L) { return kPairCost + max(1, (L + kUnit - 1) / kUnit); };  // of a pair
   const bool cut = p.cut != 0;
-  // (cut pairs' pieces have their places when a share is two partitions long)
-  long long n = gridDim.x;
-  if (cut) n = min(n, max(1ll, U * kUnit / (2ll * p.partition_size)));
   const long long b = blockIdx.x;
-  const long long u0 = b * U / n;
-  long long left = b < n ? (b + 1) * U / n - u0 : 0;  // units of the share not yet taken
-  // the sequence that holds unit u0, and the units before it
-  if (left > 0 && before <= u0 && u0 < before + mine) {
-    long long base = before;
-    int s = a0;
-    for (; s < a1 - 1; ++s) {
-      const long long x = static_cast<long long>(units(length(s))) * H;
-      if (u0 < base + x) break;
-      base += x;
+  int s, h, off = 0, number = 0;
+  long long left;
+  if (!cut && gridDim.x == static_cast<long long>(S) * H) {  // a CTA for each pair
+    s = blockIdx.x / H;
+    h = blockIdx.x - s * H;
+    left = units(checked_length(s, h == 0 && tid == 0));
+    grid_dependency_wait();
+    launch_dependents();
+  } else {
+    // units of all pairs before each thread's run of sequences
+    const int per = (S + kFpThreads - 1) / kFpThreads;
+    const int a0 = min(S, tid * per), a1 = min(S, a0 + per);
+    long long mine = 0;
+    for (int i = a0; i < a1; ++i) mine += static_cast<long long>(units(checked_length(i, blockIdx.x == 0))) * H;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
     }
-    s_first = s;
-    s_base = base;
-  }
-  __syncthreads();
-  grid_dependency_wait();
-  launch_dependents();  // the merge (or the next call, which waits for this grid before it writes)
-  if (left <= 0) return;
-  // the next piece: KV head h of sequence s from unit off of the pair
-  int s = s_first, h, off, number = 0;  // number: the first piece's among its pair's
-  {
+    if (lane == 31) s_wsum[warp] = upto;
+    __syncthreads();
+    long long U = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_wsum[w];
+      U += s_wsum[w];
+    }
+    before += upto - mine;  // units before this thread's run
+    // (cut pairs' pieces have their places when a share is two partitions long)
+    long long n = gridDim.x;
+    if (cut) n = min(n, max(1ll, U * kUnit / (2ll * p.partition_size)));
+    const long long u0 = b * U / n;
+    left = b < n ? (b + 1) * U / n - u0 : 0;
+    // the sequence that holds unit u0, and the units before it
+    if (left > 0 && before <= u0 && u0 < before + mine) {
+      long long base = before;
+      int i = a0;
+      for (; i < a1 - 1; ++i) {
+        const long long x = static_cast<long long>(units(length(i))) * H;
+        if (u0 < base + x) break;
+        base += x;
+      }
+      s_first = i;
+      s_base = base;
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    launch_dependents();  // the merge (or the next call, which waits for this grid before it writes)
+    if (left <= 0) return;
+    s = s_first;
     const int nu = units(length(s));
     const long long rel = u0 - s_base;
     h = static_cast<int>(rel / nu);

@@ -25,3 +25,27 @@ def test_tiny_queries_beside_ordinary_ones(op, q, scale, G, D):
     g = c.device()
     getattr(c, op)(g)
     c.check(g, f"{q} {scale}")
+
+
+@pytest.mark.parametrize("G,D", [(1, 128), (8, 64)])
+@pytest.mark.parametrize("S,H", [(1, 1), (4, 4), (303, 2), (304, 2), (305, 2), (609, 1)])
+def test_short_pairs_around_one_a_cta(S, H, G, D):
+    """Pairs dealt out whole: fewer, as many and more than four CTAs an SM on
+    152 SMs, empty sequences among them, a bad length reported."""
+    rng = np.random.default_rng(S)
+    lens = rng.integers(0, 513, S)
+    lens[0], lens[-1] = 512, rng.integers(0, 3)
+    c = Case(75, lens.tolist(), G, H, D, 16, "bf16", per_head=True)
+    g = c.device()
+    c.decode(g, max_len=512)
+    c.check(g, f"{S} x {H}")
+    want = g.out.clone()
+    for bad in (-1, 10 ** 6):
+        g.err.zero_()
+        g.lens[-1] = bad
+        g.table[-1].fill_(0)
+        g.out.fill_(float("nan"))
+        c.decode(g, max_len=512)
+        torch.cuda.synchronize()
+        assert int(g.err.item()) == 3
+        assert torch.equal(g.out[:-1], want[:-1])
