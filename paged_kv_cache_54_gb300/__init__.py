@@ -22,7 +22,11 @@ Caches are ``[num_blocks, kv_heads, block_size, head_dim]`` tensors of the
 stored type (FP8 and INT8 also as uint8).  A four-bit cache
 (``cache_dtype="fp4"``) is a uint8 tensor ``[num_blocks, kv_heads, block_size,
 head_dim * 9 / 16]``: ``fp4_cache_shape`` gives it; the last two dimensions
-together are one tile of codes and scales (laid out in ``include/pa.h``).
+together are one tile of codes and scales (laid out in ``include/pa.h``).  Its
+decode reads every sequence's blocks for itself; where sequences share most of
+their blocks (a common prefix, beams) the other types' decode reads a shared
+block once for several of them and is faster.  Calls on a four-bit cache, the
+read-back and the compaction take tensors of the current device only.
 
 PyTorch supplies the device memory and the stream; there is no CPU or
 PyTorch fallback: if ``libpa.so`` is missing, every call raises.

@@ -22,9 +22,10 @@
 // stream through a two-slot ring of its own in shared memory: 16-byte
 // asynchronous copies bring the next step, which may be the next piece's
 // first, while one is worked on, so warps wait for one another only where a
-// piece ends.  (Tensor copies of whole tiles would be fewer instructions, but
-// an SM starts about one per 100 clocks, and a tile of 16 tokens is 1152
-// bytes: half the HBM rate.)
+// piece ends.  (Bulk copies of whole tiles would be fewer instructions, but a
+// thread starts one per 113 ns and an SM one per 30: with four threads at it,
+// and nothing else to do, tiles of 1152 bytes (16 tokens at head_dim 128) come
+// at 5.9 TB/s and tiles of 576 at 3.0, the ring's copies at 6.6.)
 //
 // A step is two slices of 16 tokens; a slice is two small products on
 // mma.sync m16n8k16 with fp16 operands and fp32 accumulation, S^T = K Q^T and
@@ -38,7 +39,10 @@
 // copies alone take 184 us, the products alone 188 us, at 285 warp
 // instructions a slice, 62% of the issue slots.  32/32 heads of 64 sequences
 // of 512..4096 tokens (681 MB): 116 us, 5.9 TB/s.  128 sequences of 256..32768
-// tokens, 64/8 heads (1.0 GB): 181 us, 5.5 TB/s.  The rest of a short call:
+// tokens, 64/8 heads (1.0 GB): 181 us, 5.5 TB/s.  head_dim 64 spreads the
+// softmax and the shuffles of a slice over half the bytes: the same two
+// batches take 76 us (340 MB, 4.5 TB/s) and 119 us (502 MB, 4.2 TB/s), with
+// blocks of 8 81 and 122, of 32 73 and 115.  The rest of a short call:
 // 1.2 us until the shares are known, 5 us until the first steps have landed,
 // 1 us a piece for its end, 4 us for the merge.  Five CTAs an SM (96
 // registers) took 3% longer than four, two CTAs of eight warps 8%, copies two

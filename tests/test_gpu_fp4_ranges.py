@@ -49,3 +49,18 @@ def test_short_pairs_around_one_a_cta(S, H, G, D):
         torch.cuda.synchronize()
         assert int(g.err.item()) == 3
         assert torch.equal(g.out[:-1], want[:-1])
+
+
+@pytest.mark.parametrize("op", ["decode", "prefill"])
+@pytest.mark.parametrize("G,H,D,bs", [(1, 8, 128, 16), (2, 4, 64, 8), (8, 2, 128, 32)])
+def test_sequences_that_share_blocks(op, G, H, D, bs):
+    """A prefix of 2048 tokens that 24 sequences share, their tails of any
+    length behind it."""
+    rng = np.random.default_rng(77)
+    lens = (2048 + rng.integers(0, 700, 24)).tolist()
+    lens[3] = 2048
+    c = Case(77, lens, G, H, D, bs, "bf16", per_head=True, new=None if op == "decode" else [3] * 24)
+    c.table[:, :2048 // bs] = c.table[0, :2048 // bs]
+    g = c.device()
+    getattr(c, op)(g)
+    c.check(g)
