@@ -163,8 +163,8 @@ typedef struct {
  * For PA_FP4 caches the same quotients y are taken 16 dimensions at a time:
  * the group's scale g is the largest |y| that is not NaN, divided by 6 and
  * rounded to the nearest e4m3 value (ties to even, at most 448); a code is
- * the e2m1 value nearest to y / g (ties to even, saturated to +-6), 0 for
- * NaN, and 0 throughout when g is 0.
+ * the e2m1 value nearest to y / g (ties to even, saturated to +-6; a zero
+ * keeps its sign), 0 for NaN, and 0 throughout when g is 0.
  * Slots must be distinct among the call's tokens.  A slot >= num_blocks *
  * block_size is skipped and reported as device error 2.
  */
