@@ -18,7 +18,17 @@
  *   pa_compact_blocks     whole-block moves that draw a pool's live blocks
  *                         together, with the block tables renamed to match;
  *   pa_swap_blocks        whole-block moves between the device caches and a
- *                         pool in host memory (swap-out / swap-in).
+ *                         pool in host memory (swap-out / swap-in);
+ *   pa_decode_weights     pa_decode that also adds every token's attention
+ *                         weight to an accumulator;
+ *   pa_evict_tokens       each head's most heavily weighted and most recent
+ *                         tokens moved to new blocks;
+ *   pa_latent_write       write new tokens into a latent cache (one vector a
+ *                         token, shared by all heads);
+ *   pa_latent_decode      absorbed attention of one or a few new tokens a
+ *                         sequence over a latent cache;
+ *   pa_latent_prefill     expanded causal attention of several new tokens
+ *                         per sequence over a latent cache.
  *
  * and one host-side structure that hands out the blocks:
  *
@@ -429,6 +439,152 @@ PA_API pa_status pa_swap_blocks(void *k_cache, void *v_cache, const pa_cache_des
                                 void *host_k, void *host_v, int64_t host_num_blocks,
                                 const int64_t *block_mapping, int32_t num_pairs,
                                 int32_t direction, int *device_error, pa_stream_t stream);
+
+/*
+ * pa_decode_weights — pa_decode, and every token's attention weight added to
+ * an accumulator: what an eviction goes by.  The pages free whole requests
+ * or blocks ([P1] §5.1); weighing single tokens has no counterpart there.
+ *
+ *   out, q, caches, block_tables, seq_lens, max_seq_len, scale   as in
+ *                  pa_decode.
+ *   weights_out    device float32 [num_seqs, kv_heads, weights_width],
+ *                  weights_width >= max_seq_len: for i < L_s
+ *                    weights_out[s, h, i] = decay * weights_in[s, h, i] +
+ *                                           sum over h's G query heads of softmax_i
+ *                  and entries from L_s on are left as they were.
+ *   weights_in     the same shape; may be weights_out itself (an accumulator
+ *                  updated in place).  NULL counts as zeros.
+ *   decay          what the earlier weights are multiplied by (1 keeps them).
+ *   workspace      at least pa_decode_weights_workspace_size(...) bytes,
+ *                  256-byte aligned, uninitialised; calls sharing one must be
+ *                  stream-ordered.
+ * A sequence without tokens gives zeros, and so does a row none of whose
+ * scores is above -infinity (its weights are zero too).
+ * Supported set: num_q_heads / kv_heads in {1, 2, 4, 8}; 16-bit, FP8 and INT8
+ * caches (not PA_FP4); q as in pa_decode.  With a one-byte cache the products
+ * run on fp16 operands: a bf16 q is rounded to fp16 after scaling each row by
+ * a power of two, as for a PA_FP4 cache in pa_decode.
+ * Device checks: a length outside [0, min(max_seq_len, max_blocks_per_seq *
+ * block_size)] counts as 0 and is reported as error 3; a block id out of range
+ * reads block 0 instead and is reported as error 1.
+ */
+PA_API size_t pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t max_seq_len);
+PA_API pa_status pa_decode_weights(void *out, float *weights_out, const float *weights_in, float decay,
+                                   int64_t weights_width, const void *q, int32_t q_dtype, int32_t num_seqs,
+                                   int32_t num_q_heads, const void *k_cache, const void *v_cache,
+                                   const pa_cache_desc *cache, const int32_t *block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len,
+                                   float scale, void *workspace, size_t workspace_bytes, int *device_error,
+                                   pa_stream_t stream);
+
+/*
+ * pa_evict_tokens — bring sequences down to `budget` tokens a head: of the
+ * L_s tokens of every (sequence, KV head) the last `recent` stay, and of the
+ * others those of largest weight (the lower index where weights are equal; a
+ * NaN counts as less than any number).  Each head keeps its own tokens;
+ * every head of a sequence keeps min(L_s, budget).
+ *
+ *   block_tables, seq_lens   the sequences as they are (only read).
+ *   weights        device float32 [num_seqs, kv_heads, weights_width], as
+ *                  pa_decode_weights accumulates them; L_s <= weights_width.
+ *   new_tables     device int32 [num_seqs, max_new_blocks]: the blocks that
+ *                  the kept tokens move to, ceil(min(L_s, budget) /
+ *                  block_size) for each sequence, max_new_blocks * block_size
+ *                  >= budget.  They must be distinct and none of the blocks
+ *                  that block_tables names: the old blocks may be shared with
+ *                  other sequences and are left as they were.
+ *   new_lens       device int32 [num_seqs], written: min(L_s, budget).
+ *   new_weights    device float32 [num_seqs, kv_heads, new_width], new_width
+ *                  >= budget, written: the kept tokens' weights, in their new
+ *                  order; entries from new_lens[s] on are left as they were.
+ *                  Must not overlap `weights`.
+ * Kept tokens stay in their order, so the last `recent` of the moved sequence
+ * are the last ones again.  new_tables, new_lens and new_weights then stand
+ * in for block_tables, seq_lens and weights; freeing the old blocks is the
+ * caller's.
+ *   workspace      at least pa_evict_workspace_size(...) bytes, 16-byte
+ *                  aligned, uninitialised; calls sharing one must be
+ *                  stream-ordered.
+ * Requires 0 <= recent <= budget, budget >= 1.  Supported set: 16-bit, FP8 and
+ * INT8 caches (not PA_FP4); num_blocks * block_size < 2^31.
+ * Device checks: a length outside [0, min(weights_width, max_blocks_per_seq *
+ * block_size)] moves nothing of the sequence, sets its new length to 0 and is
+ * reported as error 3; a block id out of range leaves its tokens' rows
+ * unmoved and is reported as error 1.
+ */
+PA_API size_t pa_evict_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t budget);
+PA_API pa_status pa_evict_tokens(void *k_cache, void *v_cache, const pa_cache_desc *cache,
+                                 const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                 const int32_t *seq_lens, const float *weights, int64_t weights_width,
+                                 const int32_t *new_tables, int32_t max_new_blocks, int32_t *new_lens,
+                                 float *new_weights, int64_t new_width, int32_t budget, int32_t recent,
+                                 void *workspace, size_t workspace_bytes, int *device_error, pa_stream_t stream);
+
+/*
+ * Latent cache — a paged cache of one vector a token that all heads share:
+ * keys and values are linear functions of it, so it is what has to be kept.
+ * The pages have no counterpart (their caches hold every head's K and V); the
+ * definitions below are the textbook attention with
+ *   key of head h   = (Uk_h c, r),   value of head h = Uv_h c
+ * for a token's latent vector c (latent_dim) and rotary key r (rope_dim).
+ * Layout: [num_blocks, block_size, latent_dim + rope_dim] elements of dtype,
+ * row-major, c before r; slots and block tables as everywhere in this header.
+ * Its blocks hold block_size * 576 elements, as those of a cache of kv_heads 9,
+ * head_dim 64: pa_copy_blocks, pa_swap_blocks and pa_compact_blocks move the
+ * blocks of two layers' latent caches under such a pa_cache_desc.
+ * Supported set: latent_dim 512, rope_dim 64; PA_F16 and PA_BF16; block_size
+ * in {8, 16, 32}; num_blocks * block_size < 2^31.
+ */
+typedef struct {
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t latent_dim;
+  int32_t rope_dim;
+  int32_t dtype;  /* pa_dtype */
+} pa_latent_desc;
+
+/*
+ * pa_latent_write — write T new tokens into a latent cache.
+ *   latent, rope   device, rows of latent_dim and rope_dim elements of
+ *                  src_dtype (the cache's), latent_stride and rope_stride
+ *                  elements apart (multiples of 8; both may be views of one
+ *                  projection's output).
+ *   slot_mapping   device int64 [num_tokens]; -1 marks a padding row that is
+ *                  skipped.  Any other slot outside the cache is skipped and
+ *                  reported as device error 2.  Slots must be distinct.
+ */
+PA_API pa_status pa_latent_write(const void *latent, const void *rope, int64_t latent_stride, int64_t rope_stride,
+                                 int32_t src_dtype, const int64_t *slot_mapping, int32_t num_tokens, void *cache,
+                                 const pa_latent_desc *desc, int *device_error, pa_stream_t stream);
+
+/*
+ * pa_latent_decode — absorbed attention of the last new_tokens tokens of
+ * every sequence (1 for plain decoding; more to verify drafted tokens).
+ * The caller folds Uk_h into the query and applies Uv_h to the result:
+ *   out[s, j, h, :] = sum_{i < L_s - (new_tokens - 1 - j)}
+ *       softmax_i(scale * <q[s, j, h, :], row_i>) row_i[: latent_dim]
+ * with row_i token i's row of the cache.  A row that sees no token, or none
+ * with a score above -infinity, gives zeros.
+ *   out            device [num_seqs, new_tokens, num_heads, latent_dim]
+ *   q              device [num_seqs, new_tokens, num_heads, latent_dim +
+ *                  rope_dim] (the query times Uk_h, then its rotary part)
+ *   block_tables, max_blocks_per_seq, seq_lens, max_seq_len   as in pa_decode;
+ *                  seq_lens includes the new tokens.
+ *   workspace      at least pa_latent_decode_workspace_size(...) bytes,
+ *                  256-byte aligned, uninitialised; calls sharing one must be
+ *                  stream-ordered.
+ * Any number of heads.  Device checks: a length outside [0, min(max_seq_len,
+ * max_blocks_per_seq * block_size)] counts as 0 and is reported as error 3; a
+ * block id out of range reads block 0 instead and is reported as error 1; a
+ * stalled pipeline reports error 4.
+ */
+PA_API size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t new_tokens, int32_t num_heads);
+PA_API pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t new_tokens,
+                                  int32_t num_heads, const void *cache, const pa_latent_desc *desc,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                  int32_t max_seq_len, float scale, void *workspace, size_t workspace_bytes,
+                                  int *device_error, pa_stream_t stream);
 
 /*
  * Prefix cache (host) — the block pool behind the block tables, with

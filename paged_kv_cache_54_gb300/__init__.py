@@ -14,7 +14,16 @@ functions carry the C ABI's names:
                            together, with the block tables renamed
     pa_swap_blocks         whole-block moves between the device caches and
                            a pool in page-locked host memory
-    pa_decode_workspace_size
+    pa_decode_weights      paged decode attention that also adds every token's
+                           attention weight to an accumulator
+    pa_evict_tokens        each head's most heavily weighted and most recent
+                           tokens moved to new blocks
+    pa_latent_write        write new tokens into a latent cache (one vector a
+                           token, shared by all heads)
+    pa_latent_decode       absorbed attention of one or a few new tokens a
+                           sequence over a latent cache
+    pa_decode_workspace_size, pa_decode_weights_workspace_size,
+    pa_evict_workspace_size, pa_latent_decode_workspace_size
     PrefixCache            the host block pool with prefix caching
                            (pa_prefix_cache_*)
 
@@ -27,6 +36,11 @@ decode reads every sequence's blocks for itself; where sequences share most of
 their blocks (a common prefix, beams) the other types' decode reads a shared
 block once for several of them and is faster.  Calls on a four-bit cache, the
 read-back and the compaction take tensors of the current device only.
+
+A latent cache is a float16 or bfloat16 tensor ``[num_blocks, block_size,
+576]`` (``latent_cache_shape``): a token's latent vector of 512 and its rotary
+key of 64.  The latent calls, ``pa_decode_weights`` and ``pa_evict_tokens``
+take tensors of the current device only.
 
 PyTorch supplies the device memory and the stream; there is no CPU or
 PyTorch fallback: if ``libpa.so`` is missing, every call raises.
@@ -54,6 +68,8 @@ if hasattr(torch, "float8_e5m2"):
 
 EXPORTED = ("pa_reshape_and_cache", "pa_gather_cache", "pa_decode_workspace_size", "pa_decode",
             "pa_prefill", "pa_decode_static_scratch", "pa_copy_blocks", "pa_compact_blocks",
+            "pa_decode_weights_workspace_size", "pa_decode_weights", "pa_evict_workspace_size",
+            "pa_evict_tokens", "pa_latent_write", "pa_latent_decode_workspace_size", "pa_latent_decode",
             "pa_swap_blocks", "pa_prefix_cache_fork_sequence", "pa_prefix_cache_compact",
             "pa_status_string", "pa_last_cuda_error", "pa_selftest_wait_timeout",
             "pa_prefix_cache_create", "pa_prefix_cache_destroy", "pa_prefix_cache_add_sequence",
@@ -62,6 +78,7 @@ EXPORTED = ("pa_reshape_and_cache", "pa_gather_cache", "pa_decode_workspace_size
             "pa_prefix_cache_get_stats", "pa_prefix_cache_free_order", "pa_prefix_cache_ref_count")
 PA_ERR_OUT_OF_BLOCKS = 5
 PA_SWAP_OUT, PA_SWAP_IN = 0, 1
+LATENT_DIM, ROPE_DIM = 512, 64    # of a latent cache's rows
 STATIC_SCRATCH_BYTES = 16 << 20   # PA_DECODE_STATIC_SCRATCH_BYTES
 
 
@@ -71,6 +88,10 @@ class PaCacheDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float), ("k_head_scales", ctypes.c_void_p),
                 ("v_head_scales", ctypes.c_void_p)]
+
+
+class PaLatentDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_blocks", "block_size", "latent_dim", "rope_dim", "dtype")]
 
 
 class PaError(RuntimeError):
@@ -125,6 +146,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                    vp, i32, i32, vp, vp]
     lib.pa_swap_blocks.restype = ctypes.c_int
     i64, i32p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int32)
+    f32, size = ctypes.c_float, ctypes.c_size_t
+    cache_p, latent_p = ctypes.POINTER(PaCacheDesc), ctypes.POINTER(PaLatentDesc)
+    lib.pa_decode_weights_workspace_size.argtypes = [i32] * 5
+    lib.pa_evict_workspace_size.argtypes = [i32] * 3
+    lib.pa_latent_decode_workspace_size.argtypes = [i32] * 3
+    for name in ("pa_decode_weights_workspace_size", "pa_evict_workspace_size", "pa_latent_decode_workspace_size"):
+        getattr(lib, name).restype = size
+    lib.pa_decode_weights.argtypes = [vp, vp, vp, f32, i64, vp, i32, i32, i32, vp, vp, cache_p, vp, i32, vp, i32,
+                                      f32, vp, size, vp, vp]
+    lib.pa_evict_tokens.argtypes = [vp, vp, cache_p, vp, i32, i32, vp, vp, i64, vp, i32, vp, vp, i64, i32, i32, vp,
+                                    size, vp, vp]
+    lib.pa_latent_write.argtypes = [vp, vp, i64, i64, i32, vp, i32, vp, latent_p, vp, vp]
+    lib.pa_latent_decode.argtypes = [vp, vp, i32, i32, i32, i32, vp, latent_p, vp, i32, vp, i32, f32, vp, size, vp, vp]
+    for name in ("pa_decode_weights", "pa_evict_tokens", "pa_latent_write", "pa_latent_decode"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.pa_prefix_cache_create.argtypes = [i32, i32, vp]
     lib.pa_prefix_cache_create.restype = vp
     lib.pa_prefix_cache_destroy.argtypes = [vp]
@@ -516,6 +552,181 @@ def pa_swap_blocks(k_cache, v_cache, host_k, host_v, block_mapping, direction: s
                               block_mapping.data_ptr(), block_mapping.shape[0], codes[direction],
                               _ptr(device_error), _stream(stream)),
            "pa_swap_blocks")
+
+
+def _check_tables(block_tables, seq_lens, seqs: int) -> None:
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise ValueError("block_tables and seq_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != seqs or seq_lens.shape != (seqs,):
+        raise ValueError(f"block_tables must be [{seqs}, width] and seq_lens [{seqs}]")
+
+
+def _check_here(names: str, *tensors) -> None:
+    """Contiguous CUDA tensors, all on the current device."""
+    _require_here(_require_all(names, *tensors))
+
+
+def _check_error_word(device_error) -> None:
+    if device_error is not None:
+        _check_here("device_error", device_error)
+        if device_error.dtype != torch.int32 or device_error.numel() < 1:
+            raise ValueError("device_error must be int32")
+
+
+def _workspace_of(need: int) -> torch.Tensor:
+    return torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+
+
+def pa_decode_weights_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                     max_seq_len: int) -> int:
+    return int(load_library().pa_decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                               max_seq_len))
+
+
+def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len: int, scale: float,
+                      weights_in=None, decay: float = 1.0, cache_dtype=None, k_scale=1.0, v_scale=1.0, workspace=None,
+                      device_error=None, stream=None) -> torch.Tensor:
+    """``pa_decode``, and ``weights_out[s, h, i] = decay * weights_in[s, h, i]
+    + sum of softmax_i over h's query heads`` for i < seq_lens[s] (float32
+    ``[S, kv_heads, width]``).  ``weights_in`` may be ``weights_out`` (an
+    accumulator updated in place) or None (zeros).  Not for four-bit caches."""
+    _check_here("out weights_out q k_cache v_cache block_tables seq_lens", out, weights_out, q, k_cache, v_cache,
+                block_tables, seq_lens)
+    _check_error_word(device_error)
+    if q.dim() != 3:
+        raise ValueError("q/out must be [S, Hq, head_dim]")
+    S, Hq, D = q.shape
+    _check_tables(block_tables, seq_lens, S)
+    H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
+    qcode = _TORCH_CODES.get(q.dtype)
+    if qcode not in (PA_F16, PA_BF16) or out.dtype != q.dtype or out.shape != q.shape or D != d:
+        raise ValueError(f"q/out must be float16 or bfloat16 [S, Hq, {d}] of one dtype")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and dtype")
+    if weights_out.dtype != torch.float32 or weights_out.dim() != 3 or weights_out.shape[:2] != (S, H):
+        raise ValueError(f"weights_out must be float32 [{S}, {H}, width]")
+    if weights_in is not None:
+        _check_here("weights_in", weights_in)
+        if weights_in.dtype != torch.float32 or weights_in.shape != weights_out.shape:
+            raise ValueError("weights_in must be like weights_out")
+    if workspace is None:
+        workspace = _workspace_of(pa_decode_weights_workspace_size(S, Hq, H, D, max_seq_len))
+    else:
+        _check_here("workspace", workspace)
+    _check(load_library().pa_decode_weights(
+        out.data_ptr(), weights_out.data_ptr(), _ptr(weights_in), decay, weights_out.shape[2], q.data_ptr(), qcode, S,
+        Hq, k_cache.data_ptr(), v_cache.data_ptr(), ref, block_tables.data_ptr(), block_tables.shape[1],
+        seq_lens.data_ptr(), max_seq_len, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _ptr(device_error), _stream(stream)), "pa_decode_weights")
+    return out
+
+
+def pa_evict_workspace_size(num_seqs: int, num_kv_heads: int, budget: int) -> int:
+    return int(load_library().pa_evict_workspace_size(num_seqs, num_kv_heads, budget))
+
+
+def pa_evict_tokens(k_cache, v_cache, block_tables, seq_lens, weights, new_tables, new_lens, new_weights, budget: int,
+                    recent: int, cache_dtype=None, workspace=None, device_error=None, stream=None) -> None:
+    """Keep ``min(seq_lens[s], budget)`` tokens of every sequence and KV head:
+    the last ``recent`` and, of the others, those of largest ``weights``
+    (float32 ``[S, kv_heads, width]``), in their order.  Their rows are copied
+    to the blocks of ``new_tables`` (int32 ``[S, width]``, distinct, none of them
+    in ``block_tables``), their weights to ``new_weights``, and the new lengths
+    to ``new_lens``.  Not for four-bit caches."""
+    _check_here("k_cache v_cache block_tables seq_lens weights new_tables new_lens new_weights", k_cache, v_cache,
+                block_tables, seq_lens, weights, new_tables, new_lens, new_weights)
+    _check_error_word(device_error)
+    H, _, _, ref = _describe(k_cache, cache_dtype, 1.0, 1.0)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and dtype")
+    S = seq_lens.numel()
+    _check_tables(block_tables, seq_lens, S)
+    if new_tables.dtype != torch.int32 or new_tables.dim() != 2 or new_tables.shape[0] != S:
+        raise ValueError(f"new_tables must be int32 [{S}, width]")
+    if new_lens.dtype != torch.int32 or new_lens.shape != (S,):
+        raise ValueError(f"new_lens must be int32 [{S}]")
+    for t, n in ((weights, "weights"), (new_weights, "new_weights")):
+        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[:2] != (S, H):
+            raise ValueError(f"{n} must be float32 [{S}, {H}, width]")
+    if workspace is None:
+        workspace = _workspace_of(pa_evict_workspace_size(S, H, budget))
+    else:
+        _check_here("workspace", workspace)
+    _check(load_library().pa_evict_tokens(
+        k_cache.data_ptr(), v_cache.data_ptr(), ref, block_tables.data_ptr(), S, max(1, block_tables.shape[1]),
+        seq_lens.data_ptr(), weights.data_ptr(), weights.shape[2], new_tables.data_ptr(), max(1, new_tables.shape[1]),
+        new_lens.data_ptr(), new_weights.data_ptr(), new_weights.shape[2], budget, recent, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _ptr(device_error), _stream(stream)), "pa_evict_tokens")
+
+
+def latent_cache_shape(num_blocks: int, block_size: int):
+    """Shape of a latent cache's tensor."""
+    return num_blocks, block_size, LATENT_DIM + ROPE_DIM
+
+
+@functools.lru_cache(maxsize=256)
+def _described_latent(shape, dtype):
+    if len(shape) != 3 or dtype not in (torch.float16, torch.bfloat16) or shape[2] != LATENT_DIM + ROPE_DIM:
+        raise ValueError(f"a latent cache is float16 or bfloat16 [num_blocks, block_size, {LATENT_DIM + ROPE_DIM}]")
+    code = _TORCH_CODES[dtype]
+    return code, ctypes.byref(PaLatentDesc(shape[0], shape[1], LATENT_DIM, ROPE_DIM, code))
+
+
+def _require_rows(t, name: str, width: int, dtype) -> None:
+    """A CUDA tensor [T, width] on the current device whose rows are dense."""
+    if not t.is_cuda or t.get_device() != _current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if t.dim() != 2 or t.shape[1] != width or t.dtype != dtype or (t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{name} must be {dtype} [T, {width}] with dense rows")
+
+
+def pa_latent_write(latent, rope, slot_mapping, cache, device_error=None, stream=None) -> None:
+    """Write rows ``latent [T, 512]`` and ``rope [T, 64]`` into the latent
+    cache.  Both may be views whose rows lie a multiple of 8 elements apart."""
+    _check_here("slot_mapping cache", slot_mapping, cache)
+    _check_error_word(device_error)
+    code, ref = _described_latent(cache.shape, cache.dtype)
+    _require_rows(latent, "latent", LATENT_DIM, cache.dtype)
+    _require_rows(rope, "rope", ROPE_DIM, cache.dtype)
+    n = slot_mapping.numel()
+    if slot_mapping.dtype != torch.int64 or latent.shape[0] != n or rope.shape[0] != n:
+        raise ValueError("slot_mapping must be int64 with one slot a row")
+    # (one row's stride says nothing)
+    strides = (latent.stride(0), rope.stride(0)) if n > 1 else (LATENT_DIM, ROPE_DIM)
+    _check(load_library().pa_latent_write(latent.data_ptr(), rope.data_ptr(), *strides, code, slot_mapping.data_ptr(),
+                                          n, cache.data_ptr(), ref, _ptr(device_error), _stream(stream)),
+           "pa_latent_write")
+
+
+def pa_latent_decode_workspace_size(num_seqs: int, new_tokens: int, num_heads: int) -> int:
+    return int(load_library().pa_latent_decode_workspace_size(num_seqs, new_tokens, num_heads))
+
+
+def pa_latent_decode(out, q, cache, block_tables, seq_lens, max_seq_len: int, scale: float, workspace=None,
+                     device_error=None, stream=None) -> torch.Tensor:
+    """Absorbed attention of each sequence's last tokens over a latent cache:
+    ``q [S, H, 576]`` (one token) or ``[S, n, H, 576]`` against the rows, and
+    ``out`` (512 in place of 576) their weighted sums."""
+    _check_here("out q cache block_tables seq_lens", out, q, cache, block_tables, seq_lens)
+    _check_error_word(device_error)
+    code, ref = _described_latent(cache.shape, cache.dtype)
+    if q.dim() not in (3, 4) or q.shape[-1] != LATENT_DIM + ROPE_DIM or q.dtype != cache.dtype:
+        raise ValueError(f"q must be [S, H, {LATENT_DIM + ROPE_DIM}] or [S, n, H, {LATENT_DIM + ROPE_DIM}] of the "
+                         "cache's dtype")
+    if out.shape != q.shape[:-1] + (LATENT_DIM,) or out.dtype != q.dtype:
+        raise ValueError(f"out must be like q with {LATENT_DIM} in place of its last size")
+    S, n, H = q.shape[0], q.shape[1] if q.dim() == 4 else 1, q.shape[-2]
+    _check_tables(block_tables, seq_lens, S)
+    if workspace is None:
+        workspace = _workspace_of(pa_latent_decode_workspace_size(S, n, H))
+    else:
+        _check_here("workspace", workspace)
+    _check(load_library().pa_latent_decode(out.data_ptr(), q.data_ptr(), code, S, n, H, cache.data_ptr(), ref,
+                                           block_tables.data_ptr(), max(1, block_tables.shape[1]),
+                                           seq_lens.data_ptr(), max_seq_len, scale, workspace.data_ptr(),
+                                           workspace.numel() * workspace.element_size(), _ptr(device_error),
+                                           _stream(stream)), "pa_latent_decode")
+    return out
 
 
 class PrefixCache:

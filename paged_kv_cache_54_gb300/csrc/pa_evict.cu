@@ -1,0 +1,301 @@
+// pa_evict_tokens: each head's most heavily weighted tokens, and the most
+// recent ones, moved to new blocks in their order.
+//
+// Select: one block a (sequence, KV head) pair.  The weights become unsigned
+// keys that ascend with them; a radix selection in three digits (11, 11 and
+// 10 bits) finds the k-th largest key T and how many of the keys equal to it
+// are kept.  Counts of two passes then place every kept token, in order:
+// keys above T, the first of those equal to it, and the recent ones.
+// Move: rows copied from their old slots to their new ones, every warp with
+// several rows of K and of V in flight.
+#include <limits.h>
+
+#include "pa_common.cuh"
+#include "pa_host.h"
+
+namespace pa {
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMoveThreads = 256;
+
+struct EvictParams {
+  const uint8_t *k, *v;
+  uint8_t *k_out, *v_out;  // the same caches
+  const int32_t *tables, *lens, *new_tables;
+  int32_t *new_lens;
+  const float *weights;
+  float *new_weights;
+  int32_t *list;  // [pairs, budget] source slots
+  int num_seqs, kv_heads, num_blocks, bs_shift, max_blocks, max_new_blocks, budget, recent, limit;
+  long long width, new_width;
+  int *err;
+};
+
+// Ascends with the weight; a NaN lies below every number, -0 equals 0.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t b = __float_as_uint(w + 0.f);  // (-0 + 0 = 0)
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// Exclusive sum of x over the block's threads; `tmp` holds kSelWarps ints.
+__device__ __forceinline__ int block_exclusive(int x, int *tmp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int z = __shfl_up_sync(0xffffffffu, y, d);
+    if (lane >= d) y += z;
+  }
+  __syncthreads();
+  if (lane == 31) tmp[warp] = y;
+  __syncthreads();
+  if (warp == 0) {
+    int v = tmp[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += z;
+    }
+    tmp[lane] = v;
+  }
+  __syncthreads();
+  return y - x + (warp > 0 ? tmp[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+  __shared__ int hist[kBins];
+  __shared__ int tmp[kSelWarps];
+  __shared__ int above[kSelWarps], equal[kSelWarps];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need;
+  launch_dependents();
+  const long long pair = blockIdx.x;
+  const int s = static_cast<int>(pair / p.kv_heads), h = static_cast<int>(pair % p.kv_heads);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int L = __ldg(p.lens + s);
+  if (L < 0 || L > p.limit) {
+    if (tid == 0) {
+      record_error(p.err, kErrSeqLen);
+      if (h == 0) p.new_lens[s] = 0;
+    }
+    return;
+  }
+  const int B = min(L, p.budget), r = min(p.recent, B), n = L - r, k = B - r;
+  if (tid == 0 && h == 0) p.new_lens[s] = B;
+  const float *w = p.weights + pair * p.width;
+  uint32_t prefix = 0;
+  int need = k;  // of the keys that share the prefix, how many are kept
+  if (k > 0 && k < n) {
+    for (int level = 0; level < 3; ++level) {
+      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
+      const uint32_t mask = level == 0 ? 0u : level == 1 ? 0xffe00000u : 0xfffffc00u;
+      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t key = weight_key(__ldg(w + i));
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1);
+      }
+      __syncthreads();
+      // bins from the top: thread t has bins kBins - 1 - 2t and the one below
+      const int b0 = kBins - 1 - 2 * tid;
+      const int c0 = hist[b0], c1 = hist[b0 - 1];
+      const int before = block_exclusive(c0 + c1, tmp);
+      if (before < need && need <= before + c0 + c1) {
+        const bool low = need > before + c0;
+        s_prefix = prefix | (static_cast<uint32_t>(low ? b0 - 1 : b0) << shift);
+        s_need = need - before - (low ? c0 : 0);
+      }
+      __syncthreads();
+      prefix = s_prefix;
+      need = s_need;
+    }
+  }
+  const bool all = k >= n;  // every candidate is kept
+  // each warp places a run of tokens
+  const int run = (L + kSelThreads - 1) / kSelThreads * 32;
+  const int i0 = min(warp * run, L), i1 = min(i0 + run, L);
+  int gt = 0, eq = 0;
+  for (int i = i0 + lane; i < i1; i += 32) {
+    const uint32_t key = i < n ? weight_key(__ldg(w + i)) : 0u;
+    const bool sure = i >= n || all || (k > 0 && key > prefix);
+    gt += sure;
+    eq += !sure && k > 0 && key == prefix;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    above[warp] = gt;
+    equal[warp] = eq;
+  }
+  __syncthreads();
+  int gt0 = 0, eq0 = 0;
+  for (int i = 0; i < warp; ++i) {
+    gt0 += above[i];
+    eq0 += equal[i];
+  }
+  int at = gt0 + min(eq0, need);
+  const int32_t *table = p.tables + static_cast<size_t>(s) * p.max_blocks;
+  const int bmask = (1 << p.bs_shift) - 1;
+  for (int base = i0; base < i1; base += 32) {
+    const int i = base + lane;
+    const bool in = i < i1;
+    const float x = in ? __ldg(w + i) : 0.f;
+    const uint32_t key = in && i < n ? weight_key(x) : 0u;
+    const bool sure = in && (i >= n || all || (k > 0 && key > prefix));
+    const bool tie = in && !sure && k > 0 && key == prefix;
+    const unsigned ties = __ballot_sync(0xffffffffu, tie), below = (1u << lane) - 1u;
+    const bool keep = sure || (tie && eq0 + __popc(ties & below) < need);
+    const unsigned kept = __ballot_sync(0xffffffffu, keep);
+    if (keep) {
+      const int to = at + __popc(kept & below);
+      const int block = __ldg(table + (i >> p.bs_shift));
+      int slot = -1;
+      if (block >= 0 && block < p.num_blocks) slot = (block << p.bs_shift) + (i & bmask);
+      else record_error(p.err, kErrBlockIndex);
+      p.list[pair * p.budget + to] = slot;
+      p.new_weights[pair * p.new_width + to] = x;
+    }
+    at += __popc(kept);
+    eq0 += __popc(ties);
+  }
+}
+
+template <int ROW>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, long long items, int per_pair) {
+  constexpr int LPR = ROW / 16;  // lanes of a row
+  constexpr int RPI = 32 / LPR;  // rows of one access
+  constexpr int U = 4;           // accesses of K and of V in flight
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  const long long warps = static_cast<long long>(gridDim.x) * (kMoveThreads / 32);
+  const int bmask = (1 << p.bs_shift) - 1;
+  const int col = (lane % LPR) * 16;
+  for (long long i = blockIdx.x * static_cast<long long>(kMoveThreads / 32) + (threadIdx.x >> 5); i < items; i += warps) {
+    const long long pair = i / per_pair;
+    const int first = static_cast<int>(i - pair * per_pair) * (U * RPI) + lane / LPR;
+    const int s = static_cast<int>(pair / p.kv_heads), h = static_cast<int>(pair - static_cast<long long>(s) * p.kv_heads);
+    const int count = p.new_lens[s];
+    size_t from[U], to[U];
+    bool ok[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = first + u * RPI;
+      ok[u] = row < count;
+      from[u] = to[u] = 0;
+      if (ok[u]) {
+        const int slot = p.list[pair * p.budget + row];
+        const int block = __ldg(p.new_tables + static_cast<size_t>(s) * p.max_new_blocks + (row >> p.bs_shift));
+        ok[u] = slot >= 0;
+        if (block < 0 || block >= p.num_blocks) {
+          record_error(p.err, kErrBlockIndex);
+          ok[u] = false;
+        }
+        from[u] = ((static_cast<size_t>(slot >> p.bs_shift) * p.kv_heads + h) << p.bs_shift) + (slot & bmask);
+        to[u] = ((static_cast<size_t>(block) * p.kv_heads + h) << p.bs_shift) + (row & bmask);
+      }
+    }
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (ok[u]) {
+        a[u] = *reinterpret_cast<const uint4 *>(p.k + from[u] * ROW + col);
+        b[u] = *reinterpret_cast<const uint4 *>(p.v + from[u] * ROW + col);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (ok[u]) {
+        *reinterpret_cast<uint4 *>(p.k_out + to[u] * ROW + col) = a[u];
+        *reinterpret_cast<uint4 *>(p.v_out + to[u] * ROW + col) = b[u];
+      }
+  }
+}
+
+template <int ROW>
+pa_status launch_move(const EvictParams &p, cudaStream_t stream) {
+  constexpr int rows = 4 * (32 / (ROW / 16));  // of a warp's step
+  const int per_pair = (p.budget + rows - 1) / rows;
+  const long long items = static_cast<long long>(p.num_seqs) * p.kv_heads * per_pair;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid_for(items * 32, kMoveThreads));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_move_kernel<ROW>, p, items, per_pair);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_evict_workspace_size(int32_t num_seqs, int32_t num_kv_heads, int32_t budget) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || budget < 0) return 0;
+  return static_cast<size_t>(num_seqs) * num_kv_heads * budget * sizeof(int32_t) + 256;
+}
+
+extern "C" pa_status pa_evict_tokens(void *k_cache, void *v_cache, const pa_cache_desc *cache,
+                                     const int32_t *block_tables, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                     const int32_t *seq_lens, const float *weights, int64_t weights_width,
+                                     const int32_t *new_tables, int32_t max_new_blocks, int32_t *new_lens,
+                                     float *new_weights, int64_t new_width, int32_t budget, int32_t recent,
+                                     void *workspace, size_t workspace_bytes, int *device_error, pa_stream_t stream) {
+  if (!valid_cache_desc(cache) || num_seqs < 0 || max_blocks_per_seq <= 0 || max_new_blocks <= 0 || budget <= 0 ||
+      recent < 0 || recent > budget || weights_width < 0 || new_width < budget)
+    return PA_ERR_INVALID;
+  if (static_cast<long long>(max_new_blocks) * cache->block_size < budget) return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !seq_lens || !weights || !new_tables || !new_lens || !new_weights ||
+      !workspace)
+    return PA_ERR_INVALID;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(seq_lens) |
+        reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(new_tables) |
+        reinterpret_cast<uintptr_t>(new_lens) | reinterpret_cast<uintptr_t>(new_weights)) & 3u))
+    return PA_ERR_INVALID;
+  if (!supported_cache_shape(cache) || cache->dtype == PA_FP4) return PA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(cache->num_blocks) * cache->block_size > INT_MAX) return PA_ERR_UNSUPPORTED;  // 32-bit slots
+  if (static_cast<long long>(num_seqs) * cache->kv_heads > INT_MAX) return PA_ERR_UNSUPPORTED;             // the grid
+  if (workspace_bytes < pa_evict_workspace_size(num_seqs, cache->kv_heads, budget)) return PA_ERR_INVALID;
+  EvictParams p{};
+  p.k = p.k_out = static_cast<uint8_t *>(k_cache);
+  p.v = p.v_out = static_cast<uint8_t *>(v_cache);
+  p.tables = block_tables;
+  p.lens = seq_lens;
+  p.new_tables = new_tables;
+  p.new_lens = new_lens;
+  p.weights = weights;
+  p.new_weights = new_weights;
+  p.list = static_cast<int32_t *>(workspace);
+  p.num_seqs = num_seqs;
+  p.kv_heads = cache->kv_heads;
+  p.num_blocks = cache->num_blocks;
+  p.bs_shift = cache->block_size == 8 ? 3 : cache->block_size == 16 ? 4 : 5;
+  p.max_blocks = max_blocks_per_seq;
+  p.max_new_blocks = max_new_blocks;
+  p.budget = budget;
+  p.recent = recent;
+  long long limit = static_cast<long long>(max_blocks_per_seq) * cache->block_size;
+  if (weights_width < limit) limit = weights_width;
+  p.limit = limit < INT_MAX - kSelThreads ? static_cast<int>(limit) : INT_MAX - kSelThreads;
+  p.width = weights_width;
+  p.new_width = new_width;
+  p.err = device_error;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  evict_select_kernel<<<num_seqs * cache->kv_heads, kSelThreads, 0, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  switch (cache->head_dim * (cache->dtype >= PA_FP8_E4M3 ? 1 : 2)) {
+    case 64: return launch_move<64>(p, st);
+    case 128: return launch_move<128>(p, st);
+  }
+  return launch_move<256>(p, st);
+}

@@ -1,0 +1,751 @@
+// pa_latent_decode: absorbed attention of one or a few new tokens a sequence
+// over the latent paged cache.
+//
+// All heads share the token's 576-element row: a (token, head) row r of
+// queries gives
+//   x[r, i] = scale <q_r, row_i>,   out[r] = sum_i softmax_i(x[r, i]) row_i[:512],
+// so a sequence's n * H query rows read its cache once.  Per token of the
+// cache that is 1152 bytes and 2176 operations a row.
+//
+// The products run on the 5th-generation tensor cores with the tokens and the
+// latent dimensions as rows and the query rows as columns, so that the tile's
+// cost follows the number of query rows:
+//   S^T = K Q^T    M = 64 tokens, N = 16, 32 or 64 query rows, K = 576
+//   O^T += V^T P^T M = 128 dimensions (four times), N query rows, K = 64 tokens
+// K and V are one tile of shared memory: rows of nine 128-byte columns, in
+// groups of 8 rows of 8-row x 128-byte swizzled atoms.  The first product
+// reads it token-major, the second dimension-major.  O^T takes 4 N columns of
+// tensor memory, S^T 2 N.
+//
+// A block takes N query rows and an equal share of all sequences' 64-token
+// tiles (pa_shares.cuh).  Warps:
+//   0..3  softmax: a thread owns a token, its registers the query rows.  The
+//         maximum of a query row is kept for all threads in shared memory and
+//         raised only when a score passes it by 2^8, so that almost every
+//         tile needs one vote of the block instead of a reduction over
+//         tokens; the total weights stay per thread until a sequence ends.
+//   4     TMA: q, then the tiles, a 16-token slot at a time
+//   5, 6  issue the S^T and O^T products
+#include <limits.h>
+#include <math.h>
+
+#include "pa_common.cuh"
+#include "pa_latent.h"
+#include "pa_shares.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kTile = 64;              // tokens of a tile
+constexpr int kSlots = 4;              // 16-token slots of a tile, freed one by one
+constexpr int kStages = 2;
+constexpr int kCols = kLatentRow / 64; // 128-byte columns of a row
+constexpr int kAtom = 1024;
+constexpr int kGroup = kCols * kAtom;  // 8 rows
+constexpr int kTileBytes = kTile / 8 * kGroup;
+constexpr int kDims = 128;             // of one O^T product
+constexpr int kBlocksO = kLatentDim / kDims;
+constexpr int kTmaWarp = 4, kQkWarp = 5;  // and 6: O^T
+constexpr int kThreads = 7 * 32;
+constexpr int kSoftmaxThreads = 128;
+constexpr int kMaxWorkers = 152;       // shares of one row tile, at most; sizes the workspace
+constexpr int kMinTiles = 2;           // a smaller share only adds joining
+constexpr float kLazy = 8.f;
+
+struct LatentParams {
+  CUtensorMap tmap_q;  // [S n H, 576] in boxes of {64, N}
+  CUtensorMap tmap_c;  // the cache, boxes of a slot (or of a block of 8)
+  void *out;
+  const int32_t *tables, *lens;
+  float2 *part_ml;     // [row tiles, workers, 2, N]
+  float *part_o;       // [row tiles, workers, 2, N, 512]
+  long long *prefix;   // [S + 1] tiles before sequence s
+  int num_seqs, new_tokens, heads, rows, row_tiles, num_blocks, bs_shift, max_blocks, limit;
+  float scale_log2;
+  int *err;
+};
+
+template <int N>
+struct Layout {
+  static constexpr int Q_COL = N * 128;  // a 128-byte column of the query rows
+  static constexpr int Q_OFF = 2048;
+  static constexpr int P_OFF = Q_OFF + kCols * Q_COL;
+  static constexpr int P_BYTES = kTile * 128;
+  static constexpr int KV_OFF = P_OFF + P_BYTES;
+  static constexpr int SMEM = KV_OFF + kStages * kTileBytes;
+  static constexpr uint32_t TMEM_S = kBlocksO * N;  // columns: O^T, then two S^T
+  static constexpr uint32_t TMEM_COLS = N == 16 ? 128 : N == 32 ? 256 : 512;
+};
+
+struct Header {
+  uint64_t kv_full[kStages], kv_empty[kStages][kSlots];
+  uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, q_empty, fin[2];
+  uint32_t tmem;
+  int abort;
+  alignas(16) float m[64];  // the query rows' maxima (base 2), read four at a time
+  float top[4][64];   // a warp's maxima, then its total weights
+  int see[64];        // tokens a query row sees
+};
+static_assert(sizeof(Header) <= 2048, "the header's place");
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return y != 0;
+}
+
+// NCOL consecutive columns of the warp's lanes
+template <int NCOL>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[NCOL]) {
+  if constexpr (NCOL >= 32) {
+#pragma unroll
+    for (int c = 0; c < NCOL; c += 32) {
+      uint32_t r[32];
+      tc_ld32(taddr + c, r);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[c + j] = __uint_as_float(r[j]);
+    }
+  } else {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+  }
+}
+template <int NCOL>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[NCOL]) {
+  if constexpr (NCOL >= 32) {
+#pragma unroll
+    for (int c = 0; c < NCOL; c += 32) {
+      uint32_t r[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(v[c + j]);
+      tc_st32(taddr + c, r);
+    }
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+  }
+}
+
+__host__ __device__ inline long long worker_count(long long tiles, long long most) {
+  const long long n = (tiles + kMinTiles - 1) / kMinTiles;
+  return n < most ? n : most;
+}
+
+// One piece of a block's share: tiles [t0, t1) of a sequence, in order.
+struct Walk {
+  long long u, end, first;
+  int s, L, tiles, t0, t1;
+  __device__ __forceinline__ bool next(const LatentParams &p) {
+    while (u < end) {
+      L = checked_len(p.lens, s, p.limit, nullptr);
+      tiles = (L + kTile - 1) / kTile;
+      if (tiles == 0) {
+        ++s;
+        continue;
+      }
+      t0 = static_cast<int>(u - first);
+      t1 = end - u < tiles - t0 ? t0 + static_cast<int>(end - u) : tiles;
+      return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ void advance() {
+    u += t1 - t0;
+    if (t1 == tiles) {
+      first += tiles;
+      ++s;
+    }
+  }
+};
+
+template <int DT, int N>
+__global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid_constant__ LatentParams p,
+                                                                    int max_workers) {
+  using Lay = Layout<N>;
+  constexpr int AB = DT == kF16 ? 0 : 1;
+  constexpr uint32_t IDESC_QK = umma_idesc_f16(AB, kTile, N, false);
+  constexpr uint32_t IDESC_PV = umma_idesc_f16(AB, kDims, N, true) | (1u << 15);  // (A dimension-major too)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // (the scan is over before the weights' buffer is first written)
+  ShareScan<128> &scan = *reinterpret_cast<ShareScan<128> *>(smem + Lay::P_OFF);
+  static_assert(sizeof(ShareScan<128>) <= Lay::P_BYTES, "the scan's place");
+  Header &hdr = *reinterpret_cast<Header *>(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rt = blockIdx.x % p.row_tiles, w = blockIdx.x / p.row_tiles;
+  launch_dependents();
+  auto tiles_of = [&](int s) -> long long { return (checked_len(p.lens, s, p.limit, p.err) + kTile - 1) / kTile; };
+  // (the scan's barriers take the whole block; threads past its 128 only keep step)
+  {
+    const int n = ShareScan<128>::run(p.num_seqs), t = threadIdx.x;
+    long long sum = 0;
+    if (t < 128) {
+      for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) sum += tiles_of(s);
+      scan.base[t + 1] = sum;
+      if (t == 0) scan.base[0] = 0;
+    }
+    __syncthreads();
+    for (int d = 1; d < 128; d <<= 1) {
+      const long long x = t < 128 && t >= d ? scan.base[t + 1 - d] : 0;
+      __syncthreads();
+      if (t < 128) scan.base[t + 1] += x;
+      __syncthreads();
+    }
+    if (blockIdx.x == 0 && t < 128) {
+      long long at = scan.base[t];
+      for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
+        p.prefix[s] = at;
+        at += tiles_of(s);
+      }
+      if (t == 0) p.prefix[p.num_seqs] = scan.total();
+    }
+  }
+  const long long total = scan.total(), workers = worker_count(total, max_workers);
+  if (w >= workers) return;
+  Walk walk;
+  walk.u = share_begin(w, total, workers);
+  walk.end = share_begin(w + 1, total, workers);
+  if (walk.u >= walk.end) return;
+  walk.s = scan.find(walk.u, p.num_seqs, tiles_of, walk.first);
+  if ((smem_addr(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) record_error(p.err, kErrSmemAlign);
+    return;
+  }
+  volatile int *abort = &hdr.abort;
+  uint8_t *qs = smem + Lay::Q_OFF, *ps = smem + Lay::P_OFF, *kv = smem + Lay::KV_OFF;
+  const int n_rows = min(N, p.rows - rt * N);  // query rows of this tile
+  if (warp == kTmaWarp && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_c)) : "memory");
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&hdr.kv_full[i], 1);
+      for (int j = 0; j < kSlots; ++j) mbar_init(&hdr.kv_empty[i][j], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&hdr.s_full[i], 1);
+      mbar_init(&hdr.s_empty[i], kSoftmaxThreads);
+      mbar_init(&hdr.fin[i], 1);
+    }
+    mbar_init(&hdr.p_full, kSoftmaxThreads);
+    mbar_init(&hdr.pv_done, 1);
+    mbar_init(&hdr.q_full, 1);
+    mbar_init(&hdr.q_empty, 1);
+    hdr.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kQkWarp) tc_alloc(&hdr.tmem, Lay::TMEM_COLS);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = hdr.tmem;
+
+  if (warp < 4) {
+    // ---------------------------------------------------------------- softmax
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int token = lane < 16 ? 16 * warp + lane : INT_MAX / 2;  // M = 64 fills 16 lanes of each warp
+    // a wait that gave up leaves the warp in step with the others, whose
+    // barriers count on it: it goes on without waiting, and nothing is stored
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+      tc_fence_after_sync();
+    };
+    int i = 0;  // tiles so far
+    for (int seg = 0; walk.next(p); ++seg) {
+      float l[N];
+#pragma unroll
+      for (int h = 0; h < N; ++h) l[h] = 0.f;
+      softmax_sync();  // the last piece's maxima and totals have been read
+      for (int h = threadIdx.x; h < N; h += kSoftmaxThreads) {
+        hdr.m[h] = -INFINITY;
+        hdr.see[h] = h < n_rows ? walk.L - (p.new_tokens - 1 - (rt * N + h) / p.heads) : 0;
+      }
+      softmax_sync();
+      // tokens that every query row sees
+      const int all_see = n_rows < N ? 0 : walk.L - (p.new_tokens - 1 - rt * N / p.heads);
+      for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
+        wait(&hdr.s_full[i & 1], (i >> 1) & 1);
+        float x[N];
+        tmem_load<N>(tlane + Lay::TMEM_S + (i & 1) * N, x);
+        tc_fence_before_sync();
+        mbar_arrive(&hdr.s_empty[i & 1]);
+        const int key = tile * kTile + token;
+        if ((tile + 1) * kTile > all_see) {
+#pragma unroll
+          for (int h = 0; h < N; ++h) x[h] = key < hdr.see[h] ? x[h] * p.scale_log2 : -INFINITY;
+        } else {
+#pragma unroll
+          for (int h = 0; h < N; ++h) x[h] = lane < 16 ? x[h] * p.scale_log2 : -INFINITY;
+        }
+        float over = -INFINITY;
+        const float4 *m4 = reinterpret_cast<const float4 *>(hdr.m);
+#pragma unroll
+        for (int h = 0; h < N; h += 4) {
+          const float4 m = m4[h / 4];
+          over = fmaxf(over, fmaxf(fmaxf(x[h] - m.x, x[h + 1] - m.y), fmaxf(x[h + 2] - m.z, x[h + 3] - m.w)));
+        }
+        // (a first tile's maxima are -inf, and inf - inf of no score at all is a NaN, which is not over)
+        if (softmax_any(over > kLazy)) {
+          // raise the maxima: each warp's over its tokens, then all four
+#pragma unroll
+          for (int h = 0; h < N; ++h) {
+            const int b = __float_as_int(x[h] == x[h] ? x[h] : -INFINITY);
+            const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+            if (lane == 0) hdr.top[warp][h] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+          }
+          softmax_sync();
+          float f[N];
+#pragma unroll
+          for (int h = 0; h < N; ++h) {
+            const float was = hdr.m[h];
+            const float top = fmaxf(fmaxf(hdr.top[0][h], hdr.top[1][h]), fmaxf(hdr.top[2][h], hdr.top[3][h]));
+            f[h] = top > was + kLazy ? exp2_fast(was - top) : 1.f;
+            l[h] *= f[h];
+          }
+          softmax_sync();
+          for (int h = threadIdx.x; h < N; h += kSoftmaxThreads) {
+            const float was = hdr.m[h];
+            const float top = fmaxf(fmaxf(hdr.top[0][h], hdr.top[1][h]), fmaxf(hdr.top[2][h], hdr.top[3][h]));
+            if (top > was + kLazy) hdr.m[h] = top;
+          }
+          softmax_sync();
+          if (tile > walk.t0) {  // O^T holds the tiles before
+            wait(&hdr.pv_done, (i - 1) & 1);
+#pragma unroll 1
+            for (int b = 0; b < kBlocksO; ++b) {
+              float o[N];
+              tmem_load<N>(tlane + b * N, o);
+#pragma unroll
+              for (int h = 0; h < N; ++h) o[h] *= f[h];
+              tmem_store<N>(tlane + b * N, o);
+            }
+          }
+        }
+        // weights, rounded to the operand type (half a step each)
+        uint32_t pw[N / 2];
+#pragma unroll
+        for (int h = 0; h < N; h += 4) {
+          float4 m = m4[h / 4];
+          m.x = m.x == -INFINITY ? 0.f : m.x;
+          m.y = m.y == -INFINITY ? 0.f : m.y;
+          m.z = m.z == -INFINITY ? 0.f : m.z;
+          m.w = m.w == -INFINITY ? 0.f : m.w;
+          const float a = exp2_fast(x[h] - m.x), b = exp2_fast(x[h + 1] - m.y);
+          const float c = exp2_fast(x[h + 2] - m.z), d = exp2_fast(x[h + 3] - m.w);
+          l[h] += a;
+          l[h + 1] += b;
+          l[h + 2] += c;
+          l[h + 3] += d;
+          pw[h / 2] = pack2_rn<DT>(a, b);
+          pw[h / 2 + 1] = pack2_rn<DT>(c, d);
+        }
+        // the P buffer is free once the last tile's O^T products have completed
+        if (i > 0) wait(&hdr.pv_done, (i - 1) & 1);
+        if (lane < 16) {
+          const int k = 16 * warp + lane;
+          uint8_t *row = ps + k * 128;
+#pragma unroll
+          for (int c = 0; c < N / 8; ++c)
+            *reinterpret_cast<uint4 *>(row + ((c ^ (k & 7)) << 4)) =
+                make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+        }
+        if ((tile + 1) * kTile > walk.L) {
+          // rows behind the sequence's end hold anything: zero them, 0 * NaN would reach O^T
+          uint8_t *vb = kv + (i & 1) * kTileBytes;
+          const int z0 = walk.L - tile * kTile;
+          for (int idx = threadIdx.x; idx < (kTile - z0) * (kLatentDim / 8); idx += kSoftmaxThreads) {
+            const int k = z0 + idx / (kLatentDim / 8), c = idx % (kLatentDim / 8);
+            *reinterpret_cast<uint4 *>(vb + (k >> 3) * kGroup + (c >> 3) * kAtom + (k & 7) * 128 + (c & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        mbar_arrive(&hdr.p_full);
+      }
+      // the piece's sums: total weights over the tokens, then O^T as rows
+      float v[N];
+#pragma unroll
+      for (int h = 0; h < N; ++h) v[h] = l[h];
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {  // halve the columns a lane keeps, four times
+        const int o = 8 >> st, half = N >> (st + 1);
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j)
+          if (j < half) {
+            const float send = upper ? v[j] : v[j + half], keep = upper ? v[j + half] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+      }
+      softmax_sync();
+      if (lane < 16)
+#pragma unroll
+        for (int j = 0; j < N / 16; ++j) hdr.top[warp][lane * (N / 16) + j] = v[j];
+      softmax_sync();
+      wait(&hdr.pv_done, (i - 1) & 1);
+      const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
+      if (!ok) {
+      } else if (whole) {
+        const size_t row0 = static_cast<size_t>(walk.s) * p.rows + rt * N;
+        uint16_t *o16 = static_cast<uint16_t *>(p.out) + row0 * kLatentDim + 32 * warp + lane;
+#pragma unroll 1
+        for (int b = 0; b < kBlocksO; ++b) {
+          float o[N];
+          tmem_load<N>(tlane + b * N, o);
+#pragma unroll
+          for (int h = 0; h < N; ++h) {
+            const float sum = (hdr.top[0][h] + hdr.top[1][h]) + (hdr.top[2][h] + hdr.top[3][h]);
+            const float y = sum == 0.f ? 0.f : o[h] / sum;  // (a row that sees nothing)
+            if (h < n_rows) o16[static_cast<size_t>(h) * kLatentDim + b * kDims] = float_to_storage16<DT>(y);
+          }
+        }
+      } else {
+        const size_t slot = (static_cast<size_t>(rt) * max_workers + w) * 2 + (seg > 0);
+        for (int h = threadIdx.x; h < N; h += kSoftmaxThreads)
+          p.part_ml[slot * N + h] =
+              make_float2(hdr.m[h], (hdr.top[0][h] + hdr.top[1][h]) + (hdr.top[2][h] + hdr.top[3][h]));
+        float *po = p.part_o + slot * N * kLatentDim + 32 * warp + lane;
+#pragma unroll 1
+        for (int b = 0; b < kBlocksO; ++b) {
+          float o[N];
+          tmem_load<N>(tlane + b * N, o);
+#pragma unroll
+          for (int h = 0; h < N; ++h)
+            if (h < n_rows) po[static_cast<size_t>(h) * kLatentDim + b * kDims] = o[h];
+        }
+      }
+      tc_fence_before_sync();
+      walk.advance();
+    }
+    if (!ok) {
+      record_error(p.err, kErrTimeout);
+      *abort = 1;
+    }
+  } else if (warp == kTmaWarp) {
+    // -------------------------------------------------------------------- TMA
+    // a tile is four boxes of 16 tokens (eight of 8 with blocks of 8): lane j
+    // copies box j once its slot is free
+    const int box_sh = p.bs_shift < 4 ? 3 : 4, boxes = kTile >> box_sh;
+    const uint32_t box_bytes = (1u << box_sh) / 8 * kGroup;
+    bool ok = true;
+    int i = 0;
+    for (int seg = 0; ok && walk.next(p); ++seg) {
+      const int32_t *table = p.tables + static_cast<size_t>(walk.s) * p.max_blocks;
+      auto entry = [&](int tile) {  // this lane's block of a tile
+        const int tok = tile * kTile + (lane << box_sh);
+        return lane < boxes && tok < walk.L ? __ldg(table + (tok >> p.bs_shift)) : 0;
+      };
+      int phys = entry(walk.t0);
+      bool free = true;
+      if (lane == 0 && seg > 0) free = mbar_wait(&hdr.q_empty, (seg - 1) & 1, abort);
+      if (!__shfl_sync(0xffffffffu, free, 0)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&hdr.q_full, kCols * Lay::Q_COL);
+        for (int c = 0; c < kCols; ++c)
+          tma_load_2d(qs + c * Lay::Q_COL, &p.tmap_q, c * 64, walk.s * p.rows + rt * N, &hdr.q_full);
+      }
+      for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
+        const int st = i & 1;
+        const int tok = tile * kTile + (lane << box_sh);
+        const int n_box = min(boxes, ((walk.L - tile * kTile) + (1 << box_sh) - 1) >> box_sh);
+        int mine = phys;
+        if (tile + 1 < walk.t1) phys = entry(tile + 1);
+        bool got = true;
+        if (lane < n_box) {
+          if (mine < 0 || mine >= p.num_blocks) {
+            record_error(p.err, kErrBlockIndex);
+            mine = 0;
+          }
+          if (i >= kStages)
+            got = mbar_wait(&hdr.kv_empty[st][(lane << box_sh) >> 4], ((i >> 1) - 1) & 1, abort);
+        } else if (lane < boxes && i >= kStages) {
+          got = mbar_wait(&hdr.kv_empty[st][(lane << box_sh) >> 4], ((i >> 1) - 1) & 1, abort);
+        }
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&hdr.kv_full[st], n_box * box_bytes);
+        __syncwarp();
+        if (lane < n_box)
+          tma_load_4d(kv + st * kTileBytes + lane * box_bytes, &p.tmap_c, 0, 0, 0,
+                      (mine << (p.bs_shift - 3)) + ((tok & ((1 << p.bs_shift) - 1)) >> 3), &hdr.kv_full[st]);
+      }
+      if (ok) walk.advance();
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) {
+      record_error(p.err, kErrTimeout);
+      *abort = 1;
+      // wait, within the limit, for the copies still in flight
+      for (int j = max(0, i - kStages); j < i; ++j) mbar_wait(&hdr.kv_full[j & 1], (j >> 1) & 1, nullptr);
+    }
+  } else if (warp == kQkWarp) {
+    // -------------------------------------------------------------------- S^T
+    if (lane == 0) {
+      bool ok = true;
+      int i = 0;
+      const uint32_t qa = smem_addr(qs), ka = smem_addr(kv);
+      for (int seg = 0; ok && walk.next(p); ++seg) {
+        ok = mbar_wait(&hdr.q_full, seg & 1, abort);
+        for (int tile = walk.t0; ok && tile < walk.t1; ++tile, ++i) {
+          if (i >= 2) ok = mbar_wait(&hdr.s_empty[i & 1], ((i >> 1) - 1) & 1, abort);
+          if (ok) ok = mbar_wait(&hdr.kv_full[i & 1], (i >> 1) & 1, abort);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t a0 = umma_desc_sw128(ka + (i & 1) * kTileBytes, 16, kGroup);
+          const uint64_t b0 = umma_desc_sw128(qa, 16, 1024);
+          const uint32_t d = tmem + Lay::TMEM_S + (i & 1) * N;
+#pragma unroll 4
+          for (int kk = 0; kk < kLatentRow / 16; ++kk) {
+            const uint32_t off = (kk % 4) * 32;
+            tc_mma_f16(d, a0 + (((kk / 4) * kAtom + off) >> 4), b0 + (((kk / 4) * Lay::Q_COL + off) >> 4), IDESC_QK,
+                       kk > 0);
+          }
+          tc_commit(&hdr.s_full[i & 1]);
+        }
+        if (ok) tc_commit(&hdr.q_empty);
+        if (ok) walk.advance();
+      }
+      if (!ok) {
+        record_error(p.err, kErrTimeout);
+        *abort = 1;
+      }
+      tc_commit(&hdr.fin[0]);
+      mbar_wait(&hdr.fin[0], 0, nullptr);
+    }
+  } else {
+    // -------------------------------------------------------------------- O^T
+    if (lane == 0) {
+      bool ok = true;
+      int i = 0;
+      const uint32_t pa_ = smem_addr(ps), ka = smem_addr(kv);
+      while (ok && walk.next(p)) {
+        for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
+          if (!mbar_wait(&hdr.p_full, i & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint64_t a0 = umma_desc_sw128(ka + (i & 1) * kTileBytes, kAtom, kGroup);
+          const uint64_t b0 = umma_desc_sw128(pa_, kAtom, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kSlots; ++kk) {  // 16 tokens: two row groups
+#pragma unroll
+            for (int b = 0; b < kBlocksO; ++b)
+              tc_mma_f16(tmem + b * N, a0 + ((kk * 2 * kGroup + b * 2 * kAtom) >> 4), b0 + ((kk * 2 * 1024) >> 4),
+                         IDESC_PV, (tile > walk.t0 || kk > 0) ? 1u : 0u);
+            tc_commit(&hdr.kv_empty[i & 1][kk]);
+          }
+          tc_commit(&hdr.pv_done);
+        }
+        if (ok) walk.advance();
+      }
+      if (!ok) {
+        record_error(p.err, kErrTimeout);
+        *abort = 1;
+      }
+      tc_commit(&hdr.fin[1]);
+      mbar_wait(&hdr.fin[1], 0, nullptr);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kQkWarp) {
+    tc_fence_after_sync();
+    tc_dealloc(tmem, Lay::TMEM_COLS);
+  }
+}
+
+// Joins the pieces of sequences that several blocks shared, and writes the
+// rows of sequences without tokens.  A block a query row.
+template <int DT, int N>
+__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentParams p, int max_workers) {
+  grid_dependency_wait();
+  const int s = blockIdx.x / p.rows, r = blockIdx.x % p.rows, rt = r / N, h = r % N;
+  const long long u0 = p.prefix[s], u1 = p.prefix[s + 1], total = p.prefix[p.num_seqs];
+  uint16_t *row = static_cast<uint16_t *>(p.out) + static_cast<size_t>(blockIdx.x) * kLatentDim + threadIdx.x * 4;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (u1 > u0) {
+    const long long workers = worker_count(total, max_workers);
+    const long long w0 = share_owner(u0, total, workers), w1 = share_owner(u1 - 1, total, workers);
+    if (w0 == w1) return;  // written whole
+    const size_t base = static_cast<size_t>(rt) * max_workers * 2;
+    // a block's first piece is in its place 0; the sequence is not the first of its first block if that began earlier
+    const int late = share_begin(w0, total, workers) < u0;
+    auto slot = [&](long long w) { return (base + w * 2 + (w == w0 ? late : 0)) * N + h; };
+    float m = -INFINITY, l = 0.f;
+    for (long long w = w0; w <= w1; ++w) m = fmaxf(m, p.part_ml[slot(w)].x);
+    if (m == -INFINITY) m = 0.f;
+#pragma unroll 4
+    for (long long w = w0; w <= w1; ++w) {
+      const size_t at = slot(w);
+      const float2 ml = p.part_ml[at];
+      const float f = exp2_fast(ml.x - m);
+      const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * kLatentDim + threadIdx.x * 4);
+      l += f * ml.y;
+      o.x += f * x.x;
+      o.y += f * x.y;
+      o.z += f * x.z;
+      o.w += f * x.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+    o.x *= inv;
+    o.y *= inv;
+    o.z *= inv;
+    o.w *= inv;
+  }
+  *reinterpret_cast<uint2 *>(row) = make_uint2(pack2_rn<DT>(o.x, o.y), pack2_rn<DT>(o.z, o.w));
+}
+
+int columns_for(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+struct Sizes {
+  size_t prefix, ml, o, total;
+};
+bool sizes_of(int S, int n, int H, Sizes *z) {
+  if (S < 0 || n <= 0 || H <= 0) return false;
+  const long long rows = static_cast<long long>(n) * H;
+  if (rows > INT_MAX / 2 || rows * S > INT_MAX / 2) return false;
+  const int N = columns_for(rows);
+  const size_t slots = static_cast<size_t>((rows + N - 1) / N) * kMaxWorkers * 2;
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  z->prefix = up(8 * (static_cast<size_t>(S) + 1));
+  z->ml = up(slots * N * sizeof(float2));
+  z->o = up(slots * N * kLatentDim * sizeof(float));
+  z->total = z->prefix + z->ml + z->o;
+  return true;
+}
+
+template <int DT, int N>
+pa_status launch(LatentParams &p, const void *q, cudaStream_t stream) {
+  using Lay = Layout<N>;
+  static bool configured[64];  // per device: dynamic shared memory already allowed
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    e = cudaFuncSetAttribute(latent_decode_kernel<DT, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  DeviceInfo info;
+  if (!current_device_info(&info)) return cuda_fail(cudaGetLastError());
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return cuda_fail(cudaErrorInvalidValue);
+  const cuuint64_t dims[2] = {kLatentRow, static_cast<cuuint64_t>(p.num_seqs) * p.rows};
+  const cuuint64_t strides[1] = {kLatentRow * 2};
+  const cuuint32_t box[2] = {64, N}, estr[2] = {1, 1};
+  if (enc(&p.tmap_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(q), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cuda_fail(cudaErrorInvalidValue);
+  p.row_tiles = (p.rows + N - 1) / N;
+  const int sms = info.sm_count < kMaxWorkers ? info.sm_count : kMaxWorkers;
+  const int workers = sms / p.row_tiles > 0 ? sms / p.row_tiles : 1;
+  if (static_cast<long long>(workers) * p.row_tiles > INT_MAX) return PA_ERR_UNSUPPORTED;
+  latent_decode_kernel<DT, N><<<workers * p.row_tiles, kThreads, Lay::SMEM, stream>>>(p, workers);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.rows);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, latent_merge_kernel<DT, N>, p, workers);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+template <int DT>
+pa_status by_rows(LatentParams &p, const void *q, cudaStream_t stream) {
+  switch (columns_for(p.rows)) {
+    case 16: return launch<DT, 16>(p, q, stream);
+    case 32: return launch<DT, 32>(p, q, stream);
+  }
+  return launch<DT, 64>(p, q, stream);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t new_tokens, int32_t num_heads) {
+  Sizes z;
+  return sizes_of(num_seqs, new_tokens, num_heads, &z) ? z.total : 0;
+}
+
+extern "C" pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype, int32_t num_seqs, int32_t new_tokens,
+                                      int32_t num_heads, const void *cache, const pa_latent_desc *desc,
+                                      const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                      int32_t max_seq_len, float scale, void *workspace, size_t workspace_bytes,
+                                      int *device_error, pa_stream_t stream) {
+  if (!valid_latent_desc(desc) || num_seqs < 0 || new_tokens <= 0 || num_heads <= 0 || max_seq_len < 0 ||
+      max_blocks_per_seq <= 0 || !isfinite(scale))
+    return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !cache || !block_tables || !seq_lens || !workspace) return PA_ERR_INVALID;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(cache) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+      (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PA_ERR_INVALID;
+  if (!supported_latent_desc(desc) || q_dtype != desc->dtype) return PA_ERR_UNSUPPORTED;
+  Sizes z;
+  if (!sizes_of(num_seqs, new_tokens, num_heads, &z)) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < z.total) return PA_ERR_INVALID;
+  LatentParams p{};
+  const int box_groups = desc->block_size == 8 ? 1 : 2;
+  if (!encode_latent_view(&p.tmap_c, cache, desc, kCols, box_groups)) return cuda_fail(cudaErrorInvalidValue);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.out = out;
+  p.tables = block_tables;
+  p.lens = seq_lens;
+  p.prefix = reinterpret_cast<long long *>(ws);
+  p.part_ml = reinterpret_cast<float2 *>(ws + z.prefix);
+  p.part_o = reinterpret_cast<float *>(ws + z.prefix + z.ml);
+  p.num_seqs = num_seqs;
+  p.new_tokens = new_tokens;
+  p.heads = num_heads;
+  p.rows = new_tokens * num_heads;
+  p.num_blocks = desc->num_blocks;
+  p.bs_shift = log2_block(desc->block_size);
+  p.max_blocks = max_blocks_per_seq;
+  const long long held = static_cast<long long>(max_blocks_per_seq) * desc->block_size;
+  long long limit = held < max_seq_len ? held : max_seq_len;
+  if (limit > INT_MAX / 4) limit = INT_MAX / 4;
+  p.limit = static_cast<int>(limit);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.err = device_error;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return desc->dtype == PA_F16 ? by_rows<kF16>(p, q, st) : by_rows<kBF16>(p, q, st);
+}

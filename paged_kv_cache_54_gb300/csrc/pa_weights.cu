@@ -1,0 +1,567 @@
+// pa_decode_weights: single-query decode attention that also adds every
+// token's attention weight to an accumulator.
+//
+// For a (sequence, KV head) pair with G query heads and tokens i < L:
+//   x[g, i] = scale <q_g, k_i>,  w[g, i] = exp(x[g, i] - m_g) / l_g,
+//   out[g]  = sum_i w[g, i] v_i,  weights_out[i] = decay weights_in[i] + sum_g w[g, i].
+// A token's weight is known only once m_g and l_g are, after the whole row.
+// Reading K a second time would cost half as much again as the attention;
+// instead the first kernel leaves the scores (G fp32 a token and head, 32
+// bytes against 512 of K and V at G = 8, head_dim 128, 16 bits) and a second
+// one turns them into weights.
+//
+// First kernel: every warp takes an equal share of all (sequence, head,
+// 16-token) steps and keeps K and V in registers, loaded straight from
+// global memory a step ahead; nothing is staged in shared memory.
+//   S = Q K^T   m16n8k16: rows are queries (8 of 16 used), columns tokens;
+//   O^T += V^T P^T  rows are dimensions, columns queries.
+// A product's order of k does not matter, so a lane takes whole 16-byte
+// pieces of a row as its fragments: lane (g, t) of K reads token
+// 4 (g / 2) + g % 2 (+ 2) and feeds consecutive words to consecutive
+// products, q in the same order.  The score fragment of the lane is then
+// exactly its P^T fragment (query g, tokens 4t..4t+3), and V's words of
+// two tokens are paired by byte permutes.
+// Sums and maxima are fp32, P is rounded to the operand type (half a step of
+// it a weight, averaged over tokens); the weights that are handed out come
+// from the fp32 scores.
+//
+// Second kernel: joins the shares of a pair (out), and adds the weights.
+#include <limits.h>
+#include <math.h>
+
+#include "pa_common.cuh"
+#include "pa_fp4.cuh"
+#include "pa_host.h"
+#include "pa_shares.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kStep = 16;             // tokens of a step
+constexpr int kWarps = 4;             // of a block
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxWorkers = 152 * 16; // warps, at most; sizes the workspace
+constexpr int kMinSteps = 4;          // a share smaller than this only adds joining
+constexpr float kLazy = 8.f;          // a row's maximum is raised when it grew by more than this (base 2)
+
+struct WeighParams {
+  void *out;
+  const void *q;
+  const uint8_t *k, *v;
+  const int32_t *tables, *lens;
+  const float *weights_in;
+  float *weights_out;
+  float *logits;       // [S, Hq, width]
+  float2 *part_ml;     // [pairs + workers, G]
+  float *part_o;       // [pairs + workers, G, D]
+  long long *prefix;   // [S + 1] steps of one head before sequence s
+  int num_seqs, q_heads, kv_heads, G, num_blocks, bs_shift, max_blocks, limit, width;
+  long long weights_width;
+  float scale_log2, v_scale, decay;
+  const float *k_head_scale, *v_head_scale;
+  int *err;
+};
+
+__device__ __forceinline__ uint4 ldg_stream(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg_stream2(const void *p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+__device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+
+// workers of a call with `steps` steps in all
+__device__ __forceinline__ long long worker_count(long long steps, long long most) {
+  const long long n = (steps + kMinSteps - 1) / kMinSteps;
+  return n < most ? n : most;
+}
+
+template <int KVT, int QT, int D>
+__global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p, int max_workers) {
+  constexpr bool BYTE = is_byte(KVT);
+  constexpr int MT = BYTE ? kF16 : KVT;  // the products' type
+  constexpr int EB = elt_bytes(KVT);
+  constexpr int ROW = D * EB;
+  constexpr int KW = ROW / 64;          // 16-byte words of a K row a lane holds
+  constexpr int QWORDS = D / 8;         // 32-bit words of q a lane holds
+  constexpr int VWORDS = ROW / 32;      // 32-bit words of a V row a lane holds
+  constexpr int ACC = D / 16;           // accumulator tiles
+  __shared__ ShareScan<kThreads> scan;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  launch_dependents();
+  auto steps_of = [&](int s) {
+    return static_cast<long long>((checked_len(p.lens, s, p.limit, p.err) + kStep - 1) / kStep) * p.kv_heads;
+  };
+  scan.scan(p.num_seqs, steps_of);
+  if (blockIdx.x == 0) {  // the sequences' first steps, for the second kernel
+    const int n = scan.run(p.num_seqs);
+    long long at = scan.base[threadIdx.x];
+    for (int s = threadIdx.x * n; s < min(p.num_seqs, (static_cast<int>(threadIdx.x) + 1) * n); ++s) {
+      p.prefix[s] = at;
+      at += steps_of(s);
+    }
+    if (threadIdx.x == 0) p.prefix[p.num_seqs] = scan.total();
+  }
+  const long long total = scan.total();
+  const long long workers = worker_count(total, max_workers);
+  const long long w = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  if (total == 0 || w >= workers) return;
+  long long u = share_begin(w, total, workers);
+  const long long end = share_begin(w + 1, total, workers);
+  if (u >= end) return;
+  long long first;
+  int s = scan.find(u, p.num_seqs, steps_of, first);
+
+  const int bs = 1 << p.bs_shift, bmask = bs - 1;
+  const int ktok = 4 * (g >> 1) + (g & 1);  // this lane's K tokens in a step: ktok, ktok + 2; V: 4t .. 4t + 3
+  while (u < end) {
+    const int L = checked_len(p.lens, s, p.limit, nullptr);
+    const int steps = (L + kStep - 1) / kStep;
+    if (steps == 0) {
+      ++s;
+      continue;
+    }
+    const int h = static_cast<int>((u - first) / steps);
+    int step = static_cast<int>((u - first) - static_cast<long long>(h) * steps);
+    const int begin = step;
+    const long long left = end - u;
+    const int last = left < steps - step ? step + static_cast<int>(left) : steps;  // this piece: [step, last)
+    const long long slot = static_cast<long long>(s) * p.kv_heads + h + w;
+    const int32_t *table = p.tables + static_cast<size_t>(s) * p.max_blocks;
+    const int last_block = (L - 1) >> p.bs_shift;
+    auto block_of = [&](int token) {
+      const int b = __ldg(table + min(token >> p.bs_shift, last_block));
+      if (b >= 0 && b < p.num_blocks) return b;
+      record_error(p.err, kErrBlockIndex);
+      return 0;
+    };
+    auto row_of = [&](int block, int token) {
+      return (static_cast<size_t>(block) * p.kv_heads + h) * bs + (token & bmask);
+    };
+
+    // the query row g, in the order of the K words
+    uint32_t qw[QWORDS];
+    float c = p.scale_log2;
+    if (p.k_head_scale != nullptr) c *= __ldg(p.k_head_scale + h);
+    {
+      const uint8_t *row = static_cast<const uint8_t *>(p.q) +
+                           (static_cast<size_t>(s) * p.q_heads + h * p.G + min(g, p.G - 1)) * (D * 2);
+#pragma unroll
+      for (int i = 0; i < QWORDS / 4; ++i) {
+        const int at = BYTE ? (i / 2) * 128 + t * 32 + (i & 1) * 16 : i * 64 + t * 16;
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row + at));
+        qw[4 * i] = x.x;
+        qw[4 * i + 1] = x.y;
+        qw[4 * i + 2] = x.z;
+        qw[4 * i + 3] = x.w;
+      }
+      if constexpr (BYTE && QT == kBF16) {  // as fp16, times the row's own power of two
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < QWORDS; ++i) {
+          const float2 x = half2_bits_to_float2<kBF16>(qw[i]);
+          top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float f = query_factor(top, c);
+#pragma unroll
+        for (int i = 0; i < QWORDS; ++i) {
+          const float2 x = half2_bits_to_float2<kBF16>(qw[i]);
+          qw[i] = pack2_rn<kF16>(x.x * f, x.y * f);
+        }
+        c /= f;
+      }
+    }
+    float acc[ACC][4];
+#pragma unroll
+    for (int i = 0; i < ACC; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    float m = -INFINITY, l = 0.f;
+
+    uint4 kr[2][KW];
+    uint32_t vr[4][VWORDS];
+    auto load_k = [&](int tok0, int block) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t *row = p.k + row_of(block, tok0 + ktok + 2 * j) * ROW + t * 16;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) kr[j][i] = ldg_stream(row + i * 64);
+      }
+    };
+    auto load_v = [&](int tok0, int block) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t *row = p.v + row_of(block, tok0 + 4 * t + j) * ROW;
+        if constexpr (VWORDS >= 4) {
+#pragma unroll
+          for (int i = 0; i < VWORDS / 4; ++i) {
+            const uint4 x = ldg_stream(row + i * 128 + g * 16);
+            vr[j][4 * i] = x.x;
+            vr[j][4 * i + 1] = x.y;
+            vr[j][4 * i + 2] = x.z;
+            vr[j][4 * i + 3] = x.w;
+          }
+        } else {
+          const uint2 x = ldg_stream2(row + g * 8);
+          vr[j][0] = x.x;
+          vr[j][1] = x.y;
+        }
+      }
+    };
+    int tok0 = step * kStep;
+    load_k(tok0, block_of(tok0 + ktok));
+    load_v(tok0, block_of(tok0 + 4 * t));
+    float *logits = p.logits + (static_cast<size_t>(s) * p.q_heads + h * p.G + min(g, p.G - 1)) * p.width + 4 * t;
+    for (; step < last; ++step) {
+      const int next = min(step + 1, last - 1) * kStep;
+      const int kb = block_of(next + ktok), vb = block_of(next + 4 * t);
+      tok0 = step * kStep;
+      float sc[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          const uint32_t x[4] = {kr[j][i].x, kr[j][i].y, kr[j][i].z, kr[j][i].w};
+          if constexpr (BYTE) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t lo, hi;
+              byte4_to_half2x2<KVT>(x[e], lo, hi);
+              mma16816<MT>(sc[j], qw[8 * i + 2 * e], 0u, qw[8 * i + 2 * e + 1], 0u, lo, hi);
+            }
+          } else {
+            mma16816<MT>(sc[j], qw[4 * i], 0u, qw[4 * i + 1], 0u, x[0], x[1]);
+            mma16816<MT>(sc[j], qw[4 * i + 2], 0u, qw[4 * i + 3], 0u, x[2], x[3]);
+          }
+        }
+      }
+      load_k(next, kb);
+      float x[4] = {sc[0][0] * c, sc[0][1] * c, sc[1][0] * c, sc[1][1] * c};  // tokens 4t .. 4t + 3
+      const bool tail = tok0 + kStep > L;
+      if (tail) {  // the sequence's last step: tokens behind its end weigh nothing, whatever their rows hold
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (tok0 + 4 * t + e >= L) {
+            x[e] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < VWORDS; ++i) vr[e][i] = 0u;
+          }
+      }
+      if (g < p.G) *reinterpret_cast<float4 *>(logits + tok0) = make_float4(x[0], x[1], x[2], x[3]);
+      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const bool grow = mx > m + kLazy;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float alpha = grow ? exp2_fast(m - mx) : 1.f;
+        if (grow) m = mx;
+        l *= alpha;
+        const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t), a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < ACC; ++i) {
+          acc[i][0] *= a0;
+          acc[i][1] *= a1;
+          acc[i][2] *= a0;
+          acc[i][3] *= a1;
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(x[e] - base);
+      l += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+      const uint32_t b0 = pack2_rn<MT>(pr[0], pr[1]), b1 = pack2_rn<MT>(pr[2], pr[3]);
+#pragma unroll
+      for (int i = 0; i < VWORDS; ++i) {
+        if constexpr (BYTE) {
+          uint32_t a[4][2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) byte4_to_half2x2<KVT>(vr[e][i], a[e][0], a[e][1]);
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            mma16816<MT>(acc[2 * i + f], lows(a[0][f], a[1][f]), highs(a[0][f], a[1][f]), lows(a[2][f], a[3][f]),
+                         highs(a[2][f], a[3][f]), b0, b1);
+        } else {
+          mma16816<MT>(acc[i], lows(vr[0][i], vr[1][i]), highs(vr[0][i], vr[1][i]), lows(vr[2][i], vr[3][i]),
+                       highs(vr[2][i], vr[3][i]), b0, b1);
+        }
+      }
+      load_v(next, vb);
+    }
+    // the piece: unnormalised sums with their maximum and total weight
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (t == 0 && g < p.G) p.part_ml[slot * p.G + g] = make_float2(m, l);
+    float *po = p.part_o + slot * p.G * D;
+    constexpr int VD = BYTE ? D / 8 : 8;  // consecutive dimensions of a lane
+#pragma unroll
+    for (int i = 0; i < ACC; ++i) {
+      const int d = (2 * i / VD) * (8 * VD) + g * VD + 2 * i % VD;
+      if (2 * t < p.G) *reinterpret_cast<float2 *>(po + (2 * t) * D + d) = make_float2(acc[i][0], acc[i][2]);
+      if (2 * t + 1 < p.G) *reinterpret_cast<float2 *>(po + (2 * t + 1) * D + d) = make_float2(acc[i][1], acc[i][3]);
+    }
+    u += last - begin;
+    if (u >= first + static_cast<long long>(steps) * p.kv_heads) {
+      first += static_cast<long long>(steps) * p.kv_heads;
+      ++s;
+    }
+  }
+}
+
+// Joins a pair's pieces and adds its tokens' weights.  Blocks below
+// num_seqs * q_heads write one row of out each; the others share the steps.
+template <int QT, int D>
+__global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParams p, int max_workers) {
+  __shared__ float red[kThreads / D == 2 ? D + 1 : 1];
+  grid_dependency_wait();
+  const long long total = p.prefix[p.num_seqs];
+  const long long workers = worker_count(total, max_workers);
+  const int lane = threadIdx.x & 31;
+  const long long rows = static_cast<long long>(p.num_seqs) * p.q_heads;
+  if (blockIdx.x < rows) {
+    const int s = blockIdx.x / p.q_heads, hq = blockIdx.x % p.q_heads, h = hq / p.G, gq = hq % p.G;
+    const long long first = p.prefix[s], all = p.prefix[s + 1] - first;
+    constexpr int PARTS = kThreads / D;  // threads of a dimension
+    const int d = threadIdx.x % D, part = threadIdx.x / D;
+    float o = 0.f, l = 0.f;
+    if (all > 0) {
+      const long long steps = all / p.kv_heads, u0 = first + h * steps;
+      const long long pair = static_cast<long long>(s) * p.kv_heads + h;
+      const long long s0 = pair + share_owner(u0, total, workers), s1 = pair + share_owner(u0 + steps - 1, total, workers);
+      float m = -INFINITY;
+      for (long long i = s0; i <= s1; ++i) m = fmaxf(m, p.part_ml[i * p.G + gq].x);
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+      for (long long i = s0 + part; i <= s1; i += PARTS) {
+        const float2 ml = p.part_ml[i * p.G + gq];
+        const float f = exp2_fast(ml.x - base);
+        l += f * ml.y;
+        o += f * p.part_o[(i * p.G + gq) * D + d];
+      }
+    }
+    if constexpr (PARTS == 2) {
+      if (part == 1) {
+        red[d] = o;
+        if (d == 0) red[D] = l;
+      }
+      __syncthreads();
+      if (part == 0) {
+        o += red[d];
+        l += red[D];
+      }
+    }
+    if (part == 0) {
+      const float vs = p.v_head_scale != nullptr ? __ldg(p.v_head_scale + h) : p.v_scale;
+      const float y = l == 0.f ? 0.f : o * (vs / l);  // (no token, or none with a weight)
+      static_cast<uint16_t *>(p.out)[static_cast<size_t>(blockIdx.x) * D + d] = float_to_storage16<QT>(y);
+    }
+    return;
+  }
+  if (total == 0) return;
+  const long long nw = (static_cast<long long>(gridDim.x) - rows) * kWarps;
+  const long long w = (blockIdx.x - rows) * kWarps + (threadIdx.x >> 5);
+  long long u = share_begin(w, total, nw);
+  const long long end = share_begin(w + 1, total, nw);
+  if (u >= end) return;
+  int lo = 0, hi = p.num_seqs - 1;  // the last sequence whose first step is at or before u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.prefix[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  for (int s = lo; u < end; ++s) {
+    const long long first = p.prefix[s], all = p.prefix[s + 1] - first;
+    if (all == 0) continue;
+    const int L = __ldg(p.lens + s);
+    const long long steps = all / p.kv_heads;
+    while (u < end && u < first + all) {
+      const int h = static_cast<int>((u - first) / steps);
+      const long long u0 = first + h * steps;
+      const long long stop = end < u0 + steps ? end : u0 + steps;
+      const int i0 = static_cast<int>(u - u0) * kStep;
+      const long long i1l = (stop - u0) * kStep;
+      const int i1 = i1l < L ? static_cast<int>(i1l) : L;
+      const long long pair = static_cast<long long>(s) * p.kv_heads + h;
+      const long long s0 = pair + share_owner(u0, total, workers), s1 = pair + share_owner(u0 + steps - 1, total, workers);
+      // the pair's maximum and total of query lane / 4, four lanes along the pieces
+      const int gq = min(lane >> 2, p.G - 1);
+      float m = -INFINITY, l = 0.f;
+      for (long long i = s0 + (lane & 3); i <= s1; i += 4) m = fmaxf(m, p.part_ml[i * p.G + gq].x);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      if (m == -INFINITY) m = 0.f;
+      for (long long i = s0 + (lane & 3); i <= s1; i += 4) {
+        const float2 ml = p.part_ml[i * p.G + gq];
+        l += exp2_fast(ml.x - m) * ml.y;
+      }
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float *x = p.logits + (static_cast<size_t>(s) * p.q_heads + h * p.G) * p.width;
+      const size_t at = static_cast<size_t>(pair) * p.weights_width;
+      float bm[8], bi[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        bm[q] = __shfl_sync(0xffffffffu, m, 4 * q);
+        bi[q] = q < p.G ? __shfl_sync(0xffffffffu, inv, 4 * q) : 0.f;
+      }
+      for (int i = i0 + lane; i < i1; i += 32) {
+        float sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.G) sum += exp2_fast(__ldcs(x + static_cast<size_t>(q) * p.width + i) - bm[q]) * bi[q];
+        const float before = p.weights_in == nullptr ? 0.f : p.decay * p.weights_in[at + i];
+        p.weights_out[at + i] = before + sum;
+      }
+      u = stop;
+    }
+  }
+}
+
+struct Sizes {
+  size_t prefix, ml, o, logits, total;
+  int width;
+};
+bool sizes_of(int S, int Hq, int H, int D, int max_len, Sizes *z) {
+  if (S < 0 || Hq <= 0 || H <= 0 || Hq % H || (D != 64 && D != 128) || max_len < 0 || Hq / H > 8) return false;
+  if (max_len > INT_MAX - kStep) return false;
+  auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
+  z->width = (max_len + kStep - 1) / kStep * kStep;
+  const size_t G = Hq / H, slots = static_cast<size_t>(S) * H + kMaxWorkers;
+  z->prefix = up(8 * (static_cast<size_t>(S) + 1));
+  z->ml = up(slots * G * sizeof(float2));
+  z->o = up(slots * G * D * sizeof(float));
+  z->logits = up(static_cast<size_t>(S) * Hq * z->width * sizeof(float));
+  z->total = z->prefix + z->ml + z->o + z->logits;
+  return true;
+}
+
+template <int KVT, int QT, int D>
+pa_status launch(const WeighParams &p, cudaStream_t stream) {
+  DeviceInfo info;
+  if (!current_device_info(&info)) return cuda_fail(cudaGetLastError());
+  const int blocks = info.sm_count * 3 * kWarps > kMaxWorkers ? kMaxWorkers / kWarps : info.sm_count * 3;
+  const int workers = blocks * kWarps;
+  weigh_kernel<KVT, QT, D><<<blocks, kThreads, 0, stream>>>(p, workers);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs * p.q_heads + info.sm_count * 8));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, weigh_finish_kernel<QT, D>, p, workers);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+template <int KVT, int QT>
+pa_status by_dim(int D, const WeighParams &p, cudaStream_t stream) {
+  return D == 64 ? launch<KVT, QT, 64>(p, stream) : launch<KVT, QT, 128>(p, stream);
+}
+template <int KVT>
+pa_status by_query(int q_dtype, int D, const WeighParams &p, cudaStream_t stream) {
+  return q_dtype == kF16 ? by_dim<KVT, kF16>(D, p, stream) : by_dim<KVT, kBF16>(D, p, stream);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_decode_weights_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim, int32_t max_seq_len) {
+  Sizes z;
+  return sizes_of(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, &z) ? z.total : 0;
+}
+
+extern "C" pa_status pa_decode_weights(void *out, float *weights_out, const float *weights_in, float decay,
+                                       int64_t weights_width, const void *q, int32_t q_dtype, int32_t num_seqs,
+                                       int32_t num_q_heads, const void *k_cache, const void *v_cache,
+                                       const pa_cache_desc *cache, const int32_t *block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len,
+                                       float scale, void *workspace, size_t workspace_bytes, int *device_error,
+                                       pa_stream_t stream) {
+  if (!valid_cache_desc(cache) || num_seqs < 0 || num_q_heads <= 0 || max_seq_len < 0 || max_blocks_per_seq <= 0 ||
+      weights_width < max_seq_len || !isfinite(scale) || !isfinite(decay))
+    return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !weights_out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !workspace)
+    return PA_ERR_INVALID;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (reinterpret_cast<uintptr_t>(weights_out) & 3u) || (reinterpret_cast<uintptr_t>(weights_in) & 3u) ||
+      (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PA_ERR_INVALID;
+  if (num_q_heads % cache->kv_heads) return PA_ERR_INVALID;
+  const int G = num_q_heads / cache->kv_heads;
+  if ((G != 1 && G != 2 && G != 4 && G != 8) || !supported_cache_shape(cache) || cache->dtype == PA_FP4)
+    return PA_ERR_UNSUPPORTED;
+  const bool byte_codes = cache->dtype >= PA_FP8_E4M3;
+  if (byte_codes ? (q_dtype != PA_F16 && q_dtype != PA_BF16) : q_dtype != cache->dtype) return PA_ERR_UNSUPPORTED;
+  Sizes z;
+  if (!sizes_of(num_seqs, num_q_heads, cache->kv_heads, cache->head_dim, max_seq_len, &z)) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < z.total) return PA_ERR_INVALID;
+  if (static_cast<long long>(num_seqs) * num_q_heads > INT_MAX / 2) return PA_ERR_UNSUPPORTED;  // the grid
+
+  WeighParams p{};
+  p.out = out;
+  p.q = q;
+  p.k = static_cast<const uint8_t *>(k_cache);
+  p.v = static_cast<const uint8_t *>(v_cache);
+  p.tables = block_tables;
+  p.lens = seq_lens;
+  p.weights_in = weights_in;
+  p.weights_out = weights_out;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.prefix = reinterpret_cast<long long *>(ws);
+  p.part_ml = reinterpret_cast<float2 *>(ws + z.prefix);
+  p.part_o = reinterpret_cast<float *>(ws + z.prefix + z.ml);
+  p.logits = reinterpret_cast<float *>(ws + z.prefix + z.ml + z.o);
+  p.num_seqs = num_seqs;
+  p.q_heads = num_q_heads;
+  p.kv_heads = cache->kv_heads;
+  p.G = G;
+  p.num_blocks = cache->num_blocks;
+  p.bs_shift = cache->block_size == 8 ? 3 : cache->block_size == 16 ? 4 : 5;
+  p.max_blocks = max_blocks_per_seq;
+  const long long held = static_cast<long long>(max_blocks_per_seq) * cache->block_size;
+  p.limit = held < max_seq_len ? static_cast<int>(held) : max_seq_len;
+  p.width = z.width;
+  p.weights_width = weights_width;
+  const bool per_head = byte_codes && cache->k_head_scales != nullptr;
+  p.scale_log2 = scale * (byte_codes && !per_head ? cache->k_scale : 1.f) * 1.4426950408889634f;
+  p.v_scale = byte_codes && !per_head ? cache->v_scale : 1.f;
+  p.k_head_scale = per_head ? cache->k_head_scales : nullptr;
+  p.v_head_scale = per_head ? cache->v_head_scales : nullptr;
+  p.decay = decay;
+  p.err = device_error;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int D = cache->head_dim;
+  switch (cache->dtype) {
+    case PA_F16: return by_dim<kF16, kF16>(D, p, st);
+    case PA_BF16: return by_dim<kBF16, kBF16>(D, p, st);
+    case PA_FP8_E4M3: return by_query<kE4M3>(q_dtype, D, p, st);
+    case PA_FP8_E5M2: return by_query<kE5M2>(q_dtype, D, p, st);
+    case PA_INT8: return by_query<kI8>(q_dtype, D, p, st);
+  }
+  return PA_ERR_UNSUPPORTED;
+}

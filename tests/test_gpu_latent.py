@@ -1,0 +1,230 @@
+"""The latent cache on the GPU: rows written through a slot mapping, and
+absorbed attention of one or a few new tokens, against the definition in 64
+bits."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_cache_54_gb300 as pa
+from _eviction import DEV, DT, LATENT, ROPE, ROW, attend, check, eps, gen, i32, randn, rows_of, tables
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- write
+@pytest.mark.parametrize("tokens", [1, 3, 64, 1021])
+@pytest.mark.parametrize("dt,bs", [("f16", 8), ("bf16", 16), ("bf16", 32)])
+def test_write_is_a_copy(tokens, dt, bs):
+    g = gen(tokens + bs)
+    nb = -(-tokens // bs) + 2
+    both = randn(g, tokens, ROW + 64).to(DT[dt])      # rows of a wider projection
+    slots = torch.randperm(nb * bs, generator=g, device=DEV)[:tokens]
+    slots[::5] = -1
+    cache = randn(g, nb, bs, ROW).to(DT[dt])
+    want = cache.clone()
+    keep = slots >= 0
+    want.view(-1, ROW)[slots[keep]] = both[keep, :ROW]
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_latent_write(both[:, :LATENT], both[:, LATENT:ROW], slots, cache, device_error=err)
+    assert torch.equal(cache.view(torch.int16), want.view(torch.int16)) and int(err) == 0
+    cache2 = torch.zeros_like(cache)
+    pa.pa_latent_write(both[:, :LATENT].contiguous(), both[:, LATENT:ROW].contiguous(), slots, cache2)
+    assert torch.equal(cache2.view(-1, ROW)[slots[keep]].view(torch.int16), both[keep, :ROW].view(torch.int16))
+
+
+def test_write_reports_slots_outside_the_cache():
+    cache = torch.zeros(2, 16, ROW, dtype=torch.float16, device=DEV)
+    x = torch.ones(4, ROW, dtype=torch.float16, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    slots = torch.tensor([32, -2, 5, 2 ** 40], device=DEV)
+    pa.pa_latent_write(x[:, :LATENT], x[:, LATENT:], slots, cache, device_error=err)
+    assert int(err) == 2
+    assert float(cache.float().sum()) == ROW and float(cache.view(-1, ROW)[5].float().sum()) == ROW
+
+
+def test_write_without_tokens_and_past_four_gigabytes():
+    nb = (1 << 32) // (32 * ROW * 2) + 40
+    cache = torch.zeros(nb, 32, ROW, dtype=torch.bfloat16, device=DEV)
+    x = randn(gen(1), 3, ROW).bfloat16()
+    pa.pa_latent_write(x[:0, :LATENT], x[:0, LATENT:], torch.zeros(0, dtype=torch.int64, device=DEV), cache)
+    slots = torch.tensor([nb * 32 - 1, 0, nb * 32 - 40], device=DEV)
+    pa.pa_latent_write(x[:, :LATENT], x[:, LATENT:], slots, cache)
+    assert torch.equal(cache.view(-1, ROW)[slots], x)
+
+
+# ---------------------------------------------------------------- decode
+def make(lens, new, heads, bs, dt, seed, width=None):
+    g = gen(seed)
+    table, nb, _ = tables(lens, bs, seed, width=width)
+    cache = torch.full((nb, bs, ROW), float("nan"), dtype=DT[dt], device=DEV)
+    for s, n in enumerate(lens):   # rows behind a sequence's end stay NaN
+        for b in range(-(-n // bs)):
+            m = min(bs, n - b * bs)
+            cache[int(table[s, b]), :m] = randn(g, m, ROW).to(DT[dt])
+    q = torch.cat((0.4 * randn(g, len(lens), new, heads, LATENT), randn(g, len(lens), new, heads, ROPE)), -1)
+    return cache, table, i32(lens), q.to(DT[dt])
+
+
+def expect(cache, table, lens, q, bs, scale, e):
+    S, n, H, _ = q.shape
+    o = torch.zeros(S, n, H, LATENT, dtype=torch.float64, device=DEV)
+    tol = torch.zeros_like(o)
+    for s, L in enumerate(lens.tolist()):
+        x = rows_of(cache, table[s], L, bs)
+        for j in range(n):
+            see = L - (n - 1 - j)
+            if see > 0:
+                o[s, j], tol[s, j], _, _ = attend(q[s, j].double(), x[:see], x[:see, :LATENT], scale, e)
+    return o, tol
+
+
+def run(cache, table, lens, q, scale, max_len=None, **kw):
+    out = torch.full(q.shape[:-1] + (LATENT,), float("nan"), dtype=q.dtype, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_latent_decode(out, q, cache, table, lens, int(lens.max()) if max_len is None else max_len, scale,
+                        device_error=err, **kw)
+    assert int(err) == 0
+    return out
+
+
+SCALE = 1.0 / math.sqrt(192)
+SHAPES = [
+    # lens, new tokens, heads, block
+    ([1], 1, 16, 16),
+    ([64], 1, 16, 16),
+    ([65, 63, 128], 1, 16, 8),
+    ([1, 2, 7, 0, 33, 100], 1, 5, 16),
+    ([300, 1, 129], 1, 1, 32),
+    ([77, 500], 1, 20, 8),
+    ([77, 500, 64], 1, 64, 16),
+    ([130, 1, 700], 1, 128, 32),
+    ([1000, 3], 2, 16, 16),
+    ([2, 1, 0, 200], 4, 16, 32),       # rows that see nothing
+    ([90, 257], 3, 20, 16),
+    ([400], 5, 128, 8),
+    ([0, 0], 1, 16, 16),
+    ([5000], 1, 16, 16),
+    ([3000, 4000, 200], 1, 64, 32),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,new,heads,bs", SHAPES)
+def test_decode_matches_the_definition(lens, new, heads, bs, dt):
+    cache, table, L, q = make(lens, new, heads, bs, dt, seed=len(lens) * 100 + heads)
+    got = run(cache, table, L, q, SCALE)
+    want, tol = expect(cache, table, L, q, bs, SCALE, eps(DT[dt]))
+    check(got, want, tol)
+
+
+def test_decode_of_many_sequences_of_many_lengths():
+    lens = [(37 * s * s) % 700 for s in range(300)]
+    cache, table, L, q = make(lens, 1, 16, 16, "bf16", 7)
+    got = run(cache, table, L, q, SCALE)
+    want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.bfloat16))
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("factor", [0.0, -3.0, 40.0])
+def test_decode_scales(factor):
+    # (40 times the usual scale: maxima rise by far more than 2^8 on the way, and few tokens take all of the weight)
+    cache, table, L, q = make([700, 64, 3], 1, 32, 16, "f16", 11)
+    got = run(cache, table, L, q, SCALE * factor)
+    want, tol = expect(cache, table, L, q, 16, SCALE * factor, eps(torch.float16))
+    check(got, want, tol)
+
+
+def test_decode_with_rising_scores():
+    """Every tile's scores lie far above the last one's."""
+    cache, table, L, q = make([900], 1, 16, 16, "bf16", 13)
+    n = torch.arange(900, device=DEV)
+    rows = cache[table[0].long()].view(-1, ROW)
+    rows[:900] = (rows[:900].float() * (n[:, None] / 100.0)).bfloat16()
+    cache[table[0].long()] = rows.view(-1, 16, ROW)
+    got = run(cache, table, L, q, SCALE)
+    want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.bfloat16))
+    check(got, want, tol)
+
+
+def test_decode_infinities_stay_in_their_rows():
+    cache, table, L, q = make([100, 100], 1, 16, 16, "f16", 17)
+    q[0, 0, 3, 0] = float("nan")
+    cache[int(table[1, 2]), 5, 7] = float("inf")
+    out = run(cache, table, L, q, SCALE)
+    assert torch.isnan(out[0, 0, 3]).all()
+    clean = [h for h in range(16) if h != 3]
+    want, tol = expect(cache, table[:1], L[:1], q[:1], 16, SCALE, eps(torch.float16))
+    check(out[0, 0, clean], want[0, 0, clean], tol[0, 0, clean])
+    assert not torch.isfinite(out[1]).all(-1).any()   # every row of the sequence meets the infinity
+
+
+def test_decode_three_dimensional_queries_wider_tables_and_bounds():
+    cache, table, L, q = make([200, 70], 1, 16, 16, "bf16", 19, width=40)
+    a = run(cache, table, L, q, SCALE)
+    out = torch.empty(2, 16, LATENT, dtype=torch.bfloat16, device=DEV)
+    pa.pa_latent_decode(out, q[:, 0].contiguous(), cache, table, L, 640, SCALE)
+    want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.bfloat16))
+    check(a, want, tol)
+    check(out, want[:, 0], tol[:, 0])
+
+
+def test_decode_reports_bad_lengths_and_blocks():
+    cache, table, L, q = make([100, 100, 100], 1, 16, 16, "f16", 23)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = torch.full((3, 1, 16, LATENT), 7.0, dtype=torch.float16, device=DEV)
+    bad = L.clone()
+    bad[1] = 101
+    pa.pa_latent_decode(out, q, cache, table, bad, 100, SCALE, device_error=err)
+    assert int(err) == 3 and float(out[1].abs().sum()) == 0
+    want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.float16))
+    check(out[[0, 2]], want[[0, 2]], tol[[0, 2]])
+    err.zero_()
+    cache[0] = 0                       # (what the bad entry is read as; it may be a sequence's own block too)
+    want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.float16))
+    t = table.clone()
+    t[2, 3] = 10 ** 6
+    pa.pa_latent_decode(out, q, cache, t, L, 100, SCALE, device_error=err)
+    assert int(err) == 1
+    check(out[:2], want[:2], tol[:2])
+
+
+def test_decode_past_four_gigabytes():
+    bs, nb = 32, (1 << 32) // (32 * ROW * 2) + 200
+    cache = torch.zeros(nb, bs, ROW, dtype=torch.bfloat16, device=DEV)
+    g = gen(29)
+    table = i32([[nb - 1, 0, nb - 117, 5]])
+    cache[table[0].long()] = randn(g, 4, bs, ROW).bfloat16()
+    q = randn(g, 1, 1, 16, ROW).bfloat16()
+    L = i32([4 * bs - 3])
+    got = run(cache, table, L, q, SCALE * 0.5)
+    want, tol = expect(cache, table, L, q, bs, SCALE * 0.5, eps(torch.bfloat16))
+    check(got, want, tol)
+
+
+def test_decode_captured_and_replayed_on_another_stream():
+    cache, table, L, q = make([300, 4000, 0, 77], 2, 16, 16, "bf16", 31)
+    ws = torch.empty(pa.pa_latent_decode_workspace_size(4, 2, 16), dtype=torch.uint8, device=DEV)
+    out = torch.empty(4, 2, 16, LATENT, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        pa.pa_latent_decode(out, q, cache, table, L, 4096, SCALE, workspace=ws)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_latent_decode(out, q, cache, table, L, 4096, SCALE, workspace=ws)
+    ws.random_()
+    L.copy_(i32([299, 3001, 0, 60]))   # no longer than the blocks they have
+    q.copy_(randn(gen(37), *q.shape) * 0.5)
+    out.fill_(float("nan"))
+    graph.replay()
+    want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.bfloat16))
+    check(out, want, tol)
+
+
+def test_blocks_move_under_a_nine_head_description():
+    a, b = (randn(gen(s), 6, 16, ROW).bfloat16() for s in (41, 42))
+    want_a, want_b = a.clone(), b.clone()
+    want_a[4], want_b[4] = a[1], b[1]
+    pa.pa_copy_blocks(a.view(6, 9, 16, 64), b.view(6, 9, 16, 64), torch.tensor([[1, 4]], device=DEV))
+    assert torch.equal(a, want_a) and torch.equal(b, want_b)
