@@ -587,6 +587,46 @@ PA_API pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype, int
                                   int *device_error, pa_stream_t stream);
 
 /*
+ * pa_latent_prefill — expanded causal attention of each sequence's new
+ * tokens over all of its tokens in a latent cache (their rows are written
+ * with pa_latent_write first).
+ *
+ * Sequences, new tokens and positions as in pa_prefill.  With c_i, r_i token
+ * i's latent vector and rotary key, and up[h] the 256 rows of head h (the
+ * first 128 give its keys, the others its values):
+ *   key_i = (up[h, :128] c_i, r_i),   value_i = up[h, 128:] c_i
+ *   out[cu_q_lens[s] + j, h, :] =
+ *       sum_{i <= p} softmax_i(scale * <q[cu_q_lens[s] + j, h, :], key_i>) value_i
+ *   q              device [num_q_tokens, num_heads, 192] (128 against the
+ *                  expanded keys, then 64 rotary), num_q_tokens =
+ *                  cu_q_lens[num_seqs]
+ *   out            device [num_q_tokens, num_heads, 128]
+ *   up             device [num_heads, 256, latent_dim], the cache's type
+ *   num_kv_tokens  host upper bound of the sum of seq_lens
+ *   workspace      at least pa_latent_prefill_workspace_size(...) bytes,
+ *                  256-byte aligned, uninitialised; calls sharing one must be
+ *                  stream-ordered.  It holds the expanded keys and values,
+ *                  rounded to the cache's type: 512 bytes a head and token.
+ * The expansion costs as much as the attention of about 170 new tokens a
+ * sequence in the absorbed form; for fewer new tokens over a long context
+ * pa_latent_decode is the cheaper call.  The rows of a sequence's tokens must
+ * be finite (a later token's value reaches an earlier one's row times zero).
+ * Device checks: a length that breaks these bounds, or tokens beyond
+ * num_kv_tokens, skip the sequence (nothing of its output is written) and
+ * report error 3; a block id out of range reads block 0 instead and reports
+ * error 1; a stalled pipeline reports error 4.
+ * Supported set: num_seqs and num_heads <= 65535; num_heads * (num_kv_tokens +
+ * 127 * num_seqs + 255) < 2^31.
+ */
+PA_API size_t pa_latent_prefill_workspace_size(int32_t num_seqs, int32_t num_heads, int64_t num_kv_tokens);
+PA_API pa_status pa_latent_prefill(void *out, const void *q, int32_t q_dtype, int32_t num_q_tokens,
+                                   const int32_t *cu_q_lens, int32_t num_seqs, int32_t num_heads, int32_t max_q_len,
+                                   const void *up, const void *cache, const pa_latent_desc *desc,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                   int64_t num_kv_tokens, float scale, void *workspace, size_t workspace_bytes,
+                                   int *device_error, pa_stream_t stream);
+
+/*
  * Prefix cache (host) — the block pool behind the block tables, with
  * prefix caching ([P3] §4.2–§4.3; [P1] §3.2).
  *

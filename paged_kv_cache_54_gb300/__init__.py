@@ -22,8 +22,11 @@ functions carry the C ABI's names:
                            token, shared by all heads)
     pa_latent_decode       absorbed attention of one or a few new tokens a
                            sequence over a latent cache
+    pa_latent_prefill      expanded causal attention of several new tokens per
+                           sequence over a latent cache
     pa_decode_workspace_size, pa_decode_weights_workspace_size,
-    pa_evict_workspace_size, pa_latent_decode_workspace_size
+    pa_evict_workspace_size, pa_latent_decode_workspace_size,
+    pa_latent_prefill_workspace_size
     PrefixCache            the host block pool with prefix caching
                            (pa_prefix_cache_*)
 
@@ -70,6 +73,7 @@ EXPORTED = ("pa_reshape_and_cache", "pa_gather_cache", "pa_decode_workspace_size
             "pa_prefill", "pa_decode_static_scratch", "pa_copy_blocks", "pa_compact_blocks",
             "pa_decode_weights_workspace_size", "pa_decode_weights", "pa_evict_workspace_size",
             "pa_evict_tokens", "pa_latent_write", "pa_latent_decode_workspace_size", "pa_latent_decode",
+            "pa_latent_prefill_workspace_size", "pa_latent_prefill",
             "pa_swap_blocks", "pa_prefix_cache_fork_sequence", "pa_prefix_cache_compact",
             "pa_status_string", "pa_last_cuda_error", "pa_selftest_wait_timeout",
             "pa_prefix_cache_create", "pa_prefix_cache_destroy", "pa_prefix_cache_add_sequence",
@@ -151,7 +155,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pa_decode_weights_workspace_size.argtypes = [i32] * 5
     lib.pa_evict_workspace_size.argtypes = [i32] * 3
     lib.pa_latent_decode_workspace_size.argtypes = [i32] * 3
-    for name in ("pa_decode_weights_workspace_size", "pa_evict_workspace_size", "pa_latent_decode_workspace_size"):
+    lib.pa_latent_prefill_workspace_size.argtypes = [i32, i32, i64]
+    for name in ("pa_decode_weights_workspace_size", "pa_evict_workspace_size", "pa_latent_decode_workspace_size",
+                 "pa_latent_prefill_workspace_size"):
         getattr(lib, name).restype = size
     lib.pa_decode_weights.argtypes = [vp, vp, vp, f32, i64, vp, i32, i32, i32, vp, vp, cache_p, vp, i32, vp, i32,
                                       f32, vp, size, vp, vp]
@@ -159,7 +165,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                     size, vp, vp]
     lib.pa_latent_write.argtypes = [vp, vp, i64, i64, i32, vp, i32, vp, latent_p, vp, vp]
     lib.pa_latent_decode.argtypes = [vp, vp, i32, i32, i32, i32, vp, latent_p, vp, i32, vp, i32, f32, vp, size, vp, vp]
-    for name in ("pa_decode_weights", "pa_evict_tokens", "pa_latent_write", "pa_latent_decode"):
+    lib.pa_latent_prefill.argtypes = [vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, latent_p, vp, i32, vp, i64, f32, vp,
+                                      size, vp, vp]
+    for name in ("pa_decode_weights", "pa_evict_tokens", "pa_latent_write", "pa_latent_decode", "pa_latent_prefill"):
         getattr(lib, name).restype = ctypes.c_int
     lib.pa_prefix_cache_create.argtypes = [i32, i32, vp]
     lib.pa_prefix_cache_create.restype = vp
@@ -726,6 +734,42 @@ def pa_latent_decode(out, q, cache, block_tables, seq_lens, max_seq_len: int, sc
                                            seq_lens.data_ptr(), max_seq_len, scale, workspace.data_ptr(),
                                            workspace.numel() * workspace.element_size(), _ptr(device_error),
                                            _stream(stream)), "pa_latent_decode")
+    return out
+
+
+def pa_latent_prefill_workspace_size(num_seqs: int, num_heads: int, num_kv_tokens: int) -> int:
+    return int(load_library().pa_latent_prefill_workspace_size(num_seqs, num_heads, num_kv_tokens))
+
+
+def pa_latent_prefill(out, q, cu_q_lens, up, cache, block_tables, seq_lens, max_q_len: int, num_kv_tokens: int,
+                      scale: float, workspace=None, device_error=None, stream=None) -> torch.Tensor:
+    """Expanded causal attention of the new tokens ``q [T, H, 192]`` (rows as
+    in ``pa_prefill``) over a latent cache; writes ``out [T, H, 128]``.  ``up
+    [H, 256, 512]``: each head's key rows, then its value rows, of the
+    up-projection.  ``num_kv_tokens``: an upper bound of ``seq_lens.sum()``."""
+    _check_here("out q cu_q_lens up cache block_tables seq_lens", out, q, cu_q_lens, up, cache, block_tables, seq_lens)
+    _check_error_word(device_error)
+    code, ref = _described_latent(cache.shape, cache.dtype)
+    if q.dim() != 3 or q.shape[2] != 192 or q.dtype != cache.dtype:
+        raise ValueError("q must be [T, H, 192] of the cache's dtype")
+    T, H = q.shape[:2]
+    if out.shape != (T, H, 128) or out.dtype != q.dtype:
+        raise ValueError(f"out must be {q.dtype} [{T}, {H}, 128]")
+    if up.shape != (H, 256, LATENT_DIM) or up.dtype != q.dtype:
+        raise ValueError(f"up must be {q.dtype} [{H}, 256, {LATENT_DIM}]")
+    S = seq_lens.numel()
+    if cu_q_lens.dtype != torch.int32 or cu_q_lens.shape != (S + 1,):
+        raise ValueError(f"cu_q_lens must be int32 [{S + 1}]")
+    _check_tables(block_tables, seq_lens, S)
+    if workspace is None:
+        workspace = _workspace_of(pa_latent_prefill_workspace_size(S, H, num_kv_tokens))
+    else:
+        _check_here("workspace", workspace)
+    _check(load_library().pa_latent_prefill(out.data_ptr(), q.data_ptr(), code, T, cu_q_lens.data_ptr(), S, H, max_q_len,
+                                            up.data_ptr(), cache.data_ptr(), ref, block_tables.data_ptr(),
+                                            max(1, block_tables.shape[1]), seq_lens.data_ptr(), num_kv_tokens, scale,
+                                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                            _ptr(device_error), _stream(stream)), "pa_latent_prefill")
     return out
 
 

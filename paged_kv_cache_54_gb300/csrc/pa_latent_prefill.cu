@@ -1,0 +1,843 @@
+// pa_latent_prefill: expanded causal attention of each sequence's new tokens
+// over the latent paged cache.
+//
+// With c the tokens' latent vectors and r their rotary keys, head h has the
+// keys (Uk_h c, r) of 128 + 64 elements and the values Uv_h c of 128.  A new
+// token costs 640 operations a head and token of the context against 2176 in
+// the absorbed form, and the expansion 262144 a head and token of the
+// context, so this form is the cheaper one from about 170 new tokens a
+// sequence on.
+//
+// First kernel (expand): per sequence, tiles of 128 tokens times a head's
+// 256 rows of (Uk_h; Uv_h) on the 5th-generation tensor cores,
+//   D = C U^T   M = 128 tokens, N = 256, K = 512
+// The tile's latent rows (128 KB) stay in shared memory for all of a block's
+// heads, the weights come in chunks of 64 columns; D has two buffers in
+// tensor memory (all 512 columns), so that the products of a head run while
+// the last one's result is rounded and stored.  Blocks take equal shares of
+// all (tile, head) pairs.  The result [head, token, (key 128, value 128)] and
+// the tokens' rotary keys go to the workspace, sequences padded to 128 tokens
+// with zeros.
+//
+// Second kernel (attend): a block is one head and 256 new tokens of a
+// sequence, as two tiles of 128, the M of the products:
+//   S = Q K^T   N = 64 keys of a stage, K = 192  (S in TMEM, two buffers)
+//   O += P V    N = 128, K = 64                  (P over S, O in TMEM)
+// Warps 0..7 softmax (a warpgroup a tile, a thread a row), 8 TMA, 9 and 10
+// issue the products, one a tile.  The running maximum is raised, and O
+// rescaled, only when it grew by more than 2^8.  Sums and maxima are fp32; P
+// is rounded to the operand type, K and V were when they were expanded (half
+// a step each).
+#include <limits.h>
+#include <math.h>
+
+#include "pa_common.cuh"
+#include "pa_latent.h"
+#include "pa_shares.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kNope = 128, kValue = 128, kUp = kNope + kValue;  // of a head: keys' share of the latent, values
+constexpr int kQk = kNope + kRopeDim;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------------------------ expand
+constexpr int kExTokens = 128;
+constexpr int kExThreads = 6 * 32;
+constexpr int kExTmaWarp = 4, kExMmaWarp = 5;
+constexpr int kExColumns = kLatentDim / 64;             // 128-byte columns of the latent part
+constexpr int kExGroup = kExColumns * 1024;             // 8 rows
+constexpr int kExABytes = kExTokens / 8 * kExGroup;
+constexpr int kExBBytes = kUp * 128;                    // a chunk of 64 columns
+constexpr int kExRing = 3;
+constexpr int kExSmem = 2048 + kExABytes + kExRing * kExBBytes;
+
+struct ExpandParams {
+  CUtensorMap tmap_c;   // the cache's latent columns, a block a box
+  CUtensorMap tmap_u;   // [H * 256, 512], boxes of {64, 256}
+  const uint8_t *cache;
+  const int32_t *tables, *lens;
+  uint8_t *kv;          // [H, capacity, 256]
+  uint8_t *rope;        // [capacity, 64]
+  long long *prefix;    // [S + 1] token tiles before sequence s
+  int num_seqs, heads, num_blocks, bs_shift, max_blocks, limit;
+  long long capacity;   // tokens
+  int *err;
+};
+
+struct ExpandHeader {
+  uint64_t a_full, a_empty, b_full[kExRing], b_empty[kExRing], d_full[2], d_empty[2], fin;
+  uint32_t tmem;
+  int abort;
+  ShareScan<128> scan;
+};
+static_assert(sizeof(ExpandHeader) <= 2048, "the header's place");
+
+// 32 bytes to global memory (32-byte aligned)
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[16], int at) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[at]), "r"(w[at + 1]),
+               "r"(w[at + 2]), "r"(w[at + 3]), "r"(w[at + 4]), "r"(w[at + 5]), "r"(w[at + 6]), "r"(w[at + 7])
+               : "memory");
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __grid_constant__ ExpandParams p) {
+  constexpr uint32_t IDESC = umma_idesc_f16(DT == kF16 ? 0 : 1, kExTokens, kUp, false);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  ExpandHeader &hdr = *reinterpret_cast<ExpandHeader *>(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  launch_dependents();
+  if ((smem_addr(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) record_error(p.err, kErrSmemAlign);
+    return;
+  }
+  auto tiles_of = [&](int s) { return (checked_len(p.lens, s, p.limit, p.err) + kExTokens - 1) / kExTokens; };
+  auto units_of = [&](int s) -> long long { return static_cast<long long>(tiles_of(s)) * p.heads; };
+  ShareScan<128> &scan = hdr.scan;
+  {
+    const int n = ShareScan<128>::run(p.num_seqs), t = threadIdx.x;
+    long long sum = 0;
+    if (t < 128) {
+      for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) sum += units_of(s);
+      scan.base[t + 1] = sum;
+      if (t == 0) scan.base[0] = 0;
+    }
+    __syncthreads();
+    for (int d = 1; d < 128; d <<= 1) {
+      const long long x = t < 128 && t >= d ? scan.base[t + 1 - d] : 0;
+      __syncthreads();
+      if (t < 128) scan.base[t + 1] += x;
+      __syncthreads();
+    }
+    if (blockIdx.x == 0 && t < 128) {
+      long long at = scan.base[t] / p.heads;
+      for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
+        p.prefix[s] = at;
+        at += tiles_of(s);
+      }
+      if (t == 0) p.prefix[p.num_seqs] = scan.total() / p.heads;
+    }
+  }
+  const long long total = scan.total();
+  const long long u0 = share_begin(blockIdx.x, total, gridDim.x), u1 = share_begin(blockIdx.x + 1, total, gridDim.x);
+  if (u0 >= u1) return;
+  long long first0;
+  const int s0 = scan.find(u0, p.num_seqs, units_of, first0);
+  volatile int *abort = &hdr.abort;
+  uint8_t *as = smem + 2048, *bsm = as + kExABytes;
+  if (warp == kExTmaWarp && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_c)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_u)) : "memory");
+    mbar_init(&hdr.a_full, 1);
+    mbar_init(&hdr.a_empty, 1);
+    for (int i = 0; i < kExRing; ++i) {
+      mbar_init(&hdr.b_full[i], 1);
+      mbar_init(&hdr.b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&hdr.d_full[i], 1);
+      mbar_init(&hdr.d_empty[i], 128);
+    }
+    mbar_init(&hdr.fin, 1);
+    hdr.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kExMmaWarp) tc_alloc(&hdr.tmem, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = hdr.tmem;
+
+  // A share as runs of heads of one token tile.
+  struct Run {
+    int s, tile, h0, h1;   // heads [h0, h1) of token tile `tile` of sequence s
+    long long row;         // the tile's first row of the workspace
+    int L;
+  };
+  long long u = u0, first = first0;
+  int s = s0;
+  auto next = [&](Run &r) {
+    while (u < u1) {
+      const int tiles = (checked_len(p.lens, s, p.limit, nullptr) + kExTokens - 1) / kExTokens;
+      const long long all = static_cast<long long>(tiles) * p.heads;
+      if (u >= first + all) {
+        first += all;
+        ++s;
+        continue;
+      }
+      r.s = s;
+      r.L = checked_len(p.lens, s, p.limit, nullptr);
+      r.tile = static_cast<int>((u - first) / p.heads);
+      r.h0 = static_cast<int>((u - first) - static_cast<long long>(r.tile) * p.heads);
+      r.h1 = u1 - u < p.heads - r.h0 ? r.h0 + static_cast<int>(u1 - u) : p.heads;
+      r.row = (first / p.heads + r.tile) * kExTokens;
+      u += r.h1 - r.h0;
+      return true;
+    }
+    return false;
+  };
+  Run r;
+  if (warp < 4) {
+    // -------------------------------------------------------------- results
+    bool ok = true;
+    int i = 0;
+    const int row = threadIdx.x;
+    while (ok && next(r)) {
+      const int token = r.tile * kExTokens + row;
+      const bool fits = r.row + kExTokens <= p.capacity;
+      if (!fits && threadIdx.x == 0) record_error(p.err, kErrSeqLen);
+      if (fits && r.h0 == 0) {  // the tile's rotary keys
+        uint4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (token < r.L) {
+          int b = __ldg(p.tables + static_cast<size_t>(r.s) * p.max_blocks + (token >> p.bs_shift));
+          if (b < 0 || b >= p.num_blocks) b = 0;  // (reported by the TMA warp)
+          const uint8_t *from = p.cache +
+                                (((static_cast<size_t>(b) << p.bs_shift) + (token & ((1 << p.bs_shift) - 1))) * kLatentRow +
+                                 kLatentDim) * 2;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = __ldg(reinterpret_cast<const uint4 *>(from) + j);
+        }
+        uint4 *to = reinterpret_cast<uint4 *>(p.rope + (r.row + row) * (kRopeDim * 2));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) to[j] = x[j];
+      }
+      for (int h = r.h0; h < r.h1; ++h, ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&hdr.d_full[i & 1], (i >> 1) & 1, abort))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem + (i & 1) * kUp + (static_cast<uint32_t>(32 * warp) << 16);
+        uint8_t *to = p.kv + ((static_cast<size_t>(h) * p.capacity + r.row + row) * kUp) * 2;
+#pragma unroll
+        for (int c = 0; c < kUp; c += 32) {
+          uint32_t v[32], w[16];
+          tc_ld32(d + c, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = token < r.L ? pack2_rn<DT>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])) : 0u;
+          if (fits) {
+            st_global_32(to + c * 2, w, 0);
+            st_global_32(to + c * 2 + 32, w, 8);
+          }
+        }
+        tc_fence_before_sync();
+        mbar_arrive(&hdr.d_empty[i & 1]);
+      }
+    }
+    if (!ok) {
+      record_error(p.err, kErrTimeout);
+      *abort = 1;
+    }
+  } else if (warp == kExTmaWarp) {
+    // ------------------------------------------------------------------ TMA
+    bool ok = true;
+    int chunk = 0, runs = 0;
+    while (ok && next(r)) {
+      const int boxes = kExTokens >> p.bs_shift;
+      const int n_box = min(boxes, (r.L - r.tile * kExTokens + (1 << p.bs_shift) - 1) >> p.bs_shift);
+      const uint32_t box = (1u << p.bs_shift) / 8 * kExGroup;
+      int b = 0;
+      if (lane < n_box) {
+        b = __ldg(p.tables + static_cast<size_t>(r.s) * p.max_blocks + r.tile * boxes + lane);
+        if (b < 0 || b >= p.num_blocks) {
+          record_error(p.err, kErrBlockIndex);
+          b = 0;
+        }
+      }
+      bool got = true;
+      if (lane == 0 && runs > 0) got = mbar_wait(&hdr.a_empty, (runs - 1) & 1, abort);
+      if (!__shfl_sync(0xffffffffu, got, 0)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&hdr.a_full, n_box * box);
+      __syncwarp();
+      if (lane < n_box)
+        tma_load_4d(as + lane * box, &p.tmap_c, 0, 0, 0, b << (p.bs_shift - 3), &hdr.a_full);
+      ++runs;
+      if (lane == 0) {
+        for (int h = r.h0; ok && h < r.h1; ++h)
+          for (int c = 0; c < kExColumns; ++c, ++chunk) {
+            const int st = chunk % kExRing;
+            if (chunk >= kExRing && !mbar_wait(&hdr.b_empty[st], (chunk / kExRing - 1) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&hdr.b_full[st], kExBBytes);
+            tma_load_2d(bsm + st * kExBBytes, &p.tmap_u, c * 64, h * kUp, &hdr.b_full[st]);
+          }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0 && !ok) {
+      record_error(p.err, kErrTimeout);
+      *abort = 1;
+      if (runs > 0) mbar_wait(&hdr.a_full, (runs - 1) & 1, nullptr);  // copies in flight land first
+      for (int j = max(0, chunk - kExRing); j < chunk; ++j)
+        mbar_wait(&hdr.b_full[j % kExRing], (j / kExRing) & 1, nullptr);
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------------ MMA
+    bool ok = true;
+    int i = 0, chunk = 0;
+    for (int runs = 0; ok && next(r); ++runs) {
+      ok = mbar_wait(&hdr.a_full, runs & 1, abort);
+      for (int h = r.h0; ok && h < r.h1; ++h, ++i) {
+        if (i >= 2 && !mbar_wait(&hdr.d_empty[i & 1], ((i >> 1) - 1) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d = tmem + (i & 1) * kUp;
+        for (int c = 0; c < kExColumns; ++c, ++chunk) {
+          const int st = chunk % kExRing;
+          if (!mbar_wait(&hdr.b_full[st], (chunk / kExRing) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint64_t a0 = umma_desc_sw128(smem_addr(as) + c * 1024, 16, kExGroup);
+          const uint64_t b0 = umma_desc_sw128(smem_addr(bsm) + st * kExBBytes, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16(d, a0 + (kk * 32 >> 4), b0 + (kk * 32 >> 4), IDESC, (c > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(&hdr.b_empty[st]);
+        }
+        if (ok) tc_commit(&hdr.d_full[i & 1]);
+      }
+      if (ok) tc_commit(&hdr.a_empty);
+    }
+    if (!ok) {
+      record_error(p.err, kErrTimeout);
+      *abort = 1;
+    }
+    tc_commit(&hdr.fin);
+    mbar_wait(&hdr.fin, 0, nullptr);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kExMmaWarp) {
+    tc_fence_after_sync();
+    tc_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ attend
+constexpr int kRows = 128;                      // of a tile (M)
+constexpr int kTiles = 2;
+constexpr int kKeys = 64;                       // of a stage
+constexpr int kHalf = kKeys * 128;              // 64 keys x 128 bytes
+constexpr int kKHalves = kQk / 64, kVHalves = kValue / 64;
+constexpr int kStageBytes = (kKHalves + kVHalves) * kHalf;
+constexpr int kStages = 3;
+constexpr int kQHalf = kRows * 128;
+constexpr int kQTile = kKHalves * kQHalf;
+constexpr int kQOff = 1024, kStageOff = kQOff + kTiles * kQTile;
+constexpr int kAttnSmem = kStageOff + kStages * kStageBytes;
+constexpr int kAttnThreads = 11 * 32;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kTileCols = 256;             // TMEM columns of a tile: S 2 x 64, O 128
+constexpr float kLazy = 8.f;
+
+struct AttendParams {
+  CUtensorMap tmap_q;     // [T, H, 192], boxes {64, 1, 128}
+  CUtensorMap tmap_kv;    // [H * capacity, 256], boxes {64, 64}
+  CUtensorMap tmap_rope;  // [capacity, 64], boxes {64, 64}
+  void *out;
+  const int32_t *cu_q, *lens;
+  const long long *prefix;
+  int heads, num_q_tokens, max_q_len, limit;
+  long long capacity;
+  float scale_log2;
+  int *err;
+};
+
+struct AttendHeader {
+  uint64_t kv_full[kStages], kv_empty[kStages], s_full[kTiles][2], p_full[kTiles][2], pv_done[kTiles], o_ready[kTiles],
+      q_full, fin[kTiles];
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int AB = DT == kF16 ? 0 : 1;
+  constexpr uint32_t IDESC_QK = umma_idesc_f16(AB, kRows, kKeys, false);
+  constexpr uint32_t IDESC_PV = umma_idesc_f16(AB, kRows, kValue, true);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  AttendHeader &hdr = *reinterpret_cast<AttendHeader *>(smem);
+  const int cta = gridDim.x - 1 - blockIdx.x;  // the longest (last) ranges first
+  const int h = blockIdx.z, s = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == kTmaWarp && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_kv)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_rope)) : "memory");
+  }
+  const int q0 = __ldg(p.cu_q + s), n = __ldg(p.cu_q + s + 1) - q0, L = __ldg(p.lens + s);
+  if (n < 0 || q0 < 0 || n > p.num_q_tokens - q0 || n > p.max_q_len || L < n || L > p.limit) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) record_error(p.err, kErrSeqLen);
+    return;
+  }
+  if (cta * kTiles * kRows >= n) return;
+  if ((smem_addr(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) record_error(p.err, kErrSmemAlign);
+    return;
+  }
+  const int tok0 = cta * kTiles * kRows;
+  const int tiles = tok0 + kRows < n ? 2 : 1;
+  const int pos0 = L - n;
+  const int kv_end = pos0 + min(n, tok0 + kTiles * kRows);
+  const int n_stages = (kv_end + kKeys - 1) / kKeys;
+  auto tile_stages = [&](int t) { return (pos0 + min(n, tok0 + (t + 1) * kRows) + kKeys - 1) / kKeys; };
+  uint8_t *qs = smem + kQOff, *stages = smem + kStageOff;
+  volatile int *abort = &hdr.abort;
+  if (warp == kTmaWarp && lane == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&hdr.kv_full[i], 1);
+      mbar_init(&hdr.kv_empty[i], tiles);
+    }
+    for (int t = 0; t < kTiles; ++t) {
+      mbar_init(&hdr.s_full[t][0], 1);
+      mbar_init(&hdr.s_full[t][1], 1);
+      mbar_init(&hdr.p_full[t][0], kRows);
+      mbar_init(&hdr.p_full[t][1], kRows);
+      mbar_init(&hdr.pv_done[t], 1);
+      mbar_init(&hdr.o_ready[t], 1);
+      mbar_init(&hdr.fin[t], 1);
+    }
+    mbar_init(&hdr.q_full, 1);
+    hdr.abort = 0;
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&hdr.q_full, tiles * kQTile);
+    for (int t = 0; t < tiles; ++t)
+      for (int c = 0; c < kKHalves; ++c)
+        tma_load_3d(qs + t * kQTile + c * kQHalf, &p.tmap_q, c * 64, h, q0 + tok0 + t * kRows, &hdr.q_full);
+  }
+  if (warp == kMmaWarp) tc_alloc(&hdr.tmem, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = hdr.tmem;
+  grid_dependency_wait();  // the expansion
+  const long long row0 = p.prefix[s] * kExTokens;
+  const bool there = row0 + (static_cast<long long>(L) + kExTokens - 1) / kExTokens * kExTokens <= p.capacity;
+
+  if (!there) {
+    // more tokens than the caller's bound: nothing was expanded (reported there)
+    if (warp == kTmaWarp && lane == 0) mbar_wait(&hdr.q_full, 0, nullptr);
+  } else if (warp < 4 * kTiles) {
+    if (warp / 4 < tiles) {
+      // ------------------------------------------------------------ softmax
+      const int t = warp / 4, r = threadIdx.x & 127;
+      const int tok = tok0 + t * kRows + r;
+      const int pos = pos0 + min(tok, n - 1);
+      const uint32_t trow = tmem + t * kTileCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+      const float c = p.scale_log2;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      const int nst = tile_stages(t);
+      for (int i = 0; i < nst; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&hdr.s_full[t][i & 1], (i >> 1) & 1, abort))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const int k0 = i * kKeys;
+        float sv[kKeys];
+        {
+          uint32_t raw[32];
+          tc_ld32(trow + (i & 1) * kKeys, raw);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sv[j] = __uint_as_float(raw[j]);
+          tc_ld32(trow + (i & 1) * kKeys + 32, raw);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sv[32 + j] = __uint_as_float(raw[j]);
+        }
+        // stages wholly at or before every row of the warp need no mask, and
+        // with a positive scale the maximum is taken on the raw scores and
+        // the scale folded into the exponent's fma
+        const bool plain = __all_sync(0xffffffffu, c > 0.f && k0 + kKeys - 1 <= pos);
+        float mx, cm;
+        if (plain) {
+          float a = sv[0], b = sv[32];
+#pragma unroll
+          for (int j = 1; j < 31; j += 2) {
+            a = fmax3(a, sv[j], sv[j + 1]);
+            b = fmax3(b, sv[32 + j], sv[33 + j]);
+          }
+          mx = fmax3(a, b, fmaxf(sv[31], sv[63])) * c;
+          cm = c;
+        } else {
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < kKeys; j += 2) {
+            sv[j] = (k0 + j <= pos) ? sv[j] * c : -INFINITY;
+            sv[j + 1] = (k0 + j + 1 <= pos) ? sv[j + 1] * c : -INFINITY;
+            mx0 = fmaxf(mx0, sv[j]);
+            mx1 = fmaxf(mx1, sv[j + 1]);
+          }
+          mx = fmaxf(mx0, mx1);
+          cm = 1.f;
+        }
+        const bool grow = mx > m + kLazy;
+        if (__any_sync(0xffffffffu, grow && i > 0)) {
+          // (pv_done is at most one phase behind: S of this stage was issued
+          // after the P V before the previous one, and products complete in order)
+          if (!__all_sync(0xffffffffu, mbar_wait(&hdr.pv_done[t], (i - 1) & 1, abort))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const float alpha = grow ? exp2_fast(m - mx) : 1.f;
+#pragma unroll
+          for (int d = 0; d < kValue; d += 32) {
+            uint32_t ov[32];
+            tc_ld32(trow + 2 * kKeys + d, ov);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+            tc_st32(trow + 2 * kKeys + d, ov);
+          }
+        }
+        if (grow) {
+          l *= exp2_fast(m - mx);
+          m = mx;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const uint64_t cm2 = f2(cm, cm), nb2 = f2(-base, -base);
+        uint64_t sum0 = f2(0.f, 0.f), sum1 = sum0;
+        uint32_t pw[kKeys / 2];
+#pragma unroll
+        for (int j = 0; j < kKeys; j += 2) {
+          float x, y;
+          f2_split(ffma2(f2(sv[j], sv[j + 1]), cm2, nb2), x, y);
+          const float a = exp2_fast(x), b = exp2_fast(y);
+          pw[j / 2] = pack2_rn<DT>(a, b);
+          if ((j & 2) == 0)
+            sum0 = fadd2(sum0, f2(a, b));
+          else
+            sum1 = fadd2(sum1, f2(a, b));
+        }
+        {
+          float l0, l1, l2, l3;
+          f2_split(sum0, l0, l1);
+          f2_split(sum1, l2, l3);
+          l += (l0 + l1) + (l2 + l3);
+        }
+        tc_st32(trow + (i & 1) * kKeys, pw);  // P over the S buffer just read
+        tc_fence_before_sync();
+        mbar_arrive(&hdr.p_full[t][i & 1]);
+      }
+      if (ok && __all_sync(0xffffffffu, mbar_wait(&hdr.o_ready[t], 0, abort))) {
+        tc_fence_after_sync();
+        // O / l through this tile's q buffer, whose products have all
+        // completed, so that whole rows leave
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        constexpr int RB = kValue * 2, CPR = RB / 16;
+        uint8_t *stg = qs + t * kQTile;
+#pragma unroll
+        for (int d = 0; d < kValue; d += 32) {
+          uint32_t ov[32];
+          tc_ld32(trow + 2 * kKeys + d, ov);
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = l == 0.f ? 0u : pack2_rn<DT>(__uint_as_float(ov[j + 2 * e]) * inv,
+                                                  __uint_as_float(ov[j + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4 *>(stg + r * RB + ((((d + j) / 8) ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+        // a warp's own 32 rows
+        const int first = tok0 + t * kRows + 32 * (warp & 3);
+        const int rows = min(32, n - first);
+        uint8_t *obase = static_cast<uint8_t *>(p.out) + (static_cast<size_t>(q0 + first) * p.heads + h) * RB;
+        const size_t stride = static_cast<size_t>(p.heads) * RB;
+        const uint8_t *wst = stg + 32 * (warp & 3) * RB;
+#pragma unroll 4
+        for (int idx = lane; idx < rows * CPR; idx += 32) {
+          const int rr = idx / CPR, ch = idx % CPR;
+          *reinterpret_cast<uint4 *>(obase + rr * stride + ch * 16) =
+              *reinterpret_cast<const uint4 *>(wst + rr * RB + ((ch ^ (rr & 7)) << 4));
+        }
+      } else {
+        record_error(p.err, kErrTimeout);
+        *abort = 1;
+      }
+    }
+  } else if (warp == kTmaWarp) {
+    // ---------------------------------------------------------------- TMA
+    if (lane == 0) {
+      bool ok = true;
+      int issued = 0;
+      const int kvrow = static_cast<int>(h * p.capacity + row0), rrow = static_cast<int>(row0);
+      for (int i = 0; i < n_stages; ++i) {
+        const int st = i % kStages;
+        if (i >= kStages && !mbar_wait(&hdr.kv_empty[st], (i / kStages - 1) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        uint8_t *kb = stages + st * kStageBytes;
+        mbar_arrive_expect_tx(&hdr.kv_full[st], kStageBytes);
+#pragma unroll
+        for (int c = 0; c < kNope / 64; ++c)
+          tma_load_2d(kb + c * kHalf, &p.tmap_kv, c * 64, kvrow + i * kKeys, &hdr.kv_full[st]);
+        tma_load_2d(kb + (kNope / 64) * kHalf, &p.tmap_rope, 0, rrow + i * kKeys, &hdr.kv_full[st]);
+#pragma unroll
+        for (int c = 0; c < kVHalves; ++c)
+          tma_load_2d(kb + (kKHalves + c) * kHalf, &p.tmap_kv, kNope + c * 64, kvrow + i * kKeys, &hdr.kv_full[st]);
+        issued = i + 1;
+      }
+      if (!ok) {
+        record_error(p.err, kErrTimeout);
+        *abort = 1;
+        for (int j = max(0, issued - kStages); j < issued; ++j)
+          mbar_wait(&hdr.kv_full[j % kStages], (j / kStages) & 1, nullptr);
+      }
+      mbar_wait(&hdr.q_full, 0, nullptr);
+    }
+  } else {
+    // ---------------------------------------------------------------- MMA
+    const int t = warp - kMmaWarp;
+    if (lane == 0 && t < tiles) {
+      bool ok = mbar_wait(&hdr.q_full, 0, abort);
+      const uint32_t qt = smem_addr(qs) + t * kQTile, sa = smem_addr(stages), tt = tmem + t * kTileCols;
+      auto issue_qk = [&](int i) -> bool {
+        const int st = i % kStages;
+        if (!mbar_wait(&hdr.kv_full[st], (i / kStages) & 1, abort)) return false;
+        tc_fence_after_sync();
+        const uint64_t a0 = umma_desc_sw128(qt, 16, 1024), b0 = umma_desc_sw128(sa + st * kStageBytes, 16, 1024);
+        const uint32_t d = tt + (i & 1) * kKeys;
+#pragma unroll
+        for (int kk = 0; kk < kQk / 16; ++kk) {
+          const uint32_t off = (kk % 4) * 32;
+          tc_mma_f16(d, a0 + (((kk / 4) * kQHalf + off) >> 4), b0 + (((kk / 4) * kHalf + off) >> 4), IDESC_QK, kk > 0);
+        }
+        tc_commit(&hdr.s_full[t][i & 1]);
+        return true;
+      };
+      const int nst = tile_stages(t);
+      if (ok) ok = issue_qk(0);
+      for (int i = 0; i < nst && ok; ++i) {
+        if (i + 1 < nst && !issue_qk(i + 1)) {
+          ok = false;
+          break;
+        }
+        if (!mbar_wait(&hdr.p_full[t][i & 1], (i >> 1) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint64_t b0 = umma_desc_sw128(sa + (i % kStages) * kStageBytes + kKHalves * kHalf, kHalf, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          tc_mma_f16_ta(tt + 2 * kKeys, tt + (i & 1) * kKeys + kk * 8, b0 + kk * (2 * 1024 >> 4), IDESC_PV,
+                        (i > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(&hdr.pv_done[t]);
+        if (i + 1 == nst) tc_commit(&hdr.o_ready[t]);
+        tc_commit(&hdr.kv_empty[i % kStages]);
+      }
+      // stages behind this tile's rows: released once filled
+      for (int i = nst; i < n_stages && ok; ++i) {
+        if (!mbar_wait(&hdr.kv_full[i % kStages], (i / kStages) & 1, abort)) {
+          ok = false;
+          break;
+        }
+        tc_commit(&hdr.kv_empty[i % kStages]);
+      }
+      if (!ok) {
+        record_error(p.err, kErrTimeout);
+        *abort = 1;
+      }
+      tc_commit(&hdr.fin[t]);
+      mbar_wait(&hdr.fin[t], 0, nullptr);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after_sync();
+    tc_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host
+struct Sizes {
+  size_t prefix, rope, kv, total;
+  long long capacity;
+};
+bool sizes_of(int S, int H, long long tokens, Sizes *z) {
+  if (S < 0 || H <= 0 || tokens < 0 || tokens > INT_MAX / 4) return false;
+  // sequences padded to a tile of tokens
+  const long long tiles = (tokens + static_cast<long long>(S) * (kExTokens - 1)) / kExTokens + 1;
+  z->capacity = tiles * kExTokens;
+  if (z->capacity * H > INT_MAX) return false;  // 32-bit rows
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  z->prefix = up(8 * (static_cast<size_t>(S) + 1));
+  z->rope = up(static_cast<size_t>(z->capacity) * kRopeDim * 2);
+  z->kv = up(static_cast<size_t>(z->capacity) * H * kUp * 2);
+  z->total = z->prefix + z->rope + z->kv;
+  return true;
+}
+
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc != nullptr &&
+         enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DT>
+pa_status launch(const ExpandParams &ep, const AttendParams &ap, int num_seqs, int max_q_len, cudaStream_t stream) {
+  static bool configured[64];  // per device: dynamic shared memory already allowed
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    e = cudaFuncSetAttribute(latent_expand_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(latent_attend_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  DeviceInfo info;
+  if (!current_device_info(&info)) return cuda_fail(cudaGetLastError());
+  latent_expand_kernel<DT><<<info.sm_count, kExThreads, kExSmem, stream>>>(ep);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((max_q_len + kTiles * kRows - 1) / (kTiles * kRows), num_seqs, ap.heads);
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = kAttnSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, latent_attend_kernel<DT>, ap);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_latent_prefill_workspace_size(int32_t num_seqs, int32_t num_heads, int64_t num_kv_tokens) {
+  Sizes z;
+  return sizes_of(num_seqs, num_heads, num_kv_tokens, &z) ? z.total : 0;
+}
+
+extern "C" pa_status pa_latent_prefill(void *out, const void *q, int32_t q_dtype, int32_t num_q_tokens,
+                                       const int32_t *cu_q_lens, int32_t num_seqs, int32_t num_heads,
+                                       int32_t max_q_len, const void *up, const void *cache,
+                                       const pa_latent_desc *desc, const int32_t *block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t *seq_lens, int64_t num_kv_tokens,
+                                       float scale, void *workspace, size_t workspace_bytes, int *device_error,
+                                       pa_stream_t stream) {
+  if (!valid_latent_desc(desc) || num_seqs < 0 || num_heads <= 0 || max_q_len < 0 || num_q_tokens < 0 ||
+      num_kv_tokens < 0 || max_blocks_per_seq <= 0 || !isfinite(scale))
+    return PA_ERR_INVALID;
+  if (num_seqs == 0 || max_q_len == 0 || num_q_tokens == 0) return PA_OK;
+  if (!out || !q || !cu_q_lens || !up || !cache || !block_tables || !seq_lens || !workspace) return PA_ERR_INVALID;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(up) || !aligned16(cache) ||
+      ((reinterpret_cast<uintptr_t>(cu_q_lens) | reinterpret_cast<uintptr_t>(block_tables) |
+        reinterpret_cast<uintptr_t>(seq_lens)) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PA_ERR_INVALID;
+  if (!supported_latent_desc(desc) || q_dtype != desc->dtype) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_heads > 65535) return PA_ERR_UNSUPPORTED;  // grid limits
+  Sizes z;
+  if (!sizes_of(num_seqs, num_heads, num_kv_tokens, &z)) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < z.total) return PA_ERR_INVALID;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const long long held = static_cast<long long>(max_blocks_per_seq) * desc->block_size;
+  ExpandParams ep{};
+  ep.cache = static_cast<const uint8_t *>(cache);
+  ep.tables = block_tables;
+  ep.lens = seq_lens;
+  ep.prefix = reinterpret_cast<long long *>(ws);
+  ep.rope = ws + z.prefix;
+  ep.kv = ws + z.prefix + z.rope;
+  ep.num_seqs = num_seqs;
+  ep.heads = num_heads;
+  ep.num_blocks = desc->num_blocks;
+  ep.bs_shift = log2_block(desc->block_size);
+  ep.max_blocks = max_blocks_per_seq;
+  ep.limit = static_cast<int>(held < INT_MAX / 4 ? held : INT_MAX / 4);
+  ep.capacity = z.capacity;
+  ep.err = device_error;
+  AttendParams ap{};
+  ap.out = out;
+  ap.cu_q = cu_q_lens;
+  ap.lens = seq_lens;
+  ap.prefix = ep.prefix;
+  ap.heads = num_heads;
+  ap.num_q_tokens = num_q_tokens;
+  ap.max_q_len = max_q_len;
+  ap.limit = ep.limit;
+  ap.capacity = z.capacity;
+  ap.scale_log2 = scale * 1.4426950408889634f;
+  ap.err = device_error;
+  const cuuint64_t H = num_heads, cap = z.capacity;
+  const cuuint64_t du[2] = {kLatentDim, H * kUp}, su[1] = {kLatentDim * 2};
+  const cuuint32_t bu[2] = {64, kUp};
+  const cuuint64_t dq[3] = {kQk, H, static_cast<cuuint64_t>(num_q_tokens)}, sq[2] = {kQk * 2, H * kQk * 2};
+  const cuuint32_t bq[3] = {64, 1, kRows};
+  const cuuint64_t dk[2] = {kUp, H * cap}, sk[1] = {kUp * 2};
+  const cuuint64_t dr[2] = {kRopeDim, cap}, sr[1] = {kRopeDim * 2};
+  const cuuint32_t bk[2] = {64, kKeys};
+  if (!encode_latent_view(&ep.tmap_c, cache, desc, kExColumns, desc->block_size / 8) ||
+      !encode(&ep.tmap_u, up, 2, du, su, bu) || !encode(&ap.tmap_q, q, 3, dq, sq, bq) ||
+      !encode(&ap.tmap_kv, ep.kv, 2, dk, sk, bk) || !encode(&ap.tmap_rope, ep.rope, 2, dr, sr, bk))
+    return cuda_fail(cudaErrorInvalidValue);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return desc->dtype == PA_F16 ? launch<kF16>(ep, ap, num_seqs, max_q_len, st)
+                               : launch<kBF16>(ep, ap, num_seqs, max_q_len, st);
+}

@@ -93,7 +93,27 @@ def test_latent_decode_refuses(kw, status):
     assert decode(**kw) == status
 
 
+def prefill(**kw):
+    a = dict(out=PTR, q=PTR, qt=pa.PA_BF16, T=8, cu=PTR, S=1, H=16, most=8, up=PTR, cache=PTR, d=latent(), bt=PTR, nb=4,
+             sl=PTR, kv=64, scale=0.1, ws=PTR, wb=1 << 40, err=None, st=None)
+    a.update(kw)
+    return pa.load_library().pa_latent_prefill(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(S=0), OK), (dict(T=0), OK), (dict(most=0), OK), (dict(S=-1), INVALID), (dict(H=0), INVALID),
+    (dict(kv=-1), INVALID), (dict(d=None), INVALID), (dict(up=None), INVALID), (dict(cu=None), INVALID),
+    (dict(up=PTR + 8), INVALID), (dict(ws=PTR + 16), INVALID), (dict(wb=1000), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(qt=pa.PA_F16), UNSUPPORTED), (dict(S=70000), UNSUPPORTED),
+    (dict(kv=1 << 27), UNSUPPORTED), (dict(d=latent(rope=128)), UNSUPPORTED),
+])
+def test_latent_prefill_refuses(kw, status):
+    assert prefill(**kw) == status
+
+
 def test_workspace_sizes():
+    assert pa.pa_latent_prefill_workspace_size(2, 16, 100) >= 16 * 512 * 100
+    assert pa.pa_latent_prefill_workspace_size(2, 0, 100) == 0
     assert pa.pa_latent_decode_workspace_size(4, 1, 16) > 0
     assert pa.pa_latent_decode_workspace_size(4, 0, 16) == 0
     assert pa.pa_latent_decode_workspace_size(1, 1, 128) == pa.pa_latent_decode_workspace_size(2, 1, 128)

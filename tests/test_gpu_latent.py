@@ -222,6 +222,174 @@ def test_decode_captured_and_replayed_on_another_stream():
     check(out, want, tol)
 
 
+# ---------------------------------------------------------------- prefill
+def make_prefill(lens, new, heads, bs, dt, seed):
+    cache, table, L, _ = make(lens, 1, 1, bs, dt, seed)
+    g = gen(seed + 1)
+    T = sum(new)
+    q = randn(g, T, heads, 192).to(DT[dt])
+    up = (randn(g, heads, 256, LATENT) / math.sqrt(LATENT)).to(DT[dt])
+    cu = i32([sum(new[:s]) for s in range(len(new) + 1)])
+    return cache, table, L, q, up, cu
+
+
+def expect_prefill(cache, table, lens, q, up, cu, bs, scale, e):
+    """The definition, and the bound of `attend` with what the expansion adds:
+    keys and values are rounded to the cache's type (eps / 2 of each) after
+    sums of 512 products in 32 bits (2^-24 a partial sum, 512 of them)."""
+    o = torch.zeros(q.shape[0], q.shape[1], 128, dtype=torch.float64, device=DEV)
+    tol = torch.zeros_like(o)
+    cu = cu.tolist()
+    for s, L in enumerate(lens.tolist()):
+        x = rows_of(cache, table[s], L, bs)
+        n = cu[s + 1] - cu[s]
+        if n == 0:
+            continue
+        hidden = torch.arange(L, device=DEV)[None] > (L - n + torch.arange(n, device=DEV))[:, None]
+        for h in range(q.shape[1]):
+            u = up[h].double()
+            kv, kv_size = x[:, :LATENT] @ u.T, x[:, :LATENT].abs() @ u.abs().T
+            off = e / 2 * kv.abs() + 512 * 2.0 ** -24 * kv_size
+            key, qq = torch.cat((kv[:, :128], x[:, LATENT:]), 1), q[cu[s]:cu[s + 1], h].double()
+            w = torch.softmax((qq @ key.T * scale).masked_fill(hidden, -math.inf), -1)
+            v = kv[:, 128:]
+            out, spread = w @ v, w @ v.abs()
+            # scores: the keys' error, the sum of 192 products, the exponential
+            d = abs(scale) * ((qq[:, :128].abs() @ off[:, :128].T) + 194 * 2.0 ** -24 * (qq.abs() @ key.abs().T))
+            d = d.masked_fill(hidden, 0).amax(-1, keepdim=True) + 2.0 ** -21
+            o[cu[s]:cu[s + 1], h] = out
+            tol[cu[s]:cu[s + 1], h] = e / 2 * (out.abs() + spread) * 1.01 + 2 * d * spread + w @ off[:, 128:]
+    return o, tol
+
+
+def run_prefill(cache, table, lens, q, up, cu, scale, max_new, tokens, **kw):
+    out = torch.full((q.shape[0], q.shape[1], 128), float("nan"), dtype=q.dtype, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_latent_prefill(out, q, cu, up, cache, table, lens, max_new, tokens, scale, device_error=err, **kw)
+    assert int(err) == 0
+    return out
+
+
+PREFILL = [
+    # lens, new tokens, heads, block
+    ([1], [1], 1, 16),
+    ([128], [128], 2, 8),
+    ([129, 64], [129, 1], 3, 16),
+    ([100, 300, 0, 17], [3, 257, 0, 17], 4, 32),
+    ([1000], [600], 2, 16),
+    ([511, 512, 513], [255, 256, 257], 2, 32),
+    ([2000, 5], [40, 5], 16, 8),
+    ([70] * 20, [2] * 20, 5, 16),
+]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lens,new,heads,bs", PREFILL)
+def test_prefill_matches_the_definition(lens, new, heads, bs, dt):
+    cache, table, L, q, up, cu = make_prefill(lens, new, heads, bs, dt, seed=sum(lens) + heads)
+    got = run_prefill(cache, table, L, q, up, cu, SCALE, max(new), sum(lens))
+    want, tol = expect_prefill(cache, table, L, q, up, cu, bs, SCALE, eps(DT[dt]))
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("factor", [0.0, -2.0, 30.0])
+def test_prefill_scales(factor):
+    cache, table, L, q, up, cu = make_prefill([700, 64], [300, 64], 2, 16, "f16", 51)
+    got = run_prefill(cache, table, L, q, up, cu, SCALE * factor, 300, 764)
+    want, tol = expect_prefill(cache, table, L, q, up, cu, 16, SCALE * factor, eps(torch.float16))
+    check(got, want, tol)
+
+
+def test_prefill_bounds_above_and_rows_left_alone():
+    """Bounds larger than the lengths, rows of q behind the last sequence, a wider table."""
+    cache, table, L, q, up, cu = make_prefill([200, 30], [140, 30], 2, 16, "bf16", 53)
+    q = torch.cat((q, torch.full_like(q[:9], float("nan"))))
+    table = torch.cat((table, torch.full_like(table, -3)), 1).contiguous()
+    out = torch.full((q.shape[0], 2, 128), 5.0, dtype=q.dtype, device=DEV)
+    pa.pa_latent_prefill(out, q, cu, up, cache, table, L, 1000, 5000, SCALE)
+    want, tol = expect_prefill(cache, table, L, q[:170], up, cu, 16, SCALE, eps(torch.bfloat16))
+    check(out[:170], want, tol)
+    assert bool((out[170:] == 5.0).all())
+
+
+def test_prefill_reports_bad_lengths_blocks_and_bounds():
+    cache, table, L, q, up, cu = make_prefill([200, 300, 150], [20, 300, 150], 2, 16, "f16", 57)
+    want, tol = expect_prefill(cache, table, L, q, up, cu, 16, SCALE, eps(torch.float16))
+
+    def call(lens=L, tab=table, most=300, tokens=650):
+        out, err = torch.full((470, 2, 128), 5.0, dtype=q.dtype, device=DEV), i32([0])
+        pa.pa_latent_prefill(out, q, cu, up, cache, tab, lens, most, tokens, SCALE, device_error=err)
+        return out, int(err)
+
+    bad = L.clone()
+    bad[1] = 299                                   # fewer tokens than new ones
+    out, err = call(lens=bad)
+    assert err == 3 and bool((out[20:320] == 5).all())
+    check(out[:20], want[:20], tol[:20])
+    check(out[320:], want[320:], tol[320:])
+    out, err = call(most=299)
+    assert err == 3 and bool((out[20:320] == 5).all())
+    out, err = call(tokens=0)                      # far more tokens than the bound: the last do not fit
+    assert err == 3 and bool((out[320:] == 5).all())
+    check(out[:20], want[:20], tol[:20])
+    cache[0] = 0
+    want, tol = expect_prefill(cache, table, L, q, up, cu, 16, SCALE, eps(torch.float16))
+    t = table.clone()
+    t[1, 2] = 1 << 20
+    out, err = call(tab=t)
+    assert err == 1
+    check(out[:20], want[:20], tol[:20])
+
+
+def test_prefill_captured_and_replayed():
+    cache, table, L, q, up, cu = make_prefill([300, 260], [200, 260], 4, 32, "bf16", 59)
+    ws = torch.empty(pa.pa_latent_prefill_workspace_size(2, 4, 600), dtype=torch.uint8, device=DEV)
+    out = torch.empty(460, 4, 128, dtype=torch.bfloat16, device=DEV)
+    args = (out, q, cu, up, cache, table, L, 260, 600, SCALE)
+    pa.pa_latent_prefill(*args, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_latent_prefill(*args, workspace=ws)
+    ws.random_()
+    L.copy_(i32([250, 260]))
+    q.copy_(randn(gen(61), *q.shape))
+    up.mul_(0.5)
+    out.fill_(float("nan"))
+    graph.replay()
+    want, tol = expect_prefill(cache, table, L, q, up, cu, 32, SCALE, eps(torch.bfloat16))
+    check(out, want, tol)
+
+
+def test_serving_run_of_the_latent_calls():
+    """A prompt written and prefilled in its expanded form, then a token decoded in its absorbed form: the absorbed
+    result, projected, is what the expanded form gives for the same token."""
+    H, bs, n = 4, 16, 150
+    g = gen(67)
+    table, nb, _ = tables([n], bs, 67)
+    cache = torch.full((nb, bs, ROW), float("nan"), dtype=torch.float16, device=DEV)
+    rows = randn(g, n, ROW).half()
+    slots = (table[0].long()[:, None] * bs + torch.arange(bs, device=DEV)).flatten()[:n].contiguous()
+    up = (randn(g, H, 256, LATENT) / math.sqrt(LATENT)).half()
+    q = randn(g, n, H, 192).half()
+    pa.pa_latent_write(rows[:-1, :LATENT], rows[:-1, LATENT:], slots[:-1], cache)
+    a = run_prefill(cache, table, i32([n - 1]), q[:-1], up, i32([0, n - 1]), SCALE, n - 1, n)
+    pa.pa_latent_write(rows[-1:, :LATENT], rows[-1:, LATENT:], slots[-1:], cache)
+    b = run_prefill(cache, table, i32([n]), q, up, i32([0, n]), SCALE, n, n)
+    want, tol = expect_prefill(cache, table, i32([n]), q, up, i32([0, n]), bs, SCALE, eps(torch.float16))
+    check(a, want[:-1], tol[:-1])
+    check(b, want, tol)
+    absorbed = torch.cat((torch.einsum("hd,hdc->hc", q[-1, :, :128].double(), up[:, :128].double()),
+                          q[-1, :, 128:].double()), -1).half()
+    lat = run(cache, table, i32([n]), absorbed[None, None], SCALE)[0, 0]
+    got = torch.einsum("hc,hdc->hd", lat.double(), up[:, 128:].double())
+    # the absorbed query's and the latent result's roundings, through the up-projection
+    x = rows_of(cache, table[0], n, bs)
+    more = torch.einsum("hc,hdc->hd", eps(torch.float16) / 2 * lat.double().abs(), up[:, 128:].double().abs())
+    d = (absorbed.double().abs() * eps(torch.float16) / 2) @ x.abs().T * SCALE
+    spread = x[:, :LATENT].abs().amax(0) @ up[:, 128:].double().abs().transpose(1, 2)
+    check(got, want[-1], tol[-1] + more + 2 * d.amax(-1)[:, None] * spread)
+
+
 def test_blocks_move_under_a_nine_head_description():
     a, b = (randn(gen(s), 6, 16, ROW).bfloat16() for s in (41, 42))
     want_a, want_b = a.clone(), b.clone()
