@@ -19,13 +19,13 @@
 //
 // A block takes N query rows and an equal share of all sequences' 64-token
 // tiles (pa_shares.cuh).  Warps:
-//   0..3  softmax: a thread owns a token, its registers the query rows.  The
+//   0..7  softmax: a thread owns a token and half of the query rows.  The
 //         maximum of a query row is kept for all threads in shared memory and
 //         raised only when a score passes it by 2^8, so that almost every
 //         tile needs one vote of the block instead of a reduction over
 //         tokens; the total weights stay per thread until a sequence ends.
-//   4     TMA: q, then the tiles, a 16-token slot at a time
-//   5, 6  issue the S^T and O^T products
+//   8     TMA: q, then the tiles, a 16-token slot at a time
+//   9, 10 issue the S^T and O^T products
 #include <limits.h>
 #include <math.h>
 
@@ -45,9 +45,9 @@ constexpr int kGroup = kCols * kAtom;  // 8 rows
 constexpr int kTileBytes = kTile / 8 * kGroup;
 constexpr int kDims = 128;             // of one O^T product
 constexpr int kBlocksO = kLatentDim / kDims;
-constexpr int kTmaWarp = 4, kQkWarp = 5;  // and 6: O^T
-constexpr int kThreads = 7 * 32;
-constexpr int kSoftmaxThreads = 128;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kTmaWarp = 8, kQkWarp = 9;  // and 10: O^T
+constexpr int kThreads = 11 * 32;
 constexpr int kMaxWorkers = 152;       // shares of one row tile, at most; sizes the workspace
 constexpr int kMinTiles = 2;           // a smaller share only adds joining
 constexpr float kLazy = 8.f;
@@ -83,7 +83,7 @@ struct Header {
   uint32_t tmem;
   int abort;
   alignas(16) float m[64];  // the query rows' maxima (base 2), read four at a time
-  float top[4][64];   // a warp's maxima, then its total weights
+  float top[4][64];   // maxima of 16 tokens, then their total weights
   int see[64];        // tokens a query row sees
 };
 static_assert(sizeof(Header) <= 2048, "the header's place");
@@ -93,12 +93,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool x) {
   uint32_t y;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(y)
       : "r"(static_cast<uint32_t>(x))
       : "memory");
@@ -106,47 +106,59 @@ __device__ __forceinline__ bool softmax_any(bool x) {
 }
 
 // NCOL consecutive columns of the warp's lanes
+#define PA_R8(a, o) a(r[o]), a(r[o + 1]), a(r[o + 2]), a(r[o + 3]), a(r[o + 4]), a(r[o + 5]), a(r[o + 6]), a(r[o + 7])
 template <int NCOL>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[NCOL]) {
-  if constexpr (NCOL >= 32) {
-#pragma unroll
-    for (int c = 0; c < NCOL; c += 32) {
-      uint32_t r[32];
-      tc_ld32(taddr + c, r);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[c + j] = __uint_as_float(r[j]);
-    }
-  } else {
-    uint32_t r[16];
+  uint32_t r[NCOL];
+  if constexpr (NCOL == 32) {
+    tc_ld32(taddr, r);
+  } else if constexpr (NCOL == 16) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
         "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : PA_R8("=r", 0), PA_R8("=r", 8)
         : "r"(taddr)
         : "memory");
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+  } else {
+    static_assert(NCOL == 8, "8, 16 or 32 columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PA_R8("=r", 0)
+        : "r"(taddr)
+        : "memory");
   }
+#pragma unroll
+  for (int j = 0; j < NCOL; ++j) v[j] = __uint_as_float(r[j]);
 }
 template <int NCOL>
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[NCOL]) {
-  if constexpr (NCOL >= 32) {
+  uint32_t r[NCOL];
 #pragma unroll
-    for (int c = 0; c < NCOL; c += 32) {
-      uint32_t r[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(v[c + j]);
-      tc_st32(taddr + c, r);
-    }
-  } else {
+  for (int j = 0; j < NCOL; ++j) r[j] = __float_as_uint(v[j]);
+  if constexpr (NCOL == 32) {
+    tc_st32(taddr, r);
+  } else if constexpr (NCOL == 16) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        PA_R8("r", 0), PA_R8("r", 8)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        PA_R8("r", 0)
         : "memory");
   }
+}
+#undef PA_R8
+
+// One thread of the warp (converged).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t y;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
+  return y != 0;
 }
 
 __host__ __device__ inline long long worker_count(long long tiles, long long most) {
@@ -185,6 +197,7 @@ template <int DT, int N>
 __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid_constant__ LatentParams p,
                                                                     int max_workers) {
   using Lay = Layout<N>;
+  constexpr int NC = N / 2;  // query rows of a softmax thread
   constexpr int AB = DT == kF16 ? 0 : 1;
   constexpr uint32_t IDESC_QK = umma_idesc_f16(AB, kTile, N, false);
   constexpr uint32_t IDESC_PV = umma_idesc_f16(AB, kDims, N, true) | (1u << 15);  // (A dimension-major too)
@@ -261,10 +274,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   tc_fence_after_sync();
   const uint32_t tmem = hdr.tmem;
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-    const int token = lane < 16 ? 16 * warp + lane : INT_MAX / 2;  // M = 64 fills 16 lanes of each warp
+    const int quarter = warp & 3, c0 = (warp >> 2) * NC;  // 16 tokens, and the first of the thread's query rows
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c0;
+    const int k = 16 * quarter + lane;                       // the token, for lanes below 16 (M = 64 fills those)
+    const int token = lane < 16 ? k : INT_MAX / 2;
     // a wait that gave up leaves the warp in step with the others, whose
     // barriers count on it: it goes on without waiting, and nothing is stored
     bool ok = true;
@@ -272,13 +287,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
       tc_fence_after_sync();
     };
+    auto top_of = [&](int j) {
+      return fmaxf(fmaxf(hdr.top[0][c0 + j], hdr.top[1][c0 + j]), fmaxf(hdr.top[2][c0 + j], hdr.top[3][c0 + j]));
+    };
+    auto sum_of = [&](int j) {
+      return (hdr.top[0][c0 + j] + hdr.top[1][c0 + j]) + (hdr.top[2][c0 + j] + hdr.top[3][c0 + j]);
+    };
+    const float4 *m4 = reinterpret_cast<const float4 *>(hdr.m + c0);
     int i = 0;  // tiles so far
     for (int seg = 0; walk.next(p); ++seg) {
-      float l[N];
+      float l[NC];
 #pragma unroll
-      for (int h = 0; h < N; ++h) l[h] = 0.f;
+      for (int j = 0; j < NC; ++j) l[j] = 0.f;
       softmax_sync();  // the last piece's maxima and totals have been read
-      for (int h = threadIdx.x; h < N; h += kSoftmaxThreads) {
+      if (threadIdx.x < N) {
+        const int h = threadIdx.x;
         hdr.m[h] = -INFINITY;
         hdr.see[h] = h < n_rows ? walk.L - (p.new_tokens - 1 - (rt * N + h) / p.heads) : 0;
       }
@@ -287,88 +310,84 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       const int all_see = n_rows < N ? 0 : walk.L - (p.new_tokens - 1 - rt * N / p.heads);
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         wait(&hdr.s_full[i & 1], (i >> 1) & 1);
-        float x[N];
-        tmem_load<N>(tlane + Lay::TMEM_S + (i & 1) * N, x);
+        float x[NC];
+        tmem_load<NC>(tlane + Lay::TMEM_S + (i & 1) * N, x);
         tc_fence_before_sync();
         mbar_arrive(&hdr.s_empty[i & 1]);
         const int key = tile * kTile + token;
         if ((tile + 1) * kTile > all_see) {
 #pragma unroll
-          for (int h = 0; h < N; ++h) x[h] = key < hdr.see[h] ? x[h] * p.scale_log2 : -INFINITY;
+          for (int j = 0; j < NC; ++j) x[j] = key < hdr.see[c0 + j] ? x[j] * p.scale_log2 : -INFINITY;
         } else {
 #pragma unroll
-          for (int h = 0; h < N; ++h) x[h] = lane < 16 ? x[h] * p.scale_log2 : -INFINITY;
+          for (int j = 0; j < NC; ++j) x[j] = lane < 16 ? x[j] * p.scale_log2 : -INFINITY;
         }
         float over = -INFINITY;
-        const float4 *m4 = reinterpret_cast<const float4 *>(hdr.m);
 #pragma unroll
-        for (int h = 0; h < N; h += 4) {
-          const float4 m = m4[h / 4];
-          over = fmaxf(over, fmaxf(fmaxf(x[h] - m.x, x[h + 1] - m.y), fmaxf(x[h + 2] - m.z, x[h + 3] - m.w)));
+        for (int j = 0; j < NC; j += 4) {
+          const float4 m = m4[j / 4];
+          over = fmaxf(over, fmaxf(fmaxf(x[j] - m.x, x[j + 1] - m.y), fmaxf(x[j + 2] - m.z, x[j + 3] - m.w)));
         }
-        // (a first tile's maxima are -inf, and inf - inf of no score at all is a NaN, which is not over)
+        // (inf - inf of no score at all is a NaN, which is not over)
         if (softmax_any(over > kLazy)) {
-          // raise the maxima: each warp's over its tokens, then all four
+          // raise the maxima: over each warp's 16 tokens, then all four
 #pragma unroll
-          for (int h = 0; h < N; ++h) {
-            const int b = __float_as_int(x[h] == x[h] ? x[h] : -INFINITY);
+          for (int j = 0; j < NC; ++j) {
+            const int b = __float_as_int(x[j] == x[j] ? x[j] : -INFINITY);
             const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-            if (lane == 0) hdr.top[warp][h] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+            if (lane == 0) hdr.top[quarter][c0 + j] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
           }
           softmax_sync();
-          float f[N];
+          float f[NC];
 #pragma unroll
-          for (int h = 0; h < N; ++h) {
-            const float was = hdr.m[h];
-            const float top = fmaxf(fmaxf(hdr.top[0][h], hdr.top[1][h]), fmaxf(hdr.top[2][h], hdr.top[3][h]));
-            f[h] = top > was + kLazy ? exp2_fast(was - top) : 1.f;
-            l[h] *= f[h];
+          for (int j = 0; j < NC; ++j) {
+            const float was = hdr.m[c0 + j], top = top_of(j);
+            f[j] = top > was + kLazy ? exp2_fast(was - top) : 1.f;
+            l[j] *= f[j];
           }
           softmax_sync();
-          for (int h = threadIdx.x; h < N; h += kSoftmaxThreads) {
-            const float was = hdr.m[h];
-            const float top = fmaxf(fmaxf(hdr.top[0][h], hdr.top[1][h]), fmaxf(hdr.top[2][h], hdr.top[3][h]));
-            if (top > was + kLazy) hdr.m[h] = top;
+          if (quarter == 0 && lane < NC) {
+            const float top = top_of(lane);
+            if (top > hdr.m[c0 + lane] + kLazy) hdr.m[c0 + lane] = top;
           }
           softmax_sync();
           if (tile > walk.t0) {  // O^T holds the tiles before
             wait(&hdr.pv_done, (i - 1) & 1);
 #pragma unroll 1
             for (int b = 0; b < kBlocksO; ++b) {
-              float o[N];
-              tmem_load<N>(tlane + b * N, o);
+              float o[NC];
+              tmem_load<NC>(tlane + b * N, o);
 #pragma unroll
-              for (int h = 0; h < N; ++h) o[h] *= f[h];
-              tmem_store<N>(tlane + b * N, o);
+              for (int j = 0; j < NC; ++j) o[j] *= f[j];
+              tmem_store<NC>(tlane + b * N, o);
             }
           }
         }
         // weights, rounded to the operand type (half a step each)
-        uint32_t pw[N / 2];
+        uint32_t pw[NC / 2];
 #pragma unroll
-        for (int h = 0; h < N; h += 4) {
-          float4 m = m4[h / 4];
+        for (int j = 0; j < NC; j += 4) {
+          float4 m = m4[j / 4];
           m.x = m.x == -INFINITY ? 0.f : m.x;
           m.y = m.y == -INFINITY ? 0.f : m.y;
           m.z = m.z == -INFINITY ? 0.f : m.z;
           m.w = m.w == -INFINITY ? 0.f : m.w;
-          const float a = exp2_fast(x[h] - m.x), b = exp2_fast(x[h + 1] - m.y);
-          const float c = exp2_fast(x[h + 2] - m.z), d = exp2_fast(x[h + 3] - m.w);
-          l[h] += a;
-          l[h + 1] += b;
-          l[h + 2] += c;
-          l[h + 3] += d;
-          pw[h / 2] = pack2_rn<DT>(a, b);
-          pw[h / 2 + 1] = pack2_rn<DT>(c, d);
+          const float a = exp2_fast(x[j] - m.x), b = exp2_fast(x[j + 1] - m.y);
+          const float c = exp2_fast(x[j + 2] - m.z), d = exp2_fast(x[j + 3] - m.w);
+          l[j] += a;
+          l[j + 1] += b;
+          l[j + 2] += c;
+          l[j + 3] += d;
+          pw[j / 2] = pack2_rn<DT>(a, b);
+          pw[j / 2 + 1] = pack2_rn<DT>(c, d);
         }
         // the P buffer is free once the last tile's O^T products have completed
         if (i > 0) wait(&hdr.pv_done, (i - 1) & 1);
         if (lane < 16) {
-          const int k = 16 * warp + lane;
           uint8_t *row = ps + k * 128;
 #pragma unroll
-          for (int c = 0; c < N / 8; ++c)
-            *reinterpret_cast<uint4 *>(row + ((c ^ (k & 7)) << 4)) =
+          for (int c = 0; c < NC / 8; ++c)
+            *reinterpret_cast<uint4 *>(row + (((c0 / 8 + c) ^ (k & 7)) << 4)) =
                 make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
         }
         if ((tile + 1) * kTile > walk.L) {
@@ -376,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
           uint8_t *vb = kv + (i & 1) * kTileBytes;
           const int z0 = walk.L - tile * kTile;
           for (int idx = threadIdx.x; idx < (kTile - z0) * (kLatentDim / 8); idx += kSoftmaxThreads) {
-            const int k = z0 + idx / (kLatentDim / 8), c = idx % (kLatentDim / 8);
-            *reinterpret_cast<uint4 *>(vb + (k >> 3) * kGroup + (c >> 3) * kAtom + (k & 7) * 128 + (c & 7) * 16) =
+            const int z = z0 + idx / (kLatentDim / 8), c = idx % (kLatentDim / 8);
+            *reinterpret_cast<uint4 *>(vb + (z >> 3) * kGroup + (c >> 3) * kAtom + (z & 7) * 128 + (c & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
         }
@@ -386,55 +405,69 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         mbar_arrive(&hdr.p_full);
       }
       // the piece's sums: total weights over the tokens, then O^T as rows
-      float v[N];
+      float v[NC];
 #pragma unroll
-      for (int h = 0; h < N; ++h) v[h] = l[h];
+      for (int j = 0; j < NC; ++j) v[j] = l[j];
 #pragma unroll
-      for (int st = 0; st < 4; ++st) {  // halve the columns a lane keeps, four times
-        const int o = 8 >> st, half = N >> (st + 1);
+      for (int st = 0; st < 4; ++st) {  // halve the query rows a lane keeps, while there are several
+        const int o = 8 >> st, half = NC >> (st + 1);
         const bool upper = (lane & o) != 0;
+        if (half == 0) {
+          v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        } else {
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j)
-          if (j < half) {
-            const float send = upper ? v[j] : v[j + half], keep = upper ? v[j + half] : v[j];
-            v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
+          for (int j = 0; j < NC / 2; ++j)
+            if (j < half) {
+              const float send = upper ? v[j] : v[j + half], keep = upper ? v[j + half] : v[j];
+              v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        }
       }
       softmax_sync();
-      if (lane < 16)
+      if (lane < 16) {
+        if constexpr (NC == 8) {
+          hdr.top[quarter][c0 + (lane >> 1)] = v[0];
+        } else {
 #pragma unroll
-        for (int j = 0; j < N / 16; ++j) hdr.top[warp][lane * (N / 16) + j] = v[j];
+          for (int j = 0; j < NC / 16; ++j) hdr.top[quarter][c0 + lane * (NC / 16) + j] = v[j];
+        }
+      }
       softmax_sync();
       wait(&hdr.pv_done, (i - 1) & 1);
       const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
       if (!ok) {
       } else if (whole) {
-        const size_t row0 = static_cast<size_t>(walk.s) * p.rows + rt * N;
-        uint16_t *o16 = static_cast<uint16_t *>(p.out) + row0 * kLatentDim + 32 * warp + lane;
+        // rows of out: neighbouring lanes swap, so that each stores two
+        // dimensions of every other query row
+        const size_t row0 = static_cast<size_t>(walk.s) * p.rows + rt * N + c0;
+        const bool odd = lane & 1;
+        uint16_t *o16 = static_cast<uint16_t *>(p.out) + (row0 + odd) * kLatentDim + 32 * quarter + (lane & ~1);
 #pragma unroll 1
         for (int b = 0; b < kBlocksO; ++b) {
-          float o[N];
-          tmem_load<N>(tlane + b * N, o);
+          float o[NC];
+          tmem_load<NC>(tlane + b * N, o);
 #pragma unroll
-          for (int h = 0; h < N; ++h) {
-            const float sum = (hdr.top[0][h] + hdr.top[1][h]) + (hdr.top[2][h] + hdr.top[3][h]);
-            const float y = sum == 0.f ? 0.f : o[h] / sum;  // (a row that sees nothing)
-            if (h < n_rows) o16[static_cast<size_t>(h) * kLatentDim + b * kDims] = float_to_storage16<DT>(y);
+          for (int j = 0; j < NC; j += 2) {
+            const float s0 = sum_of(j), s1 = sum_of(j + 1);
+            const float y0 = s0 == 0.f ? 0.f : __fdividef(o[j], s0);  // (a row that sees nothing)
+            const float y1 = s1 == 0.f ? 0.f : __fdividef(o[j + 1], s1);
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+            if (c0 + j + odd < n_rows)
+              *reinterpret_cast<uint32_t *>(o16 + static_cast<size_t>(j) * kLatentDim + b * kDims) =
+                  odd ? pack2_rn<DT>(got, y1) : pack2_rn<DT>(y0, got);
           }
         }
       } else {
         const size_t slot = (static_cast<size_t>(rt) * max_workers + w) * 2 + (seg > 0);
-        for (int h = threadIdx.x; h < N; h += kSoftmaxThreads)
-          p.part_ml[slot * N + h] =
-              make_float2(hdr.m[h], (hdr.top[0][h] + hdr.top[1][h]) + (hdr.top[2][h] + hdr.top[3][h]));
-        float *po = p.part_o + slot * N * kLatentDim + 32 * warp + lane;
+        if (quarter == 0 && lane < NC) p.part_ml[slot * N + c0 + lane] = make_float2(hdr.m[c0 + lane], sum_of(lane));
+        float *po = p.part_o + (slot * N + c0) * kLatentDim + 32 * quarter + lane;
 #pragma unroll 1
         for (int b = 0; b < kBlocksO; ++b) {
-          float o[N];
-          tmem_load<N>(tlane + b * N, o);
+          float o[NC];
+          tmem_load<NC>(tlane + b * N, o);
 #pragma unroll
-          for (int h = 0; h < N; ++h)
-            if (h < n_rows) po[static_cast<size_t>(h) * kLatentDim + b * kDims] = o[h];
+          for (int j = 0; j < NC; ++j)
+            if (c0 + j < n_rows) po[static_cast<size_t>(j) * kLatentDim + b * kDims] = o[j];
         }
       }
       tc_fence_before_sync();
@@ -508,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     }
   } else if (warp == kQkWarp) {
     // -------------------------------------------------------------------- S^T
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       int i = 0;
       const uint32_t qa = smem_addr(qs), ka = smem_addr(kv);
@@ -542,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     }
   } else {
     // -------------------------------------------------------------------- O^T
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       int i = 0;
       const uint32_t pa_ = smem_addr(ps), ka = smem_addr(kv);
