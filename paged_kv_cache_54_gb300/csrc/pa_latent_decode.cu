@@ -11,15 +11,15 @@
 // latent dimensions as rows and the query rows as columns, so that the tile's
 // cost follows the number of query rows:
 //   S^T = K Q^T    M = 64 tokens, N = 16, 32 or 64 query rows, K = 576
-//   O^T += V^T P^T M = 128 dimensions (four times), N query rows, K = 64 tokens
-// K and V are one tile of shared memory: rows of nine 128-byte columns, in
+//   O^T += V^T P^T M = 128 dimensions, N query rows, K = 64 tokens
+// K and V are one tile of shared memory, rows of nine 128-byte columns in
 // groups of 8 rows of 8-row x 128-byte swizzled atoms.  The first product
 // reads it token-major, the second dimension-major.  O^T takes 4 N columns of
 // tensor memory, S^T 2 N.
 //
-// A block takes N query rows and an equal share of all sequences' 64-token
-// tiles (pa_shares.cuh).  Warps:
-//   0..7  softmax: a thread owns a token and half of the query rows.  The
+// A block takes N query rows and an equal share of all sequences'
+// 64-token tiles (pa_shares.cuh).  Warps:
+//   0..7  softmax: a thread owns a token and a quarter of the query rows.  The
 //         maximum of a query row is kept for all threads in shared memory and
 //         raised only when a score passes it by 2^8, so that almost every
 //         tile needs one vote of the block instead of a reduction over
@@ -69,12 +69,14 @@ template <int N>
 struct Layout {
   static constexpr int Q_COL = N * 128;  // a 128-byte column of the query rows
   static constexpr int Q_OFF = 2048;
-  static constexpr int P_OFF = Q_OFF + kCols * Q_COL;
+  static constexpr int Q_BYTES = kCols * Q_COL;
+  static constexpr int P_OFF = Q_OFF + Q_BYTES;
   static constexpr int P_BYTES = kTile * 128;
   static constexpr int KV_OFF = P_OFF + P_BYTES;
   static constexpr int SMEM = KV_OFF + kStages * kTileBytes;
   static constexpr uint32_t TMEM_S = kBlocksO * N;  // columns: O^T, then two S^T
-  static constexpr uint32_t TMEM_COLS = N == 16 ? 128 : N == 32 ? 256 : 512;
+  static constexpr uint32_t TMEM_COLS = 8 * N;
+  static_assert(SMEM <= 232448 && KV_OFF % 1024 == 0, "shared memory");
 };
 
 struct Header {
@@ -82,11 +84,12 @@ struct Header {
   uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, q_empty, fin[2];
   uint32_t tmem;
   int abort;
-  alignas(16) float m[64];  // the query rows' maxima (base 2), read four at a time
-  float top[4][64];   // maxima of 16 tokens, then their total weights
-  int see[64];        // tokens a query row sees
+  alignas(16) float m[64];  // what the query rows' scores are raised by: minus their maxima (base 2)
+  float top[4][64];         // maxima of 16 tokens, then their total weights
+  int see[64];              // tokens a query row sees
 };
 static_assert(sizeof(Header) <= 2048, "the header's place");
+constexpr float kNone = 3e38f;  // of a row without a maximum yet: any score passes it, none (-inf) stays -inf
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -154,6 +157,39 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[NCOL
 }
 #undef PA_R8
 
+// Half the warp's lanes are rows (M = 64): lanes 0..15 get NCOL columns from
+// taddr, lanes 16..31 the NCOL columns behind them, of the same 16 rows.
+#define PA_R4(a, o) a(r[o]), a(r[o + 1]), a(r[o + 2]), a(r[o + 3])
+template <int NCOL>
+__device__ __forceinline__ void tmem_load_rows16(uint32_t taddr, float (&v)[NCOL]) {
+  uint32_t r[NCOL];
+  if constexpr (NCOL == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16], 16;\n\ttcgen05.wait::ld.sync.aligned;"
+        : PA_R4("=r", 0), PA_R4("=r", 4), PA_R4("=r", 8), PA_R4("=r", 12)
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (NCOL == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], 8;\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PA_R4("=r", 0), PA_R4("=r", 4)
+        : "r"(taddr)
+        : "memory");
+  } else {
+    static_assert(NCOL == 4, "4, 8 or 16 columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0, %1, %2, %3}, [%4], 4;\n\ttcgen05.wait::ld.sync.aligned;"
+        : PA_R4("=r", 0)
+        : "r"(taddr)
+        : "memory");
+  }
+#pragma unroll
+  for (int j = 0; j < NCOL; ++j) v[j] = __uint_as_float(r[j]);
+}
+#undef PA_R4
+
 // One thread of the warp (converged).
 __device__ __forceinline__ bool elect_one() {
   uint32_t y;
@@ -194,10 +230,11 @@ struct Walk {
 };
 
 template <int DT, int N>
-__global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid_constant__ LatentParams p,
-                                                                    int max_workers) {
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_decode_kernel(const __grid_constant__ LatentParams p, int max_workers) {
   using Lay = Layout<N>;
-  constexpr int NC = N / 2;  // query rows of a softmax thread
+  constexpr int NQ = N / 4;  // query rows of a softmax thread
+  constexpr int NC = N / 2;  // of an O^T thread
   constexpr int AB = DT == kF16 ? 0 : 1;
   constexpr uint32_t IDESC_QK = umma_idesc_f16(AB, kTile, N, false);
   constexpr uint32_t IDESC_PV = umma_idesc_f16(AB, kDims, N, true) | (1u << 15);  // (A dimension-major too)
@@ -210,23 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   const int rt = blockIdx.x % p.row_tiles, w = blockIdx.x / p.row_tiles;
   launch_dependents();
   auto tiles_of = [&](int s) -> long long { return (checked_len(p.lens, s, p.limit, p.err) + kTile - 1) / kTile; };
-  // (the scan's barriers take the whole block; threads past its 128 only keep step)
-  {
-    const int n = ShareScan<128>::run(p.num_seqs), t = threadIdx.x;
-    long long sum = 0;
+  scan.scan(p.num_seqs, tiles_of);
+  if (blockIdx.x == 0) {  // the sequences' first tiles, for the merge
+    const int n = scan.run(p.num_seqs), t = threadIdx.x;
     if (t < 128) {
-      for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) sum += tiles_of(s);
-      scan.base[t + 1] = sum;
-      if (t == 0) scan.base[0] = 0;
-    }
-    __syncthreads();
-    for (int d = 1; d < 128; d <<= 1) {
-      const long long x = t < 128 && t >= d ? scan.base[t + 1 - d] : 0;
-      __syncthreads();
-      if (t < 128) scan.base[t + 1] += x;
-      __syncthreads();
-    }
-    if (blockIdx.x == 0 && t < 128) {
       long long at = scan.base[t];
       for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
         p.prefix[s] = at;
@@ -237,15 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
   }
   const long long total = scan.total(), workers = worker_count(total, max_workers);
   if (w >= workers) return;
-  Walk walk;
-  walk.u = share_begin(w, total, workers);
-  walk.end = share_begin(w + 1, total, workers);
-  if (walk.u >= walk.end) return;
-  walk.s = scan.find(walk.u, p.num_seqs, tiles_of, walk.first);
-  if ((smem_addr(smem) & 1023u) != 0) {
+  if ((smem_addr(smem) & 1023u) != 0) {  // the swizzle needs 1024-byte atoms
     if (threadIdx.x == 0) record_error(p.err, kErrSmemAlign);
     return;
   }
+  Walk walk;
+  walk.u = share_begin(w, total, workers);
+  walk.end = share_begin(w + 1, total, workers);
+  walk.s = scan.find(walk.u, p.num_seqs, tiles_of, walk.first);
   volatile int *abort = &hdr.abort;
   uint8_t *qs = smem + Lay::Q_OFF, *ps = smem + Lay::P_OFF, *kv = smem + Lay::KV_OFF;
   const int n_rows = min(N, p.rows - rt * N);  // query rows of this tile
@@ -258,10 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&hdr.s_full[i], 1);
-      mbar_init(&hdr.s_empty[i], kSoftmaxThreads);
+      mbar_init(&hdr.s_empty[i], kSoftmaxThreads / 32);
       mbar_init(&hdr.fin[i], 1);
     }
-    mbar_init(&hdr.p_full, kSoftmaxThreads);
+    mbar_init(&hdr.p_full, kSoftmaxThreads / 32);
     mbar_init(&hdr.pv_done, 1);
     mbar_init(&hdr.q_full, 1);
     mbar_init(&hdr.q_empty, 1);
@@ -276,10 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    const int quarter = warp & 3, c0 = (warp >> 2) * NC;  // 16 tokens, and the first of the thread's query rows
-    const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c0;
-    const int k = 16 * quarter + lane;                       // the token, for lanes below 16 (M = 64 fills those)
-    const int token = lane < 16 ? k : INT_MAX / 2;
+    const int quarter = warp & 3;
+    const int k = 16 * quarter + (lane & 15);               // the thread's token
+    const int c0 = (warp >> 2) * NC + (lane >> 4) * NQ;     // and its first query row
+    const int o0 = (warp >> 2) * NC;                        // of O^T: its first query row
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + o0;
+    const float c = p.scale_log2;
     // a wait that gave up leaves the warp in step with the others, whose
     // barriers count on it: it goes on without waiting, and nothing is stored
     bool ok = true;
@@ -287,22 +312,25 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
       tc_fence_after_sync();
     };
-    auto top_of = [&](int j) {
-      return fmaxf(fmaxf(hdr.top[0][c0 + j], hdr.top[1][c0 + j]), fmaxf(hdr.top[2][c0 + j], hdr.top[3][c0 + j]));
+    auto top_of = [&](int h) {
+      return fmaxf(fmaxf(hdr.top[0][h], hdr.top[1][h]), fmaxf(hdr.top[2][h], hdr.top[3][h]));
     };
-    auto sum_of = [&](int j) {
-      return (hdr.top[0][c0 + j] + hdr.top[1][c0 + j]) + (hdr.top[2][c0 + j] + hdr.top[3][c0 + j]);
+    auto sum_of = [&](int h) { return (hdr.top[0][h] + hdr.top[1][h]) + (hdr.top[2][h] + hdr.top[3][h]); };
+    // a row's new maximum, given what its scores were raised by, and the factor of its sums
+    auto raised = [&](float was, float top) { return was == kNone ? top > -INFINITY : top > -was + kLazy; };
+    auto factor = [&](float was, float top) {
+      return !raised(was, top) ? 1.f : was == kNone ? 0.f : exp2_fast(-was - top);
     };
     const float4 *m4 = reinterpret_cast<const float4 *>(hdr.m + c0);
     int i = 0;  // tiles so far
     for (int seg = 0; walk.next(p); ++seg) {
-      float l[NC];
+      float l[NQ];
 #pragma unroll
-      for (int j = 0; j < NC; ++j) l[j] = 0.f;
+      for (int j = 0; j < NQ; ++j) l[j] = 0.f;
       softmax_sync();  // the last piece's maxima and totals have been read
       if (threadIdx.x < N) {
         const int h = threadIdx.x;
-        hdr.m[h] = -INFINITY;
+        hdr.m[h] = kNone;
         hdr.see[h] = h < n_rows ? walk.L - (p.new_tokens - 1 - (rt * N + h) / p.heads) : 0;
       }
       softmax_sync();
@@ -310,47 +338,41 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
       const int all_see = n_rows < N ? 0 : walk.L - (p.new_tokens - 1 - rt * N / p.heads);
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         wait(&hdr.s_full[i & 1], (i >> 1) & 1);
-        float x[NC];
-        tmem_load<NC>(tlane + Lay::TMEM_S + (i & 1) * N, x);
+        float x[NQ];
+        tmem_load_rows16<NQ>(tlane + Lay::TMEM_S + (i & 1) * N, x);
         tc_fence_before_sync();
-        mbar_arrive(&hdr.s_empty[i & 1]);
-        const int key = tile * kTile + token;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hdr.s_empty[i & 1]);
+        const int key = tile * kTile + k;
         if ((tile + 1) * kTile > all_see) {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) x[j] = key < hdr.see[c0 + j] ? x[j] * p.scale_log2 : -INFINITY;
+          for (int j = 0; j < NQ; ++j) x[j] = key < hdr.see[c0 + j] ? x[j] * c : -INFINITY;
         } else {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) x[j] = lane < 16 ? x[j] * p.scale_log2 : -INFINITY;
+          for (int j = 0; j < NQ; ++j) x[j] *= c;
         }
-        float over = -INFINITY;
+        float y[NQ], over = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
+        for (int j = 0; j < NQ; j += 4) {
           const float4 m = m4[j / 4];
-          over = fmaxf(over, fmaxf(fmaxf(x[j] - m.x, x[j + 1] - m.y), fmaxf(x[j + 2] - m.z, x[j + 3] - m.w)));
+          y[j] = x[j] + m.x;
+          y[j + 1] = x[j + 1] + m.y;
+          y[j + 2] = x[j + 2] + m.z;
+          y[j + 3] = x[j + 3] + m.w;
+          over = fmaxf(over, fmaxf(fmaxf(y[j], y[j + 1]), fmaxf(y[j + 2], y[j + 3])));
         }
-        // (inf - inf of no score at all is a NaN, which is not over)
         if (softmax_any(over > kLazy)) {
           // raise the maxima: over each warp's 16 tokens, then all four
 #pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            const int b = __float_as_int(x[j] == x[j] ? x[j] : -INFINITY);
-            const int top = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-            if (lane == 0) hdr.top[quarter][c0 + j] = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
-          }
-          softmax_sync();
-          float f[NC];
+          for (int j = 0; j < NQ; ++j) {
+            float top = x[j];  // (the maximum of numbers: a NaN is passed over)
 #pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            const float was = hdr.m[c0 + j], top = top_of(j);
-            f[j] = top > was + kLazy ? exp2_fast(was - top) : 1.f;
-            l[j] *= f[j];
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if ((lane & 15) == 0) hdr.top[quarter][c0 + j] = top;
           }
           softmax_sync();
-          if (quarter == 0 && lane < NC) {
-            const float top = top_of(lane);
-            if (top > hdr.m[c0 + lane] + kLazy) hdr.m[c0 + lane] = top;
-          }
-          softmax_sync();
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) l[j] *= factor(hdr.m[c0 + j], top_of(c0 + j));
           if (tile > walk.t0) {  // O^T holds the tiles before
             wait(&hdr.pv_done, (i - 1) & 1);
 #pragma unroll 1
@@ -358,116 +380,113 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
               float o[NC];
               tmem_load<NC>(tlane + b * N, o);
 #pragma unroll
-              for (int j = 0; j < NC; ++j) o[j] *= f[j];
+              for (int j = 0; j < NC; ++j) o[j] *= factor(hdr.m[o0 + j], top_of(o0 + j));
               tmem_store<NC>(tlane + b * N, o);
             }
           }
+          softmax_sync();
+          if (threadIdx.x < N) {
+            const float top = top_of(threadIdx.x);
+            if (raised(hdr.m[threadIdx.x], top)) hdr.m[threadIdx.x] = -top;
+          }
+          softmax_sync();
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) y[j] = x[j] + hdr.m[c0 + j];
         }
         // weights, rounded to the operand type (half a step each)
-        uint32_t pw[NC / 2];
+        uint32_t pw[NQ / 2];
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
-          float4 m = m4[j / 4];
-          m.x = m.x == -INFINITY ? 0.f : m.x;
-          m.y = m.y == -INFINITY ? 0.f : m.y;
-          m.z = m.z == -INFINITY ? 0.f : m.z;
-          m.w = m.w == -INFINITY ? 0.f : m.w;
-          const float a = exp2_fast(x[j] - m.x), b = exp2_fast(x[j + 1] - m.y);
-          const float c = exp2_fast(x[j + 2] - m.z), d = exp2_fast(x[j + 3] - m.w);
+        for (int j = 0; j < NQ; j += 2) {
+          const float a = exp2_fast(y[j]), b = exp2_fast(y[j + 1]);
           l[j] += a;
           l[j + 1] += b;
-          l[j + 2] += c;
-          l[j + 3] += d;
           pw[j / 2] = pack2_rn<DT>(a, b);
-          pw[j / 2 + 1] = pack2_rn<DT>(c, d);
         }
         // the P buffer is free once the last tile's O^T products have completed
         if (i > 0) wait(&hdr.pv_done, (i - 1) & 1);
-        if (lane < 16) {
-          uint8_t *row = ps + k * 128;
+        uint8_t *row = ps + k * 128;
+        if constexpr (NQ >= 8) {
 #pragma unroll
-          for (int c = 0; c < NC / 8; ++c)
-            *reinterpret_cast<uint4 *>(row + (((c0 / 8 + c) ^ (k & 7)) << 4)) =
-                make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+          for (int u = 0; u < NQ / 8; ++u)
+            *reinterpret_cast<uint4 *>(row + (((c0 / 8 + u) ^ (k & 7)) << 4)) =
+                make_uint4(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]);
+        } else {
+          *reinterpret_cast<uint2 *>(row + ((c0 / 8 ^ (k & 7)) << 4) + (c0 & 7) * 2) = make_uint2(pw[0], pw[1]);
         }
         if ((tile + 1) * kTile > walk.L) {
           // rows behind the sequence's end hold anything: zero them, 0 * NaN would reach O^T
           uint8_t *vb = kv + (i & 1) * kTileBytes;
           const int z0 = walk.L - tile * kTile;
           for (int idx = threadIdx.x; idx < (kTile - z0) * (kLatentDim / 8); idx += kSoftmaxThreads) {
-            const int z = z0 + idx / (kLatentDim / 8), c = idx % (kLatentDim / 8);
-            *reinterpret_cast<uint4 *>(vb + (z >> 3) * kGroup + (c >> 3) * kAtom + (z & 7) * 128 + (c & 7) * 16) =
+            const int z = z0 + idx / (kLatentDim / 8), e = idx % (kLatentDim / 8);
+            *reinterpret_cast<uint4 *>(vb + (z >> 3) * kGroup + (e >> 3) * kAtom + (z & 7) * 128 + (e & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
         }
         fence_proxy_async_smem();
         tc_fence_before_sync();
-        mbar_arrive(&hdr.p_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hdr.p_full);
       }
       // the piece's sums: total weights over the tokens, then O^T as rows
-      float v[NC];
-#pragma unroll
-      for (int j = 0; j < NC; ++j) v[j] = l[j];
 #pragma unroll
       for (int st = 0; st < 4; ++st) {  // halve the query rows a lane keeps, while there are several
-        const int o = 8 >> st, half = NC >> (st + 1);
+        const int o = 8 >> st, half = NQ >> (st + 1);
         const bool upper = (lane & o) != 0;
         if (half == 0) {
-          v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
         } else {
 #pragma unroll
-          for (int j = 0; j < NC / 2; ++j)
+          for (int j = 0; j < NQ / 2; ++j)
             if (j < half) {
-              const float send = upper ? v[j] : v[j + half], keep = upper ? v[j + half] : v[j];
-              v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+              const float send = upper ? l[j] : l[j + half], keep = upper ? l[j + half] : l[j];
+              l[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
             }
         }
       }
       softmax_sync();
-      if (lane < 16) {
-        if constexpr (NC == 8) {
-          hdr.top[quarter][c0 + (lane >> 1)] = v[0];
-        } else {
-#pragma unroll
-          for (int j = 0; j < NC / 16; ++j) hdr.top[quarter][c0 + lane * (NC / 16) + j] = v[j];
-        }
-      }
+      // (lanes 16 / NQ apart hold the same row where there are fewer rows than lanes)
+      hdr.top[quarter][c0 + (lane & 15) / (16 / NQ)] = l[0];
       softmax_sync();
       wait(&hdr.pv_done, (i - 1) & 1);
       const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
+      const int d0 = 32 * quarter;  // the thread's dimensions: d0 + lane (+ 128 b)
       if (!ok) {
       } else if (whole) {
         // rows of out: neighbouring lanes swap, so that each stores two
         // dimensions of every other query row
-        const size_t row0 = static_cast<size_t>(walk.s) * p.rows + rt * N + c0;
+        const size_t row0 = static_cast<size_t>(walk.s) * p.rows + rt * N + o0;
         const bool odd = lane & 1;
-        uint16_t *o16 = static_cast<uint16_t *>(p.out) + (row0 + odd) * kLatentDim + 32 * quarter + (lane & ~1);
+        uint16_t *o16 = static_cast<uint16_t *>(p.out) + (row0 + odd) * kLatentDim + d0 + (lane & ~1);
 #pragma unroll 1
         for (int b = 0; b < kBlocksO; ++b) {
           float o[NC];
           tmem_load<NC>(tlane + b * N, o);
 #pragma unroll
           for (int j = 0; j < NC; j += 2) {
-            const float s0 = sum_of(j), s1 = sum_of(j + 1);
+            const float s0 = sum_of(o0 + j), s1 = sum_of(o0 + j + 1);
             const float y0 = s0 == 0.f ? 0.f : __fdividef(o[j], s0);  // (a row that sees nothing)
             const float y1 = s1 == 0.f ? 0.f : __fdividef(o[j + 1], s1);
             const float got = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
-            if (c0 + j + odd < n_rows)
+            if (o0 + j + odd < n_rows)
               *reinterpret_cast<uint32_t *>(o16 + static_cast<size_t>(j) * kLatentDim + b * kDims) =
                   odd ? pack2_rn<DT>(got, y1) : pack2_rn<DT>(y0, got);
           }
         }
       } else {
         const size_t slot = (static_cast<size_t>(rt) * max_workers + w) * 2 + (seg > 0);
-        if (quarter == 0 && lane < NC) p.part_ml[slot * N + c0 + lane] = make_float2(hdr.m[c0 + lane], sum_of(lane));
-        float *po = p.part_o + (slot * N + c0) * kLatentDim + 32 * quarter + lane;
+        if (threadIdx.x < N) {
+          const float m = hdr.m[threadIdx.x];
+          p.part_ml[slot * N + threadIdx.x] = make_float2(m == kNone ? -INFINITY : -m, sum_of(threadIdx.x));
+        }
+        float *po = p.part_o + (slot * N + o0) * kLatentDim + d0 + lane;
 #pragma unroll 1
         for (int b = 0; b < kBlocksO; ++b) {
           float o[NC];
           tmem_load<NC>(tlane + b * N, o);
 #pragma unroll
           for (int j = 0; j < NC; ++j)
-            if (c0 + j < n_rows) po[static_cast<size_t>(j) * kLatentDim + b * kDims] = o[j];
+            if (o0 + j < n_rows) po[static_cast<size_t>(j) * kLatentDim + b * kDims] = o[j];
         }
       }
       tc_fence_before_sync();
@@ -499,9 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         break;
       }
       if (lane == 0) {
-        mbar_arrive_expect_tx(&hdr.q_full, kCols * Lay::Q_COL);
-        for (int c = 0; c < kCols; ++c)
-          tma_load_2d(qs + c * Lay::Q_COL, &p.tmap_q, c * 64, walk.s * p.rows + rt * N, &hdr.q_full);
+        mbar_arrive_expect_tx(&hdr.q_full, Lay::Q_BYTES);
+        const int row = walk.s * p.rows + rt * N;
+        for (int e = 0; e < kCols; ++e)
+          tma_load_2d(qs + e * Lay::Q_COL, &p.tmap_q, e * 64, row, &hdr.q_full);
       }
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         const int st = i & 1;
@@ -509,29 +529,25 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
         const int n_box = min(boxes, ((walk.L - tile * kTile) + (1 << box_sh) - 1) >> box_sh);
         int mine = phys;
         if (tile + 1 < walk.t1) phys = entry(tile + 1);
-        bool got = true;
-        if (lane < n_box) {
-          if (mine < 0 || mine >= p.num_blocks) {
-            record_error(p.err, kErrBlockIndex);
-            mine = 0;
-          }
-          if (i >= kStages)
-            got = mbar_wait(&hdr.kv_empty[st][(lane << box_sh) >> 4], ((i >> 1) - 1) & 1, abort);
-        } else if (lane < boxes && i >= kStages) {
-          got = mbar_wait(&hdr.kv_empty[st][(lane << box_sh) >> 4], ((i >> 1) - 1) & 1, abort);
+        if (lane < n_box && (mine < 0 || mine >= p.num_blocks)) {
+          record_error(p.err, kErrBlockIndex);
+          mine = 0;
         }
+        bool got = true;
+        if (lane < boxes && i >= kStages)
+          got = mbar_wait(&hdr.kv_empty[st][(lane << box_sh) >> 4], ((i >> 1) - 1) & 1, abort);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         if (lane == 0) mbar_arrive_expect_tx(&hdr.kv_full[st], n_box * box_bytes);
         __syncwarp();
-        if (lane < n_box)
-          tma_load_4d(kv + st * kTileBytes + lane * box_bytes, &p.tmap_c, 0, 0, 0,
-                      (mine << (p.bs_shift - 3)) + ((tok & ((1 << p.bs_shift) - 1)) >> 3), &hdr.kv_full[st]);
+        if (lane < n_box) {
+          const int row = (mine << p.bs_shift) + (tok & ((1 << p.bs_shift) - 1));
+          tma_load_4d(kv + st * kTileBytes + lane * box_bytes, &p.tmap_c, 0, 0, 0, row >> 3, &hdr.kv_full[st]);
+        }
       }
       if (ok) walk.advance();
-      if (!ok) break;
     }
     if (!ok && lane == 0) {
       record_error(p.err, kErrTimeout);
@@ -552,11 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
           if (ok) ok = mbar_wait(&hdr.kv_full[i & 1], (i >> 1) & 1, abort);
           if (!ok) break;
           tc_fence_after_sync();
-          const uint64_t a0 = umma_desc_sw128(ka + (i & 1) * kTileBytes, 16, kGroup);
-          const uint64_t b0 = umma_desc_sw128(qa, 16, 1024);
+          const uint32_t tile_at = ka + (i & 1) * kTileBytes;
+          const uint64_t a0 = umma_desc_sw128(tile_at, 16, kGroup), b0 = umma_desc_sw128(qa, 16, 1024);
           const uint32_t d = tmem + Lay::TMEM_S + (i & 1) * N;
-#pragma unroll 4
-          for (int kk = 0; kk < kLatentRow / 16; ++kk) {
+#pragma unroll
+          for (int kk = 0; kk < kCols * 4; ++kk) {
             const uint32_t off = (kk % 4) * 32;
             tc_mma_f16(d, a0 + (((kk / 4) * kAtom + off) >> 4), b0 + (((kk / 4) * Lay::Q_COL + off) >> 4), IDESC_QK,
                        kk > 0);
@@ -617,44 +633,54 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_kernel(const __grid
 }
 
 // Joins the pieces of sequences that several blocks shared, and writes the
-// rows of sequences without tokens.  A block a query row.
+// rows of sequences without tokens.  A block a query row: half of its threads
+// take every other piece.
 template <int DT, int N>
-__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentParams p, int max_workers) {
+__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p, int max_workers) {
+  __shared__ float2 ml[kMaxWorkers];
+  __shared__ float4 other[128];
   grid_dependency_wait();
   const int s = blockIdx.x / p.rows, r = blockIdx.x % p.rows, rt = r / N, h = r % N;
   const long long u0 = p.prefix[s], u1 = p.prefix[s + 1], total = p.prefix[p.num_seqs];
-  uint16_t *row = static_cast<uint16_t *>(p.out) + static_cast<size_t>(blockIdx.x) * kLatentDim + threadIdx.x * 4;
+  const int t = threadIdx.x & 127, half = threadIdx.x >> 7;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
   if (u1 > u0) {
     const long long workers = worker_count(total, max_workers);
     const long long w0 = share_owner(u0, total, workers), w1 = share_owner(u1 - 1, total, workers);
     if (w0 == w1) return;  // written whole
-    const size_t base = static_cast<size_t>(rt) * max_workers * 2;
+    const int n = static_cast<int>(w1 - w0) + 1;
     // a block's first piece is in its place 0; the sequence is not the first of its first block if that began earlier
     const int late = share_begin(w0, total, workers) < u0;
-    auto slot = [&](long long w) { return (base + w * 2 + (w == w0 ? late : 0)) * N + h; };
-    float m = -INFINITY, l = 0.f;
-    for (long long w = w0; w <= w1; ++w) m = fmaxf(m, p.part_ml[slot(w)].x);
+    const size_t base = ((static_cast<size_t>(rt) * max_workers + w0) * 2) * N + h;
+    auto slot = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * N; };
+    for (int i = threadIdx.x; i < n; i += 256) ml[i] = p.part_ml[slot(i)];
+    __syncthreads();
+    float m = -INFINITY;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[i].x);
     if (m == -INFINITY) m = 0.f;
-#pragma unroll 4
-    for (long long w = w0; w <= w1; ++w) {
-      const size_t at = slot(w);
-      const float2 ml = p.part_ml[at];
-      const float f = exp2_fast(ml.x - m);
-      const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * kLatentDim + threadIdx.x * 4);
-      l += f * ml.y;
+    for (int i = 0; i < n; ++i) l += exp2_fast(ml[i].x - m) * ml[i].y;
+#pragma unroll 8
+    for (int i = half; i < n; i += 2) {
+      const float f = exp2_fast(ml[i].x - m);
+      const float4 x = *reinterpret_cast<const float4 *>(p.part_o + slot(i) * kLatentDim + t * 4);
       o.x += f * x.x;
       o.y += f * x.y;
       o.z += f * x.z;
       o.w += f * x.w;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-    o.x *= inv;
-    o.y *= inv;
-    o.z *= inv;
-    o.w *= inv;
+    if (half == 1) other[t] = o;
+    __syncthreads();
   }
+  if (half == 1) return;
+  if (l != 0.f) {
+    const float4 y = other[t];
+    const float inv = 1.f / l;
+    o = make_float4((o.x + y.x) * inv, (o.y + y.y) * inv, (o.z + y.z) * inv, (o.w + y.w) * inv);
+  } else {
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  uint16_t *row = static_cast<uint16_t *>(p.out) + static_cast<size_t>(blockIdx.x) * kLatentDim + t * 4;
   *reinterpret_cast<uint2 *>(row) = make_uint2(pack2_rn<DT>(o.x, o.y), pack2_rn<DT>(o.z, o.w));
 }
 
@@ -712,7 +738,7 @@ pa_status launch(LatentParams &p, const void *q, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.rows);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

@@ -100,29 +100,15 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
   auto tiles_of = [&](int s) { return (checked_len(p.lens, s, p.limit, p.err) + kExTokens - 1) / kExTokens; };
   auto units_of = [&](int s) -> long long { return static_cast<long long>(tiles_of(s)) * p.heads; };
   ShareScan<128> &scan = hdr.scan;
-  {
-    const int n = ShareScan<128>::run(p.num_seqs), t = threadIdx.x;
-    long long sum = 0;
-    if (t < 128) {
-      for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) sum += units_of(s);
-      scan.base[t + 1] = sum;
-      if (t == 0) scan.base[0] = 0;
+  scan.scan(p.num_seqs, units_of);
+  if (blockIdx.x == 0 && threadIdx.x < 128) {  // the sequences' first token tiles, for the second kernel
+    const int n = scan.run(p.num_seqs), t = threadIdx.x;
+    long long at = scan.base[t] / p.heads;
+    for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
+      p.prefix[s] = at;
+      at += tiles_of(s);
     }
-    __syncthreads();
-    for (int d = 1; d < 128; d <<= 1) {
-      const long long x = t < 128 && t >= d ? scan.base[t + 1 - d] : 0;
-      __syncthreads();
-      if (t < 128) scan.base[t + 1] += x;
-      __syncthreads();
-    }
-    if (blockIdx.x == 0 && t < 128) {
-      long long at = scan.base[t] / p.heads;
-      for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
-        p.prefix[s] = at;
-        at += tiles_of(s);
-      }
-      if (t == 0) p.prefix[p.num_seqs] = scan.total() / p.heads;
-    }
+    if (t == 0) p.prefix[p.num_seqs] = scan.total() / p.heads;
   }
   const long long total = scan.total();
   const long long u0 = share_begin(blockIdx.x, total, gridDim.x), u1 = share_begin(blockIdx.x + 1, total, gridDim.x);

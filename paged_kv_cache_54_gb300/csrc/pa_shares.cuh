@@ -26,27 +26,30 @@ __device__ __forceinline__ int checked_len(const int32_t *lens, int s, int limit
   return 0;
 }
 
-// The units of all sequences, found by the whole block: each thread sums a
-// run of sequences, the runs' sums are scanned in shared memory.
+// The units of all sequences, found by the block's first THREADS threads:
+// each sums a run of sequences, the runs' sums are scanned in shared memory.
 template <int THREADS>
 struct ShareScan {
   static_assert((THREADS & (THREADS - 1)) == 0, "a power of two");
   long long base[THREADS + 1];  // units before thread t's run; the total
   static __device__ __forceinline__ int run(int num_seqs) { return (num_seqs + THREADS - 1) / THREADS; }
 
-  // units_of(s): the units of sequence s.  All threads; ends with a barrier.
+  // units_of(s): the units of sequence s.  All threads of the block (the
+  // others only keep step); ends with a barrier.
   template <typename F>
   __device__ __forceinline__ void scan(int num_seqs, F units_of) {
     const int n = run(num_seqs), t = threadIdx.x;
-    long long sum = 0;
-    for (int s = t * n; s < min(num_seqs, (t + 1) * n); ++s) sum += units_of(s);
-    base[t + 1] = sum;
-    if (t == 0) base[0] = 0;
+    if (t < THREADS) {
+      long long sum = 0;
+      for (int s = t * n; s < min(num_seqs, (t + 1) * n); ++s) sum += units_of(s);
+      base[t + 1] = sum;
+      if (t == 0) base[0] = 0;
+    }
     __syncthreads();
     for (int d = 1; d < THREADS; d <<= 1) {
-      const long long x = t >= d ? base[t + 1 - d] : 0;
+      const long long x = t < THREADS && t >= d ? base[t + 1 - d] : 0;
       __syncthreads();
-      base[t + 1] += x;
+      if (t < THREADS) base[t + 1] += x;
       __syncthreads();
     }
   }
