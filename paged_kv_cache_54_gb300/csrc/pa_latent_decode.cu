@@ -190,13 +190,6 @@ __device__ __forceinline__ void tmem_load_rows16(uint32_t taddr, float (&v)[NCOL
 }
 #undef PA_R4
 
-// One thread of the warp (converged).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t y;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
-  return y != 0;
-}
-
 __host__ __device__ inline long long worker_count(long long tiles, long long most) {
   const long long n = (tiles + kMinTiles - 1) / kMinTiles;
   return n < most ? n : most;
@@ -633,55 +626,114 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of sequences that several blocks shared, and writes the
-// rows of sequences without tokens.  A block a query row: half of its threads
-// take every other piece.
-template <int DT, int N>
-__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentParams p, int max_workers) {
-  __shared__ float2 ml[kMaxWorkers];
-  __shared__ float4 other[128];
+// rows of sequences without tokens.  TEAM warps take one of DSPLIT parts of a
+// query row's dimensions, each every TEAM-th piece; a block is 16 warps.
+// Bound by the latency of its loads: many warps a row where rows are few (one
+// sequence in 152 pieces, 32 rows: 13 us with a block a row, 4 with four
+// blocks), one where they are many (128 sequences in two pieces, 128 rows).
+constexpr int kMergeWarps = 16;
+
+template <int DT, int N, int TEAM, int DSPLIT>
+__global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const LatentParams p, int max_workers) {
+  constexpr int DIMS = kLatentDim / DSPLIT, VEC = DIMS / 128;  // of a block, and the lane's fours of them
+  __shared__ float part[TEAM > 1 ? kMergeWarps : 1][DIMS];
+  __shared__ float sums[kMergeWarps];
   grid_dependency_wait();
-  const int s = blockIdx.x / p.rows, r = blockIdx.x % p.rows, rt = r / N, h = r % N;
-  const long long u0 = p.prefix[s], u1 = p.prefix[s + 1], total = p.prefix[p.num_seqs];
-  const int t = threadIdx.x & 127, half = threadIdx.x >> 7;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mate = warp % TEAM;
+  const int row = blockIdx.x / DSPLIT * (kMergeWarps / TEAM) + warp / TEAM, d0 = blockIdx.x % DSPLIT * DIMS;
+  const bool exists = row < p.num_seqs * p.rows;
+  bool joins = false;
+  float4 o[VEC];
   float l = 0.f;
-  if (u1 > u0) {
-    const long long workers = worker_count(total, max_workers);
-    const long long w0 = share_owner(u0, total, workers), w1 = share_owner(u1 - 1, total, workers);
-    if (w0 == w1) return;  // written whole
-    const int n = static_cast<int>(w1 - w0) + 1;
-    // a block's first piece is in its place 0; the sequence is not the first of its first block if that began earlier
-    const int late = share_begin(w0, total, workers) < u0;
-    const size_t base = ((static_cast<size_t>(rt) * max_workers + w0) * 2) * N + h;
-    auto slot = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * N; };
-    for (int i = threadIdx.x; i < n; i += 256) ml[i] = p.part_ml[slot(i)];
-    __syncthreads();
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[i].x);
-    if (m == -INFINITY) m = 0.f;
-    for (int i = 0; i < n; ++i) l += exp2_fast(ml[i].x - m) * ml[i].y;
-#pragma unroll 8
-    for (int i = half; i < n; i += 2) {
-      const float f = exp2_fast(ml[i].x - m);
-      const float4 x = *reinterpret_cast<const float4 *>(p.part_o + slot(i) * kLatentDim + t * 4);
-      o.x += f * x.x;
-      o.y += f * x.y;
-      o.z += f * x.z;
-      o.w += f * x.w;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (exists) {
+    const int s = row / p.rows, r = row % p.rows;
+    const long long u0 = p.prefix[s], u1 = p.prefix[s + 1], total = p.prefix[p.num_seqs];
+    joins = u1 == u0;  // no token: zeros
+    if (u1 > u0) {
+      const long long workers = worker_count(total, max_workers);
+      const long long w0 = share_owner(u0, total, workers), w1 = share_owner(u1 - 1, total, workers);
+      joins = w1 > w0;  // (else written whole)
+      if (joins) {
+        const int n = static_cast<int>(w1 - w0) + 1;
+        // a block's first piece is in its place 0; the sequence is not the first of its first block if that began earlier
+        const int late = share_begin(w0, total, workers) < u0;
+        const size_t base = ((static_cast<size_t>(r / N) * max_workers + w0) * 2) * N + r % N;
+        auto slot = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * N; };
+        float m = -INFINITY;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[slot(i)].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if (m == -INFINITY) m = 0.f;
+#pragma unroll 4
+        for (int i = mate; i < n; i += TEAM) {
+          const float2 ml = p.part_ml[slot(i)];
+          const float4 *x = reinterpret_cast<const float4 *>(p.part_o + slot(i) * kLatentDim + d0) + lane;
+          const float f = exp2_fast(ml.x - m);
+          l += f * ml.y;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float4 y = x[32 * e];
+            o[e].x += f * y.x;
+            o[e].y += f * y.y;
+            o[e].z += f * y.z;
+            o[e].w += f * y.w;
+          }
+        }
+      }
     }
-    if (half == 1) other[t] = o;
+  }
+  if constexpr (TEAM > 1) {
+    float4 *mine = reinterpret_cast<float4 *>(part[warp]) + lane;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) mine[32 * e] = o[e];
+    if (lane == 0) sums[warp] = l;
     __syncthreads();
+    // the team's warps each join a share of the dimensions
+    if (!joins) return;
+    const int first = warp - mate;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < TEAM; ++i) l += sums[first + i];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    constexpr int OWN = DIMS / TEAM / 2;  // pairs of dimensions of a warp
+    for (int d = lane; d < OWN; d += 32) {
+      const int at = (mate * OWN + d) * 2;
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int i = 0; i < TEAM; ++i) {
+        const float2 z = *reinterpret_cast<const float2 *>(&part[first + i][at]);
+        x += z.x;
+        y += z.y;
+      }
+      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + static_cast<size_t>(row) * kLatentDim + d0 + at) =
+          l == 0.f ? 0u : pack2_rn<DT>(x * inv, y * inv);
+    }
+  } else if (joins) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t *out = static_cast<uint16_t *>(p.out) + static_cast<size_t>(row) * kLatentDim + d0 + lane * 4;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      *reinterpret_cast<uint2 *>(out + 128 * e) =
+          l == 0.f ? make_uint2(0u, 0u)
+                   : make_uint2(pack2_rn<DT>(o[e].x * inv, o[e].y * inv), pack2_rn<DT>(o[e].z * inv, o[e].w * inv));
   }
-  if (half == 1) return;
-  if (l != 0.f) {
-    const float4 y = other[t];
-    const float inv = 1.f / l;
-    o = make_float4((o.x + y.x) * inv, (o.y + y.y) * inv, (o.z + y.z) * inv, (o.w + y.w) * inv);
-  } else {
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  uint16_t *row = static_cast<uint16_t *>(p.out) + static_cast<size_t>(blockIdx.x) * kLatentDim + t * 4;
-  *reinterpret_cast<uint2 *>(row) = make_uint2(pack2_rn<DT>(o.x, o.y), pack2_rn<DT>(o.z, o.w));
+}
+
+template <int DT, int N, int TEAM, int DSPLIT>
+cudaError_t launch_merge(const LatentParams &p, int workers, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  constexpr int rows = kMergeWarps / TEAM;  // of a block
+  cfg.gridDim = dim3(static_cast<unsigned>((p.num_seqs * p.rows + rows - 1) / rows) * DSPLIT);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<DT, N, TEAM, DSPLIT>, p, workers);
 }
 
 int columns_for(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -733,16 +785,10 @@ pa_status launch(LatentParams &p, const void *q, cudaStream_t stream) {
   latent_decode_kernel<DT, N><<<workers * p.row_tiles, kThreads, Lay::SMEM, stream>>>(p, workers);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.rows);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, latent_merge_kernel<DT, N>, p, workers);
+  const long long rows = static_cast<long long>(p.num_seqs) * p.rows;
+  e = rows <= info.sm_count * 2ll    ? launch_merge<DT, N, 16, 4>(p, workers, stream)
+      : rows <= info.sm_count * 16ll ? launch_merge<DT, N, 4, 1>(p, workers, stream)
+                                     : launch_merge<DT, N, 1, 1>(p, workers, stream);
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
       for (int j = max(0, chunk - kExRing); j < chunk; ++j)
         mbar_wait(&hdr.b_full[j % kExRing], (j / kExRing) & 1, nullptr);
     }
-  } else if (lane == 0) {
+  } else if (elect_one()) {
     // ------------------------------------------------------------------ MMA
     bool ok = true;
     int i = 0, chunk = 0;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
   } else {
     // ---------------------------------------------------------------- MMA
     const int t = warp - kMmaWarp;
-    if (lane == 0 && t < tiles) {
+    if (t < tiles && elect_one()) {
       bool ok = mbar_wait(&hdr.q_full, 0, abort);
       const uint32_t qt = smem_addr(qs) + t * kQTile, sa = smem_addr(stages), tt = tmem + t * kTileCols;
       auto issue_qk = [&](int i) -> bool {

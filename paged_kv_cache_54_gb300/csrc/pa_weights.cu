@@ -62,16 +62,20 @@ struct WeighParams {
   int *err;
 };
 
-__device__ __forceinline__ uint4 ldg_stream(const void *p) {
+// K and V are read once: they leave L2 first, so that the scores and sums
+// written on the way are still there for the second kernel.
+__device__ __forceinline__ uint4 ldg_stream(const void *p, uint64_t policy) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p), "l"(policy));
   return v;
 }
-__device__ __forceinline__ uint2 ldg_stream2(const void *p) {
+__device__ __forceinline__ uint2 ldg_stream2(const void *p, uint64_t policy) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v2.b32 {%0, %1}, [%2], %3;"
+               : "=r"(v.x), "=r"(v.y)
+               : "l"(p), "l"(policy));
   return v;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -124,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
   long long first;
   int s = scan.find(u, p.num_seqs, steps_of, first);
 
+  const uint64_t policy = l2_policy_evict_first();
   const int bs = 1 << p.bs_shift, bmask = bs - 1;
   const int ktok = 4 * (g >> 1) + (g & 1);  // this lane's K tokens in a step: ktok, ktok + 2; V: 4t .. 4t + 3
   while (u < end) {
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
       for (int j = 0; j < 2; ++j) {
         const uint8_t *row = p.k + row_of(block, tok0 + ktok + 2 * j) * ROW + t * 16;
 #pragma unroll
-        for (int i = 0; i < KW; ++i) kr[j][i] = ldg_stream(row + i * 64);
+        for (int i = 0; i < KW; ++i) kr[j][i] = ldg_stream(row + i * 64, policy);
       }
     };
     auto load_v = [&](int tok0, int block) {
@@ -209,14 +214,14 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
         if constexpr (VWORDS >= 4) {
 #pragma unroll
           for (int i = 0; i < VWORDS / 4; ++i) {
-            const uint4 x = ldg_stream(row + i * 128 + g * 16);
+            const uint4 x = ldg_stream(row + i * 128 + g * 16, policy);
             vr[j][4 * i] = x.x;
             vr[j][4 * i + 1] = x.y;
             vr[j][4 * i + 2] = x.z;
             vr[j][4 * i + 3] = x.w;
           }
         } else {
-          const uint2 x = ldg_stream2(row + g * 8);
+          const uint2 x = ldg_stream2(row + g * 8, policy);
           vr[j][0] = x.x;
           vr[j][1] = x.y;
         }
@@ -323,66 +328,97 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
   }
 }
 
-// Joins a pair's pieces and adds its tokens' weights.  Blocks below
-// num_seqs * q_heads write one row of out each; the others share the steps.
-template <int QT, int D>
-__global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParams p, int max_workers) {
-  __shared__ float red[kThreads / D == 2 ? D + 1 : 1];
+// Adds the tokens' weights and joins the pairs' pieces: the first
+// weight_blocks blocks share the steps, the others write the rows of out, TEAM
+// warps a row (four where rows are few), each every TEAM-th piece.
+template <int QT, int D, int TEAM>
+__global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParams p, int max_workers, int weight_blocks) {
+  constexpr int PER = D / 32;  // dimensions of a lane
+  __shared__ float part[TEAM > 1 ? kWarps : 1][D];
+  __shared__ float sums[kWarps];
   grid_dependency_wait();
   const long long total = p.prefix[p.num_seqs];
   const long long workers = worker_count(total, max_workers);
-  const int lane = threadIdx.x & 31;
-  const long long rows = static_cast<long long>(p.num_seqs) * p.q_heads;
-  if (blockIdx.x < rows) {
-    const int s = blockIdx.x / p.q_heads, hq = blockIdx.x % p.q_heads, h = hq / p.G, gq = hq % p.G;
-    const long long first = p.prefix[s], all = p.prefix[s + 1] - first;
-    constexpr int PARTS = kThreads / D;  // threads of a dimension
-    const int d = threadIdx.x % D, part = threadIdx.x / D;
-    float o = 0.f, l = 0.f;
-    if (all > 0) {
-      const long long steps = all / p.kv_heads, u0 = first + h * steps;
-      const long long pair = static_cast<long long>(s) * p.kv_heads + h;
-      const long long s0 = pair + share_owner(u0, total, workers), s1 = pair + share_owner(u0 + steps - 1, total, workers);
-      float m = -INFINITY;
-      for (long long i = s0; i <= s1; ++i) m = fmaxf(m, p.part_ml[i * p.G + gq].x);
-      const float base = m == -INFINITY ? 0.f : m;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (static_cast<int>(blockIdx.x) >= weight_blocks) {
+    const long long row = (static_cast<long long>(blockIdx.x) - weight_blocks) * (kWarps / TEAM) + warp / TEAM;
+    const bool exists = row < static_cast<long long>(p.num_seqs) * p.q_heads;
+    const int s = static_cast<int>(row / p.q_heads), hq = static_cast<int>(row % p.q_heads), h = hq / p.G, gq = hq % p.G;
+    const int mate = warp % TEAM;
+    float o[PER], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    if (exists) {
+      const long long first = p.prefix[s], all = p.prefix[s + 1] - first;
+      if (all > 0) {
+        const long long steps = all / p.kv_heads, u0 = first + h * steps;
+        const long long pair = static_cast<long long>(s) * p.kv_heads + h;
+        const long long s0 = pair + share_owner(u0, total, workers);
+        const int n = static_cast<int>(pair + share_owner(u0 + steps - 1, total, workers) - s0) + 1;
+        const float2 *ml = p.part_ml + s0 * p.G + gq;
+        const float *po = p.part_o + (s0 * p.G + gq) * D + lane * PER;
+        float m = -INFINITY;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[static_cast<size_t>(i) * p.G].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if (m == -INFINITY) m = 0.f;
 #pragma unroll 4
-      for (long long i = s0 + part; i <= s1; i += PARTS) {
-        const float2 ml = p.part_ml[i * p.G + gq];
-        const float f = exp2_fast(ml.x - base);
-        l += f * ml.y;
-        o += f * p.part_o[(i * p.G + gq) * D + d];
+        for (int i = mate; i < n; i += TEAM) {
+          const float2 a = ml[static_cast<size_t>(i) * p.G];
+          const float *x = po + static_cast<size_t>(i) * p.G * D;
+          const float f = exp2_fast(a.x - m);
+          l += f * a.y;
+          if constexpr (PER == 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(x);
+            o[0] += f * y.x;
+            o[1] += f * y.y;
+            o[2] += f * y.z;
+            o[3] += f * y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2 *>(x);
+            o[0] += f * y.x;
+            o[1] += f * y.y;
+          }
+        }
       }
     }
-    if constexpr (PARTS == 2) {
-      if (part == 1) {
-        red[d] = o;
-        if (d == 0) red[D] = l;
-      }
+    if constexpr (TEAM > 1) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) part[warp][lane * PER + e] = o[e];
+      if (lane == 0) sums[warp] = l;
       __syncthreads();
-      if (part == 0) {
-        o += red[d];
-        l += red[D];
+      if (mate > 0) return;
+#pragma unroll
+      for (int i = 1; i < TEAM; ++i) {
+        l += sums[warp + i];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] += part[warp + i][lane * PER + e];
       }
     }
-    if (part == 0) {
-      const float vs = p.v_head_scale != nullptr ? __ldg(p.v_head_scale + h) : p.v_scale;
-      const float y = l == 0.f ? 0.f : o * (vs / l);  // (no token, or none with a weight)
-      static_cast<uint16_t *>(p.out)[static_cast<size_t>(blockIdx.x) * D + d] = float_to_storage16<QT>(y);
-    }
+    if (!exists) return;
+    const float vs = p.v_head_scale != nullptr ? __ldg(p.v_head_scale + h) : p.v_scale;
+    const float f = l == 0.f ? 0.f : vs / l;  // (no token, or none with a weight)
+    uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + static_cast<size_t>(row) * D) +
+                    lane * (PER / 2);
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) out[e / 2] = l == 0.f ? 0u : pack2_rn<QT>(o[e] * f, o[e + 1] * f);
     return;
   }
   if (total == 0) return;
-  const long long nw = (static_cast<long long>(gridDim.x) - rows) * kWarps;
-  const long long w = (blockIdx.x - rows) * kWarps + (threadIdx.x >> 5);
+  const long long nw = static_cast<long long>(weight_blocks) * kWarps;
+  const long long w = static_cast<long long>(blockIdx.x) * kWarps + warp;
   long long u = share_begin(w, total, nw);
   const long long end = share_begin(w + 1, total, nw);
   if (u >= end) return;
-  int lo = 0, hi = p.num_seqs - 1;  // the last sequence whose first step is at or before u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.prefix[mid] <= u) lo = mid;
-    else hi = mid - 1;
+  // the last sequence whose first step is at or before u: 32 places are
+  // looked at together, then as many between two of them
+  int lo = 0;
+  for (int n = p.num_seqs; n > 1;) {
+    const int gap = (n + 31) / 32, at = lane * gap;
+    const unsigned before = __ballot_sync(0xffffffffu, at < n && p.prefix[lo + min(at, n - 1)] <= u);
+    const int j = 31 - __clz(before);  // (place 0 is always before)
+    lo += j * gap;
+    n = min(gap, n - j * gap);
   }
   for (int s = lo; u < end; ++s) {
     const long long first = p.prefix[s], all = p.prefix[s + 1] - first;
@@ -420,13 +456,38 @@ __global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParam
         bm[q] = __shfl_sync(0xffffffffu, m, 4 * q);
         bi[q] = q < p.G ? __shfl_sync(0xffffffffu, inv, 4 * q) : 0.f;
       }
-      for (int i = i0 + lane; i < i1; i += 32) {
+      const float *win = p.weights_in == nullptr ? nullptr : p.weights_in + at;
+      float *wout = p.weights_out + at;
+      int i = i0;
+      // four tokens a lane (the scores' rows are aligned; the weights' may not be)
+      for (; i + 128 <= i1; i += 128) {
+        const int j = i + 4 * lane;
+        float4 sc[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.G) sc[q] = __ldcs(reinterpret_cast<const float4 *>(x + static_cast<size_t>(q) * p.width + j));
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        if (win != nullptr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = p.decay * win[j + e];
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.G) {
+            sum[0] += exp2_fast(sc[q].x - bm[q]) * bi[q];
+            sum[1] += exp2_fast(sc[q].y - bm[q]) * bi[q];
+            sum[2] += exp2_fast(sc[q].z - bm[q]) * bi[q];
+            sum[3] += exp2_fast(sc[q].w - bm[q]) * bi[q];
+          }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wout[j + e] = w[e] + sum[e];
+      }
+      for (i += lane; i < i1; i += 32) {
         float sum = 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (q < p.G) sum += exp2_fast(__ldcs(x + static_cast<size_t>(q) * p.width + i) - bm[q]) * bi[q];
-        const float before = p.weights_in == nullptr ? 0.f : p.decay * p.weights_in[at + i];
-        p.weights_out[at + i] = before + sum;
+        wout[i] = (win == nullptr ? 0.f : p.decay * win[i]) + sum;
       }
       u = stop;
     }
@@ -451,6 +512,21 @@ bool sizes_of(int S, int Hq, int H, int D, int max_len, Sizes *z) {
   return true;
 }
 
+template <int QT, int D, int TEAM>
+cudaError_t launch_finish(const WeighParams &p, int workers, int weight_blocks, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int per = kWarps / TEAM;  // rows of a block
+  cfg.gridDim = dim3(static_cast<unsigned>((p.num_seqs * p.q_heads + per - 1) / per + weight_blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weigh_finish_kernel<QT, D, TEAM>, p, workers, weight_blocks);
+}
+
 template <int KVT, int QT, int D>
 pa_status launch(const WeighParams &p, cudaStream_t stream) {
   DeviceInfo info;
@@ -460,16 +536,10 @@ pa_status launch(const WeighParams &p, cudaStream_t stream) {
   weigh_kernel<KVT, QT, D><<<blocks, kThreads, 0, stream>>>(p, workers);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs * p.q_heads + info.sm_count * 8));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, weigh_finish_kernel<QT, D>, p, workers);
+  const long long rows = static_cast<long long>(p.num_seqs) * p.q_heads;
+  // (six blocks an SM share the steps, in one wave)
+  e = rows <= info.sm_count * 8ll ? launch_finish<QT, D, 4>(p, workers, info.sm_count * 6, stream)
+                                  : launch_finish<QT, D, 1>(p, workers, info.sm_count * 6, stream);
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
