@@ -25,7 +25,7 @@ SOURCES = ["pa_host.cu", "pa_cache_ops.cu", "pa_decode_api.cu", "pa_decode_f16.c
            "pa_prefill_i8.cu", "pa_fp4_cache.cu", "pa_decode_fp4_b8.cu",
            "pa_decode_fp4_b16.cu", "pa_decode_fp4_b32.cu", "pa_prefill_fp4.cu",
            "pa_gather.cu", "pa_compact.cu", "pa_weights.cu", "pa_evict.cu", "pa_latent.cu",
-           "pa_latent_decode.cu", "pa_latent_prefill.cu", "pa_prefix_cache.cpp"]
+           "pa_latent_decode.cu", "pa_latent_pair.cu", "pa_latent_prefill.cu", "pa_prefix_cache.cpp"]
 
 
 def _nvcc() -> str:

@@ -30,8 +30,7 @@
 #include <math.h>
 
 #include "pa_common.cuh"
-#include "pa_latent.h"
-#include "pa_shares.cuh"
+#include "pa_latent_decode.cuh"
 
 namespace pa {
 namespace {
@@ -45,25 +44,9 @@ constexpr int kGroup = kCols * kAtom;  // 8 rows
 constexpr int kTileBytes = kTile / 8 * kGroup;
 constexpr int kDims = 128;             // of one O^T product
 constexpr int kBlocksO = kLatentDim / kDims;
-constexpr int kSoftmaxThreads = 256;
 constexpr int kTmaWarp = 8, kQkWarp = 9;  // and 10: O^T
 constexpr int kThreads = 11 * 32;
 constexpr int kMaxWorkers = 152;       // shares of one row tile, at most; sizes the workspace
-constexpr int kMinTiles = 2;           // a smaller share only adds joining
-constexpr float kLazy = 8.f;
-
-struct LatentParams {
-  CUtensorMap tmap_q;  // [S n H, 576] in boxes of {64, N}
-  CUtensorMap tmap_c;  // the cache, boxes of a slot (or of a block of 8)
-  void *out;
-  const int32_t *tables, *lens;
-  float2 *part_ml;     // [row tiles, workers, 2, N]
-  float *part_o;       // [row tiles, workers, 2, N, 512]
-  long long *prefix;   // [S + 1] tiles before sequence s
-  int num_seqs, new_tokens, heads, rows, row_tiles, num_blocks, bs_shift, max_blocks, limit;
-  float scale_log2;
-  int *err;
-};
 
 template <int N>
 struct Layout {
@@ -90,23 +73,6 @@ struct Header {
 };
 static_assert(sizeof(Header) <= 2048, "the header's place");
 constexpr float kNone = 3e38f;  // of a row without a maximum yet: any score passes it, none (-inf) stays -inf
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool x) {
-  uint32_t y;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(y)
-      : "r"(static_cast<uint32_t>(x))
-      : "memory");
-  return y != 0;
-}
 
 // NCOL consecutive columns of the warp's lanes
 #define PA_R8(a, o) a(r[o]), a(r[o + 1]), a(r[o + 2]), a(r[o + 3]), a(r[o + 4]), a(r[o + 5]), a(r[o + 6]), a(r[o + 7])
@@ -190,38 +156,6 @@ __device__ __forceinline__ void tmem_load_rows16(uint32_t taddr, float (&v)[NCOL
 }
 #undef PA_R4
 
-__host__ __device__ inline long long worker_count(long long tiles, long long most) {
-  const long long n = (tiles + kMinTiles - 1) / kMinTiles;
-  return n < most ? n : most;
-}
-
-// One piece of a block's share: tiles [t0, t1) of a sequence, in order.
-struct Walk {
-  long long u, end, first;
-  int s, L, tiles, t0, t1;
-  __device__ __forceinline__ bool next(const LatentParams &p) {
-    while (u < end) {
-      L = checked_len(p.lens, s, p.limit, nullptr);
-      tiles = (L + kTile - 1) / kTile;
-      if (tiles == 0) {
-        ++s;
-        continue;
-      }
-      t0 = static_cast<int>(u - first);
-      t1 = end - u < tiles - t0 ? t0 + static_cast<int>(end - u) : tiles;
-      return true;
-    }
-    return false;
-  }
-  __device__ __forceinline__ void advance() {
-    u += t1 - t0;
-    if (t1 == tiles) {
-      first += tiles;
-      ++s;
-    }
-  }
-};
-
 template <int DT, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ LatentParams p, int max_workers) {
@@ -258,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) record_error(p.err, kErrSmemAlign);
     return;
   }
-  Walk walk;
+  Walk<kTile> walk;
   walk.u = share_begin(w, total, workers);
   walk.end = share_begin(w + 1, total, workers);
   walk.s = scan.find(walk.u, p.num_seqs, tiles_of, walk.first);
@@ -526,19 +460,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           record_error(p.err, kErrBlockIndex);
           mine = 0;
         }
-        bool got = true;
-        if (lane < boxes && i >= kStages)
-          got = mbar_wait(&hdr.kv_empty[st][(lane << box_sh) >> 4], ((i >> 1) - 1) & 1, abort);
-        if (!__all_sync(0xffffffffu, got)) {
+        const int row = (mine << p.bs_shift) + (tok & ((1 << p.bs_shift) - 1));
+        if (lane == 0 && i >= kStages) free = mbar_wait(&hdr.kv_empty[st][0], ((i >> 1) - 1) & 1, abort);
+        if (!__shfl_sync(0xffffffffu, free, 0)) {
           ok = false;
           break;
         }
         if (lane == 0) mbar_arrive_expect_tx(&hdr.kv_full[st], n_box * box_bytes);
         __syncwarp();
-        if (lane < n_box) {
-          const int row = (mine << p.bs_shift) + (tok & ((1 << p.bs_shift) - 1));
-          tma_load_4d(kv + st * kTileBytes + lane * box_bytes, &p.tmap_c, 0, 0, 0, row >> 3, &hdr.kv_full[st]);
+        for (int g = 0; ok && g < kSlots; ++g) {  // slot by slot, each as soon as it is free
+          if (g > 0 && i >= kStages)
+            ok = __all_sync(0xffffffffu, mbar_wait(&hdr.kv_empty[st][g], ((i >> 1) - 1) & 1, abort));
+          if (ok && lane < n_box && (lane << box_sh) >> 4 == g)
+            tma_load_4d(kv + st * kTileBytes + lane * box_bytes, &p.tmap_c, 0, 0, 0, row >> 3, &hdr.kv_full[st]);
         }
+        if (!ok) break;
       }
       if (ok) walk.advance();
     }
@@ -736,7 +672,7 @@ cudaError_t launch_merge(const LatentParams &p, int workers, cudaStream_t stream
   return cudaLaunchKernelEx(&cfg, latent_merge_kernel<DT, N, TEAM, DSPLIT>, p, workers);
 }
 
-int columns_for(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int columns_for(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kPairRows; }
 
 struct Sizes {
   size_t prefix, ml, o, total;
@@ -746,13 +682,22 @@ bool sizes_of(int S, int n, int H, Sizes *z) {
   const long long rows = static_cast<long long>(n) * H;
   if (rows > INT_MAX / 2 || rows * S > INT_MAX / 2) return false;
   const int N = columns_for(rows);
-  const size_t slots = static_cast<size_t>((rows + N - 1) / N) * kMaxWorkers * 2;
+  const size_t slots = static_cast<size_t>((rows + N - 1) / N) * (N == kPairRows ? kMaxPairs : kMaxWorkers) * 2;
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   z->prefix = up(8 * (static_cast<size_t>(S) + 1));
   z->ml = up(slots * N * sizeof(float2));
   z->o = up(slots * N * kLatentDim * sizeof(float));
   z->total = z->prefix + z->ml + z->o;
   return true;
+}
+
+template <int DT, int N>
+pa_status join(const LatentParams &p, int workers, int sms, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.num_seqs) * p.rows;
+  const cudaError_t e = rows <= sms * 2ll    ? launch_merge<DT, N, 16, 4>(p, workers, stream)
+                        : rows <= sms * 16ll ? launch_merge<DT, N, 4, 1>(p, workers, stream)
+                                             : launch_merge<DT, N, 1, 1>(p, workers, stream);
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
 template <int DT, int N>
@@ -785,20 +730,20 @@ pa_status launch(LatentParams &p, const void *q, cudaStream_t stream) {
   latent_decode_kernel<DT, N><<<workers * p.row_tiles, kThreads, Lay::SMEM, stream>>>(p, workers);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  const long long rows = static_cast<long long>(p.num_seqs) * p.rows;
-  e = rows <= info.sm_count * 2ll    ? launch_merge<DT, N, 16, 4>(p, workers, stream)
-      : rows <= info.sm_count * 16ll ? launch_merge<DT, N, 4, 1>(p, workers, stream)
-                                     : launch_merge<DT, N, 1, 1>(p, workers, stream);
-  return e == cudaSuccess ? PA_OK : cuda_fail(e);
+  return join<DT, N>(p, workers, info.sm_count, stream);
 }
 
 template <int DT>
-pa_status by_rows(LatentParams &p, const void *q, cudaStream_t stream) {
+pa_status by_rows(LatentParams &p, const void *q, const void *cache, const pa_latent_desc *desc, cudaStream_t stream) {
   switch (columns_for(p.rows)) {
     case 16: return launch<DT, 16>(p, q, stream);
     case 32: return launch<DT, 32>(p, q, stream);
   }
-  return launch<DT, 64>(p, q, stream);
+  if (p.rows <= 64) return launch<DT, 64>(p, q, stream);
+  int workers = 0;
+  const pa_status st = launch_latent_pair(DT, p, q, cache, desc, &workers, stream);
+  DeviceInfo info;
+  return st != PA_OK || !current_device_info(&info) ? st : join<DT, kPairRows>(p, workers, info.sm_count, stream);
 }
 
 }  // namespace
@@ -852,5 +797,5 @@ extern "C" pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype,
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = device_error;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return desc->dtype == PA_F16 ? by_rows<kF16>(p, q, st) : by_rows<kBF16>(p, q, st);
+  return desc->dtype == PA_F16 ? by_rows<kF16>(p, q, cache, desc, st) : by_rows<kBF16>(p, q, cache, desc, st);
 }

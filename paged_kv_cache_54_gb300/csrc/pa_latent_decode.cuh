@@ -1,0 +1,88 @@
+// What the kernels of pa_latent_decode share: parameters, shares of the work,
+// the softmax warps' barriers.
+#pragma once
+
+#include "pa_common.cuh"
+#include "pa_latent.h"
+#include "pa_shares.cuh"
+
+namespace pa {
+
+constexpr int kMinTiles = 2;     // a share of fewer tiles only adds joining
+constexpr float kLazy = 8.f;     // a row's maximum is raised when a score passes it by more (base 2)
+constexpr int kSoftmaxThreads = 256;
+
+struct LatentParams {
+  CUtensorMap tmap_q;  // [S n H, 576] in boxes of {64, N} (64 rows for a pair)
+  CUtensorMap tmap_c;  // the cache, boxes of a slot (or of a block of 8); for a pair, of three of its columns
+  CUtensorMap tmap_v;  // for a pair: of two columns
+  void *out;
+  const int32_t *tables, *lens;
+  float2 *part_ml;     // [row tiles, workers, 2, N]
+  float *part_o;       // [row tiles, workers, 2, N, 512]
+  long long *prefix;   // [S + 1] tiles before sequence s
+  int num_seqs, new_tokens, heads, rows, row_tiles, num_blocks, bs_shift, max_blocks, limit;
+  float scale_log2;
+  int *err;
+};
+
+// 64 < rows: a row tile of 128 query rows to a pair of blocks (pa_latent_pair.cu).
+// Sets p.row_tiles and *workers, the shares of one row tile.
+constexpr int kPairRows = 128, kMaxPairs = 76;
+pa_status launch_latent_pair(int dtype, LatentParams &p, const void *q, const void *cache, const pa_latent_desc *desc,
+                             int *workers, cudaStream_t stream);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return y != 0;
+}
+
+__host__ __device__ inline long long worker_count(long long tiles, long long most) {
+  const long long n = (tiles + kMinTiles - 1) / kMinTiles;
+  return n < most ? n : most;
+}
+
+// One piece of a share: tiles [t0, t1), of TILE tokens, of a sequence, in
+// order.
+template <int TILE>
+struct Walk {
+  long long u, end, first;
+  int s, L, tiles, t0, t1;
+  __device__ __forceinline__ bool next(const LatentParams &p) {
+    while (u < end) {
+      L = checked_len(p.lens, s, p.limit, nullptr);
+      tiles = (L + TILE - 1) / TILE;
+      if (tiles == 0) {
+        ++s;
+        continue;
+      }
+      t0 = static_cast<int>(u - first);
+      t1 = end - u < tiles - t0 ? t0 + static_cast<int>(end - u) : tiles;
+      return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ void advance() {
+    u += t1 - t0;
+    if (t1 == tiles) {
+      first += tiles;
+      ++s;
+    }
+  }
+};
+#endif
+
+}  // namespace pa

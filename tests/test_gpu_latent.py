@@ -106,6 +106,10 @@ SHAPES = [
     ([0, 0], 1, 16, 16),
     ([5000], 1, 16, 16),
     ([3000, 4000, 200], 1, 64, 32),
+    ([128, 256], 1, 128, 16),
+    ([129, 0, 2000, 64], 1, 100, 8),   # 128 rows a tile, some of them none
+    ([3000, 1], 2, 96, 32),
+    ([9000, 300], 1, 128, 16),
 ]
 
 
@@ -126,18 +130,20 @@ def test_decode_of_many_sequences_of_many_lengths():
     check(got, want, tol)
 
 
+@pytest.mark.parametrize("heads", [32, 128])
 @pytest.mark.parametrize("factor", [0.0, -3.0, 40.0])
-def test_decode_scales(factor):
+def test_decode_scales(factor, heads):
     # (40 times the usual scale: maxima rise by far more than 2^8 on the way, and few tokens take all of the weight)
-    cache, table, L, q = make([700, 64, 3], 1, 32, 16, "f16", 11)
+    cache, table, L, q = make([700, 64, 3], 1, heads, 16, "f16", 11)
     got = run(cache, table, L, q, SCALE * factor)
     want, tol = expect(cache, table, L, q, 16, SCALE * factor, eps(torch.float16))
     check(got, want, tol)
 
 
-def test_decode_with_rising_scores():
+@pytest.mark.parametrize("heads", [16, 128])
+def test_decode_with_rising_scores(heads):
     """Every tile's scores lie far above the last one's."""
-    cache, table, L, q = make([900], 1, 16, 16, "bf16", 13)
+    cache, table, L, q = make([900], 1, heads, 16, "bf16", 13)
     n = torch.arange(900, device=DEV)
     rows = cache[table[0].long()].view(-1, ROW)
     rows[:900] = (rows[:900].float() * (n[:, None] / 100.0)).bfloat16()
