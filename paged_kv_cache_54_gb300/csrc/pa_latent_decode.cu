@@ -437,7 +437,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = tile * kTile + (lane << box_sh);
         return lane < boxes && tok < walk.L ? __ldg(table + (tok >> p.bs_shift)) : 0;
       };
-      int phys = entry(walk.t0);
+      // A tile is fetched into L2 two tiles ahead of its copy: the copy then
+      // takes about 1500 clocks in place of 2500 to 4000, and two tiles in
+      // shared memory keep up.
+      auto row_of = [&](int block, int tile) {
+        const int tok = tile * kTile + (lane << box_sh);
+        return (block << p.bs_shift) + (tok & ((1 << p.bs_shift) - 1));
+      };
+      auto fetch = [&](int block, int tile) {
+        if (tile < walk.t1 && lane < boxes && tile * kTile + (lane << box_sh) < walk.L && block >= 0 &&
+            block < p.num_blocks)
+          tma_prefetch_4d(&p.tmap_c, 0, 0, 0, row_of(block, tile) >> 3);
+      };
+      int phys = entry(walk.t0), phys1 = entry(walk.t0 + 1), phys2 = entry(walk.t0 + 2);
       bool free = true;
       if (lane == 0 && seg > 0) free = mbar_wait(&hdr.q_empty, (seg - 1) & 1, abort);
       if (!__shfl_sync(0xffffffffu, free, 0)) {
@@ -452,15 +464,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         const int st = i & 1;
-        const int tok = tile * kTile + (lane << box_sh);
         const int n_box = min(boxes, ((walk.L - tile * kTile) + (1 << box_sh) - 1) >> box_sh);
         int mine = phys;
-        if (tile + 1 < walk.t1) phys = entry(tile + 1);
         if (lane < n_box && (mine < 0 || mine >= p.num_blocks)) {
           record_error(p.err, kErrBlockIndex);
           mine = 0;
         }
-        const int row = (mine << p.bs_shift) + (tok & ((1 << p.bs_shift) - 1));
+        const int row = row_of(mine, tile);
         if (lane == 0 && i >= kStages) free = mbar_wait(&hdr.kv_empty[st][0], ((i >> 1) - 1) & 1, abort);
         if (!__shfl_sync(0xffffffffu, free, 0)) {
           ok = false;
@@ -475,6 +485,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(kv + st * kTileBytes + lane * box_bytes, &p.tmap_c, 0, 0, 0, row >> 3, &hdr.kv_full[st]);
         }
         if (!ok) break;
+        if (tile == walk.t0) fetch(phys1, tile + 1);
+        fetch(phys2, tile + 2);
+        phys = phys1;
+        phys1 = phys2;
+        phys2 = entry(tile + 3);
       }
       if (ok) walk.advance();
     }

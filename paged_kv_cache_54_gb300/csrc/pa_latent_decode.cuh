@@ -15,7 +15,7 @@ constexpr int kSoftmaxThreads = 256;
 struct LatentParams {
   CUtensorMap tmap_q;  // [S n H, 576] in boxes of {64, N} (64 rows for a pair)
   CUtensorMap tmap_c;  // the cache, boxes of a slot (or of a block of 8); for a pair, of three of its columns
-  CUtensorMap tmap_v;  // for a pair: of two columns
+  CUtensorMap tmap_v;  // for a pair: of four columns
   void *out;
   const int32_t *tables, *lens;
   float2 *part_ml;     // [row tiles, workers, 2, N]

@@ -24,7 +24,7 @@
 //         raised, and O rescaled, only when a score passes it by 2^8.
 //   8     TMA: q, then K in three parts of three 128-byte columns
 //   9, 10 (first block) issue the products of both
-//   11    TMA: V in four parts of 64 tokens, 128 dimensions
+//   11    TMA: V in two parts of 64 tokens
 #include <limits.h>
 #include <math.h>
 
@@ -41,7 +41,7 @@ constexpr int kQBytes = kCols * kQCol;
 constexpr int kKParts = 3, kKCols = kCols / kKParts;    // parts of K, and their columns
 constexpr int kKGroup = kKCols * 1024;                  // 8 tokens of a part
 constexpr int kKBytes = 8 * kKGroup;                    // 64 tokens
-constexpr int kVParts = 4, kVGroup = 2 * 1024;          // (64 tokens, 128 dimensions) each
+constexpr int kVParts = 2, kVGroup = 4 * 1024;          // of V: 64 tokens, 256 dimensions each
 constexpr int kVBytes = 8 * kVGroup;
 constexpr int kPBlock = kHalfRows * 128;                // 64 tokens of P
 constexpr int kQOff = 2048, kPOff = kQOff + kQBytes, kKOff = kPOff + 2 * kPBlock, kVOff = kKOff + kKParts * kKBytes;
@@ -53,7 +53,7 @@ constexpr uint32_t kTmemS = 256, kTmemCols = 512;
 static_assert(kSmem <= 232448 && kKOff % 1024 == 0, "shared memory");
 
 struct Header {
-  uint64_t q_full, q_empty, k_full[kKParts], k_empty[kKParts], v_full, v_empty[kVParts], s_full[2], s_empty[2], p_full,
+  uint64_t q_full, q_empty, k_full[kKParts], k_empty[kKParts], v_full, v_last, v_empty[kVParts], s_full[2], s_empty[2], p_full,
       pv_done, fin;
   uint32_t tmem;
   int abort;
@@ -67,24 +67,11 @@ __device__ __forceinline__ uint32_t in_block(const void *p, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(smem_addr(p)), "r"(rank));
   return y;
 }
-__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Wait for arrivals of both blocks.
-__device__ __forceinline__ bool cluster_wait(uint64_t *bar, uint32_t parity, const volatile int *abort) {
-  const uint32_t a = smem_addr(bar);
-  const unsigned long long t0 = global_timer_ns();
-  for (uint32_t i = 1;; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if ((i & 63u) == 0 && (*abort || global_timer_ns() - t0 > kWaitLimitNs)) return false;
-  }
+// An arrival on an mbarrier of either block.  (What it follows is read by this
+// block's own tensor cores, behind a proxy fence: no release to the cluster,
+// which costs about 1000 clocks.)
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Tiled loads whose bytes count on an mbarrier of either block of the pair.
 __device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
@@ -170,6 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&hdr.k_empty[i], 1);
     }
     mbar_init(&hdr.v_full, 1);
+    mbar_init(&hdr.v_last, 1);
     for (int i = 0; i < kVParts; ++i) mbar_init(&hdr.v_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&hdr.s_full[i], 1);
@@ -211,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
       tc_fence_after_sync();
     };
-    int i = 0;  // tiles so far
+    int i = 0, lasts = 0;  // tiles so far, and those that end past their sequence
     for (int seg = 0; walk.next(p); ++seg) {
       const int see = row < p.rows ? walk.L - (p.new_tokens - 1 - row / p.heads) : 0;  // tokens the row sees
       const int all_see = (rt + 1) * kPairRows > p.rows ? 0 : walk.L - (p.new_tokens - 1 - rt * kPairRows / p.heads);
@@ -222,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_ld32(tlane + kTmemS + (i & 1) * 64 + 32 * part, raw);
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) cluster_arrive(s_empty[i & 1]);
+        if (lane == 0) pair_arrive(s_empty[i & 1]);
         float x[32], top = -INFINITY;
         const int key = tile * kTile + 32 * q4;
         if ((tile + 1) * kTile > all_see) {
@@ -274,20 +262,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = 0; u < 4; ++u)
           *reinterpret_cast<uint4 *>(to + (((4 * part + u) ^ (r & 7)) << 4)) =
               make_uint4(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]);
-        wait(&hdr.v_full, i & 1);  // (what the first block takes as V being there in both)
         if ((tile + 1) * kTile > walk.L) {
           // rows behind the sequence's end hold anything: zero them, 0 * NaN would reach O
+          wait(&hdr.v_last, lasts++ & 1);
           const int z0 = walk.L - tile * kTile;
           for (int idx = threadIdx.x; idx < (kTile - z0) * 32; idx += kSoftmaxThreads) {
             const int z = z0 + idx / 32, e = idx % 32;  // token, and 16 bytes of its 256 dimensions
-            *reinterpret_cast<uint4 *>(vs + ((z >> 6) * 2 + (e >> 4)) * kVBytes + ((z & 63) >> 3) * kVGroup +
-                                       ((e >> 3) & 1) * 1024 + (z & 7) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(vs + (z >> 3) * kVGroup + (e >> 3) * 1024 + (z & 7) * 128 + (e & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
           }
         }
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) cluster_arrive(p_full);
+        if (lane == 0) pair_arrive(p_full);
       }
       softmax_sync();  // (the maxima have been read)
       hdr.top[q4][r] = l;
@@ -337,28 +325,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kKTmaWarp || warp == kVTmaWarp) {
     // -------------------------------------------------------------------- TMA
     // boxes of 16 tokens (of 8 with blocks of 8): K, of the block's 64 tokens
-    // of a tile, lane (part, box); V, of all 128, lane (64 tokens, dimensions, box)
+    // of a tile, lane (part, box); V, of all 128, lane (64 tokens, box).  Bytes
+    // count in the first block, for the products' issue, but for V tiles that
+    // end past their sequence: those count in each block, whose softmax warps
+    // zero the rows behind its end before the weights are announced.
     const bool is_k = warp == kKTmaWarp;
     const int box_sh = p.bs_shift < 4 ? 3 : 4, boxes = 64 >> box_sh;  // boxes of 64 tokens
     const int piece = lane / boxes, box = lane % boxes;               // this lane's part, and box in it
     const int parts = is_k ? kKParts : kVParts;
     const bool in = piece < parts;
-    const int tok0 = (is_k ? 64 * rank : 64 * (piece >> 1)) + (box << box_sh);  // its first token in a tile
+    const int tok0 = (is_k ? 64 * rank : 64 * piece) + (box << box_sh);  // its first token in a tile
     const uint32_t bytes = (1u << box_sh) / 8 * (is_k ? kKGroup : kVGroup);
     uint8_t *to = is_k ? ks + piece * kKBytes + box * bytes : vs + piece * kVBytes + box * bytes;
-    const int column = is_k ? piece * kKCols : 4 * rank + 2 * (piece & 1);
+    const int column = is_k ? piece * kKCols : 4 * rank;
     uint64_t *empty = is_k ? hdr.k_empty : hdr.v_empty;
     const uint32_t q_full = in_block(&hdr.q_full, 0);
-    const uint32_t k_full = in_block(&hdr.k_full[in && is_k ? piece : 0], 0);
+    const uint32_t full = in_block(is_k ? &hdr.k_full[in ? piece : 0] : &hdr.v_full, 0);
     bool ok = true;
-    int i = 0;
+    int i = 0, fulls = 1;  // (V tiles counted in v_full, less one)
     for (int seg = 0; ok && walk.next(p); ++seg) {
       const int32_t *table = p.tables + static_cast<size_t>(walk.s) * p.max_blocks;
       auto entry = [&](int tile) {
         const int tok = tile * kTile + tok0;
         return in && tok < walk.L ? __ldg(table + (tok >> p.bs_shift)) : 0;
       };
-      int phys = entry(walk.t0);
+      // K is fetched into L2 two tiles ahead of its copy (V then comes from there)
+      auto row8_of = [&](int block, int tile) {
+        const int tok = tile * kTile + tok0;
+        return ((block << p.bs_shift) + (tok & ((1 << p.bs_shift) - 1))) >> 3;
+      };
+      auto fetch = [&](int block, int tile) {
+        if (is_k && in && tile < walk.t1 && tile * kTile + tok0 < walk.L && block >= 0 && block < p.num_blocks)
+          tma_prefetch_4d(&p.tmap_c, 0, 0, column, row8_of(block, tile));
+      };
+      int phys = entry(walk.t0), phys1 = entry(walk.t0 + 1), phys2 = entry(walk.t0 + 2);
       if (is_k) {
         bool free = true;
         if (lane == 0 && seg > 0) free = mbar_wait(&hdr.q_empty, (seg - 1) & 1, abort);
@@ -375,7 +375,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         const int tok = tile * kTile + tok0;
         int mine = phys;
-        if (tile + 1 < walk.t1) phys = entry(tile + 1);
         const bool loads = in && tok < walk.L;
         if (loads && (mine < 0 || mine >= p.num_blocks)) {
           record_error(p.err, kErrBlockIndex);
@@ -383,25 +382,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int left = walk.L - tile * kTile;  // tokens of the tile, and boxes of them
         const int n = (min(left, kTile) + (1 << box_sh) - 1) >> box_sh;
-        const int row8 = ((mine << p.bs_shift) + (tok & ((1 << p.bs_shift) - 1))) >> 3;
+        const bool last = left < kTile;
+        fulls += !last;
+        const int row8 = row8_of(mine, tile);
         // part by part, each as soon as it is free
         for (int g = 0; ok && g < parts; ++g) {
           if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty + g, (i - 1) & 1, abort));
           if (!ok) break;
-          // (a K part's bytes, of both blocks, count in the first one; V's in each, for all parts)
           if (lane == 0) {
             if (is_k && rank == 0) mbar_arrive_expect_tx(&hdr.k_full[g], n * bytes);
-            if (!is_k && g == 0) mbar_arrive_expect_tx(&hdr.v_full, 2 * n * bytes);
+            if (!is_k && g == 0 && last) mbar_arrive_expect_tx(&hdr.v_last, n * bytes);
+            if (!is_k && g == 0 && !last && rank == 0) mbar_arrive_expect_tx(&hdr.v_full, 2 * n * bytes);
           }
           __syncwarp();
           if (loads && piece == g) {
-            if (is_k)
-              pair_load_4d(to, &p.tmap_c, 0, 0, column, row8, k_full);
+            if (!is_k && last)
+              tma_load_4d(to, &p.tmap_v, 0, 0, column, row8, &hdr.v_last);
             else
-              tma_load_4d(to, &p.tmap_v, 0, 0, column, row8, &hdr.v_full);
+              pair_load_4d(to, is_k ? &p.tmap_c : &p.tmap_v, 0, 0, column, row8, full);
           }
         }
         if (!ok) break;
+        if (tile == walk.t0) fetch(phys1, tile + 1);
+        fetch(phys2, tile + 2);
+        phys = phys1;
+        phys1 = phys2;
+        phys2 = entry(tile + 3);
       }
       if (ok) walk.advance();
     }
@@ -409,9 +415,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       record_error(p.err, kErrTimeout);
       *abort = 1;
       // wait, within the limit, for the copies still in flight
-      if (i > 0 && !is_k) mbar_wait(&hdr.v_full, (i - 1) & 1, nullptr);
-      if (i > 0 && is_k && rank == 0)
-        for (int j = 0; j < kKParts; ++j) mbar_wait(&hdr.k_full[j], (i - 1) & 1, nullptr);
+      if (i > 0 && rank == 0) {
+        if (is_k)
+          for (int j = 0; j < kKParts; ++j) mbar_wait(&hdr.k_full[j], (i - 1) & 1, nullptr);
+        else
+          mbar_wait(&hdr.v_full, fulls & 1, nullptr);
+      }
     }
   } else if (warp == kQkWarp) {
     // -------------------------------------------------------------------- S
@@ -420,12 +429,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int i = 0;
       const uint32_t qa = smem_addr(qs), ka = smem_addr(ks);
       for (int seg = 0; ok && walk.next(p); ++seg) {
-        ok = cluster_wait(&hdr.q_full, seg & 1, abort);
+        ok = mbar_wait(&hdr.q_full, seg & 1, abort);
         for (int tile = walk.t0; ok && tile < walk.t1; ++tile, ++i) {
-          if (i >= 2) ok = cluster_wait(&hdr.s_empty[i & 1], ((i >> 1) - 1) & 1, abort);
+          if (i >= 2) ok = mbar_wait(&hdr.s_empty[i & 1], ((i >> 1) - 1) & 1, abort);
           const uint32_t d = tmem + kTmemS + (i & 1) * 64;
           for (int g = 0; ok && g < kKParts; ++g) {
-            ok = cluster_wait(&hdr.k_full[g], i & 1, abort);
+            ok = mbar_wait(&hdr.k_full[g], i & 1, abort);
             if (!ok) break;
             tc_fence_after_sync();
             const uint64_t a0 = umma_desc_sw128(qa + g * kKCols * kQCol, 16, 1024);
@@ -452,23 +461,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------------- O
     if (rank == 0 && elect_one()) {
       bool ok = true;
-      int i = 0;
+      int i = 0, fulls = 0;
       const uint32_t pa_ = smem_addr(ps), va = smem_addr(vs);
       while (ok && walk.next(p)) {
         for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
-          if (!cluster_wait(&hdr.p_full, i & 1, abort)) {
+          if (!mbar_wait(&hdr.p_full, i & 1, abort)) {
+            ok = false;
+            break;
+          }
+          // (of a tile that ends past its sequence, the weights' arrival says that V is there)
+          if ((tile + 1) * kTile <= walk.L && !mbar_wait(&hdr.v_full, fulls++ & 1, abort)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
 #pragma unroll
-          for (int g = 0; g < kVParts; ++g) {  // 64 tokens g >> 1, block of dimensions g & 1
-            const uint64_t a0 = umma_desc_sw128(pa_ + (g >> 1) * kPBlock, 16, 1024);
+          for (int g = 0; g < kVParts; ++g) {  // 64 tokens
+            const uint64_t a0 = umma_desc_sw128(pa_ + g * kPBlock, 16, 1024);
             const uint64_t b0 = umma_desc_sw128(va + g * kVBytes, 1024, kVGroup);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              pair_mma(tmem + (g & 1) * 128, a0 + (kk * 32 >> 4), b0 + (kk * 2 * kVGroup >> 4), IDESC_PV,
-                       (tile > walk.t0 || g > 1 || kk > 0) ? 1u : 0u);
+#pragma unroll
+              for (int b = 0; b < 2; ++b)  // 128 dimensions of either block
+                pair_mma(tmem + b * 128, a0 + (kk * 32 >> 4), b0 + ((kk * 2 * kVGroup + b * 2 * 1024) >> 4), IDESC_PV,
+                         (tile > walk.t0 || g > 0 || kk > 0) ? 1u : 0u);
             pair_commit(&hdr.v_empty[g]);
           }
           pair_commit(&hdr.pv_done);
@@ -524,7 +540,7 @@ pa_status launch_latent_pair(int dtype, LatentParams &p, const void *q, const vo
       enc(&p.tmap_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(q), dims, strides, box, estr,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-      !encode_latent_view(&p.tmap_c, cache, desc, kKCols, groups) || !encode_latent_view(&p.tmap_v, cache, desc, 2, groups))
+      !encode_latent_view(&p.tmap_c, cache, desc, kKCols, groups) || !encode_latent_view(&p.tmap_v, cache, desc, 4, groups))
     return cuda_fail(cudaErrorInvalidValue);
   p.row_tiles = (p.rows + kPairRows - 1) / kPairRows;
   const int pairs = info.sm_count / 2 < kMaxPairs ? info.sm_count / 2 : kMaxPairs;
