@@ -576,115 +576,182 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of sequences that several blocks shared, and writes the
-// rows of sequences without tokens.  TEAM warps take one of DSPLIT parts of a
-// query row's dimensions, each every TEAM-th piece; a block is 16 warps.
-// Bound by the latency of its loads: many warps a row where rows are few (one
-// sequence in 152 pieces, 32 rows: 13 us with a block a row, 4 with four
-// blocks), one where they are many (128 sequences in two pieces, 128 rows).
+// Join the pieces of sequences that several blocks shared, and write the rows
+// of sequences without tokens.  Bound by the latency of a chain of small
+// loads: where rows are few, many warps take one of them (latent_merge_few),
+// where they are many a block takes many rows of one sequence
+// (latent_merge_many).
 constexpr int kMergeWarps = 16;
 
-template <int DT, int N, int TEAM, int DSPLIT>
-__global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const LatentParams p, int max_workers) {
-  constexpr int DIMS = kLatentDim / DSPLIT, VEC = DIMS / 128;  // of a block, and the lane's fours of them
-  __shared__ float part[TEAM > 1 ? kMergeWarps : 1][DIMS];
-  __shared__ float sums[kMergeWarps];
-  grid_dependency_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mate = warp % TEAM;
-  const int row = blockIdx.x / DSPLIT * (kMergeWarps / TEAM) + warp / TEAM, d0 = blockIdx.x % DSPLIT * DIMS;
-  const bool exists = row < p.num_seqs * p.rows;
-  bool joins = false;
-  float4 o[VEC];
-  float l = 0.f;
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (exists) {
-    const int s = row / p.rows, r = row % p.rows;
+// Where a row's pieces lie: n of them, or none where it was written whole.
+template <int N>
+struct Pieces {
+  int n, late;
+  size_t base;
+  bool empty;
+  __device__ __forceinline__ Pieces(const LatentParams &p, int max_workers, int s) {
     const long long u0 = p.prefix[s], u1 = p.prefix[s + 1], total = p.prefix[p.num_seqs];
-    joins = u1 == u0;  // no token: zeros
-    if (u1 > u0) {
-      const long long workers = worker_count(total, max_workers);
-      const long long w0 = share_owner(u0, total, workers), w1 = share_owner(u1 - 1, total, workers);
-      joins = w1 > w0;  // (else written whole)
-      if (joins) {
-        const int n = static_cast<int>(w1 - w0) + 1;
-        // a block's first piece is in its place 0; the sequence is not the first of its first block if that began earlier
-        const int late = share_begin(w0, total, workers) < u0;
-        const size_t base = ((static_cast<size_t>(r / N) * max_workers + w0) * 2) * N + r % N;
-        auto slot = [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * N; };
-        float m = -INFINITY;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[slot(i)].x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (m == -INFINITY) m = 0.f;
-#pragma unroll 4
-        for (int i = mate; i < n; i += TEAM) {
-          const float2 ml = p.part_ml[slot(i)];
-          const float4 *x = reinterpret_cast<const float4 *>(p.part_o + slot(i) * kLatentDim + d0) + lane;
-          const float f = exp2_fast(ml.x - m);
-          l += f * ml.y;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float4 y = x[32 * e];
-            o[e].x += f * y.x;
-            o[e].y += f * y.y;
-            o[e].z += f * y.z;
-            o[e].w += f * y.w;
-          }
-        }
-      }
-    }
+    n = late = 0;
+    base = 0;
+    empty = u1 == u0;
+    if (empty) return;
+    const long long workers = worker_count(total, max_workers);
+    const long long w0 = share_owner(u0, total, workers), w1 = share_owner(u1 - 1, total, workers);
+    if (w0 == w1) return;
+    n = static_cast<int>(w1 - w0) + 1;
+    // a block's first piece is in its place 0; the sequence is not the first of its first block if that began earlier
+    late = share_begin(w0, total, workers) < u0;
+    base = static_cast<size_t>(w0) * 2 * N;
   }
-  if constexpr (TEAM > 1) {
-    float4 *mine = reinterpret_cast<float4 *>(part[warp]) + lane;
+  // piece i of query row r
+  __device__ __forceinline__ size_t at(int i, int r, int max_workers) const {
+    return static_cast<size_t>(r / N) * max_workers * 2 * N + base + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * N +
+           r % N;
+  }
+};
+
+// A block joins rows [r0, r0 + per) of a sequence, a warp every 16th, a lane
+// 16 of the dimensions.
+template <int DT, int N>
+__global__ void __launch_bounds__(kMergeWarps * 32, 2) latent_merge_many(const LatentParams p, int max_workers, int per) {
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (p.rows + per - 1) / per, s = blockIdx.x / chunks, r0 = blockIdx.x % chunks * per;
+  const Pieces<N> pieces(p, max_workers, s);
+  if (pieces.n == 0 && !pieces.empty) return;
+  for (int r = r0 + warp; r < min(p.rows, r0 + per); r += kMergeWarps) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < pieces.n; i += 32) m = fmaxf(m, p.part_ml[pieces.at(i, r, max_workers)].x);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) mine[32 * e] = o[e];
-    if (lane == 0) sums[warp] = l;
-    __syncthreads();
-    // the team's warps each join a share of the dimensions
-    if (!joins) return;
-    const int first = warp - mate;
-    l = 0.f;
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (m == -INFINITY) m = 0.f;
+    float4 o[4];
 #pragma unroll
-    for (int i = 0; i < TEAM; ++i) l += sums[first + i];
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    constexpr int OWN = DIMS / TEAM / 2;  // pairs of dimensions of a warp
-    for (int d = lane; d < OWN; d += 32) {
-      const int at = (mate * OWN + d) * 2;
-      float x = 0.f, y = 0.f;
+    for (int e = 0; e < 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < pieces.n; ++i) {
+      const size_t at = pieces.at(i, r, max_workers);
+      const float2 ml = p.part_ml[at];
+      const float4 *x = reinterpret_cast<const float4 *>(p.part_o + at * kLatentDim) + lane;
+      const float f = exp2_fast(ml.x - m);
+      l += f * ml.y;
 #pragma unroll
-      for (int i = 0; i < TEAM; ++i) {
-        const float2 z = *reinterpret_cast<const float2 *>(&part[first + i][at]);
-        x += z.x;
-        y += z.y;
+      for (int e = 0; e < 4; ++e) {
+        const float4 y = x[32 * e];
+        o[e].x += f * y.x;
+        o[e].y += f * y.y;
+        o[e].z += f * y.z;
+        o[e].w += f * y.w;
       }
-      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + static_cast<size_t>(row) * kLatentDim + d0 + at) =
-          l == 0.f ? 0u : pack2_rn<DT>(x * inv, y * inv);
     }
-  } else if (joins) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *out = static_cast<uint16_t *>(p.out) + static_cast<size_t>(row) * kLatentDim + d0 + lane * 4;
+    uint16_t *out = static_cast<uint16_t *>(p.out) + (static_cast<size_t>(s) * p.rows + r) * kLatentDim + lane * 4;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e)
+    for (int e = 0; e < 4; ++e)
       *reinterpret_cast<uint2 *>(out + 128 * e) =
           l == 0.f ? make_uint2(0u, 0u)
                    : make_uint2(pack2_rn<DT>(o[e].x * inv, o[e].y * inv), pack2_rn<DT>(o[e].z * inv, o[e].w * inv));
   }
 }
 
+// TEAM warps take one of DSPLIT parts of a row's dimensions, each every
+// TEAM-th piece.
 template <int DT, int N, int TEAM, int DSPLIT>
-cudaError_t launch_merge(const LatentParams &p, int workers, cudaStream_t stream) {
+__global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_few(const LatentParams p, int max_workers) {
+  constexpr int DIMS = kLatentDim / DSPLIT, VEC = DIMS / 128;  // of a block, and the lane's fours of them
+  __shared__ float part[kMergeWarps][DIMS];
+  __shared__ float sums[kMergeWarps];
+  grid_dependency_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mate = warp % TEAM;
+  const int row = blockIdx.x / DSPLIT * (kMergeWarps / TEAM) + warp / TEAM, d0 = blockIdx.x % DSPLIT * DIMS;
+  bool joins = false;
+  float4 o[VEC];
+  float l = 0.f;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row < p.num_seqs * p.rows) {
+    const int r = row % p.rows;
+    const Pieces<N> pieces(p, max_workers, row / p.rows);
+    joins = pieces.n > 0 || pieces.empty;
+    float m = -INFINITY;
+    for (int i = lane; i < pieces.n; i += 32) m = fmaxf(m, p.part_ml[pieces.at(i, r, max_workers)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (m == -INFINITY) m = 0.f;
+#pragma unroll 8
+    for (int i = mate; i < pieces.n; i += TEAM) {
+      const size_t at = pieces.at(i, r, max_workers);
+      const float2 ml = p.part_ml[at];
+      const float4 *x = reinterpret_cast<const float4 *>(p.part_o + at * kLatentDim + d0) + lane;
+      const float f = exp2_fast(ml.x - m);
+      l += f * ml.y;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float4 y = x[32 * e];
+        o[e].x += f * y.x;
+        o[e].y += f * y.y;
+        o[e].z += f * y.z;
+        o[e].w += f * y.w;
+      }
+    }
+  }
+  float4 *mine = reinterpret_cast<float4 *>(part[warp]) + lane;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) mine[32 * e] = o[e];
+  if (lane == 0) sums[warp] = l;
+  __syncthreads();
+  // the team's warps each join a share of the dimensions
+  if (!joins) return;
+  const int first = warp - mate;
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < TEAM; ++i) l += sums[first + i];
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  constexpr int OWN = DIMS / TEAM / 2;  // pairs of dimensions of a warp
+  for (int d = lane; d < OWN; d += 32) {
+    const int at = (mate * OWN + d) * 2;
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int i = 0; i < TEAM; ++i) {
+      const float2 z = *reinterpret_cast<const float2 *>(&part[first + i][at]);
+      x += z.x;
+      y += z.y;
+    }
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + static_cast<size_t>(row) * kLatentDim + d0 + at) =
+        l == 0.f ? 0u : pack2_rn<DT>(x * inv, y * inv);
+  }
+}
+
+template <typename... ARGS>
+cudaError_t launch_after(void (*kernel)(ARGS...), unsigned blocks, cudaStream_t stream, ARGS... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  constexpr int rows = kMergeWarps / TEAM;  // of a block
-  cfg.gridDim = dim3(static_cast<unsigned>((p.num_seqs * p.rows + rows - 1) / rows) * DSPLIT);
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<DT, N, TEAM, DSPLIT>, p, workers);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int DT, int N>
+pa_status join(const LatentParams &p, int workers, int sms, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.num_seqs) * p.rows;
+  cudaError_t e;
+  if (rows <= sms * 2ll) {
+    e = launch_after(latent_merge_few<DT, N, 16, 4>, static_cast<unsigned>(rows * 4), stream, p, workers);
+  } else if (rows <= sms * 16ll) {
+    e = launch_after(latent_merge_few<DT, N, 4, 1>, static_cast<unsigned>((rows + 3) / 4), stream, p, workers);
+  } else {
+    // as many rows a block as leave one wave of blocks, whole warps of them
+    const long long want = rows / (sms * 2ll);
+    const int per = want >= p.rows ? p.rows : static_cast<int>((want + kMergeWarps - 1) / kMergeWarps * kMergeWarps);
+    e = launch_after(latent_merge_many<DT, N>, static_cast<unsigned>(p.num_seqs) * ((p.rows + per - 1) / per), stream, p,
+                     workers, per);
+  }
+  return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
 int columns_for(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kPairRows; }
@@ -704,15 +771,6 @@ bool sizes_of(int S, int n, int H, Sizes *z) {
   z->o = up(slots * N * kLatentDim * sizeof(float));
   z->total = z->prefix + z->ml + z->o;
   return true;
-}
-
-template <int DT, int N>
-pa_status join(const LatentParams &p, int workers, int sms, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(p.num_seqs) * p.rows;
-  const cudaError_t e = rows <= sms * 2ll    ? launch_merge<DT, N, 16, 4>(p, workers, stream)
-                        : rows <= sms * 16ll ? launch_merge<DT, N, 4, 1>(p, workers, stream)
-                                             : launch_merge<DT, N, 1, 1>(p, workers, stream);
-  return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
 template <int DT, int N>

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
   long long first;
   int s = scan.find(u, p.num_seqs, steps_of, first);
 
-  const uint64_t policy = l2_policy_evict_first();
+  const uint64_t policy = l2_policy_evict_first(), keep = l2_policy_evict_last();
   const int bs = 1 << p.bs_shift, bmask = bs - 1;
   const int ktok = 4 * (g >> 1) + (g & 1);  // this lane's K tokens in a step: ktok, ktok + 2; V: 4t .. 4t + 3
   while (u < end) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
             for (int i = 0; i < VWORDS; ++i) vr[e][i] = 0u;
           }
       }
-      if (g < p.G) *reinterpret_cast<float4 *>(logits + tok0) = make_float4(x[0], x[1], x[2], x[3]);
+      if (g < p.G) st_global_f4_hint(logits + tok0, make_float4(x[0], x[1], x[2], x[3]), keep);
       float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
