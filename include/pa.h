@@ -605,8 +605,10 @@ PA_API pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype, int
  *   num_kv_tokens  host upper bound of the sum of seq_lens
  *   workspace      at least pa_latent_prefill_workspace_size(...) bytes,
  *                  256-byte aligned, uninitialised; calls sharing one must be
- *                  stream-ordered.  It holds the expanded keys and values,
- *                  rounded to the cache's type: 512 bytes a head and token.
+ *                  stream-ordered.  It holds the expanded keys, rounded to
+ *                  the cache's type, and values, rounded to fp16 times a power
+ *                  of two for every 32 tokens of a head (1 where fp16 holds
+ *                  them well): 512 bytes a head and token.
  * The expansion costs as much as the attention of about 170 new tokens a
  * sequence in the absorbed form; for fewer new tokens over a long context
  * pa_latent_decode is the cheaper call.  The rows of a sequence's tokens must

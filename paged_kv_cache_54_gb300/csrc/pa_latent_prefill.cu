@@ -8,16 +8,20 @@
 // context, so this form is the cheaper one from about 170 new tokens a
 // sequence on.
 //
-// First kernel (expand): per sequence, tiles of 128 tokens times a head's
-// 256 rows of (Uk_h; Uv_h) on the 5th-generation tensor cores,
-//   D = C U^T   M = 128 tokens, N = 256, K = 512
-// The tile's latent rows (128 KB) stay in shared memory for all of a block's
-// heads, the weights come in chunks of 64 columns; D has two buffers in
-// tensor memory (all 512 columns), so that the products of a head run while
-// the last one's result is rounded and stored.  Blocks take equal shares of
-// all (tile, head) pairs.  The result [head, token, (key 128, value 128)] and
-// the tokens' rotary keys go to the workspace, sequences padded to 128 tokens
-// with zeros.
+// First kernel (expand): tiles of 128 tokens of a sequence times a head's 256
+// rows of (Uk_h; Uv_h) on the 5th-generation tensor cores, two tiles to a pair
+// of blocks whose tensor cores work as one (tcgen05 cta_group::2):
+//   D = C U^T   M = 256 tokens, N = 256, K = 512
+// Each block holds its tile's latent rows (128 KB) for all heads of its share
+// and half of the weights' rows, in chunks of 64 columns: a block alone would
+// read 64 bytes of weights a clock, more than L2 gives it, a pair reads half
+// of that.  D has two buffers in tensor memory (all 512 columns), so that the
+// products of a head run while the last one's result is rounded and stored.
+// Pairs take equal shares of all (two tiles, head) units.  The result [head,
+// token, (key 128, value 128)] and the tokens' rotary keys go to the workspace,
+// sequences padded to 128 tokens with zeros.  Keys are rounded to the cache's
+// type; values always to fp16, whose step is an eighth of bf16's, times a power
+// of two for every 32 tokens of a head where they would leave its range.
 //
 // Second kernel (attend): a block is one head and 256 new tokens of a
 // sequence, as two tiles of 128, the M of the products:
@@ -26,8 +30,10 @@
 // Warps 0..7 softmax (a warpgroup a tile, a thread a row), 8 TMA, 9 and 10
 // issue the products, one a tile.  The running maximum is raised, and O
 // rescaled, only when it grew by more than 2^8.  Sums and maxima are fp32; P
-// is rounded to the operand type, K and V were when they were expanded (half
-// a step each).
+// is rounded to fp16, K and V were when they were expanded (half a step each).
+// With an fp16 cache P's rounding would show beside the output's where a row
+// follows few tokens, so sequences of up to 512 tokens take P as two fp16
+// parts.
 #include <limits.h>
 #include <math.h>
 
@@ -51,20 +57,23 @@ __device__ __forceinline__ float exp2_fast(float x) {
 constexpr int kExTokens = 128;
 constexpr int kExThreads = 6 * 32;
 constexpr int kExTmaWarp = 4, kExMmaWarp = 5;
+constexpr int kExGroup32 = 32;                          // tokens with one power of two
 constexpr int kExColumns = kLatentDim / 64;             // 128-byte columns of the latent part
 constexpr int kExGroup = kExColumns * 1024;             // 8 rows
 constexpr int kExABytes = kExTokens / 8 * kExGroup;
-constexpr int kExBBytes = kUp * 128;                    // a chunk of 64 columns
-constexpr int kExRing = 3;
+constexpr int kExBRows = kUp / 2;                       // of the weights, a block
+constexpr int kExBBytes = kExBRows * 128;               // a chunk of 64 columns
+constexpr int kExRing = 6;
 constexpr int kExSmem = 2048 + kExABytes + kExRing * kExBBytes;
 
 struct ExpandParams {
   CUtensorMap tmap_c;   // the cache's latent columns, a block a box
-  CUtensorMap tmap_u;   // [H * 256, 512], boxes of {64, 256}
+  CUtensorMap tmap_u;   // [H * 256, 512], boxes of {64, 128}
   const uint8_t *cache;
   const int32_t *tables, *lens;
   uint8_t *kv;          // [H, capacity, 256]
   uint8_t *rope;        // [capacity, 64]
+  int32_t *powers;      // [H, capacity / 32]: values are these powers of two times what is stored
   long long *prefix;    // [S + 1] token tiles before sequence s
   int num_seqs, heads, num_blocks, bs_shift, max_blocks, limit;
   long long capacity;   // tokens
@@ -86,41 +95,47 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[16], i
                : "memory");
 }
 
+// The power of two e for which values of largest magnitude `top` are stored
+// as x 2^-e: 0 where fp16 holds them well.
+__device__ __forceinline__ int value_power(float top) {
+  if (!(top > 0.f && top < INFINITY) || (top >= 0x1p-4f && top <= 0x1p15f)) return 0;
+  return min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 127) - 13;
+}
+
 template <int DT>
-__global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __grid_constant__ ExpandParams p) {
-  constexpr uint32_t IDESC = umma_idesc_f16(DT == kF16 ? 0 : 1, kExTokens, kUp, false);
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1)
+    latent_expand_kernel(const __grid_constant__ ExpandParams p) {
+  constexpr uint32_t IDESC = umma_idesc_f16(DT == kF16 ? 0 : 1, 2 * kExTokens, kUp, false);
   extern __shared__ __align__(1024) uint8_t smem[];
   ExpandHeader &hdr = *reinterpret_cast<ExpandHeader *>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = cluster_rank();
   launch_dependents();
-  if ((smem_addr(smem) & 1023u) != 0) {
-    if (threadIdx.x == 0) record_error(p.err, kErrSmemAlign);
-    return;
-  }
-  auto tiles_of = [&](int s) { return (checked_len(p.lens, s, p.limit, p.err) + kExTokens - 1) / kExTokens; };
-  auto units_of = [&](int s) -> long long { return static_cast<long long>(tiles_of(s)) * p.heads; };
+  auto tiles_of = [&](int s) -> long long { return (checked_len(p.lens, s, p.limit, p.err) + kExTokens - 1) / kExTokens; };
   ShareScan<128> &scan = hdr.scan;
-  scan.scan(p.num_seqs, units_of);
+  scan.scan(p.num_seqs, tiles_of);
   if (blockIdx.x == 0 && threadIdx.x < 128) {  // the sequences' first token tiles, for the second kernel
     const int n = scan.run(p.num_seqs), t = threadIdx.x;
-    long long at = scan.base[t] / p.heads;
+    long long at = scan.base[t];
     for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
       p.prefix[s] = at;
       at += tiles_of(s);
     }
-    if (t == 0) p.prefix[p.num_seqs] = scan.total() / p.heads;
+    if (t == 0) p.prefix[p.num_seqs] = scan.total();
   }
-  const long long total = scan.total();
-  const long long u0 = share_begin(blockIdx.x, total, gridDim.x), u1 = share_begin(blockIdx.x + 1, total, gridDim.x);
-  if (u0 >= u1) return;
-  long long first0;
-  const int s0 = scan.find(u0, p.num_seqs, units_of, first0);
+  // units: (two token tiles, head)
+  const long long tiles = scan.total(), total = (tiles + 1) / 2 * p.heads;
+  const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const long long u0 = share_begin(pair, total, pairs), u1 = share_begin(pair + 1, total, pairs);
+  if (u0 >= u1) return;  // (both blocks)
+  long long u = u0, first;
+  int s = scan.find(min(u0 / p.heads * 2 + rank, tiles - 1), p.num_seqs, tiles_of, first);
   volatile int *abort = &hdr.abort;
   uint8_t *as = smem + 2048, *bsm = as + kExABytes;
   if (warp == kExTmaWarp && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_c)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_u)) : "memory");
-    mbar_init(&hdr.a_full, 1);
+    mbar_init(&hdr.a_full, 2);  // a block each
     mbar_init(&hdr.a_empty, 1);
     for (int i = 0; i < kExRing; ++i) {
       mbar_init(&hdr.b_full[i], 1);
@@ -128,45 +143,47 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&hdr.d_full[i], 1);
-      mbar_init(&hdr.d_empty[i], 128);
+      mbar_init(&hdr.d_empty[i], 8);  // the warps of both blocks
     }
     mbar_init(&hdr.fin, 1);
     hdr.abort = 0;
     fence_mbar_init();
   }
-  if (warp == kExMmaWarp) tc_alloc(&hdr.tmem, 512);
+  if (warp == kExMmaWarp) pair_alloc(&hdr.tmem, 512);
   tc_fence_before_sync();
   __syncthreads();
+  cluster_sync();  // the other block's mbarriers and tensor memory are there
   tc_fence_after_sync();
   const uint32_t tmem = hdr.tmem;
 
-  // A share as runs of heads of one token tile.
+  // A share as runs of heads of two token tiles, of which this block's is
+  // `tile` of sequence s (none past the last: there is nothing to load or
+  // store for it, the products of whatever is there go unused).
   struct Run {
-    int s, tile, h0, h1;   // heads [h0, h1) of token tile `tile` of sequence s
-    long long row;         // the tile's first row of the workspace
-    int L;
+    int s, tile, h0, h1, L;
+    long long row;  // the tile's first row of the workspace
+    bool there;
   };
-  long long u = u0, first = first0;
-  int s = s0;
   auto next = [&](Run &r) {
-    while (u < u1) {
-      const int tiles = (checked_len(p.lens, s, p.limit, nullptr) + kExTokens - 1) / kExTokens;
-      const long long all = static_cast<long long>(tiles) * p.heads;
-      if (u >= first + all) {
-        first += all;
-        ++s;
-        continue;
+    if (u >= u1) return false;
+    const long long two = u / p.heads, t = two * 2 + rank;
+    r.h0 = static_cast<int>(u - two * p.heads);
+    r.h1 = u1 - u < p.heads - r.h0 ? r.h0 + static_cast<int>(u1 - u) : p.heads;
+    u += r.h1 - r.h0;
+    r.there = t < tiles;
+    r.row = t * kExTokens;
+    r.s = r.tile = r.L = 0;
+    if (r.there) {
+      for (;; ++s) {
+        r.L = checked_len(p.lens, s, p.limit, nullptr);
+        const long long n = (r.L + kExTokens - 1) / kExTokens;
+        if (t < first + n) break;
+        first += n;
       }
       r.s = s;
-      r.L = checked_len(p.lens, s, p.limit, nullptr);
-      r.tile = static_cast<int>((u - first) / p.heads);
-      r.h0 = static_cast<int>((u - first) - static_cast<long long>(r.tile) * p.heads);
-      r.h1 = u1 - u < p.heads - r.h0 ? r.h0 + static_cast<int>(u1 - u) : p.heads;
-      r.row = (first / p.heads + r.tile) * kExTokens;
-      u += r.h1 - r.h0;
-      return true;
+      r.tile = static_cast<int>(t - first);
     }
-    return false;
+    return true;
   };
   Run r;
   if (warp < 4) {
@@ -174,10 +191,11 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
     bool ok = true;
     int i = 0;
     const int row = threadIdx.x;
+    const uint32_t d_empty[2] = {in_block(&hdr.d_empty[0], 0), in_block(&hdr.d_empty[1], 0)};
     while (ok && next(r)) {
       const int token = r.tile * kExTokens + row;
-      const bool fits = r.row + kExTokens <= p.capacity;
-      if (!fits && threadIdx.x == 0) record_error(p.err, kErrSeqLen);
+      const bool fits = r.there && r.row + kExTokens <= p.capacity;
+      if (r.there && !fits && threadIdx.x == 0) record_error(p.err, kErrSeqLen);
       if (fits && r.h0 == 0) {  // the tile's rotary keys
         uint4 x[8];
 #pragma unroll
@@ -203,20 +221,50 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
         tc_fence_after_sync();
         const uint32_t d = tmem + (i & 1) * kUp + (static_cast<uint32_t>(32 * warp) << 16);
         uint8_t *to = p.kv + ((static_cast<size_t>(h) * p.capacity + r.row + row) * kUp) * 2;
+        const bool real = token < r.L;
 #pragma unroll
-        for (int c = 0; c < kUp; c += 32) {
+        for (int c = 0; c < kNope; c += 32) {
           uint32_t v[32], w[16];
           tc_ld32(d + c, v);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            w[j] = token < r.L ? pack2_rn<DT>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])) : 0u;
+            w[j] = real ? pack2_rn<DT>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])) : 0u;
           if (fits) {
             st_global_32(to + c * 2, w, 0);
             st_global_32(to + c * 2 + 32, w, 8);
           }
         }
+        float top = 0.f;
+        uint32_t v[kValue];
+#pragma unroll
+        for (int c = 0; c < kValue; c += 32) {
+          uint32_t part[32];
+          tc_ld32(d + kNope + c, part);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            v[c + j] = part[j];
+            top = fmaxf(top, fabsf(__uint_as_float(part[j])));
+          }
+        }
         tc_fence_before_sync();
-        mbar_arrive(&hdr.d_empty[i & 1]);
+        __syncwarp();
+        if (lane == 0) pair_arrive(d_empty[i & 1]);
+        // (magnitudes compare as their bits do)
+        const int e = value_power(__uint_as_float(__reduce_max_sync(0xffffffffu, real ? __float_as_uint(top) : 0u)));
+        if (fits && lane == 0)
+          p.powers[static_cast<size_t>(h) * (p.capacity / kExGroup32) + r.row / kExGroup32 + warp] = e;
+        const float f = e == 0 ? 1.f : exp2f(static_cast<float>(-e));
+#pragma unroll
+        for (int c = 0; c < kValue; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = real ? pack2_rn<kF16>(__uint_as_float(v[c + 2 * j]) * f, __uint_as_float(v[c + 2 * j + 1]) * f) : 0u;
+          if (fits) {
+            st_global_32(to + (kNope + c) * 2, w, 0);
+            st_global_32(to + (kNope + c) * 2 + 32, w, 8);
+          }
+        }
       }
     }
     if (!ok) {
@@ -225,11 +273,13 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
     }
   } else if (warp == kExTmaWarp) {
     // ------------------------------------------------------------------ TMA
+    // (bytes count in the first block, where the products are issued)
     bool ok = true;
     int chunk = 0, runs = 0;
+    const uint32_t a_full = in_block(&hdr.a_full, 0);
     while (ok && next(r)) {
       const int boxes = kExTokens >> p.bs_shift;
-      const int n_box = min(boxes, (r.L - r.tile * kExTokens + (1 << p.bs_shift) - 1) >> p.bs_shift);
+      const int n_box = r.there ? min(boxes, (r.L - r.tile * kExTokens + (1 << p.bs_shift) - 1) >> p.bs_shift) : 0;
       const uint32_t box = (1u << p.bs_shift) / 8 * kExGroup;
       int b = 0;
       if (lane < n_box) {
@@ -239,16 +289,14 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
           b = 0;
         }
       }
-      bool got = true;
-      if (lane == 0 && runs > 0) got = mbar_wait(&hdr.a_empty, (runs - 1) & 1, abort);
-      if (!__shfl_sync(0xffffffffu, got, 0)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&hdr.a_full, n_box * box);
+      if (runs > 0) ok = __all_sync(0xffffffffu, mbar_wait(&hdr.a_empty, (runs - 1) & 1, abort));
+      if (!ok) break;
+      // each block announces its own tile's bytes
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(a_full), "r"(n_box * box)
+                     : "memory");
       __syncwarp();
-      if (lane < n_box)
-        tma_load_4d(as + lane * box, &p.tmap_c, 0, 0, 0, b << (p.bs_shift - 3), &hdr.a_full);
+      if (lane < n_box) pair_load_4d(as + lane * box, &p.tmap_c, 0, 0, 0, b << (p.bs_shift - 3), a_full);
       ++runs;
       if (lane == 0) {
         for (int h = r.h0; ok && h < r.h1; ++h)
@@ -258,8 +306,8 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(&hdr.b_full[st], kExBBytes);
-            tma_load_2d(bsm + st * kExBBytes, &p.tmap_u, c * 64, h * kUp, &hdr.b_full[st]);
+            if (rank == 0) mbar_arrive_expect_tx(&hdr.b_full[st], 2 * kExBBytes);
+            pair_load_2d(bsm + st * kExBBytes, &p.tmap_u, c * 64, h * kUp + rank * kExBRows, in_block(&hdr.b_full[st], 0));
           }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -267,11 +315,13 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
     if (lane == 0 && !ok) {
       record_error(p.err, kErrTimeout);
       *abort = 1;
-      if (runs > 0) mbar_wait(&hdr.a_full, (runs - 1) & 1, nullptr);  // copies in flight land first
-      for (int j = max(0, chunk - kExRing); j < chunk; ++j)
-        mbar_wait(&hdr.b_full[j % kExRing], (j / kExRing) & 1, nullptr);
+      if (rank == 0) {  // copies in flight land first, within the limit
+        if (runs > 0) mbar_wait(&hdr.a_full, (runs - 1) & 1, nullptr);
+        for (int j = max(0, chunk - kExRing); j < chunk; ++j)
+          mbar_wait(&hdr.b_full[j % kExRing], (j / kExRing) & 1, nullptr);
+      }
     }
-  } else if (elect_one()) {
+  } else if (rank == 0 && elect_one()) {
     // ------------------------------------------------------------------ MMA
     bool ok = true;
     int i = 0, chunk = 0;
@@ -294,26 +344,28 @@ __global__ void __launch_bounds__(kExThreads, 1) latent_expand_kernel(const __gr
           const uint64_t b0 = umma_desc_sw128(smem_addr(bsm) + st * kExBBytes, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16(d, a0 + (kk * 32 >> 4), b0 + (kk * 32 >> 4), IDESC, (c > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(&hdr.b_empty[st]);
+            pair_mma(d, a0 + (kk * 32 >> 4), b0 + (kk * 32 >> 4), IDESC, (c > 0 || kk > 0) ? 1u : 0u);
+          pair_commit(&hdr.b_empty[st]);
         }
-        if (ok) tc_commit(&hdr.d_full[i & 1]);
+        if (ok) pair_commit(&hdr.d_full[i & 1]);
       }
-      if (ok) tc_commit(&hdr.a_empty);
+      if (ok) pair_commit(&hdr.a_empty);
     }
     if (!ok) {
       record_error(p.err, kErrTimeout);
       *abort = 1;
     }
-    tc_commit(&hdr.fin);
+    pair_commit(&hdr.fin);
     mbar_wait(&hdr.fin, 0, nullptr);
   }
   tc_fence_before_sync();
   __syncthreads();
+  cluster_sync();  // both blocks are done with the other's shared memory and tensor memory
   if (warp == kExMmaWarp) {
     tc_fence_after_sync();
-    tc_dealloc(tmem, 512);
+    pair_dealloc(tmem, 512);
   }
+  cluster_sync();
 }
 
 // ------------------------------------------------------------------ attend
@@ -332,6 +384,7 @@ constexpr int kAttnThreads = 11 * 32;
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr uint32_t kTileCols = 256;             // TMEM columns of a tile: S 2 x 64, O 128
 constexpr float kLazy = 8.f;
+constexpr int kFineTokens = 512;
 
 struct AttendParams {
   CUtensorMap tmap_q;     // [T, H, 192], boxes {64, 1, 128}
@@ -340,6 +393,7 @@ struct AttendParams {
   void *out;
   const int32_t *cu_q, *lens;
   const long long *prefix;
+  const int32_t *powers;
   int heads, num_q_tokens, max_q_len, limit;
   long long capacity;
   float scale_log2;
@@ -388,7 +442,7 @@ template <int DT>
 __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __grid_constant__ AttendParams p) {
   constexpr int AB = DT == kF16 ? 0 : 1;
   constexpr uint32_t IDESC_QK = umma_idesc_f16(AB, kRows, kKeys, false);
-  constexpr uint32_t IDESC_PV = umma_idesc_f16(AB, kRows, kValue, true);
+  constexpr uint32_t IDESC_PV = umma_idesc_f16(0, kRows, kValue, true);  // P and V are fp16
   extern __shared__ __align__(1024) uint8_t smem[];
   AttendHeader &hdr = *reinterpret_cast<AttendHeader *>(smem);
   const int cta = gridDim.x - 1 - blockIdx.x;  // the longest (last) ranges first
@@ -414,6 +468,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
   const int pos0 = L - n;
   const int kv_end = pos0 + min(n, tok0 + kTiles * kRows);
   const int n_stages = (kv_end + kKeys - 1) / kKeys;
+  const bool fine = DT == kF16 && L <= kFineTokens;  // P in two parts
   auto tile_stages = [&](int t) { return (pos0 + min(n, tok0 + (t + 1) * kRows) + kKeys - 1) / kKeys; };
   uint8_t *qs = smem + kQOff, *stages = smem + kStageOff;
   volatile int *abort = &hdr.abort;
@@ -462,6 +517,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       const int nst = tile_stages(t);
+      // powers of two of the values, 32 keys each; O is in units of 2^unit,
+      // the largest power of those the row has followed
+      const int2 *powers =
+          reinterpret_cast<const int2 *>(p.powers + (static_cast<size_t>(h) * p.capacity + row0) / kExGroup32);
+      int2 power = __ldg(powers);
+      int unit = pos >= 32 ? max(power.x, power.y) : power.x;
       for (int i = 0; i < nst; ++i) {
         if (!__all_sync(0xffffffffu, mbar_wait(&hdr.s_full[t][i & 1], (i >> 1) & 1, abort))) {
           ok = false;
@@ -469,6 +530,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
         }
         tc_fence_after_sync();
         const int k0 = i * kKeys;
+        const int2 here = power;
+        if (i + 1 < nst) power = __ldg(powers + i + 1);
         float sv[kKeys];
         {
           uint32_t raw[32];
@@ -506,7 +569,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
           cm = 1.f;
         }
         const bool grow = mx > m + kLazy;
-        if (__any_sync(0xffffffffu, grow && i > 0)) {
+        const int up = max(max(k0 <= pos ? here.x : unit, k0 + 32 <= pos ? here.y : unit) - unit, 0);
+        if (__any_sync(0xffffffffu, (grow && i > 0) || up > 0)) {
           // (pv_done is at most one phase behind: S of this stage was issued
           // after the P V before the previous one, and products complete in order)
           if (!__all_sync(0xffffffffu, mbar_wait(&hdr.pv_done[t], (i - 1) & 1, abort))) {
@@ -514,7 +578,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
             break;
           }
           tc_fence_after_sync();
-          const float alpha = grow ? exp2_fast(m - mx) : 1.f;
+          const float alpha = (grow ? exp2_fast(m - mx) : 1.f) * exp2_fast(static_cast<float>(-up));
+          unit += up;
 #pragma unroll
           for (int d = 0; d < kValue; d += 32) {
             uint32_t ov[32];
@@ -537,7 +602,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
           float x, y;
           f2_split(ffma2(f2(sv[j], sv[j + 1]), cm2, nb2), x, y);
           const float a = exp2_fast(x), b = exp2_fast(y);
-          pw[j / 2] = pack2_rn<DT>(a, b);
+          sv[j] = a;
+          sv[j + 1] = b;
+          pw[j / 2] = pack2_rn<kF16>(a, b);
           if ((j & 2) == 0)
             sum0 = fadd2(sum0, f2(a, b));
           else
@@ -549,7 +616,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
           f2_split(sum1, l2, l3);
           l += (l0 + l1) + (l2 + l3);
         }
+        if ((here.x ^ unit) | (here.y ^ unit)) {  // (rare: values in other powers of two)
+          const float f0 = exp2_fast(static_cast<float>(min(here.x - unit, 0)));  // (above: masked keys)
+          const float f1 = exp2_fast(static_cast<float>(min(here.y - unit, 0)));
+#pragma unroll
+          for (int j = 0; j < kKeys; j += 2) {
+            sv[j] *= j < 32 ? f0 : f1;
+            sv[j + 1] *= j < 32 ? f0 : f1;
+            pw[j / 2] = pack2_rn<kF16>(sv[j], sv[j + 1]);
+          }
+        }
         tc_st32(trow + (i & 1) * kKeys, pw);  // P over the S buffer just read
+        if (fine) {  // and what its rounding left
+#pragma unroll
+          for (int j = 0; j < kKeys; j += 2) {
+            const float2 a = half2_bits_to_float2<kF16>(pw[j / 2]);
+            pw[j / 2] = pack2_rn<kF16>(sv[j] - a.x, sv[j + 1] - a.y);
+          }
+          tc_st32(trow + (i & 1) * kKeys + kKeys / 2, pw);
+        }
         tc_fence_before_sync();
         mbar_arrive(&hdr.p_full[t][i & 1]);
       }
@@ -557,7 +642,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
         tc_fence_after_sync();
         // O / l through this tile's q buffer, whose products have all
         // completed, so that whole rows leave
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : exp2f(static_cast<float>(unit)) / l;
         constexpr int RB = kValue * 2, CPR = RB / 16;
         uint8_t *stg = qs + t * kQTile;
 #pragma unroll
@@ -661,6 +746,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
         for (int kk = 0; kk < kKeys / 16; ++kk)
           tc_mma_f16_ta(tt + 2 * kKeys, tt + (i & 1) * kKeys + kk * 8, b0 + kk * (2 * 1024 >> 4), IDESC_PV,
                         (i > 0 || kk > 0) ? 1u : 0u);
+        if (fine)
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            tc_mma_f16_ta(tt + 2 * kKeys, tt + (i & 1) * kKeys + kKeys / 2 + kk * 8, b0 + kk * (2 * 1024 >> 4), IDESC_PV, 1u);
         tc_commit(&hdr.pv_done[t]);
         if (i + 1 == nst) tc_commit(&hdr.o_ready[t]);
         tc_commit(&hdr.kv_empty[i % kStages]);
@@ -691,7 +780,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
 
 // ------------------------------------------------------------------ host
 struct Sizes {
-  size_t prefix, rope, kv, total;
+  size_t prefix, powers, rope, kv, total;
   long long capacity;
 };
 bool sizes_of(int S, int H, long long tokens, Sizes *z) {
@@ -702,9 +791,10 @@ bool sizes_of(int S, int H, long long tokens, Sizes *z) {
   if (z->capacity * H > INT_MAX) return false;  // 32-bit rows
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   z->prefix = up(8 * (static_cast<size_t>(S) + 1));
+  z->powers = up(static_cast<size_t>(z->capacity / kExGroup32) * H * sizeof(int32_t));
   z->rope = up(static_cast<size_t>(z->capacity) * kRopeDim * 2);
   z->kv = up(static_cast<size_t>(z->capacity) * H * kUp * 2);
-  z->total = z->prefix + z->rope + z->kv;
+  z->total = z->prefix + z->powers + z->rope + z->kv;
   return true;
 }
 
@@ -733,7 +823,7 @@ pa_status launch(const ExpandParams &ep, const AttendParams &ap, int num_seqs, i
   }
   DeviceInfo info;
   if (!current_device_info(&info)) return cuda_fail(cudaGetLastError());
-  latent_expand_kernel<DT><<<info.sm_count, kExThreads, kExSmem, stream>>>(ep);
+  latent_expand_kernel<DT><<<info.sm_count / 2 * 2, kExThreads, kExSmem, stream>>>(ep);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchAttribute attr[1];
@@ -789,8 +879,9 @@ extern "C" pa_status pa_latent_prefill(void *out, const void *q, int32_t q_dtype
   ep.tables = block_tables;
   ep.lens = seq_lens;
   ep.prefix = reinterpret_cast<long long *>(ws);
-  ep.rope = ws + z.prefix;
-  ep.kv = ws + z.prefix + z.rope;
+  ep.powers = reinterpret_cast<int32_t *>(ws + z.prefix);
+  ep.rope = ws + z.prefix + z.powers;
+  ep.kv = ws + z.prefix + z.powers + z.rope;
   ep.num_seqs = num_seqs;
   ep.heads = num_heads;
   ep.num_blocks = desc->num_blocks;
@@ -804,6 +895,7 @@ extern "C" pa_status pa_latent_prefill(void *out, const void *q, int32_t q_dtype
   ap.cu_q = cu_q_lens;
   ap.lens = seq_lens;
   ap.prefix = ep.prefix;
+  ap.powers = ep.powers;
   ap.heads = num_heads;
   ap.num_q_tokens = num_q_tokens;
   ap.max_q_len = max_q_len;
@@ -813,7 +905,7 @@ extern "C" pa_status pa_latent_prefill(void *out, const void *q, int32_t q_dtype
   ap.err = device_error;
   const cuuint64_t H = num_heads, cap = z.capacity;
   const cuuint64_t du[2] = {kLatentDim, H * kUp}, su[1] = {kLatentDim * 2};
-  const cuuint32_t bu[2] = {64, kUp};
+  const cuuint32_t bu[2] = {64, kExBRows};
   const cuuint64_t dq[3] = {kQk, H, static_cast<cuuint64_t>(num_q_tokens)}, sq[2] = {kQk * 2, H * kQk * 2};
   const cuuint32_t bq[3] = {64, 1, kRows};
   const cuuint64_t dk[2] = {kUp, H * cap}, sk[1] = {kUp * 2};

@@ -306,6 +306,31 @@ def test_prefill_scales(factor):
     check(got, want, tol)
 
 
+def test_prefill_values_of_all_magnitudes():
+    """Groups of 32 tokens whose values lie many powers of two apart, up and down, beside fp16's range."""
+    L = [400, 90]
+    cache, table, lens, q, up, cu = make_prefill(L, [300, 90], 2, 16, "bf16", 55)
+    up[:, :128] = 0                                          # (scores from the rotary part alone)
+    power = [0, 40, -30, 17, 16, -20, 60, 0, 61, 3, -60, 30, 0]
+    for s, n in enumerate(L):
+        for b in range(-(-n // 16)):
+            cache[int(table[s, b]), :, :LATENT] *= 2.0 ** power[(b // 2 + s) % len(power)]
+    cache[torch.isnan(cache)] = 0                            # (rows behind the ends; the factor of 0 * NaN)
+    got = run_prefill(cache, table, lens, q, up, cu, SCALE, 300, 490)
+    want, tol = expect_prefill(cache, table, lens, q, up, cu, 16, SCALE, eps(torch.bfloat16))
+    # beside that: a value is a step of 2^-25 of its group's largest off (times 2^-13 of its scaling), a weight 2^-25 in
+    # the units of the largest group a row follows, over all keys
+    big = torch.zeros_like(want)
+    for s, n in enumerate(L):
+        x = rows_of(cache, table[s], n, 16)
+        for h in range(2):
+            v = (x[:, :LATENT] @ up[h, 128:].double().T).abs().amax(-1)
+            seen = torch.cummax(torch.cat([v[i:i + 32].max().expand(len(v[i:i + 32])) for i in range(0, n, 32)]), 0).values
+            m = int(cu[s + 1] - cu[s])
+            big[cu[s]:cu[s + 1], h] = seen[n - m:, None] * (torch.arange(n - m, n, device=DEV)[:, None] + 64)
+    check(got, want, tol + 2.0 ** -24 * big)
+
+
 def test_prefill_bounds_above_and_rows_left_alone():
     """Bounds larger than the lengths, rows of q behind the last sequence, a wider table."""
     cache, table, L, q, up, cu = make_prefill([200, 30], [140, 30], 2, 16, "bf16", 53)
