@@ -507,7 +507,7 @@ PA_API pa_status pa_decode_weights(void *out, float *weights_out, const float *w
  *                  aligned, uninitialised; calls sharing one must be
  *                  stream-ordered.
  * Requires 0 <= recent <= budget, budget >= 1.  Supported set: 16-bit, FP8 and
- * INT8 caches (not PA_FP4); num_blocks * block_size < 2^31.
+ * INT8 caches (not PA_FP4); num_blocks * block_size * kv_heads < 2^31.
  * Device checks: a length outside [0, min(weights_width, max_blocks_per_seq *
  * block_size)] moves nothing of the sequence, sets its new length to 0 and is
  * reported as error 3; a block id out of range leaves its tokens' rows

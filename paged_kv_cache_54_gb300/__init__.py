@@ -563,22 +563,26 @@ def pa_swap_blocks(k_cache, v_cache, host_k, host_v, block_mapping, direction: s
 
 
 def _check_tables(block_tables, seq_lens, seqs: int) -> None:
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+    if block_tables.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
         raise ValueError("block_tables and seq_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != seqs or seq_lens.shape != (seqs,):
+    if block_tables.dim() != 2 or block_tables.size(0) != seqs or seq_lens.dim() != 1 or seq_lens.size(0) != seqs:
         raise ValueError(f"block_tables must be [{seqs}, width] and seq_lens [{seqs}]")
 
 
 def _check_here(names: str, *tensors) -> None:
     """Contiguous CUDA tensors, all on the current device."""
-    _require_here(_require_all(names, *tensors))
+    if not tensors[0].is_cuda:  # (no question to a driver that may not be there)
+        _require(tensors[0], names.split()[0])
+    device = _current_device()
+    for t in tensors:
+        if t.get_device() != device or not t.is_contiguous():
+            _require_here(_require_all(names, *tensors))
 
 
 def _check_error_word(device_error) -> None:
-    if device_error is not None:
-        _check_here("device_error", device_error)
-        if device_error.dtype != torch.int32 or device_error.numel() < 1:
-            raise ValueError("device_error must be int32")
+    if device_error is not None and (device_error.dtype is not torch.int32
+                                     or device_error.get_device() != _current_device()):
+        raise ValueError("device_error must be int32 on the current CUDA device")
 
 
 def _workspace_of(need: int) -> torch.Tensor:
@@ -601,31 +605,35 @@ def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_l
     _check_here("out weights_out q k_cache v_cache block_tables seq_lens", out, weights_out, q, k_cache, v_cache,
                 block_tables, seq_lens)
     _check_error_word(device_error)
-    if q.dim() != 3:
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
         raise ValueError("q/out must be [S, Hq, head_dim]")
-    S, Hq, D = q.shape
+    S, Hq, D = shape
     _check_tables(block_tables, seq_lens, S)
     H, d, code, ref = _describe(k_cache, cache_dtype, k_scale, v_scale)
-    qcode = _TORCH_CODES.get(q.dtype)
-    if qcode not in (PA_F16, PA_BF16) or out.dtype != q.dtype or out.shape != q.shape or D != d:
+    qcode = _TORCH_CODES.get(dtype)
+    if qcode not in (PA_F16, PA_BF16) or out.dtype is not dtype or out.shape != shape or D != d:
         raise ValueError(f"q/out must be float16 or bfloat16 [S, Hq, {d}] of one dtype")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    if v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype:
         raise ValueError("k_cache and v_cache must have one shape and dtype")
-    if weights_out.dtype != torch.float32 or weights_out.dim() != 3 or weights_out.shape[:2] != (S, H):
+    if weights_out.dtype is not torch.float32 or weights_out.dim() != 3 or weights_out.shape[:2] != (S, H):
         raise ValueError(f"weights_out must be float32 [{S}, {H}, width]")
+    win = None
     if weights_in is not None:
-        _check_here("weights_in", weights_in)
-        if weights_in.dtype != torch.float32 or weights_in.shape != weights_out.shape:
-            raise ValueError("weights_in must be like weights_out")
+        if weights_in is not weights_out:
+            _check_here("weights_in", weights_in)
+            if weights_in.dtype is not torch.float32 or weights_in.shape != weights_out.shape:
+                raise ValueError("weights_in must be like weights_out")
+        win = weights_in.data_ptr()
     if workspace is None:
         workspace = _workspace_of(pa_decode_weights_workspace_size(S, Hq, H, D, max_seq_len))
     else:
         _check_here("workspace", workspace)
     _check(load_library().pa_decode_weights(
-        out.data_ptr(), weights_out.data_ptr(), _ptr(weights_in), decay, weights_out.shape[2], q.data_ptr(), qcode, S,
-        Hq, k_cache.data_ptr(), v_cache.data_ptr(), ref, block_tables.data_ptr(), block_tables.shape[1],
-        seq_lens.data_ptr(), max_seq_len, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _ptr(device_error), _stream(stream)), "pa_decode_weights")
+        out.data_ptr(), weights_out.data_ptr(), win, decay, weights_out.size(2), q.data_ptr(), qcode, S, Hq,
+        k_cache.data_ptr(), v_cache.data_ptr(), ref, block_tables.data_ptr(), max(1, block_tables.size(1)),
+        seq_lens.data_ptr(), max_seq_len, scale, workspace.data_ptr(), workspace.nbytes, _ptr(device_error),
+        _stream(stream)), "pa_decode_weights")
     return out
 
 
@@ -645,26 +653,26 @@ def pa_evict_tokens(k_cache, v_cache, block_tables, seq_lens, weights, new_table
                 block_tables, seq_lens, weights, new_tables, new_lens, new_weights)
     _check_error_word(device_error)
     H, _, _, ref = _describe(k_cache, cache_dtype, 1.0, 1.0)
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    if v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype:
         raise ValueError("k_cache and v_cache must have one shape and dtype")
     S = seq_lens.numel()
     _check_tables(block_tables, seq_lens, S)
-    if new_tables.dtype != torch.int32 or new_tables.dim() != 2 or new_tables.shape[0] != S:
+    if new_tables.dtype is not torch.int32 or new_tables.dim() != 2 or new_tables.size(0) != S:
         raise ValueError(f"new_tables must be int32 [{S}, width]")
-    if new_lens.dtype != torch.int32 or new_lens.shape != (S,):
+    if new_lens.dtype is not torch.int32 or new_lens.dim() != 1 or new_lens.size(0) != S:
         raise ValueError(f"new_lens must be int32 [{S}]")
     for t, n in ((weights, "weights"), (new_weights, "new_weights")):
-        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[:2] != (S, H):
+        if t.dtype is not torch.float32 or t.dim() != 3 or t.shape[:2] != (S, H):
             raise ValueError(f"{n} must be float32 [{S}, {H}, width]")
     if workspace is None:
         workspace = _workspace_of(pa_evict_workspace_size(S, H, budget))
     else:
         _check_here("workspace", workspace)
     _check(load_library().pa_evict_tokens(
-        k_cache.data_ptr(), v_cache.data_ptr(), ref, block_tables.data_ptr(), S, max(1, block_tables.shape[1]),
-        seq_lens.data_ptr(), weights.data_ptr(), weights.shape[2], new_tables.data_ptr(), max(1, new_tables.shape[1]),
-        new_lens.data_ptr(), new_weights.data_ptr(), new_weights.shape[2], budget, recent, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _ptr(device_error), _stream(stream)), "pa_evict_tokens")
+        k_cache.data_ptr(), v_cache.data_ptr(), ref, block_tables.data_ptr(), S, max(1, block_tables.size(1)),
+        seq_lens.data_ptr(), weights.data_ptr(), weights.size(2), new_tables.data_ptr(), max(1, new_tables.size(1)),
+        new_lens.data_ptr(), new_weights.data_ptr(), new_weights.size(2), budget, recent, workspace.data_ptr(),
+        workspace.nbytes, _ptr(device_error), _stream(stream)), "pa_evict_tokens")
 
 
 def latent_cache_shape(num_blocks: int, block_size: int):
@@ -732,8 +740,7 @@ def pa_latent_decode(out, q, cache, block_tables, seq_lens, max_seq_len: int, sc
     _check(load_library().pa_latent_decode(out.data_ptr(), q.data_ptr(), code, S, n, H, cache.data_ptr(), ref,
                                            block_tables.data_ptr(), max(1, block_tables.shape[1]),
                                            seq_lens.data_ptr(), max_seq_len, scale, workspace.data_ptr(),
-                                           workspace.numel() * workspace.element_size(), _ptr(device_error),
-                                           _stream(stream)), "pa_latent_decode")
+                                           workspace.nbytes, _ptr(device_error), _stream(stream)), "pa_latent_decode")
     return out
 
 
@@ -768,8 +775,7 @@ def pa_latent_prefill(out, q, cu_q_lens, up, cache, block_tables, seq_lens, max_
     _check(load_library().pa_latent_prefill(out.data_ptr(), q.data_ptr(), code, T, cu_q_lens.data_ptr(), S, H, max_q_len,
                                             up.data_ptr(), cache.data_ptr(), ref, block_tables.data_ptr(),
                                             max(1, block_tables.shape[1]), seq_lens.data_ptr(), num_kv_tokens, scale,
-                                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                            _ptr(device_error), _stream(stream)), "pa_latent_prefill")
+                                            workspace.data_ptr(), workspace.nbytes, _ptr(device_error), _stream(stream)), "pa_latent_prefill")
     return out
 
 

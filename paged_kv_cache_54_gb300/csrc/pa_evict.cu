@@ -4,10 +4,16 @@
 // Select: one block a (sequence, KV head) pair.  The weights become unsigned
 // keys that ascend with them; a radix selection in three digits (11, 11 and
 // 10 bits) finds the k-th largest key T and how many of the keys equal to it
-// are kept.  Counts of two passes then place every kept token, in order:
-// keys above T, the first of those equal to it, and the recent ones.
+// are kept.  The weights are read three times: for the first digit's
+// histogram; to gather the keys of T's bin, on which the other digits are
+// found; and to place the kept tokens in order (keys above T, the first of
+// those equal to it, and the recent ones).  Where the bin holds more than fits
+// (many equal weights), the other digits read all weights too.  Bound by
+// issued instructions: 256 pairs of 4096..16384 tokens took 32 us with two
+// more passes over the weights.
 // Move: rows copied from their old slots to their new ones, every warp with
-// several rows of K and of V in flight.
+// several rows of K and of V in flight.  (Looking the tokens' blocks up here
+// costs 15 us of 180: a load more ahead of the rows.)
 #include <limits.h>
 
 #include "pa_common.cuh"
@@ -19,6 +25,7 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kGathered = 4096;  // keys of a bin that fit
 constexpr int kMoveThreads = 256;
 
 struct EvictParams {
@@ -28,7 +35,7 @@ struct EvictParams {
   int32_t *new_lens;
   const float *weights;
   float *new_weights;
-  int32_t *list;  // [pairs, budget] source slots
+  int32_t *list;  // [pairs, budget] the kept tokens' slots, -1 for a bad block
   int num_seqs, kv_heads, num_blocks, bs_shift, max_blocks, max_new_blocks, budget, recent, limit;
   long long width, new_width;
   int *err;
@@ -54,24 +61,26 @@ __device__ __forceinline__ int block_exclusive(int x, int *tmp) {
   if (lane == 31) tmp[warp] = y;
   __syncthreads();
   if (warp == 0) {
-    int v = tmp[lane];
+    int v = lane < kSelWarps ? tmp[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int z = __shfl_up_sync(0xffffffffu, v, d);
       if (lane >= d) v += z;
     }
-    tmp[lane] = v;
+    if (lane < kSelWarps) tmp[lane] = v;
   }
   __syncthreads();
   return y - x + (warp > 0 ? tmp[warp - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictParams p) {
   __shared__ int hist[kBins];
   __shared__ int tmp[kSelWarps];
   __shared__ int above[kSelWarps], equal[kSelWarps];
+  __shared__ uint32_t bin_key[kGathered];
+  __shared__ uint8_t bin_warp[kGathered];
   __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ int s_need, s_gathered;
   launch_dependents();
   const long long pair = blockIdx.x;
   const int s = static_cast<int>(pair / p.kv_heads), h = static_cast<int>(pair % p.kv_heads);
@@ -87,81 +96,180 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
   const int B = min(L, p.budget), r = min(p.recent, B), n = L - r, k = B - r;
   if (tid == 0 && h == 0) p.new_lens[s] = B;
   const float *w = p.weights + pair * p.width;
-  uint32_t prefix = 0;
-  int need = k;  // of the keys that share the prefix, how many are kept
-  if (k > 0 && k < n) {
-    for (int level = 0; level < 3; ++level) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-      const uint32_t mask = level == 0 ? 0u : level == 1 ? 0xffe00000u : 0xfffffc00u;
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t key = weight_key(__ldg(w + i));
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1);
-      }
-      __syncthreads();
-      // bins from the top: thread t has bins kBins - 1 - 2t and the one below
-      const int b0 = kBins - 1 - 2 * tid;
-      const int c0 = hist[b0], c1 = hist[b0 - 1];
-      const int before = block_exclusive(c0 + c1, tmp);
-      if (before < need && need <= before + c0 + c1) {
-        const bool low = need > before + c0;
-        s_prefix = prefix | (static_cast<uint32_t>(low ? b0 - 1 : b0) << shift);
-        s_need = need - before - (low ? c0 : 0);
-      }
-      __syncthreads();
-      prefix = s_prefix;
-      need = s_need;
-    }
-  }
-  const bool all = k >= n;  // every candidate is kept
-  // each warp places a run of tokens
+  // a warp has a run of tokens, a lane every 32nd of it; f(first token, keys)
+  // for four steps of the warp at a time, in order
   const int run = (L + kSelThreads - 1) / kSelThreads * 32;
   const int i0 = min(warp * run, L), i1 = min(i0 + run, L);
-  int gt = 0, eq = 0;
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const uint32_t key = i < n ? weight_key(__ldg(w + i)) : 0u;
-    const bool sure = i >= n || all || (k > 0 && key > prefix);
-    gt += sure;
-    eq += !sure && k > 0 && key == prefix;
+  constexpr int kBatch = 4;
+  auto each = [&](auto f) {
+    for (int base = i0; base < i1; base += 32 * kBatch) {
+      uint32_t x[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = base + 32 * j + lane;
+        x[j] = i < i1 ? __float_as_uint(__ldg(w + i)) : 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) x[j] = weight_key(__uint_as_float(x[j]));
+      f(base, x);
+    }
+  };
+  // the digit, from the top, in which the need-th key lies (all threads; a
+  // thread has four bins, the highest first)
+  uint32_t prefix = 0;
+  int need = k;  // of the keys that share the prefix, how many are kept
+  auto pick = [&](int shift) {
+    constexpr int kOwn = kBins / kSelThreads;
+    const int b0 = kBins - 1 - kOwn * tid;
+    int c[kOwn], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) sum += c[j] = hist[b0 - j];
+    int before = block_exclusive(sum, tmp);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      if (before < need && need <= before + c[j]) {
+        s_prefix = prefix | (static_cast<uint32_t>(b0 - j) << shift);
+        s_need = need - before;
+      }
+      before += c[j];
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    need = s_need;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+  };
+  int gt = 0, eq = 0;  // of the warp's candidates: surely kept, and equal to T
+  const int end = min(i1, n);
+  if (k > 0 && k < n) {
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    if (tid == 0) s_gathered = 0;
+    if (lane == 0) above[warp] = equal[warp] = 0;
+    __syncthreads();
+    each([&](int base, const uint32_t (&x)[kBatch]) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (base + 32 * j + lane < end) atomicAdd(&hist[x[j] >> 21], 1);
+    });
+    __syncthreads();
+    pick(21);
+    // the bin's keys, and how many lie above it
+    each([&](int base, const uint32_t (&x)[kBatch]) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const bool in = base + 32 * j + lane < end;
+        const uint32_t digit = x[j] >> 21;
+        gt += in && digit > (prefix >> 21);
+        const bool here = in && digit == (prefix >> 21);
+        const unsigned mask = __ballot_sync(0xffffffffu, here);
+        if (mask != 0) {
+          int at = 0;
+          if (lane == 0) at = atomicAdd(&s_gathered, __popc(mask));
+          at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1u));
+          if (here && at < kGathered) {
+            bin_key[at] = x[j];
+            bin_warp[at] = static_cast<uint8_t>(warp);
+          }
+        }
+      }
+    });
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    __syncthreads();
+    const int gathered = s_gathered;
+    for (int level = 1; level < 3; ++level) {
+      const int shift = level == 1 ? 10 : 0;
+      const uint32_t mask = level == 1 ? 0xffe00000u : 0xfffffc00u, digit = level == 1 ? 0x7ffu : 0x3ffu;
+      if (gathered <= kGathered) {
+        for (int i = tid; i < gathered; i += kSelThreads)
+          if ((bin_key[i] & mask) == prefix) atomicAdd(&hist[(bin_key[i] >> shift) & digit], 1);
+      } else {
+        each([&](int base, const uint32_t (&x)[kBatch]) {
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (base + 32 * j + lane < end && (x[j] & mask) == prefix) atomicAdd(&hist[(x[j] >> shift) & digit], 1);
+        });
+      }
+      __syncthreads();
+      pick(shift);
+    }
+    if (gathered <= kGathered) {
+      for (int i = tid; i < gathered; i += kSelThreads) {
+        if (bin_key[i] > prefix) atomicAdd(&above[bin_warp[i]], 1);
+        if (bin_key[i] == prefix) atomicAdd(&equal[bin_warp[i]], 1);
+      }
+    } else {
+      int g = 0;
+      each([&](int base, const uint32_t (&x)[kBatch]) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const bool in = base + 32 * j + lane < end;
+          g += in && x[j] > prefix && (x[j] >> 21) == (prefix >> 21);
+          eq += in && x[j] == prefix;
+        }
+      });
+      g = __reduce_add_sync(0xffffffffu, g);
+      eq = __reduce_add_sync(0xffffffffu, eq);
+      if (lane == 0) {
+        above[warp] = g;
+        equal[warp] = eq;
+      }
+    }
+    __syncthreads();
+    gt += above[warp];
+    eq = equal[warp];
+  } else {
+    // every candidate is kept, or none: no key is T
+    prefix = 0xffffffffu;
+    need = 0;
+    gt = k > 0 ? max(end - i0, 0) : 0;
+    eq = 0;
   }
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
+  __syncthreads();
   if (lane == 0) {
-    above[warp] = gt;
+    above[warp] = gt + max(i1 - max(i0, n), 0);  // and the recent ones
     equal[warp] = eq;
   }
   __syncthreads();
-  int gt0 = 0, eq0 = 0;
-  for (int i = 0; i < warp; ++i) {
-    gt0 += above[i];
-    eq0 += equal[i];
-  }
+  const int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? above[lane & (kSelWarps - 1)] : 0);
+  int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? equal[lane & (kSelWarps - 1)] : 0);
   int at = gt0 + min(eq0, need);
+  const int from = k >= n ? 0 : n;  // tokens from here on are kept whatever their weight
+  int32_t *list = p.list + pair * p.budget;
+  float *new_weights = p.new_weights + pair * p.new_width;
   const int32_t *table = p.tables + static_cast<size_t>(s) * p.max_blocks;
   const int bmask = (1 << p.bs_shift) - 1;
-  for (int base = i0; base < i1; base += 32) {
-    const int i = base + lane;
-    const bool in = i < i1;
-    const float x = in ? __ldg(w + i) : 0.f;
-    const uint32_t key = in && i < n ? weight_key(x) : 0u;
-    const bool sure = in && (i >= n || all || (k > 0 && key > prefix));
-    const bool tie = in && !sure && k > 0 && key == prefix;
-    const unsigned ties = __ballot_sync(0xffffffffu, tie), below = (1u << lane) - 1u;
-    const bool keep = sure || (tie && eq0 + __popc(ties & below) < need);
-    const unsigned kept = __ballot_sync(0xffffffffu, keep);
-    if (keep) {
-      const int to = at + __popc(kept & below);
-      const int block = __ldg(table + (i >> p.bs_shift));
-      int slot = -1;
-      if (block >= 0 && block < p.num_blocks) slot = (block << p.bs_shift) + (i & bmask);
-      else record_error(p.err, kErrBlockIndex);
-      p.list[pair * p.budget + to] = slot;
-      p.new_weights[pair * p.new_width + to] = x;
+  each([&](int base, const uint32_t (&x)[kBatch]) {
+    const unsigned below = (1u << lane) - 1u;
+    int to[kBatch], block[kBatch];
+    float weight[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = base + 32 * j + lane;
+      const bool sure = i < i1 && (i >= from || x[j] > prefix);
+      const bool tie = i < i1 && !sure && x[j] == prefix;
+      const unsigned ties = __ballot_sync(0xffffffffu, tie);
+      const bool keep = sure || (tie && eq0 + __popc(ties & below) < need);
+      const unsigned kept = __ballot_sync(0xffffffffu, keep);
+      to[j] = keep ? at + __popc(kept & below) : -1;
+      at += __popc(kept);
+      eq0 += __popc(ties);
     }
-    at += __popc(kept);
-    eq0 += __popc(ties);
-  }
+    // (the kept tokens' blocks and weights are on their way together)
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = base + 32 * j + lane;
+      block[j] = to[j] >= 0 ? __ldg(table + (i >> p.bs_shift)) : 0;
+      weight[j] = to[j] >= 0 ? __ldg(w + i) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (to[j] >= 0) {
+        const bool ok = block[j] >= 0 && block[j] < p.num_blocks;
+        if (!ok) record_error(p.err, kErrBlockIndex);
+        list[to[j]] = ok ? (block[j] << p.bs_shift) + ((base + 32 * j + lane) & bmask) : -1;
+        new_weights[to[j]] = weight[j];
+      }
+  });
 }
 
 template <int ROW>
@@ -179,7 +287,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     const int first = static_cast<int>(i - pair * per_pair) * (U * RPI) + lane / LPR;
     const int s = static_cast<int>(pair / p.kv_heads), h = static_cast<int>(pair - static_cast<long long>(s) * p.kv_heads);
     const int count = p.new_lens[s];
-    size_t from[U], to[U];
+    uint32_t from[U], to[U];  // (rows of the caches, fewer than 2^31)
     bool ok[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -194,22 +302,24 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
           record_error(p.err, kErrBlockIndex);
           ok[u] = false;
         }
-        from[u] = ((static_cast<size_t>(slot >> p.bs_shift) * p.kv_heads + h) << p.bs_shift) + (slot & bmask);
-        to[u] = ((static_cast<size_t>(block) * p.kv_heads + h) << p.bs_shift) + (row & bmask);
+        if (ok[u]) {
+          from[u] = ((static_cast<uint32_t>(slot >> p.bs_shift) * p.kv_heads + h) << p.bs_shift) + (slot & bmask);
+          to[u] = ((static_cast<uint32_t>(block) * p.kv_heads + h) << p.bs_shift) + (row & bmask);
+        }
       }
     }
     uint4 a[U], b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (ok[u]) {
-        a[u] = *reinterpret_cast<const uint4 *>(p.k + from[u] * ROW + col);
-        b[u] = *reinterpret_cast<const uint4 *>(p.v + from[u] * ROW + col);
+        a[u] = *reinterpret_cast<const uint4 *>(p.k + static_cast<size_t>(from[u]) * ROW + col);
+        b[u] = *reinterpret_cast<const uint4 *>(p.v + static_cast<size_t>(from[u]) * ROW + col);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (ok[u]) {
-        *reinterpret_cast<uint4 *>(p.k_out + to[u] * ROW + col) = a[u];
-        *reinterpret_cast<uint4 *>(p.v_out + to[u] * ROW + col) = b[u];
+        *reinterpret_cast<uint4 *>(p.k_out + static_cast<size_t>(to[u]) * ROW + col) = a[u];
+        *reinterpret_cast<uint4 *>(p.v_out + static_cast<size_t>(to[u]) * ROW + col) = b[u];
       }
   }
 }
@@ -262,7 +372,8 @@ extern "C" pa_status pa_evict_tokens(void *k_cache, void *v_cache, const pa_cach
         reinterpret_cast<uintptr_t>(new_lens) | reinterpret_cast<uintptr_t>(new_weights)) & 3u))
     return PA_ERR_INVALID;
   if (!supported_cache_shape(cache) || cache->dtype == PA_FP4) return PA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(cache->num_blocks) * cache->block_size > INT_MAX) return PA_ERR_UNSUPPORTED;  // 32-bit slots
+  if (static_cast<long long>(cache->num_blocks) * cache->block_size * cache->kv_heads > INT_MAX)
+    return PA_ERR_UNSUPPORTED;  // 32-bit rows
   if (static_cast<long long>(num_seqs) * cache->kv_heads > INT_MAX) return PA_ERR_UNSUPPORTED;             // the grid
   if (workspace_bytes < pa_evict_workspace_size(num_seqs, cache->kv_heads, budget)) return PA_ERR_INVALID;
   EvictParams p{};

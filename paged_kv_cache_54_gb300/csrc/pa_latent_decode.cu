@@ -173,11 +173,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rt = blockIdx.x % p.row_tiles, w = blockIdx.x / p.row_tiles;
   launch_dependents();
+  const int n_rows = min(N, p.rows - rt * N);  // query rows of this tile
   auto tiles_of = [&](int s) -> long long { return (checked_len(p.lens, s, p.limit, p.err) + kTile - 1) / kTile; };
-  scan.scan(p.num_seqs, tiles_of);
-  if (blockIdx.x == 0) {  // the sequences' first tiles, for the merge
-    const int n = scan.run(p.num_seqs), t = threadIdx.x;
-    if (t < 128) {
+  Walk<kTile> walk;
+  if (p.whole) {
+    walk.u = walk.first = 0;
+    walk.s = w;
+    walk.end = tiles_of(w);
+    if (walk.end == 0) {
+      zero_rows(p.out, static_cast<long long>(w) * p.rows + rt * N, n_rows);
+      return;
+    }
+  } else {
+    scan.scan(p.num_seqs, tiles_of);
+    if (blockIdx.x == 0 && threadIdx.x < 128) {  // the sequences' first tiles, for the merge
+      const int n = scan.run(p.num_seqs), t = threadIdx.x;
       long long at = scan.base[t];
       for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
         p.prefix[s] = at;
@@ -185,20 +195,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (t == 0) p.prefix[p.num_seqs] = scan.total();
     }
+    const long long total = scan.total(), workers = worker_count(total, max_workers);
+    if (w >= workers) return;
+    walk.u = share_begin(w, total, workers);
+    walk.end = share_begin(w + 1, total, workers);
+    walk.s = scan.find(walk.u, p.num_seqs, tiles_of, walk.first);
   }
-  const long long total = scan.total(), workers = worker_count(total, max_workers);
-  if (w >= workers) return;
   if ((smem_addr(smem) & 1023u) != 0) {  // the swizzle needs 1024-byte atoms
     if (threadIdx.x == 0) record_error(p.err, kErrSmemAlign);
     return;
   }
-  Walk<kTile> walk;
-  walk.u = share_begin(w, total, workers);
-  walk.end = share_begin(w + 1, total, workers);
-  walk.s = scan.find(walk.u, p.num_seqs, tiles_of, walk.first);
   volatile int *abort = &hdr.abort;
   uint8_t *qs = smem + Lay::Q_OFF, *ps = smem + Lay::P_OFF, *kv = smem + Lay::KV_OFF;
-  const int n_rows = min(N, p.rows - rt * N);  // query rows of this tile
   if (warp == kTmaWarp && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_c)) : "memory");
@@ -798,12 +806,12 @@ pa_status launch(LatentParams &p, const void *q, cudaStream_t stream) {
     return cuda_fail(cudaErrorInvalidValue);
   p.row_tiles = (p.rows + N - 1) / N;
   const int sms = info.sm_count < kMaxWorkers ? info.sm_count : kMaxWorkers;
-  const int workers = sms / p.row_tiles > 0 ? sms / p.row_tiles : 1;
+  const int workers = p.whole ? p.num_seqs : sms / p.row_tiles > 0 ? sms / p.row_tiles : 1;
   if (static_cast<long long>(workers) * p.row_tiles > INT_MAX) return PA_ERR_UNSUPPORTED;
   latent_decode_kernel<DT, N><<<workers * p.row_tiles, kThreads, Lay::SMEM, stream>>>(p, workers);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  return join<DT, N>(p, workers, info.sm_count, stream);
+  return p.whole ? PA_OK : join<DT, N>(p, workers, info.sm_count, stream);
 }
 
 template <int DT>
@@ -816,7 +824,7 @@ pa_status by_rows(LatentParams &p, const void *q, const void *cache, const pa_la
   int workers = 0;
   const pa_status st = launch_latent_pair(DT, p, q, cache, desc, &workers, stream);
   DeviceInfo info;
-  return st != PA_OK || !current_device_info(&info) ? st : join<DT, kPairRows>(p, workers, info.sm_count, stream);
+  return st != PA_OK || p.whole || !current_device_info(&info) ? st : join<DT, kPairRows>(p, workers, info.sm_count, stream);
 }
 
 }  // namespace
@@ -867,6 +875,7 @@ extern "C" pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype,
   long long limit = held < max_seq_len ? held : max_seq_len;
   if (limit > INT_MAX / 4) limit = INT_MAX / 4;
   p.limit = static_cast<int>(limit);
+  p.whole = max_seq_len <= kWholeTokens;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = device_error;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

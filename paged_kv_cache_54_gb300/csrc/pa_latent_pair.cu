@@ -77,22 +77,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, rt = pair % p.row_tiles, w = pair / p.row_tiles;
   launch_dependents();
   auto tiles_of = [&](int s) -> long long { return (checked_len(p.lens, s, p.limit, p.err) + kTile - 1) / kTile; };
-  scan.scan(p.num_seqs, tiles_of);
-  if (blockIdx.x == 0 && threadIdx.x < 128) {  // the sequences' first tiles, for the merge
-    const int n = scan.run(p.num_seqs), t = threadIdx.x;
-    long long at = scan.base[t];
-    for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
-      p.prefix[s] = at;
-      at += tiles_of(s);
-    }
-    if (t == 0) p.prefix[p.num_seqs] = scan.total();
-  }
-  const long long total = scan.total(), workers = worker_count(total, max_workers);
-  if (w >= workers) return;  // (both blocks)
   Walk<kTile> walk;
-  walk.u = share_begin(w, total, workers);
-  walk.end = share_begin(w + 1, total, workers);
-  walk.s = scan.find(walk.u, p.num_seqs, tiles_of, walk.first);
+  if (p.whole) {
+    walk.u = walk.first = 0;
+    walk.s = w;
+    walk.end = tiles_of(w);
+    if (walk.end == 0) {  // (both blocks)
+      const int first = rt * kPairRows + kHalfRows * rank;
+      zero_rows(p.out, static_cast<long long>(w) * p.rows + first, min(kHalfRows, p.rows - first));
+      return;
+    }
+  } else {
+    scan.scan(p.num_seqs, tiles_of);
+    if (blockIdx.x == 0 && threadIdx.x < 128) {  // the sequences' first tiles, for the merge
+      const int n = scan.run(p.num_seqs), t = threadIdx.x;
+      long long at = scan.base[t];
+      for (int s = t * n; s < min(p.num_seqs, (t + 1) * n); ++s) {
+        p.prefix[s] = at;
+        at += tiles_of(s);
+      }
+      if (t == 0) p.prefix[p.num_seqs] = scan.total();
+    }
+    const long long total = scan.total(), workers = worker_count(total, max_workers);
+    if (w >= workers) return;  // (both blocks)
+    walk.u = share_begin(w, total, workers);
+    walk.end = share_begin(w + 1, total, workers);
+    walk.s = scan.find(walk.u, p.num_seqs, tiles_of, walk.first);
+  }
   volatile int *abort = &hdr.abort;
   uint8_t *qs = smem + kQOff, *ps = smem + kPOff, *ks = smem + kKOff, *vs = smem + kVOff;
   if (warp == kKTmaWarp && lane == 0) {
@@ -490,7 +501,7 @@ pa_status launch_latent_pair(int dtype, LatentParams &p, const void *q, const vo
     return cuda_fail(cudaErrorInvalidValue);
   p.row_tiles = (p.rows + kPairRows - 1) / kPairRows;
   const int pairs = info.sm_count / 2 < kMaxPairs ? info.sm_count / 2 : kMaxPairs;
-  *workers = pairs / p.row_tiles > 0 ? pairs / p.row_tiles : 1;
+  *workers = p.whole ? p.num_seqs : pairs / p.row_tiles > 0 ? pairs / p.row_tiles : 1;
   if (2ll * *workers * p.row_tiles > INT_MAX) return PA_ERR_UNSUPPORTED;
   return dtype == kF16 ? launch<kF16>(p, *workers, stream) : launch<kBF16>(p, *workers, stream);
 }

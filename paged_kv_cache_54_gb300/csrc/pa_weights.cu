@@ -42,6 +42,9 @@ constexpr int kWarps = 4;             // of a block
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxWorkers = 152 * 16; // warps, at most; sizes the workspace
 constexpr int kMinSteps = 4;          // a share smaller than this only adds joining
+// Pairs of up to this many tokens are not split: one warp weighs, joins and
+// writes them, and there is no second kernel.
+constexpr int kWholeTokens = 128;
 constexpr float kLazy = 8.f;          // a row's maximum is raised when it grew by more than this (base 2)
 
 struct WeighParams {
@@ -58,6 +61,7 @@ struct WeighParams {
   int num_seqs, q_heads, kv_heads, G, num_blocks, bs_shift, max_blocks, limit, width;
   long long weights_width;
   float scale_log2, v_scale, decay;
+  bool whole;          // a warp takes all of a pair: nothing to join
   const float *k_head_scale, *v_head_scale;
   int *err;
 };
@@ -108,25 +112,39 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
   auto steps_of = [&](int s) {
     return static_cast<long long>((checked_len(p.lens, s, p.limit, p.err) + kStep - 1) / kStep) * p.kv_heads;
   };
-  scan.scan(p.num_seqs, steps_of);
-  if (blockIdx.x == 0) {  // the sequences' first steps, for the second kernel
-    const int n = scan.run(p.num_seqs);
-    long long at = scan.base[threadIdx.x];
-    for (int s = threadIdx.x * n; s < min(p.num_seqs, (static_cast<int>(threadIdx.x) + 1) * n); ++s) {
-      p.prefix[s] = at;
-      at += steps_of(s);
-    }
-    if (threadIdx.x == 0) p.prefix[p.num_seqs] = scan.total();
-  }
-  const long long total = scan.total();
-  const long long workers = worker_count(total, max_workers);
   const long long w = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  if (total == 0 || w >= workers) return;
-  long long u = share_begin(w, total, workers);
-  const long long end = share_begin(w + 1, total, workers);
-  if (u >= end) return;
-  long long first;
-  int s = scan.find(u, p.num_seqs, steps_of, first);
+  long long u, end, first;
+  int s;
+  if (p.whole) {
+    if (w >= static_cast<long long>(p.num_seqs) * p.kv_heads) return;
+    s = static_cast<int>(w / p.kv_heads);
+    const int h = static_cast<int>(w - static_cast<long long>(s) * p.kv_heads);
+    const long long steps = steps_of(s) / p.kv_heads;
+    first = 0;
+    u = h * steps;
+    end = u + steps;
+    if (steps == 0)  // no token
+      for (int i = lane; i < p.G * D / 2; i += 32)
+        reinterpret_cast<uint32_t *>(p.out)[(static_cast<size_t>(s) * p.q_heads + h * p.G) * (D / 2) + i] = 0u;
+  } else {
+    scan.scan(p.num_seqs, steps_of);
+    if (blockIdx.x == 0) {  // the sequences' first steps, for the second kernel
+      const int n = scan.run(p.num_seqs);
+      long long at = scan.base[threadIdx.x];
+      for (int i = threadIdx.x * n; i < min(p.num_seqs, (static_cast<int>(threadIdx.x) + 1) * n); ++i) {
+        p.prefix[i] = at;
+        at += steps_of(i);
+      }
+      if (threadIdx.x == 0) p.prefix[p.num_seqs] = scan.total();
+    }
+    const long long total = scan.total();
+    const long long workers = worker_count(total, max_workers);
+    if (total == 0 || w >= workers) return;
+    u = share_begin(w, total, workers);
+    end = share_begin(w + 1, total, workers);
+    if (u >= end) return;
+    s = scan.find(u, p.num_seqs, steps_of, first);
+  }
 
   const uint64_t policy = l2_policy_evict_first(), keep = l2_policy_evict_last();
   const int bs = 1 << p.bs_shift, bmask = bs - 1;
@@ -308,12 +326,44 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
       }
       load_v(next, vb);
     }
-    // the piece: unnormalised sums with their maximum and total weight
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    constexpr int VD = BYTE ? D / 8 : 8;  // consecutive dimensions of a lane
+    if (p.whole) {
+      const float vs = p.v_head_scale != nullptr ? __ldg(p.v_head_scale + h) : p.v_scale;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // (no score above -inf)
+      const float i0 = __shfl_sync(0xffffffffu, inv, 8 * t) * vs, i1 = __shfl_sync(0xffffffffu, inv, 8 * t + 4) * vs;
+      uint16_t *out = static_cast<uint16_t *>(p.out) + (static_cast<size_t>(s) * p.q_heads + h * p.G + 2 * t) * D;
+#pragma unroll
+      for (int i = 0; i < ACC; ++i) {
+        const int d = (2 * i / VD) * (8 * VD) + g * VD + 2 * i % VD;
+        if (2 * t < p.G)
+          *reinterpret_cast<uint32_t *>(out + d) = i0 == 0.f ? 0u : pack2_rn<QT>(acc[i][0] * i0, acc[i][2] * i0);
+        if (2 * t + 1 < p.G)
+          *reinterpret_cast<uint32_t *>(out + D + d) = i1 == 0.f ? 0u : pack2_rn<QT>(acc[i][1] * i1, acc[i][3] * i1);
+      }
+      __syncwarp();  // the warp's scores are there
+      const float base = m == -INFINITY ? 0.f : m;
+      const float *x = p.logits + (static_cast<size_t>(s) * p.q_heads + h * p.G) * p.width;
+      const size_t at = (static_cast<size_t>(s) * p.kv_heads + h) * p.weights_width;
+      float bm[8], bi[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        bm[q] = __shfl_sync(0xffffffffu, base, 4 * q);
+        bi[q] = q < p.G ? __shfl_sync(0xffffffffu, inv, 4 * q) : 0.f;
+      }
+      for (int i = lane; i < L; i += 32) {
+        float sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.G) sum += exp2_fast(__ldcg(x + static_cast<size_t>(q) * p.width + i) - bm[q]) * bi[q];
+        p.weights_out[at + i] = (p.weights_in == nullptr ? 0.f : p.decay * p.weights_in[at + i]) + sum;
+      }
+      return;
+    }
+    // the piece: unnormalised sums with their maximum and total weight
     if (t == 0 && g < p.G) p.part_ml[slot * p.G + g] = make_float2(m, l);
     float *po = p.part_o + slot * p.G * D;
-    constexpr int VD = BYTE ? D / 8 : 8;  // consecutive dimensions of a lane
 #pragma unroll
     for (int i = 0; i < ACC; ++i) {
       const int d = (2 * i / VD) * (8 * VD) + g * VD + 2 * i % VD;
@@ -533,6 +583,12 @@ pa_status launch(const WeighParams &p, cudaStream_t stream) {
   if (!current_device_info(&info)) return cuda_fail(cudaGetLastError());
   const int blocks = info.sm_count * 3 * kWarps > kMaxWorkers ? kMaxWorkers / kWarps : info.sm_count * 3;
   const int workers = blocks * kWarps;
+  if (p.whole) {
+    const long long pairs = static_cast<long long>(p.num_seqs) * p.kv_heads;
+    weigh_kernel<KVT, QT, D><<<static_cast<unsigned>((pairs + kWarps - 1) / kWarps), kThreads, 0, stream>>>(p, 0);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? PA_OK : cuda_fail(e);
+  }
   weigh_kernel<KVT, QT, D><<<blocks, kThreads, 0, stream>>>(p, workers);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
@@ -623,6 +679,7 @@ extern "C" pa_status pa_decode_weights(void *out, float *weights_out, const floa
   p.k_head_scale = per_head ? cache->k_head_scales : nullptr;
   p.v_head_scale = per_head ? cache->v_head_scales : nullptr;
   p.decay = decay;
+  p.whole = max_seq_len <= kWholeTokens;
   p.err = device_error;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int D = cache->head_dim;
