@@ -876,6 +876,7 @@ extern "C" pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype,
   if (limit > INT_MAX / 4) limit = INT_MAX / 4;
   p.limit = static_cast<int>(limit);
   p.whole = max_seq_len <= kWholeTokens;
+  p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = device_error;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

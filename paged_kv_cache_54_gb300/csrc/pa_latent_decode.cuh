@@ -27,6 +27,7 @@ struct LatentParams {
   long long *prefix;   // [S + 1] tiles before sequence s
   int num_seqs, new_tokens, heads, rows, row_tiles, num_blocks, bs_shift, max_blocks, limit;
   bool whole;          // every share is one sequence: nothing to join
+  bool out_sectors;    // out is 32-byte aligned
   float scale_log2;
   int *err;
 };

@@ -253,9 +253,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 16; ++j)
             y[j] = l == 0.f ? 0u
                             : pack2_rn<DT>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-          if (mine) {
+          if (mine && p.out_sectors) {
             store32(to + d * 2, y);
             store32(to + d * 2 + 32, y + 8);
+          } else if (mine) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              *reinterpret_cast<uint4 *>(to + d * 2 + j * 4) = make_uint4(y[j], y[j + 1], y[j + 2], y[j + 3]);
           }
         }
       } else {

@@ -484,43 +484,52 @@ __global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParam
       const int i1 = i1l < L ? static_cast<int>(i1l) : L;
       const long long pair = static_cast<long long>(s) * p.kv_heads + h;
       const long long s0 = pair + share_owner(u0, total, workers), s1 = pair + share_owner(u0 + steps - 1, total, workers);
+      const float *x = p.logits + (static_cast<size_t>(s) * p.q_heads + h * p.G) * p.width;
+      const size_t at = static_cast<size_t>(pair) * p.weights_width;
+      const float *win = p.weights_in == nullptr ? nullptr : p.weights_in + at;
+      float *wout = p.weights_out + at;
+      // four tokens a lane (the scores' rows are aligned; the weights' may not
+      // be); the first ones are on their way while the pair's sums are joined
+      float4 sc[8];
+      float before[4];
+      auto load = [&](int j) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < p.G) sc[q] = __ldcs(reinterpret_cast<const float4 *>(x + static_cast<size_t>(q) * p.width + j));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) before[e] = win == nullptr ? 0.f : win[j + e];
+      };
+      int i = i0;
+      if (i + 128 <= i1) load(i + 4 * lane);
       // the pair's maximum and total of query lane / 4, four lanes along the pieces
       const int gq = min(lane >> 2, p.G - 1);
       float m = -INFINITY, l = 0.f;
-      for (long long i = s0 + (lane & 3); i <= s1; i += 4) m = fmaxf(m, p.part_ml[i * p.G + gq].x);
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      if (m == -INFINITY) m = 0.f;
-      for (long long i = s0 + (lane & 3); i <= s1; i += 4) {
-        const float2 ml = p.part_ml[i * p.G + gq];
-        l += exp2_fast(ml.x - m) * ml.y;
+      for (long long j = s0 + (lane & 3); j <= s1; j += 4) {
+        const float2 ml = p.part_ml[j * p.G + gq];
+        const float top = fmaxf(m, ml.x);
+        if (top > -INFINITY) l = l * exp2_fast(m - top) + ml.y * exp2_fast(ml.x - top);
+        m = top;
       }
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, m, d), ol = __shfl_xor_sync(0xffffffffu, l, d);
+        const float top = fmaxf(m, om);
+        if (top > -INFINITY) l = l * exp2_fast(m - top) + ol * exp2_fast(om - top);
+        m = top;
+      }
+      if (m == -INFINITY) m = 0.f;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float *x = p.logits + (static_cast<size_t>(s) * p.q_heads + h * p.G) * p.width;
-      const size_t at = static_cast<size_t>(pair) * p.weights_width;
       float bm[8], bi[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         bm[q] = __shfl_sync(0xffffffffu, m, 4 * q);
         bi[q] = q < p.G ? __shfl_sync(0xffffffffu, inv, 4 * q) : 0.f;
       }
-      const float *win = p.weights_in == nullptr ? nullptr : p.weights_in + at;
-      float *wout = p.weights_out + at;
-      int i = i0;
-      // four tokens a lane (the scores' rows are aligned; the weights' may not be)
       for (; i + 128 <= i1; i += 128) {
         const int j = i + 4 * lane;
-        float4 sc[8];
+        float sum[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < p.G) sc[q] = __ldcs(reinterpret_cast<const float4 *>(x + static_cast<size_t>(q) * p.width + j));
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-        if (win != nullptr)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = p.decay * win[j + e];
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int e = 0; e < 4; ++e) sum[e] = p.decay * before[e];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (q < p.G) {
@@ -529,15 +538,16 @@ __global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParam
             sum[2] += exp2_fast(sc[q].z - bm[q]) * bi[q];
             sum[3] += exp2_fast(sc[q].w - bm[q]) * bi[q];
           }
+        if (i + 256 <= i1) load(j + 128);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) wout[j + e] = w[e] + sum[e];
+        for (int e = 0; e < 4; ++e) wout[j + e] = sum[e];
       }
       for (i += lane; i < i1; i += 32) {
-        float sum = 0.f;
+        float sum = win == nullptr ? 0.f : p.decay * win[i];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           if (q < p.G) sum += exp2_fast(__ldcs(x + static_cast<size_t>(q) * p.width + i) - bm[q]) * bi[q];
-        wout[i] = (win == nullptr ? 0.f : p.decay * win[i]) + sum;
+        wout[i] = sum;
       }
       u = stop;
     }

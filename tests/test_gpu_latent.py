@@ -175,6 +175,36 @@ def test_decode_three_dimensional_queries_wider_tables_and_bounds():
     check(out, want[:, 0], tol[:, 0])
 
 
+def offset(t, elements=8):
+    """The tensor's values in a tensor that lies 16 bytes further on."""
+    x = torch.empty(t.numel() + elements, dtype=t.dtype, device=t.device)[elements:].view(t.shape)
+    return x.copy_(t)
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_tensors_aligned_to_16_bytes_only(heads):
+    cache, table, L, q = make([300, 70], 1, heads, 16, "bf16", 21)
+    cache, q, out = offset(cache), offset(q), offset(torch.empty(2, 1, heads, LATENT, dtype=q.dtype, device=DEV))
+    assert out.data_ptr() % 32 == 16
+    want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.bfloat16))
+    for most in (300, 5000):
+        out.fill_(float("nan"))
+        pa.pa_latent_decode(out, q, cache, table, L, most, SCALE)
+        check(out, want, tol)
+    new = torch.zeros_like(cache)
+    slots = torch.arange(7, device=DEV)
+    pa.pa_latent_write(cache.view(-1, ROW)[:7, :LATENT], cache.view(-1, ROW)[:7, LATENT:], slots, new)
+    assert torch.equal(new.view(-1, ROW)[:7].view(torch.int16), cache.view(-1, ROW)[:7].view(torch.int16))
+
+
+def test_prefill_tensors_aligned_to_16_bytes_only():
+    cache, table, L, q, up, cu = make_prefill([200, 30], [140, 30], 3, 16, "f16", 22)
+    cache, q, up, out = (offset(x) for x in (cache, q, up, torch.zeros(170, 3, 128, dtype=q.dtype, device=DEV)))
+    pa.pa_latent_prefill(out, q, cu, up, cache, table, L, 140, 230, SCALE)
+    want, tol = expect_prefill(cache, table, L, q, up, cu, 16, SCALE, eps(torch.float16))
+    check(out, want, tol)
+
+
 def test_decode_reports_bad_lengths_and_blocks():
     cache, table, L, q = make([100, 100, 100], 1, 16, 16, "f16", 23)
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
@@ -286,6 +316,7 @@ PREFILL = [
     ([511, 512, 513], [255, 256, 257], 2, 32),
     ([2000, 5], [40, 5], 16, 8),
     ([70] * 20, [2] * 20, 5, 16),
+    ([600, 40, 1000, 257, 300] * 6, [300, 1, 513, 257, 128] * 6, 7, 16),   # several items a block
 ]
 
 
