@@ -379,10 +379,12 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
 }
 
 // Adds the tokens' weights and joins the pairs' pieces: the first
-// weight_blocks blocks share the steps, the others write the rows of out, TEAM
-// warps a row (four where rows are few), each every TEAM-th piece.
+// weight_blocks blocks take `chunk` tokens of a pair each, the others write the
+// rows of out, TEAM warps a row (four where rows are few), each every TEAM-th
+// piece.
 template <int QT, int D, int TEAM>
-__global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParams p, int max_workers, int weight_blocks) {
+__global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParams p, int max_workers, int weight_blocks,
+                                                                int chunk) {
   constexpr int PER = D / 32;  // dimensions of a lane
   __shared__ float part[TEAM > 1 ? kWarps : 1][D];
   __shared__ float sums[kWarps];
@@ -454,103 +456,80 @@ __global__ void __launch_bounds__(kThreads) weigh_finish_kernel(const WeighParam
     for (int e = 0; e < PER; e += 2) out[e / 2] = l == 0.f ? 0u : pack2_rn<QT>(o[e] * f, o[e + 1] * f);
     return;
   }
-  if (total == 0) return;
-  const long long nw = static_cast<long long>(weight_blocks) * kWarps;
-  const long long w = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  long long u = share_begin(w, total, nw);
-  const long long end = share_begin(w + 1, total, nw);
-  if (u >= end) return;
-  // the last sequence whose first step is at or before u: 32 places are
-  // looked at together, then as many between two of them
-  int lo = 0;
-  for (int n = p.num_seqs; n > 1;) {
-    const int gap = (n + 31) / 32, at = lane * gap;
-    const unsigned before = __ballot_sync(0xffffffffu, at < n && p.prefix[lo + min(at, n - 1)] <= u);
-    const int j = 31 - __clz(before);  // (place 0 is always before)
-    lo += j * gap;
-    n = min(gap, n - j * gap);
+  const int chunks = (p.limit + chunk - 1) / chunk;
+  const long long pair = blockIdx.x / chunks;
+  const int s = static_cast<int>(pair / p.kv_heads), h = static_cast<int>(pair - static_cast<long long>(s) * p.kv_heads);
+  const long long first = p.prefix[s], all = p.prefix[s + 1] - first;
+  if (all == 0) return;
+  const int L = __ldg(p.lens + s);
+  const int i0 = static_cast<int>(blockIdx.x - pair * chunks) * chunk, i1 = min(L, i0 + chunk);
+  if (i0 >= L) return;
+  const long long steps = all / p.kv_heads, u0 = first + h * steps;
+  const long long s0 = pair + share_owner(u0, total, workers), s1 = pair + share_owner(u0 + steps - 1, total, workers);
+  const float *x = p.logits + (static_cast<size_t>(s) * p.q_heads + h * p.G) * p.width;
+  const size_t at = static_cast<size_t>(pair) * p.weights_width;
+  const float *win = p.weights_in == nullptr ? nullptr : p.weights_in + at;
+  float *wout = p.weights_out + at;
+  // four tokens a lane (the scores' rows are aligned; the weights' may not
+  // be); the first ones are on their way while the pair's sums are joined
+  float4 sc[8];
+  float before[4];
+  auto load = [&](int j) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < p.G) sc[q] = __ldcs(reinterpret_cast<const float4 *>(x + static_cast<size_t>(q) * p.width + j));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) before[e] = win == nullptr ? 0.f : win[j + e];
+  };
+  int i = i0 + 128 * warp;
+  if (i + 128 <= i1) load(i + 4 * lane);
+  // the pair's maximum and total of query lane / 4, four lanes along the pieces
+  const int gq = min(lane >> 2, p.G - 1);
+  float m = -INFINITY, l = 0.f;
+  for (long long j = s0 + (lane & 3); j <= s1; j += 4) {
+    const float2 ml = p.part_ml[j * p.G + gq];
+    const float top = fmaxf(m, ml.x);
+    if (top > -INFINITY) l = l * exp2_fast(m - top) + ml.y * exp2_fast(ml.x - top);
+    m = top;
   }
-  for (int s = lo; u < end; ++s) {
-    const long long first = p.prefix[s], all = p.prefix[s + 1] - first;
-    if (all == 0) continue;
-    const int L = __ldg(p.lens + s);
-    const long long steps = all / p.kv_heads;
-    while (u < end && u < first + all) {
-      const int h = static_cast<int>((u - first) / steps);
-      const long long u0 = first + h * steps;
-      const long long stop = end < u0 + steps ? end : u0 + steps;
-      const int i0 = static_cast<int>(u - u0) * kStep;
-      const long long i1l = (stop - u0) * kStep;
-      const int i1 = i1l < L ? static_cast<int>(i1l) : L;
-      const long long pair = static_cast<long long>(s) * p.kv_heads + h;
-      const long long s0 = pair + share_owner(u0, total, workers), s1 = pair + share_owner(u0 + steps - 1, total, workers);
-      const float *x = p.logits + (static_cast<size_t>(s) * p.q_heads + h * p.G) * p.width;
-      const size_t at = static_cast<size_t>(pair) * p.weights_width;
-      const float *win = p.weights_in == nullptr ? nullptr : p.weights_in + at;
-      float *wout = p.weights_out + at;
-      // four tokens a lane (the scores' rows are aligned; the weights' may not
-      // be); the first ones are on their way while the pair's sums are joined
-      float4 sc[8];
-      float before[4];
-      auto load = [&](int j) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < p.G) sc[q] = __ldcs(reinterpret_cast<const float4 *>(x + static_cast<size_t>(q) * p.width + j));
+  for (int d = 1; d < 4; d <<= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, d), ol = __shfl_xor_sync(0xffffffffu, l, d);
+    const float top = fmaxf(m, om);
+    if (top > -INFINITY) l = l * exp2_fast(m - top) + ol * exp2_fast(om - top);
+    m = top;
+  }
+  if (m == -INFINITY) m = 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float bm[8], bi[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) before[e] = win == nullptr ? 0.f : win[j + e];
-      };
-      int i = i0;
-      if (i + 128 <= i1) load(i + 4 * lane);
-      // the pair's maximum and total of query lane / 4, four lanes along the pieces
-      const int gq = min(lane >> 2, p.G - 1);
-      float m = -INFINITY, l = 0.f;
-      for (long long j = s0 + (lane & 3); j <= s1; j += 4) {
-        const float2 ml = p.part_ml[j * p.G + gq];
-        const float top = fmaxf(m, ml.x);
-        if (top > -INFINITY) l = l * exp2_fast(m - top) + ml.y * exp2_fast(ml.x - top);
-        m = top;
+  for (int q = 0; q < 8; ++q) {
+    bm[q] = __shfl_sync(0xffffffffu, m, 4 * q);
+    bi[q] = q < p.G ? __shfl_sync(0xffffffffu, inv, 4 * q) : 0.f;
+  }
+  for (; i + 128 <= i1; i += kThreads * 4) {
+    const int j = i + 4 * lane;
+    float sum[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = p.decay * before[e];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < p.G) {
+        sum[0] += exp2_fast(sc[q].x - bm[q]) * bi[q];
+        sum[1] += exp2_fast(sc[q].y - bm[q]) * bi[q];
+        sum[2] += exp2_fast(sc[q].z - bm[q]) * bi[q];
+        sum[3] += exp2_fast(sc[q].w - bm[q]) * bi[q];
       }
+    if (i + kThreads * 4 + 128 <= i1) load(j + kThreads * 4);
 #pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        const float om = __shfl_xor_sync(0xffffffffu, m, d), ol = __shfl_xor_sync(0xffffffffu, l, d);
-        const float top = fmaxf(m, om);
-        if (top > -INFINITY) l = l * exp2_fast(m - top) + ol * exp2_fast(om - top);
-        m = top;
-      }
-      if (m == -INFINITY) m = 0.f;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      float bm[8], bi[8];
+    for (int e = 0; e < 4; ++e) wout[j + e] = sum[e];
+  }
+  for (i += lane; i < i1; i += 32) {  // the chunk's last tokens, where they are this warp's
+    float sum = win == nullptr ? 0.f : p.decay * win[i];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        bm[q] = __shfl_sync(0xffffffffu, m, 4 * q);
-        bi[q] = q < p.G ? __shfl_sync(0xffffffffu, inv, 4 * q) : 0.f;
-      }
-      for (; i + 128 <= i1; i += 128) {
-        const int j = i + 4 * lane;
-        float sum[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] = p.decay * before[e];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < p.G) {
-            sum[0] += exp2_fast(sc[q].x - bm[q]) * bi[q];
-            sum[1] += exp2_fast(sc[q].y - bm[q]) * bi[q];
-            sum[2] += exp2_fast(sc[q].z - bm[q]) * bi[q];
-            sum[3] += exp2_fast(sc[q].w - bm[q]) * bi[q];
-          }
-        if (i + 256 <= i1) load(j + 128);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) wout[j + e] = sum[e];
-      }
-      for (i += lane; i < i1; i += 32) {
-        float sum = win == nullptr ? 0.f : p.decay * win[i];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < p.G) sum += exp2_fast(__ldcs(x + static_cast<size_t>(q) * p.width + i) - bm[q]) * bi[q];
-        wout[i] = sum;
-      }
-      u = stop;
-    }
+    for (int q = 0; q < 8; ++q)
+      if (q < p.G) sum += exp2_fast(__ldcs(x + static_cast<size_t>(q) * p.width + i) - bm[q]) * bi[q];
+    wout[i] = sum;
   }
 }
 
@@ -560,7 +539,7 @@ struct Sizes {
 };
 bool sizes_of(int S, int Hq, int H, int D, int max_len, Sizes *z) {
   if (S < 0 || Hq <= 0 || H <= 0 || Hq % H || (D != 64 && D != 128) || max_len < 0 || Hq / H > 8) return false;
-  if (max_len > INT_MAX - kStep) return false;
+  if (max_len > INT_MAX - 8192) return false;
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   z->width = (max_len + kStep - 1) / kStep * kStep;
   const size_t G = Hq / H, slots = static_cast<size_t>(S) * H + kMaxWorkers;
@@ -573,18 +552,25 @@ bool sizes_of(int S, int Hq, int H, int D, int max_len, Sizes *z) {
 }
 
 template <int QT, int D, int TEAM>
-cudaError_t launch_finish(const WeighParams &p, int workers, int weight_blocks, cudaStream_t stream) {
+cudaError_t launch_finish(const WeighParams &p, int workers, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   const int per = kWarps / TEAM;  // rows of a block
-  cfg.gridDim = dim3(static_cast<unsigned>((p.num_seqs * p.q_heads + per - 1) / per + weight_blocks));
+  // 2048 tokens a block, more where the bound on the lengths would make many blocks without any
+  const long long pairs = static_cast<long long>(p.num_seqs) * p.kv_heads;
+  const long long most = pairs >= 16384 ? 1 : 16384 / pairs;  // of a pair
+  long long chunk = (p.limit + most - 1) / most;
+  chunk = chunk < 2048 ? 2048 : (chunk + 127) / 128 * 128;
+  const long long blocks = pairs * ((p.limit + chunk - 1) / chunk);
+  cfg.gridDim = dim3(static_cast<unsigned>((p.num_seqs * p.q_heads + per - 1) / per + blocks));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weigh_finish_kernel<QT, D, TEAM>, p, workers, weight_blocks);
+  return cudaLaunchKernelEx(&cfg, weigh_finish_kernel<QT, D, TEAM>, p, workers, static_cast<int>(blocks),
+                            static_cast<int>(chunk));
 }
 
 template <int KVT, int QT, int D>
@@ -603,9 +589,8 @@ pa_status launch(const WeighParams &p, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
   const long long rows = static_cast<long long>(p.num_seqs) * p.q_heads;
-  // (six blocks an SM share the steps, in one wave)
-  e = rows <= info.sm_count * 8ll ? launch_finish<QT, D, 4>(p, workers, info.sm_count * 6, stream)
-                                  : launch_finish<QT, D, 1>(p, workers, info.sm_count * 6, stream);
+  e = rows <= info.sm_count * 8ll ? launch_finish<QT, D, 4>(p, workers, stream)
+                                  : launch_finish<QT, D, 1>(p, workers, stream);
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
