@@ -453,7 +453,8 @@ PA_API pa_status pa_swap_blocks(void *k_cache, void *v_cache, const pa_cache_des
  *                                           sum over h's G query heads of softmax_i
  *                  and entries from L_s on are left as they were.
  *   weights_in     the same shape; may be weights_out itself (an accumulator
- *                  updated in place).  NULL counts as zeros.
+ *                  updated in place), else must not overlap it.  NULL counts
+ *                  as zeros.
  *   decay          what the earlier weights are multiplied by (1 keeps them).
  *   workspace      at least pa_decode_weights_workspace_size(...) bytes,
  *                  256-byte aligned, uninitialised; calls sharing one must be
@@ -612,7 +613,8 @@ PA_API pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype, int
  * The expansion costs as much as the attention of about 170 new tokens a
  * sequence in the absorbed form; for fewer new tokens over a long context
  * pa_latent_decode is the cheaper call.  The rows of a sequence's tokens must
- * be finite (a later token's value reaches an earlier one's row times zero).
+ * be finite (a later token's value reaches an earlier one's row times zero),
+ * and the expanded keys lie in the cache type's range.
  * Device checks: a length that breaks these bounds, or tokens beyond
  * num_kv_tokens, skip the sequence (nothing of its output is written) and
  * report error 3; a block id out of range reads block 0 instead and reports

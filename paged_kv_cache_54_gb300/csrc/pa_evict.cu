@@ -396,7 +396,7 @@ extern "C" pa_status pa_evict_tokens(void *k_cache, void *v_cache, const pa_cach
   p.recent = recent;
   long long limit = static_cast<long long>(max_blocks_per_seq) * cache->block_size;
   if (weights_width < limit) limit = weights_width;
-  p.limit = limit < INT_MAX - kSelThreads ? static_cast<int>(limit) : INT_MAX - kSelThreads;
+  p.limit = limit < INT_MAX / 2 ? static_cast<int>(limit) : INT_MAX / 2;  // (steps past the end must not wrap)
   p.width = weights_width;
   p.new_width = new_width;
   p.err = device_error;

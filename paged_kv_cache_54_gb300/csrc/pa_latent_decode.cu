@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Header &hdr = *reinterpret_cast<Header *>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rt = blockIdx.x % p.row_tiles, w = blockIdx.x / p.row_tiles;
-  launch_dependents();
+  if (!p.whole) launch_dependents();  // (the merge)
   const int n_rows = min(N, p.rows - rt * N);  // query rows of this tile
   auto tiles_of = [&](int s) -> long long { return (checked_len(p.lens, s, p.limit, p.err) + kTile - 1) / kTile; };
   Walk<kTile> walk;

@@ -75,7 +75,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = cluster_rank();
   const int pair = blockIdx.x >> 1, rt = pair % p.row_tiles, w = pair / p.row_tiles;
-  launch_dependents();
+  if (!p.whole) launch_dependents();  // (the merge)
   auto tiles_of = [&](int s) -> long long { return (checked_len(p.lens, s, p.limit, p.err) + kTile - 1) / kTile; };
   Walk<kTile> walk;
   if (p.whole) {

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
   constexpr int ACC = D / 16;           // accumulator tiles
   __shared__ ShareScan<kThreads> scan;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  launch_dependents();
+  if (!p.whole) launch_dependents();  // (the second kernel)
   auto steps_of = [&](int s) {
     return static_cast<long long>((checked_len(p.lens, s, p.limit, p.err) + kStep - 1) / kStep) * p.kv_heads;
   };

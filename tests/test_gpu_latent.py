@@ -452,6 +452,32 @@ def test_serving_run_of_the_latent_calls():
     check(got, want[-1], tol[-1] + more + 2 * d.amax(-1)[:, None] * spread)
 
 
+def test_two_streams_at_once():
+    """Calls of both forms overlapping on two streams, each with its own workspace."""
+    sets = []
+    for i, heads in enumerate((16, 128)):
+        cache, table, L, q = make([900, 2000, 70], 1, heads, 16, "bf16", 71 + i)
+        want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.bfloat16))
+        pc = make_prefill([400, 300], [300, 20], 4, 16, "bf16", 73 + i)
+        pwant, ptol = expect_prefill(*pc, 16, SCALE, eps(torch.bfloat16))
+        ws = torch.empty(pa.pa_latent_decode_workspace_size(3, 1, heads), dtype=torch.uint8, device=DEV)
+        pws = torch.empty(pa.pa_latent_prefill_workspace_size(2, 4, 700), dtype=torch.uint8, device=DEV)
+        out, pout = torch.empty(3, 1, heads, LATENT, dtype=q.dtype, device=DEV), torch.empty(320, 4, 128, dtype=q.dtype,
+                                                                                           device=DEV)
+        sets.append((torch.cuda.Stream(), cache, table, L, q, want, tol, pc, pwant, ptol, ws, pws, out, pout))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for stream, cache, table, L, q, _, _, pc, _, _, ws, pws, out, pout in sets:
+            with torch.cuda.stream(stream):
+                pa.pa_latent_decode(out, q, cache, table, L, 2000, SCALE, workspace=ws)
+                pcache, ptable, pL, pq, up, cu = pc
+                pa.pa_latent_prefill(pout, pq, cu, up, pcache, ptable, pL, 300, 700, SCALE, workspace=pws)
+    torch.cuda.synchronize()
+    for _, _, _, _, _, want, tol, _, pwant, ptol, _, _, out, pout in sets:
+        check(out, want, tol)
+        check(pout, pwant, ptol)
+
+
 def test_blocks_move_under_a_nine_head_description():
     a, b = (randn(gen(s), 6, 16, ROW).bfloat16() for s in (41, 42))
     want_a, want_b = a.clone(), b.clone()
