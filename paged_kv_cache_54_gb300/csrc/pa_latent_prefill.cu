@@ -394,7 +394,8 @@ struct AttendParams {
   const int32_t *cu_q, *lens;
   const long long *prefix;
   const int32_t *powers;
-  int heads, num_q_tokens, max_q_len, limit;
+  unsigned num_seqs, heads, ranges, head_group;  // ranges of 256 new tokens; heads that are worked on together
+  int num_q_tokens, max_q_len, limit;
   long long capacity;
   float scale_log2;
   int *err;
@@ -445,8 +446,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
   constexpr uint32_t IDESC_PV = umma_idesc_f16(0, kRows, kValue, true);  // P and V are fp16
   extern __shared__ __align__(1024) uint8_t smem[];
   AttendHeader &hdr = *reinterpret_cast<AttendHeader *>(smem);
-  const int cta = gridDim.x - 1 - blockIdx.x;  // the longest (last) ranges first
-  const int h = blockIdx.z, s = blockIdx.y;
+  // Blocks in this order: groups of heads whose keys and values stay in L2
+  // together; in a group the ranges that end last, which follow most tokens,
+  // before the others, so that the last blocks to start are short.
+  const unsigned group = blockIdx.x / (p.ranges * p.num_seqs * p.head_group);
+  const unsigned heads = min(p.head_group, p.heads - group * p.head_group);
+  unsigned at = blockIdx.x - group * (p.ranges * p.num_seqs * p.head_group);
+  const int h = static_cast<int>(group * p.head_group + at % heads);
+  at /= heads;
+  const int s = static_cast<int>(at % p.num_seqs), cta = static_cast<int>(p.ranges - 1 - at / p.num_seqs);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kTmaWarp && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
   }
   const int q0 = __ldg(p.cu_q + s), n = __ldg(p.cu_q + s + 1) - q0, L = __ldg(p.lens + s);
   if (n < 0 || q0 < 0 || n > p.num_q_tokens - q0 || n > p.max_q_len || L < n || L > p.limit) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) record_error(p.err, kErrSeqLen);
+    if (threadIdx.x == 0) record_error(p.err, kErrSeqLen);
     return;
   }
   if (cta * kTiles * kRows >= n) return;
@@ -809,7 +817,7 @@ bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims
 }
 
 template <int DT>
-pa_status launch(const ExpandParams &ep, const AttendParams &ap, int num_seqs, int max_q_len, cudaStream_t stream) {
+pa_status launch(const ExpandParams &ep, const AttendParams &ap, cudaStream_t stream) {
   static bool configured[64];  // per device: dynamic shared memory already allowed
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -830,7 +838,7 @@ pa_status launch(const ExpandParams &ep, const AttendParams &ap, int num_seqs, i
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((max_q_len + kTiles * kRows - 1) / (kTiles * kRows), num_seqs, ap.heads);
+  cfg.gridDim = dim3(ap.ranges * ap.num_seqs * ap.heads);
   cfg.blockDim = dim3(kAttnThreads);
   cfg.dynamicSmemBytes = kAttnSmem;
   cfg.stream = stream;
@@ -868,7 +876,7 @@ extern "C" pa_status pa_latent_prefill(void *out, const void *q, int32_t q_dtype
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PA_ERR_INVALID;
   if (!supported_latent_desc(desc) || q_dtype != desc->dtype) return PA_ERR_UNSUPPORTED;
-  if (num_seqs > 65535 || num_heads > 65535) return PA_ERR_UNSUPPORTED;  // grid limits
+  if (num_seqs > 65535 || num_heads > 65535) return PA_ERR_UNSUPPORTED;
   Sizes z;
   if (!sizes_of(num_seqs, num_heads, num_kv_tokens, &z)) return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < z.total) return PA_ERR_INVALID;
@@ -896,7 +904,14 @@ extern "C" pa_status pa_latent_prefill(void *out, const void *q, int32_t q_dtype
   ap.lens = seq_lens;
   ap.prefix = ep.prefix;
   ap.powers = ep.powers;
+  ap.num_seqs = num_seqs;
   ap.heads = num_heads;
+  const long long ranges = (static_cast<long long>(max_q_len) + kTiles * kRows - 1) / (kTiles * kRows);
+  if (ranges * num_seqs * num_heads > INT_MAX / 2) return PA_ERR_UNSUPPORTED;  // the grid
+  ap.ranges = static_cast<unsigned>(ranges);
+  // keys and values of a group of heads: up to half of L2
+  const long long in_l2 = (64ll << 20) / (z.capacity * kUp * 2);
+  ap.head_group = static_cast<unsigned>(in_l2 < 1 ? 1 : in_l2 > num_heads ? num_heads : in_l2);
   ap.num_q_tokens = num_q_tokens;
   ap.max_q_len = max_q_len;
   ap.limit = ep.limit;
@@ -916,6 +931,6 @@ extern "C" pa_status pa_latent_prefill(void *out, const void *q, int32_t q_dtype
       !encode(&ap.tmap_kv, ep.kv, 2, dk, sk, bk) || !encode(&ap.tmap_rope, ep.rope, 2, dr, sr, bk))
     return cuda_fail(cudaErrorInvalidValue);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return desc->dtype == PA_F16 ? launch<kF16>(ep, ap, num_seqs, max_q_len, st)
-                               : launch<kBF16>(ep, ap, num_seqs, max_q_len, st);
+  return desc->dtype == PA_F16 ? launch<kF16>(ep, ap, st)
+                               : launch<kBF16>(ep, ap, st);
 }
