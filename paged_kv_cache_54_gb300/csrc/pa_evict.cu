@@ -9,11 +9,13 @@
 // found; and to place the kept tokens in order (keys above T, the first of
 // those equal to it, and the recent ones).  Where the bin holds more than fits
 // (many equal weights), the other digits read all weights too.  Bound by
-// issued instructions: 256 pairs of 4096..16384 tokens took 32 us with two
-// more passes over the weights.
+// issued instructions and the chain of steps between the passes: 256 pairs of
+// 4096..16384 tokens take 29 us (a pass more for each of the other digits: 32).
 // Move: rows copied from their old slots to their new ones, every warp with
-// several rows of K and of V in flight.  (Looking the tokens' blocks up here
-// costs 15 us of 180: a load more ahead of the rows.)
+// four accesses of K and four of V in flight.  The selection leaves slots, not
+// tokens: looking the blocks up here, a load more ahead of the rows, takes 15
+// us more.  4096 of those tokens a pair, 256-byte rows: 1.08 GB, 162 us at the
+// measured copy rate, in 166.
 #include <limits.h>
 
 #include "pa_common.cuh"

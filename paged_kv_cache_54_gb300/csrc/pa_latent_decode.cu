@@ -18,7 +18,10 @@
 // tensor memory, S^T 2 N.
 //
 // A block takes N query rows and an equal share of all sequences'
-// 64-token tiles (pa_shares.cuh).  Warps:
+// 64-token tiles (pa_shares.cuh).  One sequence of 131071 tokens, 32 query
+// rows: 151 MB, 22.6 us at the measured copy rate; this kernel takes 36 (the
+// loop keeps up with the memory, 5 us pass until the first tiles land, 5 from
+// the last one to the stored sums), the join of 152 pieces a row 10.  Warps:
 //   0..7  softmax: a thread owns a token and a quarter of the query rows.  The
 //         maximum of a query row is kept for all threads in shared memory and
 //         raised only when a score passes it by 2^8, so that almost every

@@ -10,10 +10,13 @@
 // tensor cores of both read the operands of either.  K and V are loaded apart,
 // V from L2 a second time: each part of shared memory is then held only from
 // its load to its own product, not through the softmax between them, and what
-// fits (one tile of each) is in flight most of the time.  A tile takes the
-// tensor cores 2200 clocks, its 147 KB a pair's share of the memory's rate
-// 3200.  (pa_latent_decode.cu with two blocks of 64 rows a tile took 3500
-// clocks for 64 tokens.)
+// fits (one tile of each) is in flight most of the time.  A tile of 128 tokens
+// takes the tensor cores 2200 clocks and, at the memory's rate, a pair's share
+// of it 3200; it takes about 4000: the 278 KB of K and V that a pair draws from
+// L2 for it, and the chain from S through the weights to O.  (pa_latent_decode.cu
+// with two blocks of 64 rows a tile took 3500 clocks for 64 tokens.)  128
+// sequences of 512..4096 tokens with 128 heads: 85 us, and 11 more for the join
+// of the pieces; 375 MB, 56 us at the measured copy rate.
 //
 // Tensor memory of a block: row r of its 64 in lanes r and r + 64, the first
 // half of a product's columns in the former, the other half in the latter.

@@ -31,6 +31,16 @@
 // issue the products, one a tile.  The running maximum is raised, and O
 // rescaled, only when it grew by more than 2^8.  Sums and maxima are fp32; P
 // is rounded to fp16, K and V were when they were expanded (half a step each).
+// Bound by shared memory, not by the tensor cores: a product's operands come
+// from it at 128 bytes a clock, 6 KB for the 32 clocks of one of S, and with
+// the stages' arrival that is 1664 clocks a stage of both tiles of the 1720
+// it takes (1280 of products).  4095 tokens after 4096, 64 heads: 81 us for the
+// expansion, 684 for the attention; 32 sequences of 16..512 after 1024, 16
+// heads: 105 and 138 (five waves of blocks of about 20 stages, whose first and
+// last microseconds and half-empty tiles count).  Tried: stages of 128 keys
+// with one S buffer a tile (733 us for the 684: the softmax is then in the
+// chain), a third of q in tensor memory (747), blocks that go on to the next
+// range (697).
 // With an fp16 cache P's rounding would show beside the output's where a row
 // follows few tokens, so sequences of up to 512 tokens take P as two fp16
 // parts.
