@@ -775,7 +775,9 @@ bool sizes_of(int S, int n, int H, Sizes *z) {
   const long long rows = static_cast<long long>(n) * H;
   if (rows > INT_MAX / 2 || rows * S > INT_MAX / 2) return false;
   const int N = columns_for(rows);
-  const size_t slots = static_cast<size_t>((rows + N - 1) / N) * (N == kPairRows ? kMaxPairs : kMaxWorkers) * 2;
+  // two pieces a share; the row tiles divide the blocks among them, or have one share each
+  const long long tiles = (rows + N - 1) / N, most = N == kPairRows ? kMaxPairs : kMaxWorkers;
+  const size_t slots = static_cast<size_t>(tiles > most ? tiles : most) * 2;
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   z->prefix = up(8 * (static_cast<size_t>(S) + 1));
   z->ml = up(slots * N * sizeof(float2));

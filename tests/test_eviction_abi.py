@@ -139,3 +139,11 @@ def test_binding_refuses_cpu_tensors_and_wrong_caches():
         pa.pa_decode_weights(kc[:, :, 0], kc, kc[:, :, 0], kc, kc, t, i, 16, 0.1)
     with pytest.raises(ValueError):
         pa.pa_evict_tokens(kc, kc, t, i, kc, t, i, kc, 4, 1)
+
+
+def test_latent_decode_workspace_follows_the_gpu_not_the_rows():
+    # 4 or 76 row tiles of 128 rows: the same shares, two pieces of 128 x (512 + 2) floats each
+    need = 76 * 2 * 128 * 514 * 4
+    for new in (1, 4, 76):
+        assert need <= pa.pa_latent_decode_workspace_size(3, new, 128) <= need + 1024
+    assert pa.pa_latent_decode_workspace_size(3, 152, 128) <= 2 * need + 1024

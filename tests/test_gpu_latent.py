@@ -258,6 +258,19 @@ def test_decode_captured_and_replayed_on_another_stream():
     check(out, want, tol)
 
 
+@pytest.mark.parametrize("lens,new,heads", [([5000, 700], 4, 128), ([900, 2500], 77, 128), ([700, 900], 3, 16)])
+def test_decode_stays_within_its_workspace(lens, new, heads):
+    # several row tiles that divide the shares among them, and more row tiles than shares
+    cache, table, L, q = make(lens, new, heads, 16, "bf16", 53)
+    need = pa.pa_latent_decode_workspace_size(len(lens), new, heads)
+    ws = torch.full((need + (1 << 20),), 0x5a, dtype=torch.uint8, device=DEV)
+    got = run(cache, table, L, q, SCALE, workspace=ws[:need])
+    assert bool((ws[need:] == 0x5a).all())
+    for h in {0, heads // 2, heads - 1}:
+        want, tol = expect(cache, table, L, q[:, :, h:h + 1], 16, SCALE, eps(torch.bfloat16))
+        check(got[:, :, h:h + 1], want, tol)
+
+
 # ---------------------------------------------------------------- prefill
 def make_prefill(lens, new, heads, bs, dt, seed):
     cache, table, L, _ = make(lens, 1, 1, bs, dt, seed)
