@@ -145,3 +145,40 @@ def test_decode_accumulate_evict_decode():
         kk, vv = k[blk, h, j % bs].double(), v[blk, h, j % bs].double()
         p = torch.softmax(q[0, h * G:(h + 1) * G].double() @ kk.T * 0.2, -1)
         assert torch.allclose(out[0, h * G:(h + 1) * G].double(), p @ vv, atol=2e-3)
+
+
+def test_past_four_gigabytes_and_weights_aligned_to_four_bytes():
+    bs, H, D, n, budget = 16, 8, 128, 700, 300
+    nb = (1 << 32) // (bs * H * D * 2) + 200
+    k, v = (torch.zeros(nb, H, bs, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    old, new = [nb - 1, 2] + list(range(nb - 60, nb - 18)), [nb - 2] + list(range(10, 28))
+    table, to = i32([old]), i32([new])
+    g = gen(30)
+    k[table[0].long()], v[table[0].long()] = (randn(g, len(old), H, bs, D).bfloat16() for _ in range(2))
+    w = torch.rand(H * (n + 1) + 1, generator=g, device=DEV)[1:].view(1, H, n + 1)
+    run_and_check(k, v, table, i32([n]), to, w, budget, 20, bs)
+
+
+def test_captured_and_replayed():
+    k, v, table, L, new = make([300, 20, 500], 2, 64, 16, "f16", 100, 31)
+    w = torch.rand(3, 2, 500, generator=gen(32), device=DEV)
+    ws = torch.empty(pa.pa_evict_workspace_size(3, 2, 100), dtype=torch.uint8, device=DEV)
+    lens, new_w = i32([0, 0, 0]), torch.zeros(3, 2, 100, device=DEV)
+    args = (k, v, table, L, w, new, lens, new_w, 100, 10)
+    pa.pa_evict_tokens(*args, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_evict_tokens(*args, workspace=ws)
+    L.copy_(i32([299, 0, 433]))
+    w.copy_(torch.rand(3, 2, 500, generator=gen(33), device=DEV))
+    k.copy_(randn(gen(34), *k.shape)), v.copy_(randn(gen(35), *v.shape))
+    before = k.clone(), v.clone()
+    ws.fill_(0x7f), new_w.zero_()
+    graph.replay()
+    assert lens.tolist() == [100, 0, 100]
+    got = k.clone(), v.clone(), new_w.clone()
+    k.copy_(before[0]), v.copy_(before[1]), new_w.zero_()
+    run_and_check(k, v, table, L, new, w, 100, 10, 16)     # the same from the same start, and right
+    assert torch.equal(k, got[0]) and torch.equal(v, got[1])
+    pa.pa_evict_tokens(k, v, table, L, w, new, lens, new_w, 100, 10)
+    assert torch.equal(new_w, got[2])

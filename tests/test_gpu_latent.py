@@ -258,6 +258,15 @@ def test_decode_captured_and_replayed_on_another_stream():
     check(out, want, tol)
 
 
+@pytest.mark.parametrize("heads,new", [(16, 1), (40, 1), (72, 2)])
+def test_decode_of_short_sequences_some_of_them_empty(heads, new):
+    lens = [0, 40, 0, 256, 1, 0, 64]     # none is split
+    cache, table, L, q = make(lens, new, heads, 16, "f16", 54)
+    got = run(cache, table, L, q, SCALE, max_len=256)
+    want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.float16))
+    check(got, want, tol)
+
+
 @pytest.mark.parametrize("lens,new,heads", [([5000, 700], 4, 128), ([900, 2500], 77, 128), ([700, 900], 3, 16)])
 def test_decode_stays_within_its_workspace(lens, new, heads):
     # several row tiles that divide the shares among them, and more row tiles than shares

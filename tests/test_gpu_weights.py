@@ -163,3 +163,54 @@ def test_captured_and_replayed():
         graph.replay()
     assert torch.allclose(acc.sum(-1), torch.tensor([[24.0, 24], [0, 0], [24, 24]], device=DEV), atol=1e-3)
     assert float(out[1].abs().sum()) == 0
+
+
+@pytest.mark.parametrize("longest", [90, 400])   # a warp a pair, and shares
+def test_many_sequences_many_of_them_empty(longest):
+    lens = [0 if s % 3 == 1 else (37 * s) % longest + 1 for s in range(333)]
+    k, v, table, L, q = make(lens, 6, 3, 64, 8, "f16", "f16", 16)
+    w, out = torch.full((333, 3, longest + 1), -1.0, device=DEV), torch.full_like(q, float("nan"))
+    pa.pa_decode_weights(out, w, q, k, v, table, L, longest, 0.125)
+    o, tol, ww, wt = expect(k, v, table, L, q, 8, 0.125, 1.0, 1.0, torch.zeros_like(w), 1.0, eps(torch.float16),
+                            eps(torch.float16))
+    check(out, o, tol, "out")
+    check(w, ww, wt, "weights")
+
+
+def test_past_four_gigabytes_and_weights_aligned_to_four_bytes():
+    bs, H, D = 16, 8, 128
+    nb = (1 << 32) // (bs * H * D * 2) + 50
+    k, v = (torch.zeros(nb, H, bs, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    blocks = [nb - 1, 3, nb - 40] + list(range(nb - 30, nb - 10))
+    table = i32([blocks])
+    g = gen(17)
+    k[table[0].long()], v[table[0].long()] = (randn(g, len(blocks), H, bs, D).bfloat16() for _ in range(2))
+    L, q = i32([len(blocks) * bs - 7]), randn(g, 1, 2 * H, D).bfloat16()
+    n = int(L)
+    buf = torch.rand(H * (n + 2) + 1, generator=g, device=DEV)
+    acc = buf[1:].view(1, H, n + 2)
+    win, out = acc.clone(), torch.empty_like(q)
+    pa.pa_decode_weights(out, acc, q, k, v, table, L, n, 0.09, weights_in=acc, decay=0.5)
+    o, tol, w, wt = expect(k, v, table, L, q, bs, 0.09, 1.0, 1.0, win, 0.5, eps(torch.bfloat16), eps(torch.bfloat16))
+    check(out, o, tol, "out")
+    check(acc[:, :, :n], w[:, :, :n], wt[:, :, :n], "weights")
+    assert torch.equal(acc[:, :, n:], win[:, :, n:])
+
+
+def test_two_streams_at_once():
+    cases = [make([1500, 40, 700], 16, 2, 128, 16, "bf16", "bf16", 18 + i) for i in range(2)]
+    streams, outs = [torch.cuda.Stream() for _ in cases], []
+    torch.cuda.synchronize()
+    for (k, v, table, L, q), st in zip(cases, streams):
+        with torch.cuda.stream(st):
+            w, out = torch.zeros(3, 2, 1500, device=DEV), torch.empty_like(q)
+            for _ in range(4):
+                pa.pa_decode_weights(out, w, q, k, v, table, L, 1500, 0.09)
+            outs.append((out, w))
+    torch.cuda.synchronize()
+    for (k, v, table, L, q), (out, w) in zip(cases, outs):
+        o, tol, ww, wt = expect(k, v, table, L, q, 16, 0.09, 1.0, 1.0, torch.zeros_like(w), 1.0, eps(torch.bfloat16),
+                                eps(torch.bfloat16))
+        check(out, o, tol)
+        for s, n in enumerate(L.tolist()):
+            check(w[s, :, :n], ww[s, :, :n], wt[s, :, :n])
