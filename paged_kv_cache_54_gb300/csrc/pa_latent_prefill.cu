@@ -390,8 +390,8 @@ constexpr int kQHalf = kRows * 128;
 constexpr int kQTile = kKHalves * kQHalf;
 constexpr int kQOff = 1024, kStageOff = kQOff + kTiles * kQTile;
 constexpr int kAttnSmem = kStageOff + kStages * kStageBytes;
-constexpr int kAttnThreads = 11 * 32;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kAttnThreads = 12 * 32;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kVTmaWarp = 11;
 constexpr uint32_t kTileCols = 256;             // TMEM columns of a tile: S 2 x 64, O 128
 constexpr float kLazy = 8.f;
 constexpr int kFineTokens = 512;
@@ -412,7 +412,7 @@ struct AttendParams {
 };
 
 struct AttendHeader {
-  uint64_t kv_full[kStages], kv_empty[kStages], s_full[kTiles][2], p_full[kTiles][2], pv_done[kTiles], o_ready[kTiles],
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], s_full[kTiles][2], p_full[kTiles][2], pv_done[kTiles], o_ready[kTiles],
       q_full, fin[kTiles];
   uint32_t tmem;
   int abort;
@@ -492,8 +492,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
   volatile int *abort = &hdr.abort;
   if (warp == kTmaWarp && lane == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&hdr.kv_full[i], 1);
-      mbar_init(&hdr.kv_empty[i], tiles);
+      mbar_init(&hdr.k_full[i], 1);
+      mbar_init(&hdr.k_empty[i], tiles);
+      mbar_init(&hdr.v_full[i], 1);
+      mbar_init(&hdr.v_empty[i], tiles);
     }
     for (int t = 0; t < kTiles; ++t) {
       mbar_init(&hdr.s_full[t][0], 1);
@@ -696,36 +698,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
         *abort = 1;
       }
     }
-  } else if (warp == kTmaWarp) {
+  } else if (warp == kTmaWarp || warp == kVTmaWarp) {
     // ---------------------------------------------------------------- TMA
+    // keys by one warp, values by the other: a stage's keys are done with
+    // before its softmax, its values long after
     if (lane == 0) {
+      const bool is_k = warp == kTmaWarp;
+      uint64_t *full = is_k ? hdr.k_full : hdr.v_full, *empty = is_k ? hdr.k_empty : hdr.v_empty;
       bool ok = true;
       int issued = 0;
       const int kvrow = static_cast<int>(h * p.capacity + row0), rrow = static_cast<int>(row0);
       for (int i = 0; i < n_stages; ++i) {
         const int st = i % kStages;
-        if (i >= kStages && !mbar_wait(&hdr.kv_empty[st], (i / kStages - 1) & 1, abort)) {
+        if (i >= kStages && !mbar_wait(&empty[st], (i / kStages - 1) & 1, abort)) {
           ok = false;
           break;
         }
-        uint8_t *kb = stages + st * kStageBytes;
-        mbar_arrive_expect_tx(&hdr.kv_full[st], kStageBytes);
+        uint8_t *to = stages + st * kStageBytes;
+        if (is_k) {
+          mbar_arrive_expect_tx(&full[st], kKHalves * kHalf);
 #pragma unroll
-        for (int c = 0; c < kNope / 64; ++c)
-          tma_load_2d(kb + c * kHalf, &p.tmap_kv, c * 64, kvrow + i * kKeys, &hdr.kv_full[st]);
-        tma_load_2d(kb + (kNope / 64) * kHalf, &p.tmap_rope, 0, rrow + i * kKeys, &hdr.kv_full[st]);
+          for (int c = 0; c < kNope / 64; ++c)
+            tma_load_2d(to + c * kHalf, &p.tmap_kv, c * 64, kvrow + i * kKeys, &full[st]);
+          tma_load_2d(to + (kNope / 64) * kHalf, &p.tmap_rope, 0, rrow + i * kKeys, &full[st]);
+        } else {
+          mbar_arrive_expect_tx(&full[st], kVHalves * kHalf);
 #pragma unroll
-        for (int c = 0; c < kVHalves; ++c)
-          tma_load_2d(kb + (kKHalves + c) * kHalf, &p.tmap_kv, kNope + c * 64, kvrow + i * kKeys, &hdr.kv_full[st]);
+          for (int c = 0; c < kVHalves; ++c)
+            tma_load_2d(to + (kKHalves + c) * kHalf, &p.tmap_kv, kNope + c * 64, kvrow + i * kKeys, &full[st]);
+        }
         issued = i + 1;
       }
       if (!ok) {
         record_error(p.err, kErrTimeout);
         *abort = 1;
         for (int j = max(0, issued - kStages); j < issued; ++j)
-          mbar_wait(&hdr.kv_full[j % kStages], (j / kStages) & 1, nullptr);
+          mbar_wait(&full[j % kStages], (j / kStages) & 1, nullptr);
       }
-      mbar_wait(&hdr.q_full, 0, nullptr);
+      if (is_k) mbar_wait(&hdr.q_full, 0, nullptr);
     }
   } else {
     // ---------------------------------------------------------------- MMA
@@ -735,7 +745,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
       const uint32_t qt = smem_addr(qs) + t * kQTile, sa = smem_addr(stages), tt = tmem + t * kTileCols;
       auto issue_qk = [&](int i) -> bool {
         const int st = i % kStages;
-        if (!mbar_wait(&hdr.kv_full[st], (i / kStages) & 1, abort)) return false;
+        if (!mbar_wait(&hdr.k_full[st], (i / kStages) & 1, abort)) return false;
         tc_fence_after_sync();
         const uint64_t a0 = umma_desc_sw128(qt, 16, 1024), b0 = umma_desc_sw128(sa + st * kStageBytes, 16, 1024);
         const uint32_t d = tt + (i & 1) * kKeys;
@@ -745,6 +755,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
           tc_mma_f16(d, a0 + (((kk / 4) * kQHalf + off) >> 4), b0 + (((kk / 4) * kHalf + off) >> 4), IDESC_QK, kk > 0);
         }
         tc_commit(&hdr.s_full[t][i & 1]);
+        tc_commit(&hdr.k_empty[st]);
         return true;
       };
       const int nst = tile_stages(t);
@@ -754,7 +765,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
           ok = false;
           break;
         }
-        if (!mbar_wait(&hdr.p_full[t][i & 1], (i >> 1) & 1, abort)) {
+        if (!mbar_wait(&hdr.v_full[i % kStages], (i / kStages) & 1, abort) ||
+            !mbar_wait(&hdr.p_full[t][i & 1], (i >> 1) & 1, abort)) {
           ok = false;
           break;
         }
@@ -770,15 +782,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
             tc_mma_f16_ta(tt + 2 * kKeys, tt + (i & 1) * kKeys + kKeys / 2 + kk * 8, b0 + kk * (2 * 1024 >> 4), IDESC_PV, 1u);
         tc_commit(&hdr.pv_done[t]);
         if (i + 1 == nst) tc_commit(&hdr.o_ready[t]);
-        tc_commit(&hdr.kv_empty[i % kStages]);
+        tc_commit(&hdr.v_empty[i % kStages]);
       }
       // stages behind this tile's rows: released once filled
       for (int i = nst; i < n_stages && ok; ++i) {
-        if (!mbar_wait(&hdr.kv_full[i % kStages], (i / kStages) & 1, abort)) {
+        if (!mbar_wait(&hdr.k_full[i % kStages], (i / kStages) & 1, abort) ||
+            !mbar_wait(&hdr.v_full[i % kStages], (i / kStages) & 1, abort)) {
           ok = false;
           break;
         }
-        tc_commit(&hdr.kv_empty[i % kStages]);
+        tc_commit(&hdr.k_empty[i % kStages]);
+        tc_commit(&hdr.v_empty[i % kStages]);
       }
       if (!ok) {
         record_error(p.err, kErrTimeout);
