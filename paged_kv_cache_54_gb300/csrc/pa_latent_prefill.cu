@@ -27,20 +27,24 @@
 // sequence, as two tiles of 128, the M of the products:
 //   S = Q K^T   N = 64 keys of a stage, K = 192  (S in TMEM, two buffers)
 //   O += P V    N = 128, K = 64                  (P over S, O in TMEM)
-// Warps 0..7 softmax (a warpgroup a tile, a thread a row), 8 TMA, 9 and 10
-// issue the products, one a tile.  The running maximum is raised, and O
-// rescaled, only when it grew by more than 2^8.  Sums and maxima are fp32; P
-// is rounded to fp16, K and V were when they were expanded (half a step each).
+// Warps 0..7 softmax (a warpgroup a tile, a thread a row), 8 and 11 load keys
+// and values, 9 and 10 issue the products, one a tile.  Keys and values have
+// rings of their own: a stage's keys are free before its softmax, and a load
+// into a freed place takes about 1500 clocks (one ring: 684 and 138 us for the
+// two cases below).  The running maximum is raised, and O rescaled, only when
+// it grew by more than 2^8.  Sums and maxima are fp32; P is rounded to fp16, K
+// and V were when they were expanded (half a step each).
 // Bound by shared memory, not by the tensor cores: a product's operands come
 // from it at 128 bytes a clock, 6 KB for the 32 clocks of one of S, and with
-// the stages' arrival that is 1664 clocks a stage of both tiles of the 1720
-// it takes (1280 of products).  4095 tokens after 4096, 64 heads: 81 us for the
-// expansion, 684 for the attention; 32 sequences of 16..512 after 1024, 16
-// heads: 105 and 138 (five waves of blocks of about 20 stages, whose first and
-// last microseconds and half-empty tiles count).  Tried: stages of 128 keys
-// with one S buffer a tile (733 us for the 684: the softmax is then in the
-// chain), a third of q in tensor memory (747), blocks that go on to the next
-// range (697).
+// the stages' arrival that makes about 1660 clocks a stage of both tiles, where
+// 1620 are measured and the products alone take 1280.  4095 tokens after 4096,
+// 64 heads: 81 us for the expansion, 661 for the attention; 32 sequences of
+// 16..512 after 1024, 16 heads: 106 and 126 (768 blocks of about 20 us, five
+// rounds of the SMs and a few of a sixth).  Tried: stages of 128 keys with one S
+// buffer a tile (733 us for the 684: the softmax is then in the chain), a third
+// of q in tensor memory (747), blocks that go on to the next range (697),
+// stages fetched into L2 ahead (even), loads before the block's first barrier
+// (even).
 // With an fp16 cache P's rounding would show beside the output's where a row
 // follows few tokens, so sequences of up to 512 tokens take P as two fp16
 // parts.
