@@ -595,19 +595,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kMergeWarps = 16;
 
 // Where a row's pieces lie: n of them, or none where it was written whole.
+// The tiles ahead of the sequence come from the lengths where those are few:
+// before the wait for the decode kernel, under whose end that stays unseen.
+constexpr int kOwnSum = 1024;
+
 template <int N>
 struct Pieces {
   int n, late;
   size_t base;
   bool empty;
+  // (all threads of the warps that call it, with one s a warp)
   __device__ __forceinline__ Pieces(const LatentParams &p, int max_workers, int s) {
-    const long long u0 = p.prefix[s], u1 = p.prefix[s + 1], total = p.prefix[p.num_seqs];
+    long long u0 = 0, mine = 0, total = 0;
+    if (p.num_seqs <= kOwnSum) {
+      constexpr int TILE = N == kPairRows ? 128 : kTile;
+      for (int i = threadIdx.x & 31; i < p.num_seqs; i += 32) {
+        const int tiles = (checked_len(p.lens, i, p.limit, nullptr) + TILE - 1) / TILE;
+        total += tiles;
+        u0 += i < s ? tiles : 0;
+        mine += i == s ? tiles : 0;
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, d);
+        u0 += __shfl_xor_sync(0xffffffffu, u0, d);
+        mine += __shfl_xor_sync(0xffffffffu, mine, d);
+      }
+    } else {
+      grid_dependency_wait();
+      u0 = p.prefix[s];
+      mine = p.prefix[s + 1] - u0;
+      total = p.prefix[p.num_seqs];
+    }
     n = late = 0;
     base = 0;
-    empty = u1 == u0;
+    empty = mine == 0;
     if (empty) return;
     const long long workers = worker_count(total, max_workers);
-    const long long w0 = share_owner(u0, total, workers), w1 = share_owner(u1 - 1, total, workers);
+    const long long w0 = share_owner(u0, total, workers), w1 = share_owner(u0 + mine - 1, total, workers);
     if (w0 == w1) return;
     n = static_cast<int>(w1 - w0) + 1;
     // a block's first piece is in its place 0; the sequence is not the first of its first block if that began earlier
@@ -621,47 +646,80 @@ struct Pieces {
   }
 };
 
+// A lane's VEC fours of dimensions of a row's pieces i, i + step, ...: their
+// sum o, its total weight l, both times 2^-top (the lane's fours are 128
+// dimensions apart, the first is d0 + 4 lane).  U pieces are on their way at
+// a time.
+template <int VEC, int U>
+struct RowSum {
+  float4 o[VEC];
+  float l, top;
+  template <int N>
+  __device__ __forceinline__ void add(const LatentParams &p, const Pieces<N> &pieces, int max_workers, int r, int d0,
+                                      int i, int step) {
+    l = 0.f;
+    top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (; i < pieces.n; i += U * step) {
+      float2 ml[U];
+      float4 x[U][VEC];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[u][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + u * step < pieces.n) {
+          const size_t at = pieces.at(i + u * step, r, max_workers);
+          ml[u] = p.part_ml[at];
+          const float4 *from = reinterpret_cast<const float4 *>(p.part_o + at * kLatentDim + d0) + (threadIdx.x & 31);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) x[u][e] = from[32 * e];
+        }
+      }
+      const float was = top;
+#pragma unroll
+      for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
+      const float base = top == -INFINITY ? 0.f : top, f = exp2_fast(was - base);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] = make_float4(o[e].x * f, o[e].y * f, o[e].z * f, o[e].w * f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float g = exp2_fast(ml[u].x - base);
+        l += g * ml[u].y;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          o[e].x += g * x[u][e].x;
+          o[e].y += g * x[u][e].y;
+          o[e].z += g * x[u][e].z;
+          o[e].w += g * x[u][e].w;
+        }
+      }
+    }
+  }
+};
+
 // A block joins rows [r0, r0 + per) of a sequence, a warp every 16th, a lane
 // 16 of the dimensions.
 template <int DT, int N>
 __global__ void __launch_bounds__(kMergeWarps * 32, 2) latent_merge_many(const LatentParams p, int max_workers, int per) {
-  grid_dependency_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int chunks = (p.rows + per - 1) / per, s = blockIdx.x / chunks, r0 = blockIdx.x % chunks * per;
   const Pieces<N> pieces(p, max_workers, s);
+  grid_dependency_wait();
   if (pieces.n == 0 && !pieces.empty) return;
   for (int r = r0 + warp; r < min(p.rows, r0 + per); r += kMergeWarps) {
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < pieces.n; i += 32) m = fmaxf(m, p.part_ml[pieces.at(i, r, max_workers)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (m == -INFINITY) m = 0.f;
-    float4 o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int i = 0; i < pieces.n; ++i) {
-      const size_t at = pieces.at(i, r, max_workers);
-      const float2 ml = p.part_ml[at];
-      const float4 *x = reinterpret_cast<const float4 *>(p.part_o + at * kLatentDim) + lane;
-      const float f = exp2_fast(ml.x - m);
-      l += f * ml.y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 y = x[32 * e];
-        o[e].x += f * y.x;
-        o[e].y += f * y.y;
-        o[e].z += f * y.z;
-        o[e].w += f * y.w;
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    RowSum<4, 2> sum;
+    sum.add(p, pieces, max_workers, r, 0, 0, 1);
+    const float l = sum.l, inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t *out = static_cast<uint16_t *>(p.out) + (static_cast<size_t>(s) * p.rows + r) * kLatentDim + lane * 4;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       *reinterpret_cast<uint2 *>(out + 128 * e) =
           l == 0.f ? make_uint2(0u, 0u)
-                   : make_uint2(pack2_rn<DT>(o[e].x * inv, o[e].y * inv), pack2_rn<DT>(o[e].z * inv, o[e].w * inv));
+                   : make_uint2(pack2_rn<DT>(sum.o[e].x * inv, sum.o[e].y * inv),
+                                pack2_rn<DT>(sum.o[e].z * inv, sum.o[e].w * inv));
   }
 }
 
@@ -671,52 +729,35 @@ template <int DT, int N, int TEAM, int DSPLIT>
 __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_few(const LatentParams p, int max_workers) {
   constexpr int DIMS = kLatentDim / DSPLIT, VEC = DIMS / 128;  // of a block, and the lane's fours of them
   __shared__ float part[kMergeWarps][DIMS];
-  __shared__ float sums[kMergeWarps];
-  grid_dependency_wait();
+  __shared__ float sums[kMergeWarps], tops[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mate = warp % TEAM;
   const int row = blockIdx.x / DSPLIT * (kMergeWarps / TEAM) + warp / TEAM, d0 = blockIdx.x % DSPLIT * DIMS;
-  bool joins = false;
-  float4 o[VEC];
-  float l = 0.f;
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (row < p.num_seqs * p.rows) {
-    const int r = row % p.rows;
-    const Pieces<N> pieces(p, max_workers, row / p.rows);
-    joins = pieces.n > 0 || pieces.empty;
-    float m = -INFINITY;
-    for (int i = lane; i < pieces.n; i += 32) m = fmaxf(m, p.part_ml[pieces.at(i, r, max_workers)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (m == -INFINITY) m = 0.f;
-#pragma unroll 8
-    for (int i = mate; i < pieces.n; i += TEAM) {
-      const size_t at = pieces.at(i, r, max_workers);
-      const float2 ml = p.part_ml[at];
-      const float4 *x = reinterpret_cast<const float4 *>(p.part_o + at * kLatentDim + d0) + lane;
-      const float f = exp2_fast(ml.x - m);
-      l += f * ml.y;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float4 y = x[32 * e];
-        o[e].x += f * y.x;
-        o[e].y += f * y.y;
-        o[e].z += f * y.z;
-        o[e].w += f * y.w;
-      }
-    }
-  }
+  const bool exists = row < p.num_seqs * p.rows;
+  const Pieces<N> pieces(p, max_workers, exists ? row / p.rows : 0);
+  grid_dependency_wait();
+  const bool joins = exists && (pieces.n > 0 || pieces.empty);
+  RowSum<VEC, VEC == 1 ? 10 : 3> sum;
+  sum.add(p, pieces, max_workers, row % p.rows, d0, joins ? mate : pieces.n, TEAM);
   float4 *mine = reinterpret_cast<float4 *>(part[warp]) + lane;
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) mine[32 * e] = o[e];
-  if (lane == 0) sums[warp] = l;
+  for (int e = 0; e < VEC; ++e) mine[32 * e] = sum.o[e];
+  if (lane == 0) {
+    sums[warp] = sum.l;
+    tops[warp] = sum.top;
+  }
   __syncthreads();
   // the team's warps each join a share of the dimensions
   if (!joins) return;
   const int first = warp - mate;
-  l = 0.f;
+  float top = -INFINITY, l = 0.f, f[TEAM];
 #pragma unroll
-  for (int i = 0; i < TEAM; ++i) l += sums[first + i];
+  for (int i = 0; i < TEAM; ++i) top = fmaxf(top, tops[first + i]);
+  if (top == -INFINITY) top = 0.f;
+#pragma unroll
+  for (int i = 0; i < TEAM; ++i) {
+    f[i] = exp2_fast(tops[first + i] - top);
+    l += f[i] * sums[first + i];
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   constexpr int OWN = DIMS / TEAM / 2;  // pairs of dimensions of a warp
   for (int d = lane; d < OWN; d += 32) {
@@ -725,8 +766,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_few(const Laten
 #pragma unroll
     for (int i = 0; i < TEAM; ++i) {
       const float2 z = *reinterpret_cast<const float2 *>(&part[first + i][at]);
-      x += z.x;
-      y += z.y;
+      x += f[i] * z.x;
+      y += f[i] * z.y;
     }
     *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + static_cast<size_t>(row) * kLatentDim + d0 + at) =
         l == 0.f ? 0u : pack2_rn<DT>(x * inv, y * inv);

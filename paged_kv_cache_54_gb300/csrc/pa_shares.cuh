@@ -10,12 +10,20 @@
 
 namespace pa {
 
+// a / b of numbers that mostly fit 32 bits (a 64-bit division is a chain of
+// about 100 instructions, and several lie ahead of a join's first loads).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  const unsigned long long x = static_cast<unsigned long long>(a), y = static_cast<unsigned long long>(b);
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return static_cast<long long>(x / y);
+}
+
 // First unit of worker w, and the worker that owns unit u.
 __device__ __forceinline__ long long share_begin(long long w, long long units, long long workers) {
-  return w * units / workers;
+  return quotient(w * units, workers);
 }
 __device__ __forceinline__ long long share_owner(long long u, long long units, long long workers) {
-  return ((u + 1) * workers - 1) / units;
+  return quotient((u + 1) * workers - 1, units);
 }
 
 // A length as the kernels use it: one outside [0, limit] counts as zero.
