@@ -19,9 +19,11 @@
 //
 // A block takes N query rows and an equal share of all sequences'
 // 64-token tiles (pa_shares.cuh).  One sequence of 131071 tokens, 32 query
-// rows: 151 MB, 22.6 us at the measured copy rate; this kernel takes 36 (the
-// loop keeps up with the memory, 5 us pass until the first tiles land, 5 from
-// the last one to the stored sums), the join of 152 pieces a row 10.  Warps:
+// rows: 151 MB, 22.6 us at the measured copy rate; this kernel takes 35 (the
+// loop keeps up with the memory, 5 us pass until the first tiles land, 3 to 5
+// from the last one to the stored sums), the join of 152 pieces a row 6 (10
+// when it looked the pieces up after its wait, and read their maxima first).
+// Warps:
 //   0..7  softmax: a thread owns a token and a quarter of the query rows.  The
 //         maximum of a query row is kept for all threads in shared memory and
 //         raised only when a score passes it by 2^8, so that almost every
@@ -655,10 +657,9 @@ struct RowSum {
   float4 o[VEC];
   float l, top;
   template <int N>
-  __device__ __forceinline__ void add(const LatentParams &p, const Pieces<N> &pieces, int max_workers, int r, int d0,
-                                      int i, int step) {
-    l = 0.f;
-    top = -INFINITY;
+  __device__ __forceinline__ RowSum(const LatentParams &p, const Pieces<N> &pieces, int max_workers, int r, int d0,
+                                    int i, int step)
+      : l(0.f), top(-INFINITY) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (; i < pieces.n; i += U * step) {
@@ -710,8 +711,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) latent_merge_many(const L
   grid_dependency_wait();
   if (pieces.n == 0 && !pieces.empty) return;
   for (int r = r0 + warp; r < min(p.rows, r0 + per); r += kMergeWarps) {
-    RowSum<4, 2> sum;
-    sum.add(p, pieces, max_workers, r, 0, 0, 1);
+    const RowSum<4, 2> sum(p, pieces, max_workers, r, 0, 0, 1);
     const float l = sum.l, inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t *out = static_cast<uint16_t *>(p.out) + (static_cast<size_t>(s) * p.rows + r) * kLatentDim + lane * 4;
 #pragma unroll
@@ -736,8 +736,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_few(const Laten
   const Pieces<N> pieces(p, max_workers, exists ? row / p.rows : 0);
   grid_dependency_wait();
   const bool joins = exists && (pieces.n > 0 || pieces.empty);
-  RowSum<VEC, VEC == 1 ? 10 : 3> sum;
-  sum.add(p, pieces, max_workers, row % p.rows, d0, joins ? mate : pieces.n, TEAM);
+  const RowSum<VEC, VEC == 1 ? 10 : 3> sum(p, pieces, max_workers, row % p.rows, d0, joins ? mate : pieces.n, TEAM);
   float4 *mine = reinterpret_cast<float4 *>(part[warp]) + lane;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) mine[32 * e] = sum.o[e];

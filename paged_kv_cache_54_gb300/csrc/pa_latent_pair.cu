@@ -15,7 +15,7 @@
 // of it 3200; it takes about 4000: the 278 KB of K and V that a pair draws from
 // L2 for it, and the chain from S through the weights to O.  (pa_latent_decode.cu
 // with two blocks of 64 rows a tile took 3500 clocks for 64 tokens.)  128
-// sequences of 512..4096 tokens with 128 heads: 85 us, and 11 more for the join
+// sequences of 512..4096 tokens with 128 heads: 85 us, and 10 more for the join
 // of the pieces; 375 MB, 56 us at the measured copy rate.
 //
 // Tensor memory of a block: row r of its 64 in lanes r and r + 64, the first

@@ -258,6 +258,16 @@ def test_decode_captured_and_replayed_on_another_stream():
     check(out, want, tol)
 
 
+@pytest.mark.parametrize("heads", [2, 16, 80])
+def test_decode_of_more_than_a_thousand_sequences(heads):
+    lens = [(s * 29) % 130 if s % 5 else 0 for s in range(1100)]
+    lens[3], lens[700], lens[1099] = 9000, 5000, 7000     # in many pieces
+    cache, table, L, q = make(lens, 1, heads, 8, "bf16", 57)
+    got = run(cache, table, L, q, SCALE)
+    want, tol = expect(cache, table, L, q, 8, SCALE, eps(torch.bfloat16))
+    check(got, want, tol)
+
+
 @pytest.mark.parametrize("heads,new", [(16, 1), (40, 1), (72, 2)])
 def test_decode_of_short_sequences_some_of_them_empty(heads, new):
     lens = [0, 40, 0, 256, 1, 0, 64]     # none is split
