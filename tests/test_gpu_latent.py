@@ -361,6 +361,21 @@ def test_prefill_matches_the_definition(lens, new, heads, bs, dt):
     check(got, want, tol)
 
 
+@pytest.mark.parametrize("seqs", [127, 128, 129, 300])
+def test_prefill_and_decode_of_many_short_sequences(seqs):
+    lens = [(s * 31) % 150 if s % 4 else 0 for s in range(seqs)]
+    lens[-1] = 300
+    new = [min(n, s % 5) for s, n in enumerate(lens)]
+    cache, table, L, q, up, cu = make_prefill(lens, new, 2, 16, "f16", 59)
+    got = run_prefill(cache, table, L, q, up, cu, SCALE, max(new), sum(lens))
+    want, tol = expect_prefill(cache, table, L, q, up, cu, 16, SCALE, eps(torch.float16))
+    check(got, want, tol)
+    for heads in (3, 70):
+        cache, table, L, q = make(lens, 1, heads, 16, "f16", 60)
+        want, tol = expect(cache, table, L, q, 16, SCALE, eps(torch.float16))
+        check(run(cache, table, L, q, SCALE), want, tol)
+
+
 @pytest.mark.parametrize("factor", [0.0, -2.0, 30.0])
 def test_prefill_scales(factor):
     cache, table, L, q, up, cu = make_prefill([700, 64], [300, 64], 2, 16, "f16", 51)

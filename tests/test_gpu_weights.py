@@ -214,3 +214,16 @@ def test_two_streams_at_once():
         check(out, o, tol)
         for s, n in enumerate(L.tolist()):
             check(w[s, :, :n], ww[s, :, :n], wt[s, :, :n])
+
+
+@pytest.mark.parametrize("seqs", [127, 128, 129])
+def test_around_the_sequences_a_warp_adds_up(seqs):
+    lens = [(s * 31) % 150 if s % 4 else 0 for s in range(seqs)]
+    lens[-1] = 900
+    k, v, table, L, q = make(lens, 4, 2, 64, 16, "bf16", "bf16", 19)
+    w, out = torch.full((seqs, 2, 900), -1.0, device=DEV), torch.full_like(q, float("nan"))
+    pa.pa_decode_weights(out, w, q, k, v, table, L, 900, 0.125)
+    o, tol, ww, wt = expect(k, v, table, L, q, 16, 0.125, 1.0, 1.0, torch.zeros_like(w), 1.0, eps(torch.bfloat16),
+                            eps(torch.bfloat16))
+    check(out, o, tol, "out")
+    check(w, ww, wt, "weights")
