@@ -458,7 +458,8 @@ PA_API pa_status pa_swap_blocks(void *k_cache, void *v_cache, const pa_cache_des
  *   decay          what the earlier weights are multiplied by (1 keeps them).
  *   workspace      at least pa_decode_weights_workspace_size(...) bytes,
  *                  256-byte aligned, uninitialised; calls sharing one must be
- *                  stream-ordered.
+ *                  stream-ordered.  Most of it are the scores: 4 bytes a
+ *                  sequence, query head and token up to max_seq_len.
  * A sequence without tokens gives zeros, and so does a row none of whose
  * scores is above -infinity (its weights are zero too).
  * Supported set: num_q_heads / kv_heads in {1, 2, 4, 8}; 16-bit, FP8 and INT8
