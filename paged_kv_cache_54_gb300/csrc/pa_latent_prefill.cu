@@ -21,7 +21,7 @@
 // token, (key 128, value 128)] and the tokens' rotary keys go to the workspace,
 // sequences padded to 128 tokens with zeros.  Keys are rounded to the cache's
 // type; values always to fp16, whose step is an eighth of bf16's, times a power
-// of two for every 32 tokens of a head where they would leave its range.
+// of two for every 32 tokens of a head where fp16 would not hold them well.
 //
 // Second kernel (attend): a block is one head and 256 new tokens of a
 // sequence, as two tiles of 128, the M of the products:
@@ -87,7 +87,7 @@ struct ExpandParams {
   const int32_t *tables, *lens;
   uint8_t *kv;          // [H, capacity, 256]
   uint8_t *rope;        // [capacity, 64]
-  int32_t *powers;      // [H, capacity / 32]: values are these powers of two times what is stored
+  int32_t *powers;      // [H, capacity / 32]: values are these powers of two times what is stored (kNoValues: zeros)
   long long *prefix;    // [S + 1] token tiles before sequence s
   int num_seqs, heads, num_blocks, bs_shift, max_blocks, limit;
   long long capacity;   // tokens
@@ -110,10 +110,22 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[16], i
 }
 
 // The power of two e for which values of largest magnitude `top` are stored
-// as x 2^-e: 0 where fp16 holds them well.
+// as x 2^-e: 0 where fp16 holds them well, from 2^-4 to 2^15 (a step of fp16's
+// smallest numbers is then 2^-20 of the largest or less); outside, the multiple
+// of four that brings the largest to the near end of that range.  A row's
+// weights are scaled by the distance of a group's power from the largest of
+// those it follows, and lose bits where that is far: groups of nearly the same
+// size have to have nearly the same power, on both sides of the range's ends.
+// (Values just below 2^-4 taken to 2^14 would cost their weights 18 bits beside
+// a group just above: outputs off by 4 to 9 % at 4096 tokens.)  Multiples of
+// four because differing powers cost a second rounding of a stage's weights.
+// Groups of zeros take no part.
+constexpr int kNoValues = -1024;
 __device__ __forceinline__ int value_power(float top) {
+  if (top == 0.f) return kNoValues;
   if (!(top > 0.f && top < INFINITY) || (top >= 0x1p-4f && top <= 0x1p15f)) return 0;
-  return min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100), 127) - 13;
+  const int lg = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -126);
+  return (top < 1.f ? lg + 4 : lg - 11) & ~3;  // to [2^-4, 1) or [2^11, 2^15)
 }
 
 template <int DT>
@@ -267,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1)
         const int e = value_power(__uint_as_float(__reduce_max_sync(0xffffffffu, real ? __float_as_uint(top) : 0u)));
         if (fits && lane == 0)
           p.powers[static_cast<size_t>(h) * (p.capacity / kExGroup32) + r.row / kExGroup32 + warp] = e;
-        const float f = e == 0 ? 1.f : exp2f(static_cast<float>(-e));
+        const float f = e == 0 || e == kNoValues ? 1.f : exp2f(static_cast<float>(-e));
 #pragma unroll
         for (int c = 0; c < kValue; c += 32) {
           uint32_t w[16];
@@ -666,7 +678,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
         tc_fence_after_sync();
         // O / l through this tile's q buffer, whose products have all
         // completed, so that whole rows leave
-        const float inv = l == 0.f ? 0.f : exp2f(static_cast<float>(unit)) / l;
+        // (two factors: 2^unit / l may leave a float's range)
+        const float inv = l == 0.f ? 0.f : 1.f / l, power_of_two = exp2f(static_cast<float>(unit));
         constexpr int RB = kValue * 2, CPR = RB / 16;
         uint8_t *stg = qs + t * kQTile;
 #pragma unroll
@@ -678,8 +691,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] = l == 0.f ? 0u : pack2_rn<DT>(__uint_as_float(ov[j + 2 * e]) * inv,
-                                                  __uint_as_float(ov[j + 2 * e + 1]) * inv);
+              w[e] = l == 0.f ? 0u : pack2_rn<DT>(__uint_as_float(ov[j + 2 * e]) * inv * power_of_two,
+                                                  __uint_as_float(ov[j + 2 * e + 1]) * inv * power_of_two);
             *reinterpret_cast<uint4 *>(stg + r * RB + ((((d + j) / 8) ^ (r & 7)) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
