@@ -26,7 +26,8 @@
 // Warps:
 //   0..7  softmax: a thread owns a token and a quarter of the query rows.  The
 //         maximum of a query row is kept for all threads in shared memory and
-//         raised only when a score passes it by 2^8, so that almost every
+//         raised only when a score passes it by 2^8 (the largest weight is then
+//         1 to 2^8, times 2^7 with fp16 operands), so that almost every
 //         tile needs one vote of the block instead of a reduction over
 //         tokens; the total weights stay per thread until a sequence ends.
 //   8     TMA: q, then the tiles, a 16-token slot at a time
@@ -72,7 +73,7 @@ struct Header {
   uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, q_empty, fin[2];
   uint32_t tmem;
   int abort;
-  alignas(16) float m[64];  // what the query rows' scores are raised by: minus their maxima (base 2)
+  alignas(16) float m[64];  // what the query rows' scores are raised by: kLift minus their maxima (base 2)
   float top[4][64];         // maxima of 16 tokens, then their total weights
   int see[64];              // tokens a query row sees
 };
@@ -256,10 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       return fmaxf(fmaxf(hdr.top[0][h], hdr.top[1][h]), fmaxf(hdr.top[2][h], hdr.top[3][h]));
     };
     auto sum_of = [&](int h) { return (hdr.top[0][h] + hdr.top[1][h]) + (hdr.top[2][h] + hdr.top[3][h]); };
-    // a row's new maximum, given what its scores were raised by, and the factor of its sums
-    auto raised = [&](float was, float top) { return was == kNone ? top > -INFINITY : top > -was + kLazy; };
+    // whether a row's maximum is raised, given what its scores were raised by, and the factor of its sums (differences,
+    // which are exact where the numbers are close)
+    constexpr float OVER = kLazy + kLift<DT>;
+    auto raised = [&](float was, float top) { return was == kNone ? top > -INFINITY : top + was > OVER; };
     auto factor = [&](float was, float top) {
-      return !raised(was, top) ? 1.f : was == kNone ? 0.f : exp2_fast(-was - top);
+      return !raised(was, top) ? 1.f : was == kNone ? 0.f : exp2_fast((kLift<DT> - top) - was);
     };
     const float4 *m4 = reinterpret_cast<const float4 *>(hdr.m + c0);
     int i = 0;  // tiles so far
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           y[j + 3] = x[j + 3] + m.w;
           over = fmaxf(over, fmaxf(fmaxf(y[j], y[j + 1]), fmaxf(y[j + 2], y[j + 3])));
         }
-        if (softmax_any(over > kLazy)) {
+        if (softmax_any(over > OVER)) {
           // raise the maxima: over each warp's 16 tokens, then all four
 #pragma unroll
           for (int j = 0; j < NQ; ++j) {
@@ -327,13 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           softmax_sync();
           if (threadIdx.x < N) {
             const float top = top_of(threadIdx.x);
-            if (raised(hdr.m[threadIdx.x], top)) hdr.m[threadIdx.x] = -top;
+            if (raised(hdr.m[threadIdx.x], top)) hdr.m[threadIdx.x] = kLift<DT> - top;
           }
           softmax_sync();
 #pragma unroll
           for (int j = 0; j < NQ; ++j) y[j] = x[j] + hdr.m[c0 + j];
         }
-        // weights, rounded to the operand type (half a step each)
+        // weights, rounded to the operand type (half a step each; see kLift)
         uint32_t pw[NQ / 2];
 #pragma unroll
         for (int j = 0; j < NQ; j += 2) {

@@ -10,6 +10,13 @@ namespace pa {
 
 constexpr int kMinTiles = 2;     // a share of fewer tiles only adds joining
 constexpr float kLazy = 8.f;     // a row's maximum is raised when a score passes it by more (base 2)
+// The largest weight of a row is held as 2^kLift or more: fp16's smallest step
+// is 2^-24, so that a weight is off by at most 2^-32 of the largest where it
+// would be lost below 2^-25, and the total keeps all of it (131071 tokens 17
+// nats below one are 0.4 % of it).  2^(kLazy + kLift) is well inside fp16.
+// bf16 has a float's range and needs none of it.
+template <int DT>
+constexpr float kLift = DT == kF16 ? 7.f : 0.f;
 constexpr int kSoftmaxThreads = 256;
 // Sequences of up to this many tokens are not split: their few tiles take less
 // than a second kernel (four sequences of 1..100 tokens, 16 heads: 10.4 us in

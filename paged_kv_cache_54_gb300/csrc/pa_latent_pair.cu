@@ -163,7 +163,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int seg = 0; walk.next(p); ++seg) {
       const int see = row < p.rows ? walk.L - (p.new_tokens - 1 - row / p.heads) : 0;  // tokens the row sees
       const int all_see = (rt + 1) * kPairRows > p.rows ? 0 : walk.L - (p.new_tokens - 1 - rt * kPairRows / p.heads);
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;  // m: the maximum less kLift
+      constexpr float OVER = kLazy + kLift<DT>;
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         wait(&hdr.s_full[i & 1], (i >> 1) & 1);
         uint32_t raw[32];
@@ -182,14 +183,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < 32; j += 4) top = fmaxf(top, fmaxf(fmaxf(x[j], x[j + 1]), fmaxf(x[j + 2], x[j + 3])));
-        if (softmax_any(top > m + kLazy)) {
+        if (softmax_any(top - m > OVER)) {  // (a difference: exact where the two are close)
           hdr.top[q4][r] = top;
           softmax_sync();
           top = fmaxf(fmaxf(hdr.top[0][r], hdr.top[1][r]), fmaxf(hdr.top[2][r], hdr.top[3][r]));
-          const bool grow = top > m + kLazy;
-          const float f = grow ? exp2_fast(m - top) : 1.f;
+          const bool grow = top - m > OVER;
+          const float next = top - kLift<DT>, f = grow ? exp2_fast(m - next) : 1.f;
           l *= f;
-          if (grow) m = top;
+          if (grow) m = next;
           if (tile > walk.t0) {  // O holds the tiles before
             wait(&hdr.pv_done, (i - 1) & 1);
 #pragma unroll 1
@@ -203,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           softmax_sync();  // the maxima have been read
         }
-        // weights, rounded to the operand type (half a step each)
+        // weights, rounded to the operand type (half a step each; see kLift)
         const float base = m == -INFINITY ? 0.f : m;
         uint32_t pw[16];
         float sum[4] = {0.f, 0.f, 0.f, 0.f};

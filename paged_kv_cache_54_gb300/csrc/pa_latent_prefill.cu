@@ -32,8 +32,8 @@
 // rings of their own: a stage's keys are free before its softmax, and a load
 // into a freed place takes about 1500 clocks (one ring: 684 and 138 us for the
 // two cases below).  The running maximum is raised, and O rescaled, only when
-// it grew by more than 2^8.  Sums and maxima are fp32; P is rounded to fp16, K
-// and V were when they were expanded (half a step each).
+// it grew by more than 2^8.  Sums and maxima are fp32; P is rounded to fp16
+// (see kLift), K and V were when they were expanded (half a step each).
 // Bound by shared memory, not by the tensor cores: a product's operands come
 // from it at 128 bytes a clock, 6 KB for the 32 clocks of one of S, and with
 // the stages' arrival that makes about 1660 clocks a stage of both tiles, where
@@ -410,6 +410,11 @@ constexpr int kAttnThreads = 12 * 32;
 constexpr int kTmaWarp = 8, kMmaWarp = 9, kVTmaWarp = 11;
 constexpr uint32_t kTileCols = 256;             // TMEM columns of a tile: S 2 x 64, O 128
 constexpr float kLazy = 8.f;
+// The largest weight of a row is held as 2^kLift or more: fp16's smallest step
+// is 2^-24, so that a weight is off by at most 2^-32 of the largest where it
+// would be lost below 2^-25, and the total keeps all of it (131071 tokens 17
+// nats below one are 0.4 % of it).  2^(kLazy + kLift) is well inside fp16.
+constexpr float kLift = 7.f;
 constexpr int kFineTokens = 512;
 
 struct AttendParams {
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
       const int pos = pos0 + min(tok, n - 1);
       const uint32_t trow = tmem + t * kTileCols + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
       const float c = p.scale_log2;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;  // m: the maximum less kLift
       bool ok = true;
       const int nst = tile_stages(t);
       // powers of two of the values, 32 keys each; O is in units of 2^unit,
@@ -604,7 +609,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
           mx = fmaxf(mx0, mx1);
           cm = 1.f;
         }
-        const bool grow = mx > m + kLazy;
+        const bool grow = mx - m > kLazy + kLift;  // (a difference: exact where the two are close)
+        const float next = mx - kLift;
         const int up = max(max(k0 <= pos ? here.x : unit, k0 + 32 <= pos ? here.y : unit) - unit, 0);
         if (__any_sync(0xffffffffu, (grow && i > 0) || up > 0)) {
           // (pv_done is at most one phase behind: S of this stage was issued
@@ -614,7 +620,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
             break;
           }
           tc_fence_after_sync();
-          const float alpha = (grow ? exp2_fast(m - mx) : 1.f) * exp2_fast(static_cast<float>(-up));
+          const float alpha = (grow ? exp2_fast(m - next) : 1.f) * exp2_fast(static_cast<float>(-up));
           unit += up;
 #pragma unroll
           for (int d = 0; d < kValue; d += 32) {
@@ -626,8 +632,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
           }
         }
         if (grow) {
-          l *= exp2_fast(m - mx);
-          m = mx;
+          l *= exp2_fast(m - next);
+          m = next;
         }
         const float base = m == -INFINITY ? 0.f : m;
         const uint64_t cm2 = f2(cm, cm), nb2 = f2(-base, -base);

@@ -22,8 +22,8 @@
 // exactly its P^T fragment (query g, tokens 4t..4t+3), and V's words of
 // two tokens are paired by byte permutes.
 // Sums and maxima are fp32, P is rounded to the operand type (half a step of
-// it a weight, averaged over tokens); the weights that are handed out come
-// from the fp32 scores.
+// it a weight, averaged over tokens; see kLift); the weights that are handed
+// out come from the fp32 scores.
 //
 // Second kernel: joins the shares of a pair (out), and adds the weights.
 //
@@ -51,6 +51,13 @@ constexpr int kMinSteps = 4;          // a share smaller than this only adds joi
 // writes them, and there is no second kernel.
 constexpr int kWholeTokens = 128;
 constexpr float kLazy = 8.f;          // a row's maximum is raised when it grew by more than this (base 2)
+// The largest weight of a row is held as 2^kLift or more: fp16's smallest step
+// is 2^-24, so that a weight is off by at most 2^-32 of the largest where it
+// would be lost below 2^-25, and the total keeps all of it (131071 tokens 17
+// nats below one are 0.4 % of it).  2^(kLazy + kLift) is well inside fp16.
+// bf16 has a float's range and needs none of it.
+template <int MT>
+constexpr float kLift = MT == kF16 ? 7.f : 0.f;
 
 struct WeighParams {
   void *out;
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
     for (int i = 0; i < ACC; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f;  // m: the maximum less kLift
 
     uint4 kr[2][KW];
     uint32_t vr[4][VWORDS];
@@ -294,10 +301,10 @@ __global__ void __launch_bounds__(kThreads, 3) weigh_kernel(const WeighParams p,
       float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const bool grow = mx > m + kLazy;
+      const bool grow = mx - m > kLazy + kLift<MT>;  // (a difference: exact where the two are close)
       if (__any_sync(0xffffffffu, grow)) {
-        const float alpha = grow ? exp2_fast(m - mx) : 1.f;
-        if (grow) m = mx;
+        const float next = mx - kLift<MT>, alpha = grow ? exp2_fast(m - next) : 1.f;
+        if (grow) m = next;
         l *= alpha;
         const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t), a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
 #pragma unroll
