@@ -568,6 +568,8 @@ PA_API pa_status pa_latent_write(const void *latent, const void *rope, int64_t l
  *       softmax_i(scale * <q[s, j, h, :], row_i>) row_i[: latent_dim]
  * with row_i token i's row of the cache.  A row that sees no token, or none
  * with a score above -infinity, gives zeros.
+ * A new token's row depends on the tokens that it sees alone: a later new
+ * token that is not finite leaves it as it is.
  *   out            device [num_seqs, new_tokens, num_heads, latent_dim]
  *   q              device [num_seqs, new_tokens, num_heads, latent_dim +
  *                  rope_dim] (the query times Uk_h, then its rotary part)

@@ -279,6 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       softmax_sync();
       // tokens that every query row sees
       const int all_see = n_rows < N ? 0 : walk.L - (p.new_tokens - 1 - rt * N / p.heads);
+      const int plain = plain_end(p, walk.L);
+      bool bad = false;  // whether this thread has taken numbers out of V
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         wait(&hdr.s_full[i & 1], (i >> 1) & 1);
         float x[NQ];
@@ -356,14 +358,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           *reinterpret_cast<uint2 *>(row + ((c0 / 8 ^ (k & 7)) << 4) + (c0 & 7) * 2) = make_uint2(pw[0], pw[1]);
         }
-        if ((tile + 1) * kTile > walk.L) {
-          // rows behind the sequence's end hold anything: zero them, 0 * NaN would reach O^T
+        if ((tile + 1) * kTile > plain) {
+          // rows behind the sequence's end hold anything: zero them, 0 * NaN would reach O^T; of drafted tokens
+          // before it what is not finite is taken out
           uint8_t *vb = kv + (i & 1) * kTileBytes;
-          const int z0 = walk.L - tile * kTile;
+          const int z0 = max(plain - tile * kTile, 0), z1 = walk.L - tile * kTile;
           for (int idx = threadIdx.x; idx < (kTile - z0) * (kLatentDim / 8); idx += kSoftmaxThreads) {
             const int z = z0 + idx / (kLatentDim / 8), e = idx % (kLatentDim / 8);
-            *reinterpret_cast<uint4 *>(vb + (z >> 3) * kGroup + (e >> 3) * kAtom + (z & 7) * 128 + (e & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+            uint4 *at = reinterpret_cast<uint4 *>(vb + (z >> 3) * kGroup + (e >> 3) * kAtom + (z & 7) * 128 + (e & 7) * 16);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            bool write = true;
+            if (z < z1) {
+              x = *at;
+              write = take_out<DT>(x);
+              bad |= write;
+            }
+            if (write) *at = x;
           }
         }
         fence_proxy_async_smem();
@@ -394,6 +404,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(&hdr.pv_done, (i - 1) & 1);
       const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
       const int d0 = 32 * quarter;  // the thread's dimensions: d0 + lane (+ 128 b)
+      // drafted tokens of this piece from which numbers were taken: not-a-number to the rows that see them
+      const bool patch = p.new_tokens > 1 && walk.t1 * kTile > plain && softmax_any(bad);
+      auto load_o = [&](int b, float (&o)[NC]) {
+        tmem_load<NC>(tlane + b * N, o);
+        if (patch) {
+          int from = max(plain, walk.t0 * kTile);  // the first such token, in this dimension
+          const int end = min(walk.L, walk.t1 * kTile);
+          while (from < end &&
+                 (__ldg(token_row(p, walk.s, from) + d0 + lane + b * kDims) & kNotFinite<DT>) != kNotFinite<DT>)
+            ++from;
+          if (from < end)
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+              if (hdr.see[o0 + j] > from) o[j] = __int_as_float(0x7fffffff);
+          __syncwarp();
+        }
+      };
       if (!ok) {
       } else if (whole) {
         // rows of out: neighbouring lanes swap, so that each stores two
@@ -404,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int b = 0; b < kBlocksO; ++b) {
           float o[NC];
-          tmem_load<NC>(tlane + b * N, o);
+          load_o(b, o);
 #pragma unroll
           for (int j = 0; j < NC; j += 2) {
             const float s0 = sum_of(o0 + j), s1 = sum_of(o0 + j + 1);
@@ -426,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int b = 0; b < kBlocksO; ++b) {
           float o[NC];
-          tmem_load<NC>(tlane + b * N, o);
+          load_o(b, o);
 #pragma unroll
           for (int j = 0; j < NC; ++j)
             if (o0 + j < n_rows) po[static_cast<size_t>(j) * kLatentDim + b * kDims] = o[j];
@@ -907,6 +934,7 @@ extern "C" pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype,
   if (!encode_latent_view(&p.tmap_c, cache, desc, kCols, box_groups)) return cuda_fail(cudaErrorInvalidValue);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p.out = out;
+  p.cache = static_cast<const uint16_t *>(cache);
   p.tables = block_tables;
   p.lens = seq_lens;
   p.prefix = reinterpret_cast<long long *>(ws);

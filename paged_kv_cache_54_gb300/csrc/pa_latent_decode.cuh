@@ -28,6 +28,7 @@ struct LatentParams {
   CUtensorMap tmap_c;  // the cache, boxes of a slot (or of a block of 8); for a pair, of three of its columns
   CUtensorMap tmap_v;  // for a pair: of four columns
   void *out;
+  const uint16_t *cache;
   const int32_t *tables, *lens;
   float2 *part_ml;     // [row tiles, workers, 2, N]
   float *part_o;       // [row tiles, workers, 2, N, 512]
@@ -66,6 +67,40 @@ __device__ __forceinline__ bool softmax_any(bool x) {
 __host__ __device__ inline long long worker_count(long long tiles, long long most) {
   const long long n = (tiles + kMinTiles - 1) / kMinTiles;
   return n < most ? n : most;
+}
+
+// A drafted token that the rows before it do not see has the weight 0 in them,
+// and 0 times a number that is not finite would reach them.  So such numbers
+// are taken out of the tokens from a sequence's plain_end on before the second
+// product; the rows that do see the token are given not-a-number in those
+// dimensions at the end.  (That is what the definition gives: its score is
+// infinite or not a number, its weight not a number or 0.)
+__device__ __forceinline__ int plain_end(const LatentParams &p, int L) { return L - (p.new_tokens - 1); }
+
+template <int DT>
+constexpr uint32_t kNotFinite = DT == kF16 ? 0x7c00u : 0x7f80u;  // an exponent of ones
+
+// Eight elements of which those that are not finite become zero; whether there was one.
+template <int DT>
+__device__ __forceinline__ bool take_out(uint4 &x) {
+  constexpr uint32_t E = kNotFinite<DT>;
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool low = (w[i] & E) == E, high = (w[i] >> 16 & E) == E;
+    any |= low || high;
+    w[i] &= (low ? 0u : 0xffffu) | (high ? 0u : 0xffff0000u);
+  }
+  x = make_uint4(w[0], w[1], w[2], w[3]);
+  return any;
+}
+
+// Token i's row of the cache.
+__device__ __forceinline__ const uint16_t *token_row(const LatentParams &p, int s, int i) {
+  int b = __ldg(p.tables + static_cast<size_t>(s) * p.max_blocks + (i >> p.bs_shift));
+  if (b < 0 || b >= p.num_blocks) b = 0;  // (reported by the TMA warp)
+  return p.cache + ((static_cast<size_t>(b) << p.bs_shift) + (i & ((1 << p.bs_shift) - 1))) * kLatentRow;
 }
 
 // Zeros to `rows` rows of out from row `first` on, by the whole block.

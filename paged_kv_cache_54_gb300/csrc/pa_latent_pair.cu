@@ -159,10 +159,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
       tc_fence_after_sync();
     };
-    int i = 0, lasts = 0;  // tiles so far, and those that end past their sequence
+    int i = 0, lasts = 0;  // tiles so far, and those that end past their sequence's plain end
     for (int seg = 0; walk.next(p); ++seg) {
       const int see = row < p.rows ? walk.L - (p.new_tokens - 1 - row / p.heads) : 0;  // tokens the row sees
       const int all_see = (rt + 1) * kPairRows > p.rows ? 0 : walk.L - (p.new_tokens - 1 - rt * kPairRows / p.heads);
+      const int plain = plain_end(p, walk.L);
       float m = -INFINITY, l = 0.f;  // m: the maximum less kLift
       constexpr float OVER = kLazy + kLift<DT>;
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
@@ -223,14 +224,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int u = 0; u < 4; ++u)
           *reinterpret_cast<uint4 *>(to + (((4 * part + u) ^ (r & 7)) << 4)) =
               make_uint4(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]);
-        if ((tile + 1) * kTile > walk.L) {
-          // rows behind the sequence's end hold anything: zero them, 0 * NaN would reach O
+        if ((tile + 1) * kTile > plain) {
+          // rows behind the sequence's end hold anything: zero them, 0 * NaN would reach O; of drafted tokens before
+          // it what is not finite is taken out
           wait(&hdr.v_last, lasts++ & 1);
-          const int z0 = walk.L - tile * kTile;
+          const int z0 = max(plain - tile * kTile, 0), z1 = walk.L - tile * kTile;
           for (int idx = threadIdx.x; idx < (kTile - z0) * 32; idx += kSoftmaxThreads) {
             const int z = z0 + idx / 32, e = idx % 32;  // token, and 16 bytes of its 256 dimensions
-            *reinterpret_cast<uint4 *>(vs + (z >> 3) * kVGroup + (e >> 3) * 1024 + (z & 7) * 128 + (e & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+            uint4 *at = reinterpret_cast<uint4 *>(vs + (z >> 3) * kVGroup + (e >> 3) * 1024 + (z & 7) * 128 + (e & 7) * 16);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (z < z1) {
+              x = *at;
+              if (!take_out<DT>(x)) continue;
+            }
+            *at = x;
           }
         }
         fence_proxy_async_smem();
@@ -242,17 +249,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       hdr.top[q4][r] = l;
       softmax_sync();
       l = (hdr.top[0][r] + hdr.top[1][r]) + (hdr.top[2][r] + hdr.top[3][r]);
+      // drafted tokens of this piece that are not finite in some dimension (V's other half lies in the other block: their
+      // rows are read again, under the last products)
+      const int from = max(plain, walk.t0 * kTile), end = min(walk.L, walk.t1 * kTile);
+      bool patch = false;
+      if (p.new_tokens > 1 && from < end) {
+        for (int idx = threadIdx.x; idx < (end - from) * (kLatentDim / 8); idx += kSoftmaxThreads) {
+          uint4 x = __ldg(reinterpret_cast<const uint4 *>(token_row(p, walk.s, from + idx / (kLatentDim / 8))) +
+                          idx % (kLatentDim / 8));
+          patch |= take_out<DT>(x);
+        }
+        patch = softmax_any(patch);
+      }
       wait(&hdr.pv_done, (i - 1) & 1);
       const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
       const int d0 = half * 256 + part * 128;  // the thread's dimensions
       const bool mine = ok && row < p.rows;
+      auto load_o = [&](int d, uint32_t (&o)[32]) {  // 32 of them
+        tc_ld32(tlane + part * 128 + d, o);
+        if (patch) {  // not-a-number where a token that the row sees is not finite
+          for (int t = from; t < min(end, see); ++t) {
+            const uint4 *x4 = reinterpret_cast<const uint4 *>(token_row(p, walk.s, t) + d0 + d);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 x = __ldg(x4 + u);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if ((w[j / 2] >> 16 * (j & 1) & kNotFinite<DT>) == kNotFinite<DT>) o[8 * u + j] = 0x7fffffffu;
+            }
+          }
+          __syncwarp();
+        }
+      };
       if (whole) {
         const float inv = l == 0.f ? 0.f : 1.f / l;  // (a row that sees nothing)
         uint8_t *to = static_cast<uint8_t *>(p.out) + ((static_cast<size_t>(walk.s) * p.rows + row) * kLatentDim + d0) * 2;
 #pragma unroll 1
         for (int d = 0; d < 128; d += 32) {
           uint32_t o[32], y[16];
-          tc_ld32(tlane + part * 128 + d, o);
+          load_o(d, o);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             y[j] = l == 0.f ? 0u
@@ -274,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int d = 0; d < 128; d += 32) {
           uint32_t o[32];
-          tc_ld32(tlane + part * 128 + d, o);
+          load_o(d, o);
           if (mine)
 #pragma unroll
             for (int j = 0; j < 32; j += 8) store32(to + (d + j) * 4, o + j);
@@ -292,8 +328,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // boxes of 16 tokens (of 8 with blocks of 8): K, of the block's 64 tokens
     // of a tile, lane (part, box); V, of all 128, lane (64 tokens, box).  Bytes
     // count in the first block, for the products' issue, but for V tiles that
-    // end past their sequence: those count in each block, whose softmax warps
-    // zero the rows behind its end before the weights are announced.
+    // end past their sequence's plain end: those count in each block, whose
+    // softmax warps put the rows behind it right before the weights are announced.
     const bool is_k = warp == kKTmaWarp;
     const int box_sh = p.bs_shift < 4 ? 3 : 4, boxes = 64 >> box_sh;  // boxes of 64 tokens
     const int piece = lane / boxes, box = lane % boxes;               // this lane's part, and box in it
@@ -347,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int left = walk.L - tile * kTile;  // tokens of the tile, and boxes of them
         const int n = (min(left, kTile) + (1 << box_sh) - 1) >> box_sh;
-        const bool last = left < kTile;
+        const bool last = (tile + 1) * kTile > plain_end(p, walk.L);
         fulls += !last;
         const int row8 = row8_of(mine, tile);
         // part by part, each as soon as it is free
@@ -434,8 +470,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          // (of a tile that ends past its sequence, the weights' arrival says that V is there)
-          if ((tile + 1) * kTile <= walk.L && !mbar_wait(&hdr.v_full, fulls++ & 1, abort)) {
+          // (of a tile that ends past its sequence's plain end, the weights' arrival says that V is there)
+          if ((tile + 1) * kTile <= plain_end(p, walk.L) && !mbar_wait(&hdr.v_full, fulls++ & 1, abort)) {
             ok = false;
             break;
           }
