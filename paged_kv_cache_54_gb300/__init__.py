@@ -45,7 +45,9 @@ A latent cache is a float16 or bfloat16 tensor ``[num_blocks, block_size,
 key of 64.  The latent calls, ``pa_decode_weights`` and ``pa_evict_tokens``
 take tensors of the current device only.
 
-PyTorch supplies the device memory and the stream; there is no CPU or
+PyTorch supplies the device memory and the stream.  A call without a
+``workspace`` allocates one on its own stream: ``stream=`` (a stream or its
+handle), or the current stream.  There is no CPU or
 PyTorch fallback: if ``libpa.so`` is missing, every call raises.
 """
 
@@ -237,6 +239,21 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _workspace_of(need: int, stream, device="cuda") -> torch.Tensor:
+    """Scratch of a call on `stream` (None: the current one) that keeps no
+    reference to it: allocated on that stream, so that the allocator hands the
+    memory on behind the call's kernels, whatever stream is the current one."""
+    handle = _stream(stream)
+    if stream is None or handle == _current_stream(_current_device()):
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    if handle == 2:  # (cudaStreamPerThread: the allocator knows streams by their own handles)
+        raise ValueError("a call on the per-thread default stream needs a workspace")
+    # 0 and 1 (cudaStreamLegacy) are the default stream
+    target = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    with torch.cuda.stream(target):
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+
+
 def _cache_code(dtype: torch.dtype, cache_dtype) -> int:
     if cache_dtype is not None:
         return DTYPE_CODES[cache_dtype] if isinstance(cache_dtype, str) else int(cache_dtype)
@@ -413,7 +430,7 @@ def pa_decode(out, q, k_cache, v_cache, block_tables, seq_lens, max_seq_len: int
         _check_fp4(away, d, k_cache, v_cache, q, S, block_tables, seq_lens)
     if workspace is None:
         need = pa_decode_workspace_size(S, Hq, H, D, max_seq_len, partition_size)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _workspace_of(need, stream, q.device)
     lib = load_library()
     _check(lib.pa_decode(out.data_ptr(), q.data_ptr(), qcode, S, Hq, k_cache.data_ptr(),
                          v_cache.data_ptr(), ref, block_tables.data_ptr(),
@@ -585,10 +602,6 @@ def _check_error_word(device_error) -> None:
         raise ValueError("device_error must be int32 on the current CUDA device")
 
 
-def _workspace_of(need: int) -> torch.Tensor:
-    return torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
-
-
 def pa_decode_weights_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                                      max_seq_len: int) -> int:
     return int(load_library().pa_decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -626,7 +639,7 @@ def pa_decode_weights(out, weights_out, q, k_cache, v_cache, block_tables, seq_l
                 raise ValueError("weights_in must be like weights_out")
         win = weights_in.data_ptr()
     if workspace is None:
-        workspace = _workspace_of(pa_decode_weights_workspace_size(S, Hq, H, D, max_seq_len))
+        workspace = _workspace_of(pa_decode_weights_workspace_size(S, Hq, H, D, max_seq_len), stream)
     else:
         _check_here("workspace", workspace)
     _check(load_library().pa_decode_weights(
@@ -665,7 +678,7 @@ def pa_evict_tokens(k_cache, v_cache, block_tables, seq_lens, weights, new_table
         if t.dtype is not torch.float32 or t.dim() != 3 or t.shape[:2] != (S, H):
             raise ValueError(f"{n} must be float32 [{S}, {H}, width]")
     if workspace is None:
-        workspace = _workspace_of(pa_evict_workspace_size(S, H, budget))
+        workspace = _workspace_of(pa_evict_workspace_size(S, H, budget), stream)
     else:
         _check_here("workspace", workspace)
     _check(load_library().pa_evict_tokens(
@@ -734,7 +747,7 @@ def pa_latent_decode(out, q, cache, block_tables, seq_lens, max_seq_len: int, sc
     S, n, H = q.shape[0], q.shape[1] if q.dim() == 4 else 1, q.shape[-2]
     _check_tables(block_tables, seq_lens, S)
     if workspace is None:
-        workspace = _workspace_of(pa_latent_decode_workspace_size(S, n, H))
+        workspace = _workspace_of(pa_latent_decode_workspace_size(S, n, H), stream)
     else:
         _check_here("workspace", workspace)
     _check(load_library().pa_latent_decode(out.data_ptr(), q.data_ptr(), code, S, n, H, cache.data_ptr(), ref,
@@ -769,7 +782,7 @@ def pa_latent_prefill(out, q, cu_q_lens, up, cache, block_tables, seq_lens, max_
         raise ValueError(f"cu_q_lens must be int32 [{S + 1}]")
     _check_tables(block_tables, seq_lens, S)
     if workspace is None:
-        workspace = _workspace_of(pa_latent_prefill_workspace_size(S, H, num_kv_tokens))
+        workspace = _workspace_of(pa_latent_prefill_workspace_size(S, H, num_kv_tokens), stream)
     else:
         _check_here("workspace", workspace)
     _check(load_library().pa_latent_prefill(out.data_ptr(), q.data_ptr(), code, T, cu_q_lens.data_ptr(), S, H, max_q_len,
