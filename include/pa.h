@@ -496,7 +496,8 @@ PA_API pa_status pa_decode_weights(void *out, float *weights_out, const float *w
  *                  >= budget.  They must be distinct and none of the blocks
  *                  that block_tables names: the old blocks may be shared with
  *                  other sequences and are left as they were.
- *   new_lens       device int32 [num_seqs], written: min(L_s, budget).
+ *   new_lens       device int32 [num_seqs], written: min(L_s, budget).  Must
+ *                  not overlap seq_lens.
  *   new_weights    device float32 [num_seqs, kv_heads, new_width], new_width
  *                  >= budget, written: the kept tokens' weights, in their new
  *                  order; entries from new_lens[s] on are left as they were.
@@ -508,8 +509,9 @@ PA_API pa_status pa_decode_weights(void *out, float *weights_out, const float *w
  *   workspace      at least pa_evict_workspace_size(...) bytes, 16-byte
  *                  aligned, uninitialised; calls sharing one must be
  *                  stream-ordered.
- * Requires 0 <= recent <= budget, budget >= 1.  Supported set: 16-bit, FP8 and
- * INT8 caches (not PA_FP4); num_blocks * block_size * kv_heads < 2^31.
+ * Requires 0 <= recent <= budget, budget >= 1; overlapping lengths or weights
+ * are refused.  Supported set: 16-bit, FP8 and INT8 caches (not PA_FP4);
+ * num_blocks * block_size * kv_heads < 2^31.
  * Device checks: a length outside [0, min(weights_width, max_blocks_per_seq *
  * block_size)] moves nothing of the sequence, sets its new length to 0 and is
  * reported as error 3; a block id out of range leaves its tokens' rows

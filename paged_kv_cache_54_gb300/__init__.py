@@ -661,7 +661,8 @@ def pa_evict_tokens(k_cache, v_cache, block_tables, seq_lens, weights, new_table
     (float32 ``[S, kv_heads, width]``), in their order.  Their rows are copied
     to the blocks of ``new_tables`` (int32 ``[S, width]``, distinct, none of them
     in ``block_tables``), their weights to ``new_weights``, and the new lengths
-    to ``new_lens``.  Not for four-bit caches."""
+    to ``new_lens``, which must not overlap ``weights`` and ``seq_lens``.  Not
+    for four-bit caches."""
     _check_here("k_cache v_cache block_tables seq_lens weights new_tables new_lens new_weights", k_cache, v_cache,
                 block_tables, seq_lens, weights, new_tables, new_lens, new_weights)
     _check_error_word(device_error)

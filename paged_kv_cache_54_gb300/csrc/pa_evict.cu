@@ -326,6 +326,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   }
 }
 
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < a_bytes : x - y < b_bytes;
+}
+
 template <int ROW>
 pa_status launch_move(const EvictParams &p, cudaStream_t stream) {
   constexpr int rows = 4 * (32 / (ROW / 16));  // of a warp's step
@@ -378,6 +383,11 @@ extern "C" pa_status pa_evict_tokens(void *k_cache, void *v_cache, const pa_cach
     return PA_ERR_UNSUPPORTED;  // 32-bit rows
   if (static_cast<long long>(num_seqs) * cache->kv_heads > INT_MAX) return PA_ERR_UNSUPPORTED;             // the grid
   if (workspace_bytes < pa_evict_workspace_size(num_seqs, cache->kv_heads, budget)) return PA_ERR_INVALID;
+  // a block writes its results while others still read the lengths and the weights
+  const size_t lens_bytes = static_cast<size_t>(num_seqs) * sizeof(int32_t), row = lens_bytes * cache->kv_heads;
+  if (overlap(new_lens, lens_bytes, seq_lens, lens_bytes) ||
+      overlap(new_weights, row * new_width, weights, row * weights_width))
+    return PA_ERR_INVALID;
   EvictParams p{};
   p.k = p.k_out = static_cast<uint8_t *>(k_cache);
   p.v = p.v_out = static_cast<uint8_t *>(v_cache);
