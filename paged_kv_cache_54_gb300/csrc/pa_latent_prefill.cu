@@ -46,8 +46,9 @@
 // stages fetched into L2 ahead (even), loads before the block's first barrier
 // (even).
 // With an fp16 cache P's rounding would show beside the output's where a row
-// follows few tokens, so sequences of up to 512 tokens take P as two fp16
-// parts.
+// follows few tokens, so rows of up to 512 tokens take P as two fp16 parts (the
+// second is zero for the other rows of their tile: a row's rounding goes by its
+// own tokens, whatever comes behind it and wherever its prompt is cut).
 #include <limits.h>
 #include <math.h>
 
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
   const int pos0 = L - n;
   const int kv_end = pos0 + min(n, tok0 + kTiles * kRows);
   const int n_stages = (kv_end + kKeys - 1) / kKeys;
-  const bool fine = DT == kF16 && L <= kFineTokens;  // P in two parts
+  auto fine_tile = [&](int t) { return DT == kF16 && pos0 + tok0 + t * kRows < kFineTokens; };  // P in two parts
   auto tile_stages = [&](int t) { return (pos0 + min(n, tok0 + (t + 1) * kRows) + kKeys - 1) / kKeys; };
   uint8_t *qs = smem + kQOff, *stages = smem + kStageOff;
   volatile int *abort = &hdr.abort;
@@ -558,6 +559,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
       float m = -INFINITY, l = 0.f;  // m: the maximum less kLift
       bool ok = true;
       const int nst = tile_stages(t);
+      const bool fine = fine_tile(t);
       // powers of two of the values, 32 keys each; O is in units of 2^unit,
       // the largest power of those the row has followed
       const int2 *powers =
@@ -669,11 +671,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
           }
         }
         tc_st32(trow + (i & 1) * kKeys, pw);  // P over the S buffer just read
-        if (fine) {  // and what its rounding left
+        if (fine) {  // and what its rounding left, to rows that follow few tokens
 #pragma unroll
           for (int j = 0; j < kKeys; j += 2) {
             const float2 a = half2_bits_to_float2<kF16>(pw[j / 2]);
-            pw[j / 2] = pack2_rn<kF16>(sv[j] - a.x, sv[j + 1] - a.y);
+            pw[j / 2] = pos < kFineTokens ? pack2_rn<kF16>(sv[j] - a.x, sv[j + 1] - a.y) : 0u;
           }
           tc_st32(trow + (i & 1) * kKeys + kKeys / 2, pw);
         }
@@ -782,6 +784,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
         return true;
       };
       const int nst = tile_stages(t);
+      const bool fine = fine_tile(t);
       if (ok) ok = issue_qk(0);
       for (int i = 0; i < nst && ok; ++i) {
         if (i + 1 < nst && !issue_qk(i + 1)) {
