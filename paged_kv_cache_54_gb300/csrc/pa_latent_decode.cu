@@ -32,6 +32,7 @@
 //         tokens; the total weights stay per thread until a sequence ends.
 //   8     TMA: q, then the tiles, a 16-token slot at a time
 //   9, 10 issue the S^T and O^T products
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -78,7 +79,10 @@ struct Header {
   int see[64];              // tokens a query row sees
 };
 static_assert(sizeof(Header) <= 2048, "the header's place");
-constexpr float kNone = 3e38f;  // of a row without a maximum yet: any score passes it, none (-inf) stays -inf
+// Of a row without a maximum yet, the largest float: with it any score passes
+// the threshold (but its own negative, which counts as none), and none (-inf)
+// stays -inf.
+constexpr float kNone = FLT_MAX;
 
 // NCOL consecutive columns of the warp's lanes
 #define PA_R8(a, o) a(r[o]), a(r[o + 1]), a(r[o + 2]), a(r[o + 3]), a(r[o + 4]), a(r[o + 5]), a(r[o + 6]), a(r[o + 7])
