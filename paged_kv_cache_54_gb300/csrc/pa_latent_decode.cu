@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int box_sh = p.bs_shift < 4 ? 3 : 4, boxes = kTile >> box_sh;
     const uint32_t box_bytes = (1u << box_sh) / 8 * kGroup;
     bool ok = true;
-    int i = 0;
+    int i = 0, tiles_issued = 0, qs_issued = 0;  // (the last tile perhaps in part)
     for (int seg = 0; ok && walk.next(p); ++seg) {
       const int32_t *table = p.tables + static_cast<size_t>(walk.s) * p.max_blocks;
       auto entry = [&](int tile) {  // this lane's block of a tile
@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < kCols; ++e)
           tma_load_2d(qs + e * Lay::Q_COL, &p.tmap_q, e * 64, row, &hdr.q_full);
       }
+      ++qs_issued;
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         const int st = i & 1;
         const int n_box = min(boxes, ((walk.L - tile * kTile) + (1 << box_sh) - 1) >> box_sh);
@@ -524,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (lane == 0) mbar_arrive_expect_tx(&hdr.kv_full[st], n_box * box_bytes);
+        tiles_issued = i + 1;
         __syncwarp();
         for (int g = 0; ok && g < kSlots; ++g) {  // slot by slot, each as soon as it is free
           if (g > 0 && i >= kStages)
@@ -544,7 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       record_error(p.err, kErrTimeout);
       *abort = 1;
       // wait, within the limit, for the copies still in flight
-      for (int j = max(0, i - kStages); j < i; ++j) mbar_wait(&hdr.kv_full[j & 1], (j >> 1) & 1, nullptr);
+      if (qs_issued > 0) mbar_wait(&hdr.q_full, (qs_issued - 1) & 1, nullptr);
+      for (int j = max(0, tiles_issued - kStages); j < tiles_issued; ++j)
+        mbar_wait(&hdr.kv_full[j & 1], (j >> 1) & 1, nullptr);
     }
   } else if (warp == kQkWarp) {
     // -------------------------------------------------------------------- S^T

@@ -57,7 +57,7 @@ static_assert(kSmem <= 232448 && kKOff % 1024 == 0, "shared memory");
 
 struct Header {
   uint64_t q_full, q_empty, k_full[kKParts], k_empty[kKParts], v_full, v_last, v_empty[kVParts], s_full[2], s_empty[2], p_full,
-      pv_done, fin;
+      pv_done, fin[2];
   uint32_t tmem;
   int abort;
   float top[4][kHalfRows];  // maxima of a row's quarters, then their total weights
@@ -128,7 +128,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(&hdr.p_full, kArrivals);
     mbar_init(&hdr.pv_done, 1);
-    mbar_init(&hdr.fin, 1);
+    mbar_init(&hdr.fin[0], 1);
+    mbar_init(&hdr.fin[1], 1);
     hdr.abort = 0;
     fence_mbar_init();
   }
@@ -343,7 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t q_full = in_block(&hdr.q_full, 0);
     const uint32_t full = in_block(is_k ? &hdr.k_full[in ? piece : 0] : &hdr.v_full, 0);
     bool ok = true;
-    int i = 0, fulls = 1;  // (V tiles counted in v_full, less one)
+    // tiles done, parts of the next one, V tiles announced in v_full and in v_last, sequences whose q is
+    int i = 0, issued = 0, fulls = 0, lasts = 0, qs_issued = 0;
     for (int seg = 0; ok && walk.next(p); ++seg) {
       const int32_t *table = p.tables + static_cast<size_t>(walk.s) * p.max_blocks;
       auto entry = [&](int tile) {
@@ -372,6 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int row = walk.s * p.rows + rt * kPairRows + kHalfRows * rank;
           for (int e = 0; e < kCols; ++e) pair_load_2d(qs + e * kQCol, &p.tmap_q, e * 64, row, q_full);
         }
+        ++qs_issued;
       }
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
         const int tok = tile * kTile + tok0;
@@ -384,12 +387,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int left = walk.L - tile * kTile;  // tokens of the tile, and boxes of them
         const int n = (min(left, kTile) + (1 << box_sh) - 1) >> box_sh;
         const bool last = (tile + 1) * kTile > plain_end(p, walk.L);
-        fulls += !last;
         const int row8 = row8_of(mine, tile);
         // part by part, each as soon as it is free
         for (int g = 0; ok && g < parts; ++g) {
           if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait(empty + g, (i - 1) & 1, abort));
           if (!ok) break;
+          if (g == 0) ++(last ? lasts : fulls);
+          issued = g + 1;
           if (lane == 0) {
             if (is_k && rank == 0) mbar_arrive_expect_tx(&hdr.k_full[g], n * bytes);
             if (!is_k && g == 0 && last) mbar_arrive_expect_tx(&hdr.v_last, n * bytes);
@@ -404,6 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
+        issued = 0;
         if (tile == walk.t0) fetch(phys1, tile + 1);
         fetch(phys2, tile + 2);
         phys = phys1;
@@ -412,15 +417,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (ok) walk.advance();
     }
+    if (ok && i > 0) {  // the last products' arrivals in this block
+      for (int g = 0; g < parts; ++g) ok = ok && mbar_wait(empty + g, (i - 1) & 1, abort);
+      if (is_k) ok = ok && mbar_wait(&hdr.q_empty, (qs_issued - 1) & 1, abort);
+      ok = __all_sync(0xffffffffu, ok);
+    }
     if (!ok && lane == 0) {
       record_error(p.err, kErrTimeout);
       *abort = 1;
-      // wait, within the limit, for the copies still in flight
-      if (i > 0 && rank == 0) {
-        if (is_k)
-          for (int j = 0; j < kKParts; ++j) mbar_wait(&hdr.k_full[j], (i - 1) & 1, nullptr);
-        else
-          mbar_wait(&hdr.v_full, fulls & 1, nullptr);
+      // wait, within the limit, for the copies still in flight (of those that count in the first block it is that block
+      // that waits, and the other stays until it has)
+      if (is_k && rank == 0) {
+        if (qs_issued > 0) mbar_wait(&hdr.q_full, (qs_issued - 1) & 1, nullptr);
+        for (int g = 0; g < kKParts; ++g) {
+          const int n = i + (g < issued);  // of this part
+          if (n > 0) mbar_wait(&hdr.k_full[g], (n - 1) & 1, nullptr);
+        }
+      } else if (!is_k) {
+        if (fulls > 0 && rank == 0) mbar_wait(&hdr.v_full, (fulls - 1) & 1, nullptr);
+        if (lasts > 0) mbar_wait(&hdr.v_last, (lasts - 1) & 1, nullptr);
       }
     }
   } else if (warp == kQkWarp) {
@@ -457,6 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         record_error(p.err, kErrTimeout);
         *abort = 1;
       }
+      pair_commit(&hdr.fin[0]);
     }
   } else {
     // -------------------------------------------------------------------- O
@@ -496,12 +512,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         record_error(p.err, kErrTimeout);
         *abort = 1;
       }
-      pair_commit(&hdr.fin);
-      mbar_wait(&hdr.fin, 0, nullptr);
+      pair_commit(&hdr.fin[1]);
     }
   }
   tc_fence_before_sync();
   __syncthreads();
+  // every product has completed, and its arrivals in this block with it, whether the block gave up or not
+  if (warp == kQkWarp) {
+    mbar_wait(&hdr.fin[0], 0, nullptr);
+    mbar_wait(&hdr.fin[1], 0, nullptr);
+    __syncwarp();
+  }
   cluster_sync();  // both blocks are done with the other's shared memory and tensor memory
   if (warp == kQkWarp) {
     tc_fence_after_sync();

@@ -339,6 +339,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1)
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
+    if (ok && runs > 0) {  // the last products' arrivals in this block
+      chunk = __shfl_sync(0xffffffffu, chunk, 0);
+      for (int j = max(0, chunk - kExRing); j < chunk; ++j)
+        ok = ok && mbar_wait(&hdr.b_empty[j % kExRing], (j / kExRing) & 1, abort);
+      ok = ok && mbar_wait(&hdr.a_empty, (runs - 1) & 1, abort);
+      ok = __all_sync(0xffffffffu, ok);
+    }
     if (lane == 0 && !ok) {
       record_error(p.err, kErrTimeout);
       *abort = 1;
@@ -383,10 +390,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1)
       *abort = 1;
     }
     pair_commit(&hdr.fin);
-    mbar_wait(&hdr.fin, 0, nullptr);
   }
   tc_fence_before_sync();
   __syncthreads();
+  // every product has completed, and its arrivals in this block with it, whether the block gave up or not
+  if (warp == kExMmaWarp) {
+    mbar_wait(&hdr.fin, 0, nullptr);
+    __syncwarp();
+  }
   cluster_sync();  // both blocks are done with the other's shared memory and tensor memory
   if (warp == kExMmaWarp) {
     tc_fence_after_sync();
