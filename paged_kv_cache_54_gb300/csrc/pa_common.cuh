@@ -425,13 +425,6 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *m
       : "memory");
 }
 
-// The same box fetched into L2 only.
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int x, int y, int z, int w) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
-}
 
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialization may start before the previous kernel in the stream ends;
@@ -455,79 +448,6 @@ __device__ __forceinline__ int cluster_ctas() {
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// One thread of the (converged) warp.  A branch on it, unlike one on a lane
-// number, is known to be taken by a single thread: the issue of matrix
-// products in it keeps its descriptors in uniform registers (36 products in
-// 900 clocks, against 2500).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t y;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
-  return y != 0;
-}
-
-// ----------------------------------------------------------------------------
-// pairs of blocks (clusters of two) whose tensor cores work as one
-// ----------------------------------------------------------------------------
-// An address of shared memory in the cluster's block `rank`.
-__device__ __forceinline__ uint32_t in_block(const void *p, int rank) {
-  uint32_t y;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(smem_addr(p)), "r"(rank));
-  return y;
-}
-// An arrival on an mbarrier of either block.  (What it follows is read by this
-// block's own tensor cores, behind a proxy fence: no release to the cluster,
-// which costs about 1000 clocks.)
-__device__ __forceinline__ void pair_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Tiled loads whose bytes count on an mbarrier of either block of the pair.
-__device__ __forceinline__ void pair_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void pair_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// An arrival on the mbarrier of this place in both blocks once every product
-// issued so far has completed.
-__device__ __forceinline__ void pair_commit(uint64_t *bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_addr(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-// 32 bytes to global memory (32-byte aligned)
-__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-// Tensor-memory allocation in both blocks of a pair (one whole warp of each).
-__device__ __forceinline__ void pair_alloc(uint32_t *dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(const void *p) {

@@ -36,7 +36,6 @@
 #include <limits.h>
 #include <math.h>
 
-#include "pa_common.cuh"
 #include "pa_latent_decode.cuh"
 
 namespace pa {

@@ -2,7 +2,7 @@
 // the softmax warps' barriers.
 #pragma once
 
-#include "pa_common.cuh"
+#include "pa_latent_common.cuh"
 #include "pa_latent.h"
 #include "pa_shares.cuh"
 
@@ -47,11 +47,6 @@ pa_status launch_latent_pair(int dtype, LatentParams &p, const void *q, const vo
                              int *workers, cudaStream_t stream);
 
 #ifdef __CUDACC__
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool x) {
   uint32_t y;

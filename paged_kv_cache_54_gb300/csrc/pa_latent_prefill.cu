@@ -52,8 +52,8 @@
 #include <limits.h>
 #include <math.h>
 
-#include "pa_common.cuh"
 #include "pa_latent.h"
+#include "pa_latent_common.cuh"
 #include "pa_shares.cuh"
 
 namespace pa {
@@ -61,12 +61,6 @@ namespace {
 
 constexpr int kNope = 128, kValue = 128, kUp = kNope + kValue;  // of a head: keys' share of the latent, values
 constexpr int kQk = kNope + kRopeDim;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // ------------------------------------------------------------------ expand
 constexpr int kExTokens = 128;
@@ -102,13 +96,6 @@ struct ExpandHeader {
   ShareScan<128> scan;
 };
 static_assert(sizeof(ExpandHeader) <= 2048, "the header's place");
-
-// 32 bytes to global memory (32-byte aligned)
-__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[16], int at) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[at]), "r"(w[at + 1]),
-               "r"(w[at + 2]), "r"(w[at + 3]), "r"(w[at + 4]), "r"(w[at + 5]), "r"(w[at + 6]), "r"(w[at + 7])
-               : "memory");
-}
 
 // The power of two e for which values of largest magnitude `top` are stored
 // as x 2^-e: 0 where fp16 holds them well, from 2^-4 to 2^15 (a step of fp16's
@@ -257,8 +244,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1)
           for (int j = 0; j < 16; ++j)
             w[j] = real ? pack2_rn<DT>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])) : 0u;
           if (fits) {
-            st_global_32(to + c * 2, w, 0);
-            st_global_32(to + c * 2 + 32, w, 8);
+            store32(to + c * 2, w);
+            store32(to + c * 2 + 32, w + 8);
           }
         }
         float top = 0.f;
@@ -288,8 +275,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExThreads, 1)
           for (int j = 0; j < 16; ++j)
             w[j] = real ? pack2_rn<kF16>(__uint_as_float(v[c + 2 * j]) * f, __uint_as_float(v[c + 2 * j + 1]) * f) : 0u;
           if (fits) {
-            st_global_32(to + (kNope + c) * 2, w, 0);
-            st_global_32(to + (kNope + c) * 2 + 32, w, 8);
+            store32(to + (kNope + c) * 2, w);
+            store32(to + (kNope + c) * 2 + 32, w + 8);
           }
         }
       }

@@ -34,9 +34,9 @@
 #include <limits.h>
 #include <math.h>
 
-#include "pa_common.cuh"
 #include "pa_fp4.cuh"
 #include "pa_host.h"
+#include "pa_latent_common.cuh"
 #include "pa_shares.cuh"
 
 namespace pa {
@@ -93,11 +93,6 @@ __device__ __forceinline__ uint2 ldg_stream2(const void *p, uint64_t policy) {
                : "=r"(v.x), "=r"(v.y)
                : "l"(p), "l"(policy));
   return v;
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 __device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
