@@ -492,11 +492,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) latent_attend_kernel(const __
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_rope)) : "memory");
   }
   const int q0 = __ldg(p.cu_q + s), n = __ldg(p.cu_q + s + 1) - q0, L = __ldg(p.lens + s);
-  if (n < 0 || q0 < 0 || n > p.num_q_tokens - q0 || n > p.max_q_len || L < n || L > p.limit) {
-    if (threadIdx.x == 0) record_error(p.err, kErrSeqLen);
+  const bool valid = n >= 0 && q0 >= 0 && n <= p.num_q_tokens - q0 && n <= p.max_q_len && L >= n && L <= p.limit;
+  if (!valid || cta * kTiles * kRows >= n) {
+    if (!valid && threadIdx.x == 0) record_error(p.err, kErrSeqLen);
+    // a call without any row must not end, and let the next one in the stream begin, before its expansion has
+    if (blockIdx.x == 0) grid_dependency_wait();
     return;
   }
-  if (cta * kTiles * kRows >= n) return;
   if ((smem_addr(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) record_error(p.err, kErrSmemAlign);
     return;
