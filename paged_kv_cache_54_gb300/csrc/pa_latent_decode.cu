@@ -17,7 +17,7 @@
 // reads it token-major, the second dimension-major.  O^T takes 4 N columns of
 // tensor memory, S^T 2 N.
 //
-// A block takes N query rows and an equal share of all sequences'
+// A block takes all query rows and an equal share of all sequences'
 // 64-token tiles (pa_shares.cuh).  One sequence of 131071 tokens, 32 query
 // rows: 151 MB, 22.6 us at the measured copy rate; this kernel takes 35 (the
 // loop keeps up with the memory, 5 us pass until the first tiles land, 3 to 5
@@ -52,7 +52,7 @@ constexpr int kDims = 128;             // of one O^T product
 constexpr int kBlocksO = kLatentDim / kDims;
 constexpr int kTmaWarp = 8, kQkWarp = 9;  // and 10: O^T
 constexpr int kThreads = 11 * 32;
-constexpr int kMaxWorkers = 152;       // shares of one row tile, at most; sizes the workspace
+constexpr int kMaxWorkers = 152;       // shares, at most; sizes the workspace
 
 template <int N>
 struct Layout {
@@ -180,9 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(sizeof(ShareScan<128>) <= Lay::P_BYTES, "the scan's place");
   Header &hdr = *reinterpret_cast<Header *>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rt = blockIdx.x % p.row_tiles, w = blockIdx.x / p.row_tiles;
+  const int w = blockIdx.x;
   if (!p.whole) launch_dependents();  // (the merge)
-  const int n_rows = min(N, p.rows - rt * N);  // query rows of this tile
+  const int n_rows = p.rows;  // (at most N)
   auto tiles_of = [&](int s) -> long long { return (checked_len(p.lens, s, p.limit, p.err) + kTile - 1) / kTile; };
   Walk<kTile> walk;
   if (p.whole) {
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     walk.s = w;
     walk.end = tiles_of(w);
     if (walk.end == 0) {
-      zero_rows(p.out, static_cast<long long>(w) * p.rows + rt * N, n_rows);
+      zero_rows(p.out, static_cast<long long>(w) * p.rows, n_rows);
       return;
     }
   } else {
@@ -277,11 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (threadIdx.x < N) {
         const int h = threadIdx.x;
         hdr.m[h] = kNone;
-        hdr.see[h] = h < n_rows ? walk.L - (p.new_tokens - 1 - (rt * N + h) / p.heads) : 0;
+        hdr.see[h] = h < n_rows ? walk.L - (p.new_tokens - 1 - h / p.heads) : 0;
       }
       softmax_sync();
       // tokens that every query row sees
-      const int all_see = n_rows < N ? 0 : walk.L - (p.new_tokens - 1 - rt * N / p.heads);
+      const int all_see = n_rows < N ? 0 : walk.L - (p.new_tokens - 1);
       const int plain = plain_end(p, walk.L);
       bool bad = false;  // whether this thread has taken numbers out of V
       for (int tile = walk.t0; tile < walk.t1; ++tile, ++i) {
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (whole) {
         // rows of out: neighbouring lanes swap, so that each stores two
         // dimensions of every other query row
-        const size_t row0 = static_cast<size_t>(walk.s) * p.rows + rt * N + o0;
+        const size_t row0 = static_cast<size_t>(walk.s) * p.rows + o0;
         const bool odd = lane & 1;
         uint16_t *o16 = static_cast<uint16_t *>(p.out) + (row0 + odd) * kLatentDim + d0 + (lane & ~1);
 #pragma unroll 1
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        const size_t slot = (static_cast<size_t>(rt) * max_workers + w) * 2 + (seg > 0);
+        const size_t slot = static_cast<size_t>(w) * 2 + (seg > 0);
         if (threadIdx.x < N) {
           const float m = hdr.m[threadIdx.x];
           p.part_ml[slot * N + threadIdx.x] = make_float2(m == kNone ? -INFINITY : -m, sum_of(threadIdx.x));
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0) {
         mbar_arrive_expect_tx(&hdr.q_full, Lay::Q_BYTES);
-        const int row = walk.s * p.rows + rt * N;
+        const int row = walk.s * p.rows;
         for (int e = 0; e < kCols; ++e)
           tma_load_2d(qs + e * Lay::Q_COL, &p.tmap_q, e * 64, row, &hdr.q_full);
       }
@@ -886,11 +886,9 @@ pa_status launch(LatentParams &p, const void *q, cudaStream_t stream) {
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cuda_fail(cudaErrorInvalidValue);
-  p.row_tiles = (p.rows + N - 1) / N;
   const int sms = info.sm_count < kMaxWorkers ? info.sm_count : kMaxWorkers;
-  const int workers = p.whole ? p.num_seqs : sms / p.row_tiles > 0 ? sms / p.row_tiles : 1;
-  if (static_cast<long long>(workers) * p.row_tiles > INT_MAX) return PA_ERR_UNSUPPORTED;
-  latent_decode_kernel<DT, N><<<workers * p.row_tiles, kThreads, Lay::SMEM, stream>>>(p, workers);
+  const int workers = p.whole ? p.num_seqs : sms;
+  latent_decode_kernel<DT, N><<<workers, kThreads, Lay::SMEM, stream>>>(p, workers);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
   return p.whole ? PA_OK : join<DT, N>(p, workers, info.sm_count, stream);

@@ -33,7 +33,7 @@ struct LatentParams {
   float2 *part_ml;     // [row tiles, workers, 2, N]
   float *part_o;       // [row tiles, workers, 2, N, 512]
   long long *prefix;   // [S + 1] tiles before sequence s
-  int num_seqs, new_tokens, heads, rows, row_tiles, num_blocks, bs_shift, max_blocks, limit;
+  int num_seqs, new_tokens, heads, rows, row_tiles /* of a pair's 128 rows */, num_blocks, bs_shift, max_blocks, limit;
   bool whole;          // every share is one sequence: nothing to join
   bool out_sectors;    // out is 32-byte aligned
   float scale_log2;
