@@ -826,11 +826,18 @@ cudaError_t launch_after(void (*kernel)(ARGS...), unsigned blocks, cudaStream_t 
 
 template <int DT, int N>
 pa_status join(const LatentParams &p, int workers, int sms, cudaStream_t stream) {
+  // A row to 64 warps, to 4, or a warp's share of 16 rows.  In us, by the rows
+  // of all sequences: one sequence of 131071 tokens, 32 rows 38.1 with 64 warps
+  // and 46.2 with 4, 64 rows 46.9 / 54.8, 128 rows 53.5 / 50.4; four of 2048,
+  // 32 rows 10.7 / 11.0, 64 rows 13.4 / 11.2, 128 rows 19.7 / 12.4.  With 4 and
+  // with a share: four sequences of 4000 tokens, 128 heads, 512 rows 19.2 /
+  // 26.7, eight (1024 rows) 28.1 / 30.6, ten (1280) 32.2 / 31.0, 20 of 2000
+  // (2560) 36.5 / 29.0, 64 of 2000 (8192) 86.6 / 55.6.
   const long long rows = static_cast<long long>(p.num_seqs) * p.rows;
   cudaError_t e;
-  if (rows <= sms * 2ll) {
+  if (rows <= sms / 2) {
     e = launch_after(latent_merge_few<DT, N, 16, 4>, static_cast<unsigned>(rows * 4), stream, p, workers);
-  } else if (rows <= sms * 16ll) {
+  } else if (rows <= sms * 7ll) {
     e = launch_after(latent_merge_few<DT, N, 4, 1>, static_cast<unsigned>((rows + 3) / 4), stream, p, workers);
   } else {
     // as many rows a block as leave one wave of blocks, whole warps of them
@@ -842,6 +849,11 @@ pa_status join(const LatentParams &p, int workers, int sms, cudaStream_t stream)
   return e == cudaSuccess ? PA_OK : cuda_fail(e);
 }
 
+// The fewest columns that hold the query rows; pairs of blocks beyond 64.  64
+// sequences of 4096 tokens (302 MB, 45 us at the measured copy rate), in us: 16
+// rows 61 with 16 columns, 62 with 32, 67 with 64; 32 rows 69 with 32, 74 with
+// 64; 40 rows 69 with 64, 74 by pairs; 64 rows 73 with 64, 78 by pairs; 65 rows
+// 79 and 128 rows 82 by pairs.
 int columns_for(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kPairRows; }
 
 struct Sizes {
@@ -956,7 +968,11 @@ extern "C" pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype,
   long long limit = held < max_seq_len ? held : max_seq_len;
   if (limit > INT_MAX / 4) limit = INT_MAX / 4;
   p.limit = static_cast<int>(limit);
-  p.whole = max_seq_len <= kWholeTokens;
+  DeviceInfo info;
+  if (!current_device_info(&info)) return cuda_fail(cudaGetLastError());
+  const bool pairs = p.rows > 64;  // of blocks
+  const long long units = pairs ? (p.rows + kPairRows - 1ll) / kPairRows * num_seqs : num_seqs;
+  p.whole = max_seq_len <= kWholeTokens && units <= kWholeWaves * (pairs ? info.sm_count / 2 : info.sm_count);
   p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = device_error;

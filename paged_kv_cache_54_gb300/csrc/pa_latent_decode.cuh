@@ -18,10 +18,14 @@ constexpr float kLazy = 8.f;     // a row's maximum is raised when a score passe
 template <int DT>
 constexpr float kLift = DT == kF16 ? 7.f : 0.f;
 constexpr int kSoftmaxThreads = 256;
-// Sequences of up to this many tokens are not split: their few tiles take less
-// than a second kernel (four sequences of 1..100 tokens, 16 heads: 10.4 us in
-// place of 16.5).
-constexpr int kWholeTokens = 256;
+// Sequences of up to this many tokens are not split while their blocks (pairs
+// of blocks) are at most kWholeWaves for each that the GPU holds: their few
+// tiles then take less than a second kernel.  Unsplit and split, in us, 16 and
+// 128 heads: 4 sequences of 256 tokens 10.4 / 12.1 and 11.0 / 12.8, of 512
+// tokens 15.3 / 12.5 and 14.7 / 15.9; 64 of 256 11.4 / 14.0 and 12.0 / 15.5;
+// 152 of 256 (two pairs each, with 128 heads) 11.2 / 20.0 and 24.2 / 23.5; 304
+// of 256 23.3 / 25.0 and 56.7 / 47.9; 512 of 64 25.5 / 24.3 and 76.5 / 54.0.
+constexpr int kWholeTokens = 256, kWholeWaves = 2;
 
 struct LatentParams {
   CUtensorMap tmap_q;  // [S n H, 576] in boxes of {64, N} (64 rows for a pair)
