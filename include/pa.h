@@ -614,7 +614,11 @@ PA_API pa_status pa_latent_decode(void *out, const void *q, int32_t q_dtype, int
  *                  stream-ordered.  It holds the expanded keys, rounded to
  *                  the cache's type, and values, rounded to fp16 times a power
  *                  of two for every 32 tokens of a head (1 where fp16 holds
- *                  them well): 512 bytes a head and token.
+ *                  them well): 512 bytes a head and token.  A value is off by
+ *                  up to 2^-11 of itself or 2^-21 of its 32 tokens' largest,
+ *                  a weight by 2^-11 of itself or 2^-32 of the row's largest
+ *                  (times the distance of its tokens' power of two from the
+ *                  largest one that the row follows).
  * The expansion costs as much as the attention of about 170 new tokens a
  * sequence in the absorbed form; for fewer new tokens over a long context
  * pa_latent_decode is the cheaper call.  The rows of a sequence's tokens must

@@ -40,7 +40,9 @@
 // 1620 are measured and the products alone take 1280.  4095 tokens after 4096,
 // 64 heads: 81 us for the expansion, 661 for the attention; 32 sequences of
 // 16..512 after 1024, 16 heads: 106 and 126 (768 blocks of about 20 us, five
-// rounds of the SMs and a few of a sixth).  Tried: stages of 128 keys with one S
+// rounds of the SMs and a few of a sixth).  That is at 2070 MHz: call after call
+// the power limit takes the clock to 1.75 and 1.7 GHz, and the two together
+// from 732 to 793 and from 222 to 244 us.  Tried: stages of 128 keys with one S
 // buffer a tile (733 us for the 684: the softmax is then in the chain), a third
 // of q in tensor memory (747), blocks that go on to the next range (697),
 // stages fetched into L2 ahead (even), loads before the block's first barrier
